@@ -9,14 +9,11 @@
 #include <cstdio>
 #include <mutex>
 
-#include "fp8bw.h"
-#include "launch.h"
+#include "api_common.h"
 
-#define FP8BW_API extern "C" __attribute__((visibility("default")))
+namespace fp8bw {
 
-namespace {
-
-thread_local char g_msg[512];
+static thread_local char g_msg[512];
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -33,22 +30,12 @@ int ok() {
 
 // The device error word: set by kernels when a bounded wait expires or a
 // device-side argument check fails; read and cleared by fp8bw_sync_status.
-__device__ int g_error_word;
-
-struct DeviceState {
-  bool probed = false;
-  bool supported = false;
-  int num_sms = 0;
-  int* error_word = nullptr;
-  char why[160] = {0};
-};
+static __device__ int g_error_word;
 
 constexpr int kMaxDevices = 64;
-std::mutex g_mu;
-DeviceState g_dev[kMaxDevices];
+static std::mutex g_mu;
+static DeviceState g_dev[kMaxDevices];
 
-// Checks (once per device) that the current device is compute capability
-// 10.3 and resolves the address of its error word.
 int current_device(DeviceState** out) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -84,27 +71,10 @@ int current_device(DeviceState** out) {
   return FP8BW_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
-
-bool dim_ok(int64_t d, int64_t mult) { return d > 0 && d <= kMaxDim && d % mult == 0; }
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
-}
-
 int launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(FP8BW_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
   return ok();
 }
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-}  // namespace
-
-namespace fp8bw {
 
 void* tensor_map_encoder() {
   static void* fn = nullptr;
@@ -121,6 +91,8 @@ void* tensor_map_encoder() {
 }
 
 }  // namespace fp8bw
+
+using namespace fp8bw;
 
 // ============================================================ quantizers
 

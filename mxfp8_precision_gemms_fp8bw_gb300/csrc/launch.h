@@ -88,6 +88,93 @@ constexpr size_t kStaticScratchBytes = size_t{16} << 20;
 cudaError_t static_scratch_address(void** out);
 cudaError_t launch_mx_grouped_gemm(const MxGroupedGemmArgs& args, cudaStream_t st);
 
+// ---- operators around the experts' products (moe_*.cu)
+
+struct MoeRouteArgs {
+  const void* logits;  // fp32 or bf16 [M, E]
+  bool bf16;
+  const float* bias;   // may be null
+  int64_t M, E, top_k, groups, groups_kept, group_top;
+  int score, renorm;
+  float scale;
+  int32_t* experts;    // forward outputs
+  float* weights;
+  const float* dweights;  // backward, when dlogits is set
+  const int32_t* experts_in;
+  void* dlogits;
+  int* status;
+};
+cudaError_t launch_moe_route(const MoeRouteArgs& args, cudaStream_t st);
+
+struct MoePlanArgs {
+  const int32_t* experts;
+  int64_t M, E, top_k, P;
+  int32_t* group_end;
+  int32_t* counts;
+  int32_t* row_of;
+  int32_t* src_of;
+  void* workspace;
+  int* status;
+  int num_sms;
+};
+size_t moe_plan_workspace_bytes(int64_t M, int64_t E, int64_t top_k);
+cudaError_t launch_moe_plan(const MoePlanArgs& args, cudaStream_t st);
+
+struct MoeGatherArgs {
+  const uint16_t* x;
+  const float* weights;  // may be null
+  const int32_t* src_of;
+  int64_t M, top_k, P, C;
+  uint8_t* q;
+  uint8_t* e8;
+  uint8_t* qT;  // may be null, with e8T
+  uint8_t* e8T;
+  int mode;
+  int* status;
+  int num_sms;
+};
+cudaError_t launch_moe_gather_quant(const MoeGatherArgs& args, cudaStream_t st);
+
+struct MoeCombineArgs {
+  const uint16_t* y;
+  const float* weights;  // may be null
+  const int32_t* row_of;
+  const uint16_t* base;  // may be null
+  int64_t M, top_k, P, C;
+  uint16_t* out;
+  const uint16_t* dout;  // combine_dweights only
+  float* dweights;
+  int* status;
+};
+cudaError_t launch_moe_combine(const MoeCombineArgs& args, cudaStream_t st);
+cudaError_t launch_moe_combine_dweights(const MoeCombineArgs& args, cudaStream_t st);
+
+struct SwigluArgs {
+  const uint16_t* h;
+  int64_t R, F;
+  uint8_t* aq;
+  uint8_t* ae;
+  uint8_t* aqT;  // may be null, with aeT
+  uint8_t* aeT;
+  uint8_t* hq;  // may be null, with he
+  uint8_t* he;
+  int mode;
+};
+cudaError_t launch_swiglu(const SwigluArgs& args, cudaStream_t st);
+
+struct SwigluBwdArgs {
+  const uint16_t* da;
+  const uint8_t* hq;
+  const uint8_t* he;
+  int64_t R, F;
+  uint8_t* dq;
+  uint8_t* de;
+  uint8_t* dqT;
+  uint8_t* deT;
+  int mode;
+};
+cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& args, cudaStream_t st);
+
 cudaError_t launch_selftest_bounded_wait(uint32_t timeout_us, int* status, cudaStream_t st);
 
 // cuTensorMapEncodeTiled, resolved once through the runtime's driver entry

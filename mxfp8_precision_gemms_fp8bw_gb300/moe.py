@@ -1,0 +1,155 @@
+"""A mixture-of-experts layer in MXFP8: the operators around the experts' products and the layer they make.
+
+Each function allocates its outputs, runs on the current stream and returns
+without waiting; the work is in libfp8bw's kernels (``include/fp8bw_moe.h`` has
+the formulas).  For ``linear``'s grouped GEMMs, ``Plan.group_end`` is the group
+table and ``MxRows`` holds their operands.
+
+    experts, weights = route(logits, top_k)          x -> experts of each token
+    p = plan(experts, num_experts)                   rows of the experts
+    rows = dispatch(x, p)                            MX codes of the gathered tokens
+    a, kept = swiglu(h)                              h = [gate | up] of the first product
+    out = combine(y, weights, p)                     y the second product
+
+and each has its ``..._backward``.  ``MxMoEFFN`` is the layer.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import binding as B
+from . import linear as L
+from . import moe_binding as MB
+
+_U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+_SCORES = {"softmax": MB.SCORE_SOFTMAX, "sigmoid": MB.SCORE_SIGMOID}
+
+
+def _score(name: str) -> int:
+    if name not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {name!r}")
+    return _SCORES[name]
+
+
+# ------------------------------------------------------------------ routing
+
+def route(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None = None, score: str = "softmax",
+          renormalize: bool = True, scale: float = 1.0, groups: int = 1, groups_kept: int = 1, group_top: int = 1):
+    """The ``top_k`` experts of each token (int32 [M, top_k], best first) and
+    their fp32 weights, from router logits [M, E] in fp32 or bf16.  ``bias``
+    (fp32 [E]) shifts the choice and not the weights; -inf logits or biases
+    mask experts, and a token left with fewer than ``top_k`` gets expert -1
+    with weight 0 in the rest."""
+    M = logits.shape[0]
+    experts = torch.empty((M, top_k), dtype=_I32, device=logits.device)
+    weights = torch.empty((M, top_k), dtype=_F32, device=logits.device)
+    MB.fp8bw_moe_route(logits, bias, top_k, experts, weights, groups, groups_kept, group_top, _score(score),
+                       renormalize, scale)
+    return experts, weights
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """Gradient of the logits (their dtype) from that of ``route``'s weights."""
+    dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    MB.fp8bw_moe_route_bwd(dweights, logits, experts, dlogits, _score(score), renormalize, scale)
+    return dlogits
+
+
+# ------------------------------------------------------------------ rows of the experts
+
+@dataclass
+class Plan:
+    """Where the entries (token, choice) of a batch go among the experts' rows."""
+    group_end: torch.Tensor   # int32 [E]: end of each expert's rows, multiples of 32; the last is the row count P
+    counts: torch.Tensor      # int32 [E]: entries of each expert
+    row_of: torch.Tensor      # int32 [M, top_k]: an entry's row, -1 without one
+    src_of: torch.Tensor      # int32 [P]: a row's entry (token * top_k + choice), -1 for an empty row
+
+    @property
+    def rows(self) -> int:
+        return self.src_of.shape[0]
+
+
+@dataclass
+class MxRows:
+    """MX codes of a matrix [R, C] in the layouts the grouped GEMMs read."""
+    q: torch.Tensor                     # e4m3 [R, C]
+    e8: torch.Tensor                    # E8M0 [R, C/32]
+    qT: torch.Tensor | None = None      # e4m3 [C, R]
+    e8T: torch.Tensor | None = None     # E8M0 [C, R/32]
+
+
+def _mx_rows(R: int, C: int, device, colwise: bool = True) -> MxRows:
+    e = lambda *shape: torch.empty(shape, dtype=_U8, device=device)  # noqa: E731
+    return MxRows(e(R, C), e(R, C // 32), *((e(C, R), e(C, R // 32)) if colwise else ()))
+
+
+def plan(experts: torch.Tensor, num_experts: int) -> Plan:
+    """Sorts the entries of ``experts`` (int32 [M, top_k]; -1: no expert) into
+    groups of whole 32-row blocks, without the host learning the counts."""
+    M, top_k = experts.shape
+    dev = experts.device
+    P = MB.fp8bw_moe_plan_rows(M, num_experts, top_k)
+    if P == 0:
+        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid plan dims: experts {tuple(experts.shape)} of {num_experts}")
+    e = lambda *shape: torch.empty(shape, dtype=_I32, device=dev)  # noqa: E731
+    p = Plan(e(num_experts), e(num_experts), e(M, top_k), e(P))
+    ws = torch.empty(MB.fp8bw_moe_plan_workspace_bytes(M, num_experts, top_k), dtype=_U8, device=dev)
+    MB.fp8bw_moe_plan(experts, num_experts, p.group_end, p.counts, p.row_of, p.src_of, ws)
+    return p
+
+
+def dispatch(x: torch.Tensor, p: Plan, colwise: bool = True, mode: int = B.MX_RCEIL) -> MxRows:
+    """MX codes of the experts' rows of x (bf16 [M, C]); ``colwise`` adds the
+    layout the weight gradient reads."""
+    out = _mx_rows(p.rows, x.shape[1], x.device, colwise)
+    MB.mxfp8_moe_gather_quant(x, None, p.src_of, p.row_of.shape[1], out.q, out.e8, out.qT, out.e8T, mode)
+    return out
+
+
+def dispatch_backward(drows: torch.Tensor, p: Plan) -> torch.Tensor:
+    """Gradient of ``dispatch``'s x from that of its rows (bf16 [P, C])."""
+    return combine(drows, None, p)
+
+
+def combine(y: torch.Tensor, weights: torch.Tensor | None, p: Plan, base: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = base[t] + the sum of token t's rows of y (bf16 [P, C]) times
+    their weights (fp32 [M, top_k]; None: one each)."""
+    out = torch.empty((p.row_of.shape[0], y.shape[1]), dtype=_BF16, device=y.device)
+    MB.fp8bw_moe_combine(y, weights, p.row_of, base, out)
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, p: Plan, mode: int = B.MX_RCEIL):
+    """Gradients of ``combine``: that of y as MX codes in both layouts, and
+    that of the weights."""
+    dy = _mx_rows(p.rows, dout.shape[1], dout.device)
+    MB.mxfp8_moe_gather_quant(dout, weights, p.src_of, p.row_of.shape[1], dy.q, dy.e8, dy.qT, dy.e8T, mode)
+    dweights = torch.empty_like(weights, memory_format=torch.contiguous_format)
+    MB.fp8bw_moe_combine_dweights(dout, y, p.row_of, dweights)
+    return dy, dweights
+
+
+# ------------------------------------------------------------------ gated activation
+
+def swiglu(h: torch.Tensor, keep: bool = True, colwise: bool = True, mode: int = B.MX_RCEIL):
+    """a = silu(gate) * up of h = [gate | up] (bf16 [R, 2F]) as MX codes, and,
+    with ``keep``, h's own rowwise codes: the 8-bit activation checkpoint that
+    ``swiglu_backward`` works from (None without)."""
+    R, F = h.shape[0], h.shape[1] // 2
+    a = _mx_rows(R, F, h.device, colwise)
+    kept = _mx_rows(R, 2 * F, h.device, colwise=False) if keep else None
+    MB.mxfp8_swiglu(h, a.q, a.e8, a.qT, a.e8T, *((kept.q, kept.e8) if keep else (None, None)), mode=mode)
+    return a, kept
+
+
+def swiglu_backward(da: torch.Tensor, kept: MxRows, mode: int = B.MX_RCEIL) -> MxRows:
+    """Gradient of ``swiglu``'s h as MX codes in both layouts, from da
+    (bf16 [R, F]) and the kept codes."""
+    R, F = da.shape
+    dh = _mx_rows(R, 2 * F, da.device)
+    MB.mxfp8_swiglu_bwd(da, kept.q, kept.e8, dh.q, dh.e8, dh.qT, dh.e8T, mode)
+    return dh
