@@ -153,3 +153,110 @@ def swiglu_backward(da: torch.Tensor, kept: MxRows, mode: int = B.MX_RCEIL) -> M
     dh = _mx_rows(R, 2 * F, da.device)
     MB.mxfp8_swiglu_bwd(da, kept.q, kept.e8, dh.q, dh.e8, dh.qT, dh.e8T, mode)
     return dh
+
+
+# ------------------------------------------------------------------ the layer
+
+def _grouped(kind: int, a, a_e8, b, b_e8, p: Plan, N: int, K: int, out: torch.Tensor) -> torch.Tensor:
+    G, P = p.group_end.shape[0], p.rows
+    ws = B.alloc_grouped_workspace(kind, G, P, N, K, out.device)
+    B.mxfp8_grouped_gemm(kind, a, a_e8, b, b_e8, p.group_end, G, P, N, K, out, ws)
+    return out
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, top_k, score, renormalize, scale, groups, groups_kept, group_top):
+        experts, weights = route(logits, top_k, bias=bias, score=score, renormalize=renormalize, scale=scale,
+                                 groups=groups, groups_kept=groups_kept, group_top=group_top)
+        ctx.how = dict(score=score, renormalize=renormalize, scale=scale)
+        ctx.save_for_backward(logits, experts)
+        ctx.mark_non_differentiable(experts)
+        return experts, weights
+
+    @staticmethod
+    def backward(ctx, _, dweights):
+        logits, experts = ctx.saved_tensors
+        return (route_backward(dweights.contiguous(), logits, experts, **ctx.how),) + (None,) * 8
+
+
+class _Experts(torch.autograd.Function):
+    """sum over a token's experts of weight * W2 (silu(Wg x) * Wu x), with [Wg; Wu] = w13.
+
+    Kept for backward: the colwise MX codes of the gathered tokens and of the
+    activation, h as rowwise codes, the weights' codes and y, the only bf16
+    one (the weights' gradient reads it)."""
+
+    @staticmethod
+    def forward(ctx, x, weights, experts, w13, w2, mode, counts):
+        E, F2, C = w13.shape
+        F = F2 // 2
+        train = any(ctx.needs_input_grad)
+        p = plan(experts, E)
+        counts.append(p.counts)
+        rows = dispatch(x, p, colwise=train, mode=mode)
+        q13, q2 = L.mx_quantize_experts(w13, mode), L.mx_quantize_experts(w2, mode)
+        bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
+        h = _grouped(B.GROUPED_FWD, rows.q, rows.e8, q13.q_row, q13.e8_row, p, F2, C, bf(p.rows, F2))
+        a, kept = swiglu(h, keep=train, colwise=train, mode=mode)
+        y = _grouped(B.GROUPED_FWD, a.q, a.e8, q2.q_row, q2.e8_row, p, C, F, bf(p.rows, C))
+        if train:
+            ctx.plan, ctx.mode, ctx.weights, ctx.y, ctx.kept = p, mode, weights, y, kept
+            ctx.xT, ctx.aT = (rows.qT, rows.e8T), (a.qT, a.e8T)
+            ctx.w13T, ctx.w2T = (q13.qT_col, q13.e8_col), (q2.qT_col, q2.e8_col)
+        return combine(y, weights, p)
+
+    @staticmethod
+    def backward(ctx, dout):
+        p, mode = ctx.plan, ctx.mode
+        E, C, F2 = ctx.w13T[0].shape
+        F = F2 // 2
+        bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=dout.device)  # noqa: E731
+        dy, dweights = combine_backward(dout.contiguous(), ctx.y, ctx.weights, p, mode=mode)
+        da = _grouped(B.GROUPED_DGRAD, dy.q, dy.e8, *ctx.w2T, p, C, F, bf(p.rows, F))
+        dw2 = _grouped(B.GROUPED_WGRAD, dy.qT, dy.e8T, *ctx.aT, p, C, F, bf(E, C, F))
+        dh = swiglu_backward(da, ctx.kept, mode=mode)
+        drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, *ctx.w13T, p, F2, C, bf(p.rows, C))
+        dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, *ctx.xT, p, F2, C, bf(E, F2, C))
+        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None
+
+
+class MxMoEFFN(torch.nn.Module):
+    """Mixture of gated feed-forward experts whose products run in MXFP8.
+
+    Inputs are 2D bf16 CUDA tensors [tokens, dim]; dim and hidden must be
+    multiples of 256, the token count is free.  The router's logits are a
+    plain fp32 product.  ``balance`` (a buffer, not a parameter) is the bias
+    that shifts the choice of experts; ``update_balance`` moves it against the
+    loads of the last forward.  ``route``'s keyword arguments are taken too.
+    """
+
+    def __init__(self, dim: int, hidden: int, num_experts: int, top_k: int, *, score: str = "softmax",
+                 renormalize: bool = True, scale: float = 1.0, groups: int = 1, groups_kept: int = 1,
+                 group_top: int = 1, mode: int = B.MX_RCEIL, device=None):
+        super().__init__()
+        new = lambda *shape, dtype=_BF16: torch.nn.Parameter(  # noqa: E731
+            torch.nn.init.normal_(torch.empty(shape, dtype=dtype, device=device), std=0.02))
+        self.router = new(num_experts, dim, dtype=_F32)
+        self.w13 = new(num_experts, 2 * hidden, dim)
+        self.w2 = new(num_experts, dim, hidden)
+        self.register_buffer("balance", torch.zeros(num_experts, dtype=_F32, device=device))
+        self.how = (top_k, score, renormalize, scale, groups, groups_kept, group_top)
+        self.mode = mode
+        self.counts = None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        logits = torch.nn.functional.linear(x.float(), self.router)
+        experts, weights = _Route.apply(logits, self.balance, *self.how)
+        counts = []
+        out = _Experts.apply(x, weights, experts, self.w13, self.w2, self.mode, counts)
+        self.counts = counts[0]
+        return out
+
+    @torch.no_grad()
+    def update_balance(self, rate: float = 1e-3) -> None:
+        """Moves each expert's bias one step up where its last load was below the mean, down where above."""
+        if self.counts is None:
+            raise RuntimeError("update_balance needs a forward pass first")
+        load = self.counts.float()
+        self.balance += rate * torch.sign(load.mean() - load)
