@@ -224,13 +224,45 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   }
 }
 
-// One CTA: per-warp counts of contiguous runs of entries, their prefix over
-// warps and experts, then the entries take their rows in order.
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+// ---------------------------------------------------------------- plan
+//
+// A stable counting sort in which the entries keep their order: block b owns
+// `chunk` consecutive entries and each of its warps a consecutive run of
+// them, so an entry's row is the start of its group + the entries of its
+// expert in earlier blocks + in earlier warps + before it in its own run (the
+// lower lanes of the same 32 that have the same expert, by a warp match).
+// Nothing depends on the order in which blocks or atomics come.
+//
+// It reads and writes a few bytes per entry and is bound by latency: one
+// launch while one block suffices, two beyond that (counts per block, then
+// the rows), of which the second starts under the first and counts its own
+// runs meanwhile.
+constexpr int kPlanChunk = 2048;     // entries per block, more where that would be over kPlanBlocks blocks
+constexpr int kPlanBlocks = 152;
+constexpr int kPlanHistogram = 1 << 14;  // blocks * E of the counts: every block reads them all
 
-__device__ __forceinline__ int checked_expert(const int32_t* experts, int64_t i, int64_t N, int E, int* status) {
-  int e = i < N ? experts[i] : -1;
+struct PlanShape {
+  int64_t N, chunk, P;
+  int E, blocks, threads;
+};
+
+PlanShape plan_shape(int64_t M, int64_t E, int64_t top_k, int64_t P) {
+  PlanShape s{};
+  s.N = M * top_k;
+  s.E = static_cast<int>(E);
+  s.P = P;
+  int64_t blocks = (s.N + kPlanChunk - 1) / kPlanChunk;
+  if (blocks > kPlanBlocks) blocks = kPlanBlocks;
+  if (blocks > kPlanHistogram / E) blocks = kPlanHistogram / E;
+  if (s.N <= 2 * kPlanChunk) blocks = 1;
+  s.blocks = static_cast<int>(blocks);
+  s.chunk = (s.N + blocks - 1) / blocks;
+  s.threads = s.N <= 1024 ? 256 : 1024;
+  return s;
+}
+
+__device__ __forceinline__ int checked_expert(const int32_t* experts, int64_t i, int64_t last, int E, int* status) {
+  int e = i < last ? experts[i] : -1;
   if (e < -1 || e >= E) {
     atomicExch(status, kStatusShape);
     e = -1;
@@ -238,63 +270,121 @@ __device__ __forceinline__ int checked_expert(const int32_t* experts, int64_t i,
   return e;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-    plan_kernel(const int32_t* __restrict__ experts, int64_t N, int E, int64_t P, int32_t* __restrict__ group_end,
-                int32_t* __restrict__ counts, int32_t* __restrict__ row_of, int32_t* __restrict__ src_of, int* status) {
-  extern __shared__ int next[];  // [kPlanWarps][E], then the group starts [E + 1]
-  int* start = next + kPlanWarps * E;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) next[i] = 0;
+__global__ void __launch_bounds__(1024)
+    plan_count_kernel(const int32_t* __restrict__ experts, PlanShape s, int32_t* __restrict__ histogram, int* status) {
+  extern __shared__ int smem[];  // [E]
+  asm volatile("griddepcontrol.launch_dependents;");
+  for (int e = threadIdx.x; e < s.E; e += s.threads) smem[e] = 0;
   __syncthreads();
-  const int64_t run = (N + kPlanThreads - 1) / kPlanThreads * 32;  // entries of a warp
-  const int64_t first = warp * run, last = min(first + run, N);
+  const int64_t first = blockIdx.x * s.chunk, last = min(first + s.chunk, s.N);
+  for (int64_t i0 = first + (threadIdx.x & ~31); i0 < last; i0 += s.threads) {
+    const int lane = threadIdx.x & 31;
+    const int e = checked_expert(experts, i0 + lane, last, s.E, status);
+    const uint32_t same = __match_any_sync(kAll, e);
+    if (e >= 0 && lane == __ffs(same) - 1) atomicAdd(&smem[e], __popc(same));
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < s.E; e += s.threads) histogram[static_cast<int64_t>(blockIdx.x) * s.E + e] = smem[e];
+}
+
+__global__ void __launch_bounds__(1024)
+    plan_place_kernel(const int32_t* __restrict__ experts, PlanShape s, const int32_t* histogram,
+                      int32_t* __restrict__ group_end, int32_t* __restrict__ counts, int32_t* __restrict__ row_of,
+                      int32_t* __restrict__ src_of, int* status) {
+  extern __shared__ int smem[];
+  const int E = s.E, T = s.threads, warps = T / 32;
+  int* next = smem;               // [warps][E]: the next row of an expert in a warp's run, less the group's start
+  int* start = next + warps * E;  // [E + 1]: the groups' first rows
+  int* total = start + E + 1;     // [E]: entries of an expert
+  int* sums = total + E;          // [33]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < warps * E; i += T) next[i] = 0;
+  for (int e = tid; e < E; e += T) total[e] = start[e] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * s.chunk, last = min(first + s.chunk, s.N);
+  const int64_t run = (s.chunk + T - 1) / T * 32;
+  const int64_t mine = first + warp * run, end = min(mine + run, last);
   int* my = next + warp * E;
-  for (int64_t i0 = first; i0 < last; i0 += 32) {
-    const int e = checked_expert(experts, i0 + lane, last, E, status);
+  for (int64_t i0 = mine; i0 < end; i0 += 32) {
+    const int e = checked_expert(experts, i0 + lane, end, E, status);
     const uint32_t same = __match_any_sync(kAll, e);
     if (e >= 0 && lane == __ffs(same) - 1) my[e] += __popc(same);
     __syncwarp();
   }
-  __syncthreads();
-  for (int e = tid; e < E; e += kPlanThreads) {
-    int sum = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int c = next[w * E + e];
-      next[w * E + e] = sum;
-      sum += c;
-    }
-    counts[e] = sum;
-    start[e + 1] = sum;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int at = 0;
-    start[0] = 0;
-    for (int e = 0; e < E; ++e) {
-      at += (start[e + 1] + 31) & ~31;
-      start[e + 1] = at;
-      group_end[e] = e + 1 == E ? static_cast<int>(P) : at;
+  if (s.blocks > 1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Threads in E columns and as many slices of blocks as fit; start[] holds
+    // the entries in earlier blocks for now.
+    const int slices = max(T / E, 1);
+    for (int i = tid; i < slices * E; i += T) {
+      const int e = i % E;
+      int all = 0, before = 0;
+      for (int b = i / E; b < s.blocks; b += slices) {
+        const int c = histogram[b * E + e];
+        all += c;
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&start[e], before);
     }
   }
   __syncthreads();
-  for (int64_t i0 = first; i0 < last; i0 += 32) {
+  // Exclusive prefix over the warps, then over the experts' padded totals.
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += T) {
+    const int e = e0 + tid;
+    int padded = 0;
+    if (e < E) {
+      int sum = start[e];
+      for (int w = 0; w < warps; ++w) {
+        const int c = next[w * E + e];
+        next[w * E + e] = sum;
+        sum += c;
+      }
+      if (s.blocks == 1) total[e] = sum;
+      padded = (total[e] + 31) & ~31;
+    }
+    int up = padded;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(kAll, up, o);
+      if (lane >= o) up += t;
+    }
+    if (lane == 31) sums[warp] = up;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      before += w < warp ? sums[w] : 0;
+      all += sums[w];
+    }
+    if (e < E) start[e] = carry + before + up - padded;
+    carry += all;
+    if (e == E - 1) start[E] = carry;
+    if (e < E && blockIdx.x == 0) {
+      counts[e] = total[e];
+      group_end[e] = e + 1 == E ? static_cast<int>(s.P) : start[e] + padded;
+    }
+    __syncthreads();
+  }
+  for (int64_t i0 = mine; i0 < end; i0 += 32) {
     const int64_t i = i0 + lane;
-    const int e = checked_expert(experts, i, last, E, status);
+    const int e = checked_expert(experts, i, end, E, status);
     const uint32_t same = __match_any_sync(kAll, e);
     int row = -1;
     if (e >= 0) row = start[e] + my[e] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (e >= 0 && lane == __ffs(same) - 1) my[e] += __popc(same);
     __syncwarp();
-    if (i < last) row_of[i] = row;
+    if (i < end) row_of[i] = row;
     if (row >= 0) src_of[row] = static_cast<int32_t>(i);
   }
-  __syncthreads();
-  for (int e = warp; e < E; e += kPlanWarps) {  // the empty rows of each group
-    const int used = start[e] + next[(kPlanWarps - 1) * E + e];
+  // The empty rows: of each group, and behind the last one.
+  const int workers = warps * s.blocks;
+  for (int e = blockIdx.x * warps + warp; e < E; e += workers) {
+    const int used = start[e] + total[e];
     if (used + lane < start[e + 1]) src_of[used + lane] = -1;
   }
-  for (int64_t p = start[E] + tid; p < P; p += kPlanThreads) src_of[p] = -1;
+  for (int64_t p = start[E] + static_cast<int64_t>(blockIdx.x) * T + tid; p < s.P; p += static_cast<int64_t>(s.blocks) * T)
+    src_of[p] = -1;
 }
 
 template <typename T>
@@ -335,18 +425,37 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t st) {
   return a.bf16 ? route_of<uint16_t>(a, st) : route_of<float>(a, st);
 }
 
-size_t moe_plan_workspace_bytes(int64_t, int64_t, int64_t) { return 16; }
+size_t moe_plan_workspace_bytes(int64_t M, int64_t E, int64_t top_k) {
+  const PlanShape s = plan_shape(M, E, top_k, 0);
+  const size_t n = s.blocks > 1 ? static_cast<size_t>(s.blocks) * s.E * sizeof(int32_t) : 0;
+  return n < 16 ? 16 : n;
+}
 
 cudaError_t launch_moe_plan(const MoePlanArgs& a, cudaStream_t st) {
-  const size_t smem = (kPlanWarps * a.E + a.E + 1) * sizeof(int);
+  const PlanShape s = plan_shape(a.M, a.E, a.top_k, a.P);
+  int32_t* histogram = static_cast<int32_t*>(a.workspace);
+  if (s.blocks > 1) {
+    plan_count_kernel<<<s.blocks, s.threads, s.E * sizeof(int), st>>>(a.experts, s, histogram, a.status);
+    if (const cudaError_t e = cudaGetLastError()) return e;
+  }
+  const size_t smem = (s.threads / 32 * s.E + 2 * s.E + 1 + 33) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  plan_kernel<<<1, kPlanThreads, smem, st>>>(a.experts, a.M * a.top_k, static_cast<int>(a.E), a.P, a.group_end,
-                                             a.counts, a.row_of, a.src_of, a.status);
-  return cudaGetLastError();
+  cudaLaunchAttribute overlap{};
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.blocks);
+  cfg.blockDim = dim3(s.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = s.blocks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, plan_place_kernel, a.experts, s, static_cast<const int32_t*>(histogram), a.group_end,
+                            a.counts, a.row_of, a.src_of, a.status);
 }
 
 }  // namespace fp8bw
