@@ -2,42 +2,131 @@
 // them back into the tokens.
 #include "common.cuh"
 #include "launch.h"
-#include "mx_fp32.cuh"
+#include "mx_tile.cuh"
 
 namespace fp8bw {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
-// 32 rows x 128 columns per CTA.
-__global__ void __launch_bounds__(128)
+constexpr int kGatherWarps = 8;
+
+// MX codes of gathered rows, v_p = w_p * x[src_p / top_k], in both layouts.
+// A warp's 32-row x 64-column tile lives in registers (mx_tile.cuh); a block
+// has 128 x 128, so that the codes of its rows and of its columns fill whole
+// 128-byte lines.  The blocks of one 128-column stripe run one after another:
+// a token is gathered up to top_k times, and a stripe of x stays in L2 between
+// them (with the columns fastest, 5120 of them and 8192 x 2 entries, x came
+// from DRAM 1.9 times).  Without weights the maxima are taken on packed bf16 pairs.  With
+// them the max of a row block is still the bf16 max, times |w| (rounding is
+// monotonic, so the product of the max is the max of the products); a column
+// block mixes weights and takes the max of the fp32 products.
+template <bool kWeighted>
+__global__ void __launch_bounds__(kGatherWarps * 32)
     gather_quant_kernel(const uint16_t* __restrict__ x, const float* __restrict__ weights,
-                        const int32_t* __restrict__ src_of, int64_t entries, int top_k, int64_t P, int64_t C,
+                        const int32_t* __restrict__ src_of, uint32_t entries, uint32_t top_k, int P, int C, int bands,
                         uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ qT,
                         uint8_t* __restrict__ e8T, int mode, int* status) {
-  __shared__ QuantTile t;
+  __shared__ ScaleTile scales;
+  const TileLane t = tile_lane();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 128, r0 = static_cast<int64_t>(blockIdx.x) * 32;
-  const int64_t col = c0 + 4 * lane;
+  const int stripe = blockIdx.x / bands;
+  const int c0 = stripe * 128 + (warp & 1) * 64 + t.cg * 8;
+  const int64_t rb = static_cast<int64_t>(blockIdx.x - stripe * bands) * 128;
+  const int64_t rw = rb + (warp >> 1) * 32;
+  const bool row_ok = rw < P;            // P % 32 == 0: a warp's rows are all in or all out
+  const bool col_ok = row_ok && c0 < C;  // C % 32 == 0: so are the columns of a block
+  // Lane l looks up row l of the warp's 32; shuffles hand the token and the weight to the row's eight lanes.
+  const uint32_t src = row_ok ? static_cast<uint32_t>(src_of[rw + lane]) : 0xffffffffu;
+  uint32_t token = 0xffffffffu;
+  float weight = 0.f;
+  if (src < entries) {
+    token = src / top_k;
+    if (kWeighted) weight = weights[src];
+  } else if (src != 0xffffffffu) {
+    atomicExch(status, kStatusShape);
+  }
+  uint4 v[8];
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = warp * 8 + i;
-    int64_t src = src_of[r0 + r];
-    if (src < -1 || src >= entries) {
-      atomicExch(status, kStatusShape);
-      src = -1;
+    const uint32_t from = __shfl_sync(kAll, token, t.rg * 8 + i);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (from != 0xffffffffu && col_ok) v[i] = ld_once_v4(x + (static_cast<uint64_t>(from) * static_cast<uint32_t>(C) + c0));
+  }
+  const uint32_t round = mx_round_f32(mode);
+  const int64_t r0 = rw + t.rg * 8;
+  uint8_t* qrow = q + r0 * C + c0;
+  // Where the thread's row and column blocks have their scale bytes.
+  uint8_t* erow = &scales.row[(warp >> 1) * 32 + t.rg * 8][(warp & 1) * 2 + (t.cg >> 2)];
+  uint8_t* ecol = &scales.col[(warp & 1) * 64 + t.cg * 8][warp >> 1];
+  uint8_t* qcol = qT + static_cast<int64_t>(c0) * P + r0;
+
+  uint32_t m[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) m[p] = block_absmax2<1>(fold2(absmax2_of8(v[2 * p]), absmax2_of8(v[2 * p + 1])));
+
+  if (!kWeighted) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t e = mx_t_bf16((m[i >> 1] >> (i & 1) * 16) & 0x7FFFu, round);
+      if (col_ok) st_codes8(qrow + static_cast<int64_t>(i) * C, codes8_row(v[i], mx_mul_bf16(e)));
+      if ((t.cg & 3) == 0) erow[4 * i] = mx_e8_of(e);
     }
-    uint2 w = make_uint2(0, 0);
-    if (src >= 0 && col < C) w = *reinterpret_cast<const uint2*>(x + src / top_k * C + col);
-    const float m = weights != nullptr && src >= 0 ? weights[src] : 1.f;
-    t.v[r][4 * lane] = bf16lo_to_f32(w.x) * m;
-    t.v[r][4 * lane + 1] = bf16hi_to_f32(w.x) * m;
-    t.v[r][4 * lane + 2] = bf16lo_to_f32(w.y) * m;
-    t.v[r][4 * lane + 3] = bf16hi_to_f32(w.y) * m;
+    if (qT != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // columns c0 + 2k and c0 + 2k + 1
+      uint32_t a = word_of(v[0], k);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) a = absmax2(a, word_of(v[i], k));
+      a = block_absmax2<8>(a);
+      const uint32_t lo = mx_t_bf16(a & 0x7FFFu, round), hi = mx_t_bf16((a >> 16) & 0x7FFFu, round);
+      if (col_ok) {
+        st_codes8(qcol + static_cast<int64_t>(2 * k) * P, codes8_col<0>(v, k, mx_mul_bf16(lo)));
+        st_codes8(qcol + static_cast<int64_t>(2 * k + 1) * P, codes8_col<1>(v, k, mx_mul_bf16(hi)));
+      }
+      if (t.rg == 0) {
+        ecol[8 * k] = mx_e8_of(lo);
+        ecol[8 * k + 4] = mx_e8_of(hi);
+      }
+    }
+    }
+  } else {
+  // Weighted: the products stay in registers between the two passes.
+  float2 f[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float w = __shfl_sync(kAll, weight, t.rg * 8 + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[i][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[i], k)), make_float2(w, w));
+    const uint32_t amax = (i & 1) ? f32_bits_hi(m[i >> 1]) : f32_bits_lo(m[i >> 1]);
+    const uint32_t e = mx_t(abs_bits(__uint_as_float(amax) * w), round);
+    if (col_ok) st_codes8(qrow + static_cast<int64_t>(i) * C, codes8(f[i], mx_mul_of(e)));
+    if ((t.cg & 3) == 0) erow[4 * i] = mx_e8_of(e);
+  }
+  if (qT != nullptr) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 lo[4] = {{f[0][k].x, f[1][k].x}, {f[2][k].x, f[3][k].x}, {f[4][k].x, f[5][k].x}, {f[6][k].x, f[7][k].x}};
+    const float2 hi[4] = {{f[0][k].y, f[1][k].y}, {f[2][k].y, f[3][k].y}, {f[4][k].y, f[5][k].y}, {f[6][k].y, f[7][k].y}};
+    // The exponent grows with the max, so the lanes reduce both columns' exponents in one word.
+    uint32_t e = mx_t(abs_bits(absmax8(0.f, lo)), round) | mx_t(abs_bits(absmax8(0.f, hi)), round) << 16;
+    e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 8));
+    e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 16));
+    const uint32_t el = e & 0xFFFFu, eh = e >> 16;
+    if (col_ok) {
+      st_codes8(qcol + static_cast<int64_t>(2 * k) * P, codes8(lo, mx_mul_of(el)));
+      st_codes8(qcol + static_cast<int64_t>(2 * k + 1) * P, codes8(hi, mx_mul_of(eh)));
+    }
+    if (t.rg == 0) {
+      ecol[8 * k] = mx_e8_of(el);
+      ecol[8 * k + 4] = mx_e8_of(eh);
+    }
+  }
+  }
   }
   __syncthreads();
-  const uint32_t round = mx_round_f32(mode);
-  quant_tile_rows(t, r0, c0, C, C, q, e8, round);
-  if (qT != nullptr) quant_tile_cols(t, r0, c0, P, C, qT, e8T, round);
+  put_scales(scales.row, threadIdx.x, rb, P, e8, stripe * 4, C / 32);
+  if (qT != nullptr) put_scales(scales.col, threadIdx.x - 128, stripe * 128, C, e8T, static_cast<int>(rb / 32), P / 32);
 }
 
 __device__ __forceinline__ int64_t checked_row(const int32_t* row_of, int64_t i, int64_t P, int* status) {
@@ -109,10 +198,15 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 cudaError_t launch_moe_gather_quant(const MoeGatherArgs& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.P / 32), static_cast<unsigned>((a.C + 127) / 128));
-  gather_quant_kernel<<<grid, 128, 0, st>>>(a.x, a.weights, a.src_of, a.M * a.top_k, static_cast<int>(a.top_k), a.P,
-                                            a.C, a.q, a.e8, a.qT, a.e8T, a.mode, a.status);
-  return cudaGetLastError();
+  const int64_t bands = (a.P + 127) / 128, blocks = bands * ((a.C + 127) / 128);
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel) {
+    kernel<<<dim3(static_cast<unsigned>(blocks)), kGatherWarps * 32, 0, st>>>(
+        a.x, a.weights, a.src_of, static_cast<uint32_t>(a.M * a.top_k), static_cast<uint32_t>(a.top_k),
+        static_cast<int>(a.P), static_cast<int>(a.C), static_cast<int>(bands), a.q, a.e8, a.qT, a.e8T, a.mode, a.status);
+    return cudaGetLastError();
+  };
+  return a.weights != nullptr ? go(gather_quant_kernel<true>) : go(gather_quant_kernel<false>);
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs& a, cudaStream_t st) {
