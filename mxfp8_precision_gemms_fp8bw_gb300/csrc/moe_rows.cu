@@ -10,123 +10,209 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 
 constexpr int kGatherWarps = 8;
+constexpr int kGatherCtasPerSm = 3;
+
+// Where a block has its copies: two tiles of x, and of four tiles in turn the
+// rows' tokens (-1: none) and weights, because the tokens are needed two
+// tiles before the weights are done with.
+struct GatherSmem {
+  uint4 x[2][128][16];
+  ScaleTile scales[2];
+  int32_t token[4][16][8];  // row r at [r % 16][r / 16]: the eight that a thread copies are contiguous
+  float weight[4][128];
+};
+
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
 
 // MX codes of gathered rows, v_p = w_p * x[src_p / top_k], in both layouts.
-// A warp's 32-row x 64-column tile lives in registers (mx_tile.cuh); a block
-// has 128 x 128, so that the codes of its rows and of its columns fill whole
-// 128-byte lines.  The blocks of one 128-column stripe run one after another:
-// a token is gathered up to top_k times, and a stripe of x stays in L2 between
-// them (with the columns fastest, 5120 of them and 8192 x 2 entries, x came
-// from DRAM 1.9 times).  Without weights the maxima are taken on packed bf16 pairs.  With
-// them the max of a row block is still the bf16 max, times |w| (rounding is
-// monotonic, so the product of the max is the max of the products); a column
-// block mixes weights and takes the max of the fp32 products.
+//
+// Bound by memory first and by the conversions next (two per element), so the
+// kernel keeps both busy: blocks are persistent, three to an SM, and walk
+// 128 x 128 tiles whose rows of x are on their way (cp.async, one 16-byte
+// chunk at a time, zeros where there is no row) while the tile before is
+// converted, and whose tokens were looked up one tile earlier still.  A
+// thread takes its 8 x 8 part into registers (mx_tile.cuh) and reads nothing
+// twice; 128 x 128 because the codes of a tile's rows and of its columns
+// then fill whole 128-byte lines.  Without weights the maxima and products are taken
+// on packed bf16 pairs.  With them the max of a row block is still the bf16
+// max, times |w| (rounding is monotonic, so the product of the max is the max
+// of the products); a column block mixes weights and takes the max of the
+// fp32 products.
+//
+// The tiles of one 128-column stripe come one after another: a token is
+// gathered up to top_k times, and a stripe of x stays in L2 between them
+// (with the columns fastest, 5120 of them and 8192 x 2 entries, x came from
+// DRAM 1.9 times).
 template <bool kWeighted>
-__global__ void __launch_bounds__(kGatherWarps * 32)
+__global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtasPerSm)
     gather_quant_kernel(const uint16_t* __restrict__ x, const float* __restrict__ weights,
                         const int32_t* __restrict__ src_of, uint32_t entries, uint32_t top_k, int P, int C, int bands,
-                        uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ qT,
+                        int tiles, uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ qT,
                         uint8_t* __restrict__ e8T, int mode, int* status) {
-  __shared__ ScaleTile scales;
+  extern __shared__ __align__(128) uint8_t gather_smem[];
+  GatherSmem& sm = *reinterpret_cast<GatherSmem*>(gather_smem);
   const TileLane t = tile_lane();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stripe = blockIdx.x / bands;
-  const int c0 = stripe * 128 + (warp & 1) * 64 + t.cg * 8;
-  const int64_t rb = static_cast<int64_t>(blockIdx.x - stripe * bands) * 128;
-  const int64_t rw = rb + (warp >> 1) * 32;
-  const bool row_ok = rw < P;            // P % 32 == 0: a warp's rows are all in or all out
-  const bool col_ok = row_ok && c0 < C;  // C % 32 == 0: so are the columns of a block
-  // Lane l looks up row l of the warp's 32; shuffles hand the token and the weight to the row's eight lanes.
-  const uint32_t src = row_ok ? static_cast<uint32_t>(src_of[rw + lane]) : 0xffffffffu;
-  uint32_t token = 0xffffffffu;
-  float weight = 0.f;
-  if (src < entries) {
-    token = src / top_k;
-    if (kWeighted) weight = weights[src];
-  } else if (src != 0xffffffffu) {
-    atomicExch(status, kStatusShape);
-  }
-  uint4 v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t from = __shfl_sync(kAll, token, t.rg * 8 + i);
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (from != 0xffffffffu && col_ok) v[i] = ld_once_v4(x + (static_cast<uint64_t>(from) * static_cast<uint32_t>(C) + c0));
-  }
+  const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t round = mx_round_f32(mode);
-  const int64_t r0 = rw + t.rg * 8;
-  uint8_t* qrow = q + r0 * C + c0;
-  // Where the thread's row and column blocks have their scale bytes.
-  uint8_t* erow = &scales.row[(warp >> 1) * 32 + t.rg * 8][(warp & 1) * 2 + (t.cg >> 2)];
-  uint8_t* ecol = &scales.col[(warp & 1) * 64 + t.cg * 8][warp >> 1];
-  uint8_t* qcol = qT + static_cast<int64_t>(c0) * P + r0;
 
-  uint32_t m[4];
+  struct Tile {
+    int stripe, band;  // band -1: behind the last tile
+  };
+  auto tile_at = [&](int n) {  // the block's n-th
+    const uint32_t i = blockIdx.x + static_cast<uint32_t>(n) * gridDim.x;
+    if (i >= static_cast<uint32_t>(tiles)) return Tile{0, -1};
+    const uint32_t stripe = i / static_cast<uint32_t>(bands);
+    return Tile{static_cast<int>(stripe), static_cast<int>(i - stripe * static_cast<uint32_t>(bands))};
+  };
+  // The entry of row `tid` of a tile, and its note in the tables of tile n.
+  auto look_up = [&](Tile w) {
+    const int64_t row = static_cast<int64_t>(w.band) * 128 + tid;
+    return tid < 128 && w.band >= 0 && row < P ? static_cast<uint32_t>(src_of[row]) : 0xffffffffu;
+  };
+  auto note = [&](int n, uint32_t src) {
+    if (tid >= 128) return;
+    int32_t token = -1;
+    float weight = 0.f;
+    if (src < entries) {
+      token = static_cast<int32_t>(src / top_k);
+      if (kWeighted) weight = weights[src];
+    } else if (src != 0xffffffffu) {
+      atomicExch(status, kStatusShape);
+    }
+    sm.token[n & 3][tid & 15][tid >> 4] = token;
+    if (kWeighted) sm.weight[n & 3][tid] = weight;
+  };
+  // Starts the copies of tile n: thread i has chunk i % 16 of rows i / 16 + 16 j.
+  auto fetch = [&](int n, Tile w) {
+    if (w.band >= 0) {
+      const int chunk = tid & 15, r0 = tid >> 4;
+      const int c = w.stripe * 128 + chunk * 8;
+      const uint16_t* xc = x + (c < C ? c : 0);
+      const int4 a = *reinterpret_cast<const int4*>(&sm.token[n & 3][r0][0]);
+      const int4 b = *reinterpret_cast<const int4*>(&sm.token[n & 3][r0][4]);
+      const int32_t token[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int p = 0; p < 4; ++p) m[p] = block_absmax2<1>(fold2(absmax2_of8(v[2 * p]), absmax2_of8(v[2 * p + 1])));
+      for (int j = 0; j < 8; ++j) {
+        const bool live = token[j] >= 0 && c < C;
+        cp_async_16(&sm.x[n & 1][r0 + 16 * j][chunk],
+                    xc + static_cast<uint64_t>(live ? token[j] : 0) * static_cast<uint32_t>(C), live);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto finish_scales = [&](int n, Tile w) {  // of tile n, once every thread has written its bytes
+    put_scales(sm.scales[n & 1].row, tid, static_cast<int64_t>(w.band) * 128, P, e8, w.stripe * 4, C / 32);
+    if (qT != nullptr)
+      put_scales(sm.scales[n & 1].col, tid - 128, static_cast<int64_t>(w.stripe) * 128, C, e8T, w.band * 4, P / 32);
+  };
 
-  if (!kWeighted) {
+  Tile last{0, -1}, now = tile_at(0), next = tile_at(1);
+  note(0, look_up(now));
+  note(1, look_up(next));
+  __syncthreads();
+  fetch(0, now);
+  int n = 0;
+  for (; now.band >= 0; ++n) {
+    // Tile n has landed; everyone has left tile n - 1 and its buffers.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    fetch(n + 1, next);
+    const Tile after = tile_at(n + 2);
+    const uint32_t src = look_up(after);
+    if (n > 0) finish_scales(n - 1, last);
+
+    const int rt = (warp >> 1) * 32 + t.rg * 8, ct = (warp & 1) * 64 + t.cg * 8;  // the thread's part of the tile
+    const int c0 = now.stripe * 128 + ct;
+    const int64_t r0 = static_cast<int64_t>(now.band) * 128 + rt;
+    const bool live = r0 < P && c0 < C;  // P and C % 32 == 0: blocks are all in or all out
+    uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t e = mx_t_bf16((m[i >> 1] >> (i & 1) * 16) & 0x7FFFu, round);
-      if (col_ok) st_codes8(qrow + static_cast<int64_t>(i) * C, codes8_row(v[i], mx_mul_bf16(e)));
-      if ((t.cg & 3) == 0) erow[4 * i] = mx_e8_of(e);
-    }
-    if (qT != nullptr) {
+    for (int i = 0; i < 8; ++i) v[i] = sm.x[n & 1][rt + i][ct / 8];
+    uint8_t* qrow = q + r0 * C + c0;
+    uint8_t* qcol = qT + static_cast<int64_t>(c0) * P + r0;
+
+    uint32_t m[4];  // of rows 2 p and 2 p + 1
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // columns c0 + 2k and c0 + 2k + 1
-      uint32_t a = word_of(v[0], k);
+    for (int p = 0; p < 4; ++p) m[p] = block_absmax2<1>(fold2(absmax2_of8(v[2 * p]), absmax2_of8(v[2 * p + 1])));
+
+    uint32_t cm[4];  // of columns 2 k and 2 k + 1
+    if (!kWeighted && qT != nullptr) {  // before the conversions, which hide the shuffles
 #pragma unroll
-      for (int i = 1; i < 8; ++i) a = absmax2(a, word_of(v[i], k));
-      a = block_absmax2<8>(a);
-      const uint32_t lo = mx_t_bf16(a & 0x7FFFu, round), hi = mx_t_bf16((a >> 16) & 0x7FFFu, round);
-      if (col_ok) {
-        st_codes8(qcol + static_cast<int64_t>(2 * k) * P, codes8_col<0>(v, k, mx_mul_bf16(lo)));
-        st_codes8(qcol + static_cast<int64_t>(2 * k + 1) * P, codes8_col<1>(v, k, mx_mul_bf16(hi)));
+      for (int k = 0; k < 4; ++k) {
+        cm[k] = word_of(v[0], k);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) cm[k] = absmax2(cm[k], word_of(v[i], k));
       }
-      if (t.rg == 0) {
-        ecol[8 * k] = mx_e8_of(lo);
-        ecol[8 * k + 4] = mx_e8_of(hi);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cm[k] = block_absmax2<8>(cm[k]);
+    }
+    uint32_t rb[4], cb[4] = {};  // scale bytes of the thread's rows and columns, two to a word
+    if (!kWeighted) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t e = mx_t2(m[p], round), mul = mx_mul2(e), byte = e - 0x00080008u;
+        st_codes8(qrow, codes8_row(v[2 * p], __byte_perm(mul, 0, 0x1010)), live);
+        st_codes8(qrow + C, codes8_row(v[2 * p + 1], __byte_perm(mul, 0, 0x3232)), live);
+        qrow += 2 * static_cast<int64_t>(C);
+        rb[p] = byte;
+      }
+      if (qT != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // columns c0 + 2k and c0 + 2k + 1
+          const uint32_t e = mx_t2(cm[k], round), byte = e - 0x00080008u;
+          const CodePair codes = codes8_cols(v, k, mx_mul2(e));
+          st_codes8(qcol, codes.lo, live);
+          st_codes8(qcol + P, codes.hi, live);
+          qcol += 2 * static_cast<int64_t>(P);
+          cb[k] = byte;
+        }
+      }
+    } else {
+      // The products stay in registers between the two passes.
+      float2 f[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = sm.weight[n & 3][rt + i];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[i][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[i], k)), make_float2(w, w));
+        const uint32_t amax = (i & 1) ? f32_bits_hi(m[i >> 1]) : f32_bits_lo(m[i >> 1]);
+        const uint32_t e = mx_t(abs_bits(__uint_as_float(amax) * w), round);
+        st_codes8(qrow, codes8(f[i], mx_mul_of(e)), live);
+        qrow += C;
+        rb[i >> 1] = (i & 1) ? rb[i >> 1] | (e - 8u) << 16 : e - 8u;
+      }
+      if (qT != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float lo[8], hi[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            lo[i] = f[i][k].x;
+            hi[i] = f[i][k].y;
+          }
+          // The exponent grows with the max, so the lanes reduce both columns' exponents in one word.
+          uint32_t e = mx_t(abs_bits(absmax_of8(lo)), round) | mx_t(abs_bits(absmax_of8(hi)), round) << 16;
+          e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 8));
+          e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 16));
+          cb[k] = e - 0x00080008u;
+          const uint32_t el = e & 0xFFFFu, eh = e >> 16;
+          st_codes8(qcol, codes8(lo, mx_mul_of(el)), live);
+          st_codes8(qcol + P, codes8(hi, mx_mul_of(eh)), live);
+          qcol += 2 * static_cast<int64_t>(P);
+        }
       }
     }
-    }
-  } else {
-  // Weighted: the products stay in registers between the two passes.
-  float2 f[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float w = __shfl_sync(kAll, weight, t.rg * 8 + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[i][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[i], k)), make_float2(w, w));
-    const uint32_t amax = (i & 1) ? f32_bits_hi(m[i >> 1]) : f32_bits_lo(m[i >> 1]);
-    const uint32_t e = mx_t(abs_bits(__uint_as_float(amax) * w), round);
-    if (col_ok) st_codes8(qrow + static_cast<int64_t>(i) * C, codes8(f[i], mx_mul_of(e)));
-    if ((t.cg & 3) == 0) erow[4 * i] = mx_e8_of(e);
-  }
-  if (qT != nullptr) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 lo[4] = {{f[0][k].x, f[1][k].x}, {f[2][k].x, f[3][k].x}, {f[4][k].x, f[5][k].x}, {f[6][k].x, f[7][k].x}};
-    const float2 hi[4] = {{f[0][k].y, f[1][k].y}, {f[2][k].y, f[3][k].y}, {f[4][k].y, f[5][k].y}, {f[6][k].y, f[7][k].y}};
-    // The exponent grows with the max, so the lanes reduce both columns' exponents in one word.
-    uint32_t e = mx_t(abs_bits(absmax8(0.f, lo)), round) | mx_t(abs_bits(absmax8(0.f, hi)), round) << 16;
-    e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 8));
-    e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 16));
-    const uint32_t el = e & 0xFFFFu, eh = e >> 16;
-    if (col_ok) {
-      st_codes8(qcol + static_cast<int64_t>(2 * k) * P, codes8(lo, mx_mul_of(el)));
-      st_codes8(qcol + static_cast<int64_t>(2 * k + 1) * P, codes8(hi, mx_mul_of(eh)));
-    }
-    if (t.rg == 0) {
-      ecol[8 * k] = mx_e8_of(el);
-      ecol[8 * k + 4] = mx_e8_of(eh);
-    }
-  }
-  }
+    put_bytes(sm.scales[n & 1], rt, ct, rb, cb);
+    note(n + 2, src);
+    last = now;
+    now = next;
+    next = after;
   }
   __syncthreads();
-  put_scales(scales.row, threadIdx.x, rb, P, e8, stripe * 4, C / 32);
-  if (qT != nullptr) put_scales(scales.col, threadIdx.x - 128, stripe * 128, C, e8T, static_cast<int>(rb / 32), P / 32);
+  finish_scales(n - 1, last);
 }
 
 __device__ __forceinline__ int64_t checked_row(const int32_t* row_of, int64_t i, int64_t P, int* status) {
@@ -198,12 +284,16 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 cudaError_t launch_moe_gather_quant(const MoeGatherArgs& a, cudaStream_t st) {
-  const int64_t bands = (a.P + 127) / 128, blocks = bands * ((a.C + 127) / 128);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t bands = (a.P + 127) / 128, tiles = bands * ((a.C + 127) / 128);
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t cap = static_cast<int64_t>(a.num_sms) * kGatherCtasPerSm;
   auto go = [&](auto kernel) {
-    kernel<<<dim3(static_cast<unsigned>(blocks)), kGatherWarps * 32, 0, st>>>(
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(GatherSmem));
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), kGatherWarps * 32, sizeof(GatherSmem), st>>>(
         a.x, a.weights, a.src_of, static_cast<uint32_t>(a.M * a.top_k), static_cast<uint32_t>(a.top_k),
-        static_cast<int>(a.P), static_cast<int>(a.C), static_cast<int>(bands), a.q, a.e8, a.qT, a.e8T, a.mode, a.status);
+        static_cast<int>(a.P), static_cast<int>(a.C), static_cast<int>(bands), static_cast<int>(tiles), a.q, a.e8, a.qT,
+        a.e8T, a.mode, a.status);
     return cudaGetLastError();
   };
   return a.weights != nullptr ? go(gather_quant_kernel<true>) : go(gather_quant_kernel<false>);

@@ -1,103 +1,261 @@
 // The gated activation of an MXFP8 layer, held as MX codes, with its input
 // kept in 8 bits, and its gradient from those 8 bits.
+//
+// Both kernels read each element once and write only codes (8.1 bytes per
+// element of a forward, 8.2 backward), with some twenty instructions per
+// element between; they are bound by memory where enough warps overlap the
+// two.  A thread has 4 rows x 8 columns, a warp 32 x 32: lane 4 i + j has
+// rows 4 i + [0, 4) and columns 8 j + [0, 8), so that a row block is four
+// neighbouring lanes and a column block the eight lanes 4 apart.  (8 x 8 per
+// thread, as in the gather, needs twice the registers here, where two
+// operands and one or two results are live at once.)  A block has 64 x 128.
 #include "common.cuh"
 #include "launch.h"
-#include "mx_fp32.cuh"
+#include "mx_tile.cuh"
 
 namespace fp8bw {
 namespace {
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return 1.f / (1.f + __expf(-x)); }
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kRows = 64, kCols = 128, kThreads = 256;
 
-// 32 rows x 128 columns of a per CTA; the same columns of gate and up.
-__global__ void __launch_bounds__(128)
+// 1 / (1 + 2^(-x log2 e)): a few ulp, against the 2^-4 of the codes it goes
+// into; exact 0 and 1 far out, NaN for NaN.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+struct Lane {
+  int rt, ct;  // first row and column of the thread in the block's tile
+};
+__device__ __forceinline__ Lane lane_of() {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  return Lane{(warp >> 2) * 32 + (lane >> 2) * 4, (warp & 3) * 32 + (lane & 3) * 8};
+}
+
+// Scale bytes of the tile, gathered to go out as words (see ScaleTile).
+struct alignas(8) Scales {
+  uint8_t row[4][kRows];  // [block][row]
+  uint8_t col[2][kCols];  // [block][column]
+};
+// t's of the thread's four rows and eight columns, two to a word.
+__device__ __forceinline__ void put_row_bytes(Scales& s, Lane l, uint32_t t01, uint32_t t23) {
+  if ((l.ct & 31) == 0)
+    *reinterpret_cast<uint32_t*>(&s.row[l.ct / 32][l.rt]) = __byte_perm(t01 - 0x00080008u, t23 - 0x00080008u, 0x6420);
+}
+__device__ __forceinline__ void put_col_bytes(Scales& s, Lane l, const uint32_t (&t)[4]) {
+  if ((l.rt & 31) == 0)
+    *reinterpret_cast<uint2*>(&s.col[l.rt / 32][l.ct]) =
+        make_uint2(__byte_perm(t[0] - 0x00080008u, t[1] - 0x00080008u, 0x6420),
+                   __byte_perm(t[2] - 0x00080008u, t[3] - 0x00080008u, 0x6420));
+}
+// Row scales of the tile at rows r0, blocks b0 .. b0 + 3 of e8 [R][per_row], by threads 0 to 63.
+__device__ __forceinline__ void flush_rows(const Scales& s, int64_t r0, int64_t R, uint8_t* __restrict__ e8,
+                                           int64_t b0, int64_t b_end, int64_t per_row) {
+  const int i = threadIdx.x;
+  if (i >= kRows || r0 + i >= R) return;
+  uint8_t* to = e8 + (r0 + i) * per_row + b0;
+  if ((reinterpret_cast<uintptr_t>(to) & 3) == 0 && b0 + 4 <= b_end) {
+    *reinterpret_cast<uint32_t*>(to) = s.row[0][i] | s.row[1][i] << 8 | s.row[2][i] << 16 | uint32_t{s.row[3][i]} << 24;
+  } else {
+    for (int b = 0; b < 4 && b0 + b < b_end; ++b) to[b] = s.row[b][i];
+  }
+}
+// Column scales of the tile at columns c0, blocks b0 and b0 + 1 of e8T [C][per_col], by threads 128 to 255.
+__device__ __forceinline__ void flush_cols(const Scales& s, int64_t c0, int64_t c_end, uint8_t* __restrict__ e8T,
+                                           int64_t b0, int64_t per_col) {
+  const int i = static_cast<int>(threadIdx.x) - 128;
+  if (i < 0 || c0 + i >= c_end) return;
+  uint8_t* to = e8T + (c0 + i) * per_col + b0;
+  if ((per_col & 1) == 0) {
+    *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(s.col[0][i] | s.col[1][i] << 8);
+  } else {
+    to[0] = s.col[0][i];
+    if (b0 + 1 < per_col) to[1] = s.col[1][i];
+  }
+}
+
+// max over a row block's lanes (xor 1, 2) or a column block's (xor 4, 8, 16)
+// of two t's in a word: the exponent grows with the max.
+__device__ __forceinline__ uint32_t row_max2(uint32_t t) {
+  t = __vmaxu2(t, __shfl_xor_sync(kAll, t, 1));
+  return __vmaxu2(t, __shfl_xor_sync(kAll, t, 2));
+}
+__device__ __forceinline__ uint32_t col_max2(uint32_t t) {
+  t = __vmaxu2(t, __shfl_xor_sync(kAll, t, 4));
+  t = __vmaxu2(t, __shfl_xor_sync(kAll, t, 8));
+  return __vmaxu2(t, __shfl_xor_sync(kAll, t, 16));
+}
+__device__ __forceinline__ uint32_t pair_t(float lo, float hi, uint32_t round) {
+  return mx_t(abs_bits(lo), round) | mx_t(abs_bits(hi), round) << 16;
+}
+
+// Both layouts of the thread's 4 x 8 values: q at (row, col) of a matrix with
+// `ld` columns, qT transposed with R rows (qT may be null).
+__device__ __forceinline__ void quant_4x8(const float2 (&v)[4][4], Lane l, bool live, uint32_t round, uint8_t* qrow,
+                                          int64_t ld, uint8_t* qcol, int64_t R, Scales& s) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m[i] = absmax3(absmax3(v[i][0].x, v[i][0].y, v[i][1].x), absmax3(v[i][1].y, v[i][2].x, v[i][2].y),
+                   absmax3(v[i][3].x, v[i][3].y, 0.f));
+  uint32_t t[2] = {row_max2(pair_t(m[0], m[1], round)), row_max2(pair_t(m[2], m[3], round))};
+  uint32_t tc[4];
+  if (qcol != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      tc[k] = pair_t(absmax3(absmax3(v[0][k].x, v[1][k].x, v[2][k].x), v[3][k].x, 0.f),
+                     absmax3(absmax3(v[0][k].y, v[1][k].y, v[2][k].y), v[3][k].y, 0.f), round);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tc[k] = col_max2(tc[k]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t e = (i & 1) ? t[i >> 1] >> 16 : t[i >> 1] & 0xFFFFu;
+    st_codes8(qrow + i * ld, codes8(v[i], mx_mul_of(e)), live);
+  }
+  put_row_bytes(s, l, t[0], t[1]);
+  if (qcol == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = mx_mul_of(tc[k] & 0xFFFFu), b = mx_mul_of(tc[k] >> 16);
+    if (live) {
+      *reinterpret_cast<uint32_t*>(qcol + (2 * k) * R) = e4m3x4(v[0][k].x * a, v[1][k].x * a, v[2][k].x * a, v[3][k].x * a);
+      *reinterpret_cast<uint32_t*>(qcol + (2 * k + 1) * R) =
+          e4m3x4(v[0][k].y * b, v[1][k].y * b, v[2][k].y * b, v[3][k].y * b);
+    }
+  }
+  put_col_bytes(s, l, tc);
+}
+
+// Rowwise codes of four rows of packed bf16.
+__device__ __forceinline__ void keep_4x8(const uint4 (&v)[4], Lane l, bool live, uint32_t round, uint8_t* qrow,
+                                         int64_t ld, Scales& s) {
+  uint32_t t[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) t[p] = mx_t2(block_absmax2<1>(fold2(absmax2_of8(v[2 * p]), absmax2_of8(v[2 * p + 1]))), round);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    st_codes8(qrow + i * ld, codes8_row(v[i], __byte_perm(mx_mul2(t[i >> 1]), 0, (i & 1) ? 0x3232 : 0x1010)), live);
+  put_row_bytes(s, l, t[0], t[1]);
+}
+
+__global__ void __launch_bounds__(kThreads)
     swiglu_kernel(const uint16_t* __restrict__ h, int64_t R, int64_t F, uint8_t* __restrict__ aq,
                   uint8_t* __restrict__ ae, uint8_t* __restrict__ aqT, uint8_t* __restrict__ aeT,
                   uint8_t* __restrict__ hq, uint8_t* __restrict__ he, int mode) {
-  __shared__ QuantTile gate, up;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 128, r0 = static_cast<int64_t>(blockIdx.x) * 32;
-  const int64_t col = c0 + 4 * lane;
+  __shared__ Scales sa, sg, su;
+  const Lane l = lane_of();
+  const int64_t tr = static_cast<int64_t>(blockIdx.x) * kRows, tc = static_cast<int64_t>(blockIdx.y) * kCols;
+  const int64_t r0 = tr + l.rt, c0 = tc + l.ct;
+  const bool live = r0 < R && c0 < F;  // R and F % 32 == 0: blocks are all in or all out
   const uint32_t round = mx_round_f32(mode);
-  for (int i = 0; i < 8; ++i) {
-    const int r = warp * 8 + i;
-    uint2 g = make_uint2(0, 0), u = g;
-    if (col < F) {
-      g = *reinterpret_cast<const uint2*>(h + (r0 + r) * 2 * F + col);
-      u = *reinterpret_cast<const uint2*>(h + (r0 + r) * 2 * F + F + col);
-    }
-    const float gv[4] = {bf16lo_to_f32(g.x), bf16hi_to_f32(g.x), bf16lo_to_f32(g.y), bf16hi_to_f32(g.y)};
-    const float uv[4] = {bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y)};
-    for (int k = 0; k < 4; ++k) {
-      gate.v[r][4 * lane + k] = gv[k];
-      up.v[r][4 * lane + k] = uv[k];
-    }
-  }
-  __syncthreads();
+  uint4 g[4], u[4];
+  const uint16_t* hp = h + (live ? r0 * 2 * F + c0 : 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = ld_once_v4(hp + i * 2 * F, live);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = ld_once_v4(hp + i * 2 * F + F, live);
   if (hq != nullptr) {
-    quant_tile_rows(gate, r0, c0, 2 * F, F, hq, he, round);
-    quant_tile_rows(up, r0, F + c0, 2 * F, 2 * F, hq, he, round);
+    keep_4x8(g, l, live, round, hq + r0 * 2 * F + c0, 2 * F, sg);
+    keep_4x8(u, l, live, round, hq + r0 * 2 * F + F + c0, 2 * F, su);
   }
-  for (int i = threadIdx.x; i < 32 * 128; i += 128) {
-    const float g = gate.v[i >> 7][i & 127];
-    gate.v[i >> 7][i & 127] = g * sigmoid_f32(g) * up.v[i >> 7][i & 127];
-  }
+  float2 a[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = bf16x2_to_f32(word_of(g[i], k)), y = bf16x2_to_f32(word_of(u[i], k));
+      a[i][k] = make_float2(x.x * sigmoid_f32(x.x) * y.x, x.y * sigmoid_f32(x.y) * y.y);
+    }
+  quant_4x8(a, l, live, round, aq + r0 * F + c0, F, aqT != nullptr ? aqT + c0 * R + r0 : nullptr, R, sa);
   __syncthreads();
-  quant_tile_rows(gate, r0, c0, F, F, aq, ae, round);
-  if (aqT != nullptr) quant_tile_cols(gate, r0, c0, R, F, aqT, aeT, round);
+  flush_rows(sa, tr, R, ae, tc / 32, F / 32, F / 32);
+  if (hq != nullptr) {
+    flush_rows(sg, tr, R, he, tc / 32, F / 32, F / 16);
+    flush_rows(su, tr, R, he, F / 32 + tc / 32, F / 16, F / 16);
+  }
+  if (aqT != nullptr) flush_cols(sa, tc, F, aeT, tr / 32, R / 32);
 }
 
-__global__ void __launch_bounds__(128)
+// Eight values of codes times a scale.
+__device__ __forceinline__ void decode8(uint2 c, float scale, float2 (&v)[4]) {
+  const float2 s = make_float2(scale, scale);
+  v[0] = __fmul2_rn(e4m3x2_to_f32(c.x & 0xFFFFu), s);
+  v[1] = __fmul2_rn(e4m3x2_to_f32(c.x >> 16), s);
+  v[2] = __fmul2_rn(e4m3x2_to_f32(c.y & 0xFFFFu), s);
+  v[3] = __fmul2_rn(e4m3x2_to_f32(c.y >> 16), s);
+}
+
+__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p, bool live) {
+  uint2 r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y)
+      : "l"(p), "r"(static_cast<int>(live)));
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads)
     swiglu_bwd_kernel(const uint16_t* __restrict__ da, const uint8_t* __restrict__ hq, const uint8_t* __restrict__ he,
                       int64_t R, int64_t F, uint8_t* __restrict__ dq, uint8_t* __restrict__ de,
                       uint8_t* __restrict__ dqT, uint8_t* __restrict__ deT, int mode) {
-  __shared__ QuantTile dgate, dup;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * 128, r0 = static_cast<int64_t>(blockIdx.x) * 32;
-  const int64_t col = c0 + 4 * lane;
+  __shared__ Scales sg, su;
+  const Lane l = lane_of();
+  const int64_t tr = static_cast<int64_t>(blockIdx.x) * kRows, tc = static_cast<int64_t>(blockIdx.y) * kCols;
+  const int64_t r0 = tr + l.rt, c0 = tc + l.ct;
+  const bool live = r0 < R && c0 < F;
   const uint32_t round = mx_round_f32(mode);
-  for (int i = 0; i < 8; ++i) {
-    const int r = warp * 8 + i;
-    const int64_t row = r0 + r;
-    float g[4] = {}, u[4] = {}, d[4] = {};
-    if (col < F) {
-      const uint32_t gc = *reinterpret_cast<const uint32_t*>(hq + row * 2 * F + col);
-      const uint32_t uc = *reinterpret_cast<const uint32_t*>(hq + row * 2 * F + F + col);
-      const float gs = e8m0_value(he[row * (2 * F / 32) + col / 32]);
-      const float us = e8m0_value(he[row * (2 * F / 32) + (F + col) / 32]);
-      const uint2 w = *reinterpret_cast<const uint2*>(da + row * F + col);
-      const float2 g0 = e4m3x2_to_f32(gc & 0xFFFF), g1 = e4m3x2_to_f32(gc >> 16);
-      const float2 u0 = e4m3x2_to_f32(uc & 0xFFFF), u1 = e4m3x2_to_f32(uc >> 16);
-      g[0] = g0.x * gs, g[1] = g0.y * gs, g[2] = g1.x * gs, g[3] = g1.y * gs;
-      u[0] = u0.x * us, u[1] = u0.y * us, u[2] = u1.x * us, u[3] = u1.y * us;
-      d[0] = bf16lo_to_f32(w.x), d[1] = bf16hi_to_f32(w.x), d[2] = bf16lo_to_f32(w.y), d[3] = bf16hi_to_f32(w.y);
-    }
+  uint4 d[4];
+  uint2 gc[4], uc[4];
+  uint8_t ge[4], ue[4];
+  const uint8_t* hp = hq + (live ? r0 * 2 * F + c0 : 0);
+  const uint8_t* ep = he + (live ? r0 * (F / 16) + c0 / 32 : 0);
+  const uint16_t* dp = da + (live ? r0 * F + c0 : 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    gc[i] = ld_codes8(hp + i * 2 * F, live);
+    uc[i] = ld_codes8(hp + i * 2 * F + F, live);
+    d[i] = ld_once_v4(dp + i * F, live);
+    ge[i] = live ? ep[i * (F / 16)] : 0;
+    ue[i] = live ? ep[i * (F / 16) + F / 32] : 0;
+  }
+  float2 dg[4][4], du[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 g[4], u[4];
+    decode8(gc[i], e8m0_value(ge[i]), g);
+    decode8(uc[i], e8m0_value(ue[i]), u);
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float sig = sigmoid_f32(g[k]);
-      dgate.v[r][4 * lane + k] = d[k] * u[k] * sig * (1.f + g[k] * (1.f - sig));
-      dup.v[r][4 * lane + k] = d[k] * g[k] * sig;
+      const float2 x = bf16x2_to_f32(word_of(d[i], k));
+      const float sx = sigmoid_f32(g[k].x), sy = sigmoid_f32(g[k].y);
+      const float px = x.x * sx, py = x.y * sy;
+      du[i][k] = make_float2(px * g[k].x, py * g[k].y);
+      dg[i][k] = make_float2(px * u[k].x * fmaf(g[k].x, 1.f - sx, 1.f), py * u[k].y * fmaf(g[k].y, 1.f - sy, 1.f));
     }
   }
+  quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sg);
+  quant_4x8(du, l, live, round, dq + r0 * 2 * F + F + c0, 2 * F, dqT + (F + c0) * R + r0, R, su);
   __syncthreads();
-  quant_tile_rows(dgate, r0, c0, 2 * F, F, dq, de, round);
-  quant_tile_rows(dup, r0, F + c0, 2 * F, 2 * F, dq, de, round);
-  quant_tile_cols(dgate, r0, c0, R, F, dqT, deT, round);
-  quant_tile_cols(dup, r0, F + c0, R, 2 * F, dqT, deT, round);
+  flush_rows(sg, tr, R, de, tc / 32, F / 32, F / 16);
+  flush_rows(su, tr, R, de, F / 32 + tc / 32, F / 16, F / 16);
+  flush_cols(sg, tc, F, deT, tr / 32, R / 32);
+  flush_cols(su, F + tc, 2 * F, deT, tr / 32, R / 32);
 }
 
 dim3 grid_of(int64_t R, int64_t F) {
-  return dim3(static_cast<unsigned>(R / 32), static_cast<unsigned>((F + 127) / 128));
+  return dim3(static_cast<unsigned>((R + kRows - 1) / kRows), static_cast<unsigned>((F + kCols - 1) / kCols));
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t st) {
-  swiglu_kernel<<<grid_of(a.R, a.F), 128, 0, st>>>(a.h, a.R, a.F, a.aq, a.ae, a.aqT, a.aeT, a.hq, a.he, a.mode);
+  swiglu_kernel<<<grid_of(a.R, a.F), kThreads, 0, st>>>(a.h, a.R, a.F, a.aq, a.ae, a.aqT, a.aeT, a.hq, a.he, a.mode);
   return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t st) {
-  swiglu_bwd_kernel<<<grid_of(a.R, a.F), 128, 0, st>>>(a.da, a.hq, a.he, a.R, a.F, a.dq, a.de, a.dqT, a.deT, a.mode);
+  swiglu_bwd_kernel<<<grid_of(a.R, a.F), kThreads, 0, st>>>(a.da, a.hq, a.he, a.R, a.F, a.dq, a.de, a.dqT, a.deT, a.mode);
   return cudaGetLastError();
 }
 

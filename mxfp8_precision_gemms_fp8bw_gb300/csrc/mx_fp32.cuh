@@ -40,53 +40,16 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
   return r;
 }
 
+// Four e4m3 codes, a's in the low byte.  One asm block, so that the two
+// 16-bit halves are not widened before they are joined.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return __byte_perm(cvt_e4m3x2(a, b), cvt_e4m3x2(c, d), 0x5410);
-}
-
-// A 32-row x 128-column fp32 tile, quantized both ways by 128 threads.
-struct QuantTile {
-  float v[32][129];
-};
-
-// Rowwise: warp w has rows 8w + [0, 8), lane l columns 4l + [0, 4), so eight
-// lanes hold a block of 32.  Row r0 + r, columns c0 + ... of q [rows, ld].
-__device__ __forceinline__ void quant_tile_rows(const QuantTile& t, int64_t r0, int64_t c0, int64_t ld, int64_t c_end,
-                                                uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint32_t round) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t col = c0 + 4 * lane;
-  for (int i = 0; i < 8; ++i) {
-    const int r = warp * 8 + i;
-    const float a = t.v[r][4 * lane], b = t.v[r][4 * lane + 1], c = t.v[r][4 * lane + 2], d = t.v[r][4 * lane + 3];
-    uint32_t x = mx_t(max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d))), round);
-    for (int o = 1; o < 8; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    const float m = mx_mul_of(x);
-    if (col < c_end) {
-      *reinterpret_cast<uint32_t*>(q + (r0 + r) * ld + col) = e4m3x4(a * m, b * m, c * m, d * m);
-      if ((lane & 7) == 0) e8[(r0 + r) * (ld / 32) + col / 32] = mx_e8_of(x);
-    }
-  }
-}
-
-// Colwise: thread i has column c0 + i, whose 32 rows are one block, written as
-// 32 contiguous bytes of qT [columns, R].
-__device__ __forceinline__ void quant_tile_cols(const QuantTile& t, int64_t r0, int64_t c0, int64_t R, int64_t c_end,
-                                                uint8_t* __restrict__ qT, uint8_t* __restrict__ e8T, uint32_t round) {
-  const int i = threadIdx.x;
-  const int64_t col = c0 + i;
-  if (col >= c_end) return;
-  uint32_t a = 0;
-  for (int r = 0; r < 32; ++r) a = max(a, abs_bits(t.v[r][i]));
-  const uint32_t x = mx_t(a, round);
-  const float m = mx_mul_of(x);
-  uint32_t w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    w[k] = e4m3x4(t.v[4 * k][i] * m, t.v[4 * k + 1][i] * m, t.v[4 * k + 2][i] * m, t.v[4 * k + 3][i] * m);
-  uint4* out = reinterpret_cast<uint4*>(qT + col * R + r0);
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  e8T[col * (R / 32) + r0 / 32] = mx_e8_of(x);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
 }  // namespace fp8bw

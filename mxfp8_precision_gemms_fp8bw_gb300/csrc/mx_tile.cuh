@@ -22,15 +22,21 @@ __device__ __forceinline__ TileLane tile_lane() {
   return TileLane{lane >> 3, lane & 7};
 }
 
-__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+// 16 bytes read once, or zeros where `live` is false (no branch around either).
+__device__ __forceinline__ uint4 ld_once_v4(const void* p, bool live = true) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"(static_cast<int>(live)));
   return r;
 }
-__device__ __forceinline__ void st_codes8(uint8_t* p, uint2 v) {
-  asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+__device__ __forceinline__ void st_codes8(uint8_t* p, uint2 v, bool live) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.global.v2.u32 [%0], {%1, %2};\n\t}" ::"l"(p),
+               "r"(v.x), "r"(v.y), "r"(static_cast<int>(live))
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
@@ -66,76 +72,94 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Of eight, with what is already there.
-__device__ __forceinline__ float absmax8(float m, const float2 (&v)[4]) {
-  m = absmax3(absmax3(m, v[0].x, v[0].y), v[1].x, v[1].y);
-  return absmax3(absmax3(m, v[2].x, v[2].y), v[3].x, v[3].y);
+__device__ __forceinline__ float absmax_of8(const float (&v)[8]) {
+  return absmax3(absmax3(absmax3(v[0], v[1], v[2]), v[3], v[4]), absmax3(v[5], v[6], v[7]), 0.f);
 }
 
-// A bf16 half times the bf16 power of two m in fp32: exact, or rounded once
-// where it falls below the fp32 range; adding -0 keeps the sign of a zero.
-// One instruction on the packed pair, where unpacking first takes two.
-template <int kHi>
-__device__ __forceinline__ float half_times(uint32_t w, uint16_t m) {
-  float r;
-  if (kHi)
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tfma.rn.f32.bf16 %0, hi, %2, %3;\n\t}"
-        : "=f"(r) : "r"(w), "h"(m), "f"(-0.0f));
-  else
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tfma.rn.f32.bf16 %0, lo, %2, %3;\n\t}"
-        : "=f"(r) : "r"(w), "h"(m), "f"(-0.0f));
-  return r;
-}
-
-// The scale rule on a block max held as bf16 magnitude bits (mx_t and
-// mx_mul_of of mx_fp32.cuh, 16 bits down).
-__device__ __forceinline__ uint32_t mx_t_bf16(uint32_t bits, uint32_t round) {
-  return min(max((bits + (round >> 16)) >> 7, 8u), 255u);
-}
-__device__ __forceinline__ uint16_t mx_mul_bf16(uint32_t t) { return static_cast<uint16_t>((262u - t) << 7); }
-
-// e4m3 codes of eight packed bf16 times m, of one row.
-__device__ __forceinline__ uint2 codes8_row(const uint4& v, uint16_t m) {
-  return make_uint2(e4m3x4(half_times<0>(v.x, m), half_times<1>(v.x, m), half_times<0>(v.y, m), half_times<1>(v.y, m)),
-                    e4m3x4(half_times<0>(v.z, m), half_times<1>(v.z, m), half_times<0>(v.w, m), half_times<1>(v.w, m)));
-}
-// The same down column 2 k + kHi of eight rows.
-template <int kHi>
-__device__ __forceinline__ uint2 codes8_col(const uint4 (&v)[8], int k, uint16_t m) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = half_times<kHi>(word_of(v[i], k), m);
-  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-}
-
-// e4m3 codes of eight fp32 values times m.
+// e4m3 codes of eight fp32 values times m, the values of one row in pairs as
+// they were unpacked: two products per instruction.
 __device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float m) {
   const float2 mm = make_float2(m, m);
   const float2 a = __fmul2_rn(v[0], mm), b = __fmul2_rn(v[1], mm), c = __fmul2_rn(v[2], mm), d = __fmul2_rn(v[3], mm);
   return make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y));
 }
+// The same down a column of eight rows, whose values are no register pairs:
+// pairing them up for the two-wide product costs more moves than it saves.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float m) {
+  return make_uint2(e4m3x4(v[0] * m, v[1] * m, v[2] * m, v[3] * m), e4m3x4(v[4] * m, v[5] * m, v[6] * m, v[7] * m));
+}
 
-// Scale bytes of a 128 x 128 tile: of each row's four 32-column blocks, and of
-// each column's four 32-row blocks.  They leave as one word per row or column:
-// as single bytes, straight from the lanes that have them, they took as many
-// L1 tag cycles as all the codes.
-struct ScaleTile {
-  alignas(4) uint8_t row[128][4];
-  alignas(4) uint8_t col[128][4];
+// The scale rule on two block maxima held as bf16 magnitudes in one word (see
+// mx_t; here in 16-bit halves, whose sums cannot carry): both t's.
+__device__ __forceinline__ uint32_t mx_t2(uint32_t w, uint32_t round) {
+  const uint32_t t = (((w & 0x7FFF7FFFu) + (round >> 16) * 0x10001u) >> 7) & 0x01FF01FFu;
+  return __vminu2(__vmaxu2(t, 0x00080008u), 0x00FF00FFu);
+}
+// 2^-E of both as packed bf16.
+__device__ __forceinline__ uint32_t mx_mul2(uint32_t t2) { return (0x01060106u - t2) << 7; }
+
+// Packed bf16 products with powers of two: exact, or, far below the smallest
+// e4m3 code, a zero or subnormal of the same sign.
+__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// e4m3 codes of eight packed bf16 of one row times a packed pair of the scale.
+__device__ __forceinline__ uint2 codes8_row(const uint4& v, uint32_t m2) {
+  const uint32_t a = mul2_bf16(v.x, m2), b = mul2_bf16(v.y, m2), c = mul2_bf16(v.z, m2), d = mul2_bf16(v.w, m2);
+  return make_uint2(e4m3x4(bf16lo_to_f32(a), bf16hi_to_f32(a), bf16lo_to_f32(b), bf16hi_to_f32(b)),
+                    e4m3x4(bf16lo_to_f32(c), bf16hi_to_f32(c), bf16lo_to_f32(d), bf16hi_to_f32(d)));
+}
+// The same down columns 2 k (first) and 2 k + 1 of eight rows, m2 their scales.
+struct CodePair {
+  uint2 lo, hi;
 };
+__device__ __forceinline__ CodePair codes8_cols(const uint4 (&v)[8], int k, uint32_t m2) {
+  uint32_t p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = mul2_bf16(word_of(v[i], k), m2);
+  return CodePair{make_uint2(e4m3x4(bf16lo_to_f32(p[0]), bf16lo_to_f32(p[1]), bf16lo_to_f32(p[2]), bf16lo_to_f32(p[3])),
+                             e4m3x4(bf16lo_to_f32(p[4]), bf16lo_to_f32(p[5]), bf16lo_to_f32(p[6]), bf16lo_to_f32(p[7]))),
+                  make_uint2(e4m3x4(bf16hi_to_f32(p[0]), bf16hi_to_f32(p[1]), bf16hi_to_f32(p[2]), bf16hi_to_f32(p[3])),
+                             e4m3x4(bf16hi_to_f32(p[4]), bf16hi_to_f32(p[5]), bf16hi_to_f32(p[6]), bf16hi_to_f32(p[7])))};
+}
+
+// Scale bytes of a 128 x 128 tile: of the rows' blocks (32 columns each) and of
+// the columns' blocks (32 rows each).  Threads leave eight bytes at a time and
+// they go out as one word per row or column: as single bytes, straight from
+// the lanes that have them, they took as many L1 tag cycles as all the codes.
+struct alignas(8) ScaleTile {
+  uint8_t row[4][128];  // [block][row]
+  uint8_t col[4][128];  // [block][column]
+};
+
+// The bytes of the thread's eight rows and columns, two to a word, from the
+// first lane of each row block and of each column block; rt and ct are the
+// thread's first row and column in the tile.
+__device__ __forceinline__ void put_bytes(ScaleTile& s, int rt, int ct, const uint32_t (&rows)[4],
+                                          const uint32_t (&cols)[4]) {
+  if ((ct & 31) == 0)
+    *reinterpret_cast<uint2*>(&s.row[ct / 32][rt]) =
+        make_uint2(__byte_perm(rows[0], rows[1], 0x6420), __byte_perm(rows[2], rows[3], 0x6420));
+  if ((rt & 31) == 0)
+    *reinterpret_cast<uint2*>(&s.col[rt / 32][ct]) =
+        make_uint2(__byte_perm(cols[0], cols[1], 0x6420), __byte_perm(cols[2], cols[3], 0x6420));
+}
 
 // Line `i` (0 to 127; others do nothing) of one side: entries b0 .. b0 + 3 of
 // line first + i of out [lines][per_line].
-__device__ __forceinline__ void put_scales(const uint8_t (&side)[128][4], int i, int64_t first, int64_t lines,
+__device__ __forceinline__ void put_scales(const uint8_t (&side)[4][128], int i, int64_t first, int64_t lines,
                                            uint8_t* __restrict__ out, int b0, int per_line) {
   if (i < 0 || i >= 128 || first + i >= lines) return;
   uint8_t* to = out + (first + i) * per_line + b0;
   if ((per_line & 3) == 0) {
-    *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(side[i]);
+    *reinterpret_cast<uint32_t*>(to) =
+        side[0][i] | side[1][i] << 8 | side[2][i] << 16 | static_cast<uint32_t>(side[3][i]) << 24;
   } else {
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-      if (b0 + b < per_line) to[b] = side[i][b];
+      if (b0 + b < per_line) to[b] = side[b][i];
   }
 }
 
