@@ -153,55 +153,68 @@ __global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtasPerSm)
     if (!kWeighted) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t e = mx_t2(m[p], round), mul = mx_mul2(e), byte = e - 0x00080008u;
+        const uint32_t e = mx_t2(m[p], round), mul = mx_mul2(e);
         st_codes8(qrow, codes8_row(v[2 * p], __byte_perm(mul, 0, 0x1010)), live);
         st_codes8(qrow + C, codes8_row(v[2 * p + 1], __byte_perm(mul, 0, 0x3232)), live);
         qrow += 2 * static_cast<int64_t>(C);
-        rb[p] = byte;
+        rb[p] = mx_bytes2(e);
       }
       if (qT != nullptr) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // columns c0 + 2k and c0 + 2k + 1
-          const uint32_t e = mx_t2(cm[k], round), byte = e - 0x00080008u;
+          const uint32_t e = mx_t2(cm[k], round);
           const CodePair codes = codes8_cols(v, k, mx_mul2(e));
           st_codes8(qcol, codes.lo, live);
           st_codes8(qcol + P, codes.hi, live);
           qcol += 2 * static_cast<int64_t>(P);
-          cb[k] = byte;
+          cb[k] = mx_bytes2(e);
         }
       }
     } else {
       // The products stay in registers between the two passes.
       float2 f[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = sm.weight[n & 3][rt + i];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[i][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[i], k)), make_float2(w, w));
-        const uint32_t amax = (i & 1) ? f32_bits_hi(m[i >> 1]) : f32_bits_lo(m[i >> 1]);
-        const uint32_t e = mx_t(abs_bits(__uint_as_float(amax) * w), round);
-        st_codes8(qrow, codes8(f[i], mx_mul_of(e)), live);
-        qrow += C;
-        rb[i >> 1] = (i & 1) ? rb[i >> 1] | (e - 8u) << 16 : e - 8u;
-      }
-      if (qT != nullptr) {
+      for (int p = 0; p < 4; ++p) {
+        const float wa = sm.weight[n & 3][rt + 2 * p], wb = sm.weight[n & 3][rt + 2 * p + 1];
+        const uint32_t e = mx_clamp2(mx_raw2(fabsf(__uint_as_float(f32_bits_lo(m[p])) * wa),
+                                             fabsf(__uint_as_float(f32_bits_hi(m[p])) * wb), round));
+        const float2 mul = mx_mul2_f32(e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float lo[8], hi[8];
+          f[2 * p][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[2 * p], k)), make_float2(wa, wa));
+          f[2 * p + 1][k] = __fmul2_rn(bf16x2_to_f32(word_of(v[2 * p + 1], k)), make_float2(wb, wb));
+        }
+        st_codes8(qrow, codes8(f[2 * p], mul.x), live);
+        st_codes8(qrow + C, codes8(f[2 * p + 1], mul.y), live);
+        qrow += 2 * static_cast<int64_t>(C);
+        rb[p] = mx_bytes2(e);
+      }
+      if (qT != nullptr) {
+        uint32_t e[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            lo[i] = f[i][k].x;
-            hi[i] = f[i][k].y;
-          }
-          // The exponent grows with the max, so the lanes reduce both columns' exponents in one word.
-          uint32_t e = mx_t(abs_bits(absmax_of8(lo)), round) | mx_t(abs_bits(absmax_of8(hi)), round) << 16;
-          e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 8));
-          e = __vmaxu2(e, __shfl_xor_sync(kAll, e, 16));
-          cb[k] = e - 0x00080008u;
-          const uint32_t el = e & 0xFFFFu, eh = e >> 16;
-          st_codes8(qcol, codes8(lo, mx_mul_of(el)), live);
-          st_codes8(qcol + P, codes8(hi, mx_mul_of(eh)), live);
+        for (int k = 0; k < 4; ++k) {
+          const float lo = absmax3(absmax3(absmax3(f[0][k].x, f[1][k].x, f[2][k].x), f[3][k].x, f[4][k].x),
+                                   absmax3(f[5][k].x, f[6][k].x, f[7][k].x), 0.f);
+          const float hi = absmax3(absmax3(absmax3(f[0][k].y, f[1][k].y, f[2][k].y), f[3][k].y, f[4][k].y),
+                                   absmax3(f[5][k].y, f[6][k].y, f[7][k].y), 0.f);
+          e[k] = mx_raw2(lo, hi, round);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          e[k] = __vmaxu2(e[k], __shfl_xor_sync(kAll, e[k], 8));
+          e[k] = mx_clamp2(__vmaxu2(e[k], __shfl_xor_sync(kAll, e[k], 16)));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 mul = mx_mul2_f32(e[k]);
+          float2 p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = __fmul2_rn(f[i][k], mul);
+          const CodePair codes = pair_of_columns(p);
+          st_codes8(qcol, codes.lo, live);
+          st_codes8(qcol + P, codes.hi, live);
           qcol += 2 * static_cast<int64_t>(P);
+          cb[k] = mx_bytes2(e[k]);
         }
       }
     }

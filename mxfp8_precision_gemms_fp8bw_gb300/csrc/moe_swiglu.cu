@@ -19,9 +19,20 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 64, kCols = 128, kThreads = 256;
 
-// 1 / (1 + 2^(-x log2 e)): a few ulp, against the 2^-4 of the codes it goes
-// into; exact 0 and 1 far out, NaN for NaN.
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)) of two values: a few ulp, against the 2^-4 of the
+// codes it goes into; exactly 0 and 1 far out, NaN for NaN.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  constexpr float kMinusLog2e = -1.4426950408889634f;
+  const float2 t = __fmul2_rn(x, make_float2(kMinusLog2e, kMinusLog2e));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  float2 s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+  return s;
+}
 
 struct Lane {
   int rt, ct;  // first row and column of the thread in the block's tile
@@ -39,13 +50,12 @@ struct alignas(8) Scales {
 // t's of the thread's four rows and eight columns, two to a word.
 __device__ __forceinline__ void put_row_bytes(Scales& s, Lane l, uint32_t t01, uint32_t t23) {
   if ((l.ct & 31) == 0)
-    *reinterpret_cast<uint32_t*>(&s.row[l.ct / 32][l.rt]) = __byte_perm(t01 - 0x00080008u, t23 - 0x00080008u, 0x6420);
+    *reinterpret_cast<uint32_t*>(&s.row[l.ct / 32][l.rt]) = __byte_perm(mx_bytes2(t01), mx_bytes2(t23), 0x6420);
 }
 __device__ __forceinline__ void put_col_bytes(Scales& s, Lane l, const uint32_t (&t)[4]) {
   if ((l.rt & 31) == 0)
     *reinterpret_cast<uint2*>(&s.col[l.rt / 32][l.ct]) =
-        make_uint2(__byte_perm(t[0] - 0x00080008u, t[1] - 0x00080008u, 0x6420),
-                   __byte_perm(t[2] - 0x00080008u, t[3] - 0x00080008u, 0x6420));
+        make_uint2(__byte_perm(mx_bytes2(t[0]), mx_bytes2(t[1]), 0x6420), __byte_perm(mx_bytes2(t[2]), mx_bytes2(t[3]), 0x6420));
 }
 // Row scales of the tile at rows r0, blocks b0 .. b0 + 3 of e8 [R][per_row], by threads 0 to 63.
 __device__ __forceinline__ void flush_rows(const Scales& s, int64_t r0, int64_t R, uint8_t* __restrict__ e8,
@@ -84,12 +94,8 @@ __device__ __forceinline__ uint32_t col_max2(uint32_t t) {
   t = __vmaxu2(t, __shfl_xor_sync(kAll, t, 8));
   return __vmaxu2(t, __shfl_xor_sync(kAll, t, 16));
 }
-__device__ __forceinline__ uint32_t pair_t(float lo, float hi, uint32_t round) {
-  return mx_t(abs_bits(lo), round) | mx_t(abs_bits(hi), round) << 16;
-}
-
 // Both layouts of the thread's 4 x 8 values: q at (row, col) of a matrix with
-// `ld` columns, qT transposed with R rows (qT may be null).
+// `ld` columns, qT transposed with R rows (qcol may be null).
 __device__ __forceinline__ void quant_4x8(const float2 (&v)[4][4], Lane l, bool live, uint32_t round, uint8_t* qrow,
                                           int64_t ld, uint8_t* qcol, int64_t R, Scales& s) {
   float m[4];
@@ -97,31 +103,32 @@ __device__ __forceinline__ void quant_4x8(const float2 (&v)[4][4], Lane l, bool 
   for (int i = 0; i < 4; ++i)
     m[i] = absmax3(absmax3(v[i][0].x, v[i][0].y, v[i][1].x), absmax3(v[i][1].y, v[i][2].x, v[i][2].y),
                    absmax3(v[i][3].x, v[i][3].y, 0.f));
-  uint32_t t[2] = {row_max2(pair_t(m[0], m[1], round)), row_max2(pair_t(m[2], m[3], round))};
+  const uint32_t t[2] = {mx_clamp2(row_max2(mx_raw2(m[0], m[1], round))), mx_clamp2(row_max2(mx_raw2(m[2], m[3], round)))};
   uint32_t tc[4];
   if (qcol != nullptr) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      tc[k] = pair_t(absmax3(absmax3(v[0][k].x, v[1][k].x, v[2][k].x), v[3][k].x, 0.f),
-                     absmax3(absmax3(v[0][k].y, v[1][k].y, v[2][k].y), v[3][k].y, 0.f), round);
+      tc[k] = mx_raw2(absmax3(absmax3(v[0][k].x, v[1][k].x, v[2][k].x), v[3][k].x, 0.f),
+                      absmax3(absmax3(v[0][k].y, v[1][k].y, v[2][k].y), v[3][k].y, 0.f), round);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tc[k] = col_max2(tc[k]);
+    for (int k = 0; k < 4; ++k) tc[k] = mx_clamp2(col_max2(tc[k]));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t e = (i & 1) ? t[i >> 1] >> 16 : t[i >> 1] & 0xFFFFu;
-    st_codes8(qrow + i * ld, codes8(v[i], mx_mul_of(e)), live);
+  for (int p = 0; p < 2; ++p) {
+    const float2 mul = mx_mul2_f32(t[p]);
+    st_codes8(qrow + 2 * p * ld, codes8(v[2 * p], mul.x), live);
+    st_codes8(qrow + (2 * p + 1) * ld, codes8(v[2 * p + 1], mul.y), live);
   }
   put_row_bytes(s, l, t[0], t[1]);
   if (qcol == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float a = mx_mul_of(tc[k] & 0xFFFFu), b = mx_mul_of(tc[k] >> 16);
-    if (live) {
-      *reinterpret_cast<uint32_t*>(qcol + (2 * k) * R) = e4m3x4(v[0][k].x * a, v[1][k].x * a, v[2][k].x * a, v[3][k].x * a);
-      *reinterpret_cast<uint32_t*>(qcol + (2 * k + 1) * R) =
-          e4m3x4(v[0][k].y * b, v[1][k].y * b, v[2][k].y * b, v[3][k].y * b);
-    }
+  for (int k = 0; k < 4; ++k) {  // two columns at a time, each with its own scale
+    const float2 mul = mx_mul2_f32(tc[k]);
+    const float2 a = __fmul2_rn(v[0][k], mul), b = __fmul2_rn(v[1][k], mul), c = __fmul2_rn(v[2][k], mul),
+                 d = __fmul2_rn(v[3][k], mul);
+    st_codes4(qcol, e4m3x4(a.x, b.x, c.x, d.x), live);
+    st_codes4(qcol + R, e4m3x4(a.y, b.y, c.y, d.y), live);
+    qcol += 2 * R;
   }
   put_col_bytes(s, l, tc);
 }
@@ -164,7 +171,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 x = bf16x2_to_f32(word_of(g[i], k)), y = bf16x2_to_f32(word_of(u[i], k));
-      a[i][k] = make_float2(x.x * sigmoid_f32(x.x) * y.x, x.y * sigmoid_f32(x.y) * y.y);
+      a[i][k] = __fmul2_rn(__fmul2_rn(x, sigmoid2(x)), y);
     }
   quant_4x8(a, l, live, round, aq + r0 * F + c0, F, aqT != nullptr ? aqT + c0 * R + r0 : nullptr, R, sa);
   __syncthreads();
@@ -228,10 +235,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 x = bf16x2_to_f32(word_of(d[i], k));
-      const float sx = sigmoid_f32(g[k].x), sy = sigmoid_f32(g[k].y);
-      const float px = x.x * sx, py = x.y * sy;
-      du[i][k] = make_float2(px * g[k].x, py * g[k].y);
-      dg[i][k] = make_float2(px * u[k].x * fmaf(g[k].x, 1.f - sx, 1.f), py * u[k].y * fmaf(g[k].y, 1.f - sy, 1.f));
+      const float2 s = sigmoid2(g[k]), one = make_float2(1.f, 1.f);
+      const float2 p = __fmul2_rn(x, s), rest = __fadd2_rn(one, make_float2(-s.x, -s.y));
+      du[i][k] = __fmul2_rn(p, g[k]);
+      dg[i][k] = __fmul2_rn(__fmul2_rn(p, u[k]), __ffma2_rn(g[k], rest, one));
     }
   }
   quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sg);

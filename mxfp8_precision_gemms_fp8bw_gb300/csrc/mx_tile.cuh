@@ -38,6 +38,11 @@ __device__ __forceinline__ void st_codes8(uint8_t* p, uint2 v, bool live) {
                "r"(v.x), "r"(v.y), "r"(static_cast<int>(live))
                : "memory");
 }
+__device__ __forceinline__ void st_codes4(uint8_t* p, uint32_t v, bool live) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.u32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+               "r"(static_cast<int>(live))
+               : "memory");
+}
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
   return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
@@ -72,10 +77,6 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float absmax_of8(const float (&v)[8]) {
-  return absmax3(absmax3(absmax3(v[0], v[1], v[2]), v[3], v[4]), absmax3(v[5], v[6], v[7]), 0.f);
-}
-
 // e4m3 codes of eight fp32 values times m, the values of one row in pairs as
 // they were unpacked: two products per instruction.
 __device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float m) {
@@ -83,20 +84,22 @@ __device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float m) {
   const float2 a = __fmul2_rn(v[0], mm), b = __fmul2_rn(v[1], mm), c = __fmul2_rn(v[2], mm), d = __fmul2_rn(v[3], mm);
   return make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y));
 }
-// The same down a column of eight rows, whose values are no register pairs:
-// pairing them up for the two-wide product costs more moves than it saves.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float m) {
-  return make_uint2(e4m3x4(v[0] * m, v[1] * m, v[2] * m, v[3] * m), e4m3x4(v[4] * m, v[5] * m, v[6] * m, v[7] * m));
+// Two blocks' exponents in the halves of one word.  `raw` is (bits(amax) +
+// round) >> 23 of mx_t before its clamp: it grows with the max, so the lanes
+// of a block reduce it (__vmaxu2) and clamp once.
+__device__ __forceinline__ uint32_t mx_raw2(float amax_lo, float amax_hi, uint32_t round) {  // both >= 0 or NaN
+  return (__float_as_uint(amax_lo) + round) >> 23 | (((__float_as_uint(amax_hi) + round) >> 7) & 0xFFFF0000u);
 }
-
-// The scale rule on two block maxima held as bf16 magnitudes in one word (see
-// mx_t; here in 16-bit halves, whose sums cannot carry): both t's.
+__device__ __forceinline__ uint32_t mx_clamp2(uint32_t raw) { return __vminu2(__vmaxu2(raw, 0x00080008u), 0x00FF00FFu); }
+// The same from two bf16 magnitudes in one word, whose sums cannot carry.
 __device__ __forceinline__ uint32_t mx_t2(uint32_t w, uint32_t round) {
-  const uint32_t t = (((w & 0x7FFF7FFFu) + (round >> 16) * 0x10001u) >> 7) & 0x01FF01FFu;
-  return __vminu2(__vmaxu2(t, 0x00080008u), 0x00FF00FFu);
+  return mx_clamp2((((w & 0x7FFF7FFFu) + (round >> 16) * 0x10001u) >> 7) & 0x01FF01FFu);
 }
-// 2^-E of both as packed bf16.
+// 2^-E of both, as packed bf16 and as fp32.
 __device__ __forceinline__ uint32_t mx_mul2(uint32_t t2) { return (0x01060106u - t2) << 7; }
+__device__ __forceinline__ float2 mx_mul2_f32(uint32_t t2) { return bf16x2_to_f32(mx_mul2(t2)); }
+// The E8M0 bytes of both, in the halves of a word.
+__device__ __forceinline__ uint32_t mx_bytes2(uint32_t t2) { return t2 - 0x00080008u; }
 
 // Packed bf16 products with powers of two: exact, or, far below the smallest
 // e4m3 code, a zero or subnormal of the same sign.
@@ -111,18 +114,19 @@ __device__ __forceinline__ uint2 codes8_row(const uint4& v, uint32_t m2) {
   return make_uint2(e4m3x4(bf16lo_to_f32(a), bf16hi_to_f32(a), bf16lo_to_f32(b), bf16hi_to_f32(b)),
                     e4m3x4(bf16lo_to_f32(c), bf16hi_to_f32(c), bf16lo_to_f32(d), bf16hi_to_f32(d)));
 }
-// The same down columns 2 k (first) and 2 k + 1 of eight rows, m2 their scales.
+// The same down columns 2 k (lo) and 2 k + 1 (hi) of eight rows, m2 their scales.
 struct CodePair {
   uint2 lo, hi;
 };
+__device__ __forceinline__ CodePair pair_of_columns(const float2 (&p)[8]) {
+  return CodePair{make_uint2(e4m3x4(p[0].x, p[1].x, p[2].x, p[3].x), e4m3x4(p[4].x, p[5].x, p[6].x, p[7].x)),
+                  make_uint2(e4m3x4(p[0].y, p[1].y, p[2].y, p[3].y), e4m3x4(p[4].y, p[5].y, p[6].y, p[7].y))};
+}
 __device__ __forceinline__ CodePair codes8_cols(const uint4 (&v)[8], int k, uint32_t m2) {
-  uint32_t p[8];
+  float2 p[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = mul2_bf16(word_of(v[i], k), m2);
-  return CodePair{make_uint2(e4m3x4(bf16lo_to_f32(p[0]), bf16lo_to_f32(p[1]), bf16lo_to_f32(p[2]), bf16lo_to_f32(p[3])),
-                             e4m3x4(bf16lo_to_f32(p[4]), bf16lo_to_f32(p[5]), bf16lo_to_f32(p[6]), bf16lo_to_f32(p[7]))),
-                  make_uint2(e4m3x4(bf16hi_to_f32(p[0]), bf16hi_to_f32(p[1]), bf16hi_to_f32(p[2]), bf16hi_to_f32(p[3])),
-                             e4m3x4(bf16hi_to_f32(p[4]), bf16hi_to_f32(p[5]), bf16hi_to_f32(p[6]), bf16hi_to_f32(p[7])))};
+  for (int i = 0; i < 8; ++i) p[i] = bf16x2_to_f32(mul2_bf16(word_of(v[i], k), m2));
+  return pair_of_columns(p);
 }
 
 // Scale bytes of a 128 x 128 tile: of the rows' blocks (32 columns each) and of
