@@ -269,5 +269,5 @@ FP8BW_API int mxfp8_swiglu_bwd(const fp8bw_bf16* da, const uint8_t* hq, const ui
     return fail(FP8BW_ERR_LAYOUT, "%s: outputs overlap an input or each other", name);
   DeviceState* d;
   if (int rc = current_device(&d)) return rc;
-  return launched(launch_swiglu_bwd(SwigluBwdArgs{da, hq, he, R, F, dq, de, dqT, deT, mode}, as_stream(stream)), name);
+  return launched(launch_swiglu_bwd(SwigluBwdArgs{da, hq, he, R, F, dq, de, dqT, deT, mode, d->num_sms}, as_stream(stream)), name);
 }

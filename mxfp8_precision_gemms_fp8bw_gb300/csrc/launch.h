@@ -172,6 +172,7 @@ struct SwigluBwdArgs {
   uint8_t* dqT;
   uint8_t* deT;
   int mode;
+  int num_sms;
 };
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& args, cudaStream_t st);
 

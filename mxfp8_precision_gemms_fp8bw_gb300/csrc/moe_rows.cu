@@ -10,7 +10,10 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 
 constexpr int kGatherWarps = 8;
-constexpr int kGatherCtasPerSm = 3;
+// Blocks per SM: three without weights; the products that the weighted form
+// keeps leave registers for two (three spill: 76 us against 70 on 8192 x 2
+// rows of 5120).
+constexpr int gather_ctas_per_sm(bool weighted) { return weighted ? 2 : 3; }
 
 // Where a block has its copies: two tiles of x, and of four tiles in turn the
 // rows' tokens (-1: none) and weights, because the tokens are needed two
@@ -30,7 +33,7 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool liv
 // MX codes of gathered rows, v_p = w_p * x[src_p / top_k], in both layouts.
 //
 // Bound by memory first and by the conversions next (two per element), so the
-// kernel keeps both busy: blocks are persistent, three to an SM, and walk
+// kernel keeps both busy: blocks are persistent, two or three to an SM, and walk
 // 128 x 128 tiles whose rows of x are on their way (cp.async, one 16-byte
 // chunk at a time, zeros where there is no row) while the tile before is
 // converted, and whose tokens were looked up one tile earlier still.  A
@@ -47,7 +50,7 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool liv
 // (with the columns fastest, 5120 of them and 8192 x 2 entries, x came from
 // DRAM 1.9 times).
 template <bool kWeighted>
-__global__ void __launch_bounds__(kGatherWarps * 32, kGatherCtasPerSm)
+__global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighted))
     gather_quant_kernel(const uint16_t* __restrict__ x, const float* __restrict__ weights,
                         const int32_t* __restrict__ src_of, uint32_t entries, uint32_t top_k, int P, int C, int bands,
                         int tiles, uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ qT,
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_moe_gather_quant(const MoeGatherArgs& a, cudaStream_t st) {
   const int64_t bands = (a.P + 127) / 128, tiles = bands * ((a.C + 127) / 128);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const int64_t cap = static_cast<int64_t>(a.num_sms) * kGatherCtasPerSm;
+  const int64_t cap = static_cast<int64_t>(a.num_sms) * gather_ctas_per_sm(a.weights != nullptr);
   auto go = [&](auto kernel) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(GatherSmem));
     if (e != cudaSuccess) return e;

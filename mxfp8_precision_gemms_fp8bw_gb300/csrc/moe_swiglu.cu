@@ -146,12 +146,14 @@ __device__ __forceinline__ void keep_4x8(const uint4 (&v)[4], Lane l, bool live,
 }
 
 __global__ void __launch_bounds__(kThreads)
-    swiglu_kernel(const uint16_t* __restrict__ h, int64_t R, int64_t F, uint8_t* __restrict__ aq,
+    swiglu_kernel(const uint16_t* __restrict__ h, int64_t R, int64_t F, uint32_t stripes, uint8_t* __restrict__ aq,
                   uint8_t* __restrict__ ae, uint8_t* __restrict__ aqT, uint8_t* __restrict__ aeT,
                   uint8_t* __restrict__ hq, uint8_t* __restrict__ he, int mode) {
   __shared__ Scales sa, sg, su;
   const Lane l = lane_of();
-  const int64_t tr = static_cast<int64_t>(blockIdx.x) * kRows, tc = static_cast<int64_t>(blockIdx.y) * kCols;
+  // Columns fastest: whole rows of h are read together (16640 x 4096: 94 us with the rows fastest, 90 so).
+  const uint32_t band = blockIdx.x / stripes;
+  const int64_t tr = static_cast<int64_t>(band) * kRows, tc = static_cast<int64_t>(blockIdx.x - band * stripes) * kCols;
   const int64_t r0 = tr + l.rt, c0 = tc + l.ct;
   const bool live = r0 < R && c0 < F;  // R and F % 32 == 0: blocks are all in or all out
   const uint32_t round = mx_round_f32(mode);
@@ -192,77 +194,166 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float2 (&v)[4]) {
   v[3] = __fmul2_rn(e4m3x2_to_f32(c.y >> 16), s);
 }
 
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p, bool live) {
-  uint2 r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
-      : "=&r"(r.x), "=&r"(r.y)
-      : "l"(p), "r"(static_cast<int>(live)));
-  return r;
+// The backward pass keeps two results of 32 values a thread, so few warps fit
+// (16 an SM), too few to wait for their own loads: blocks are persistent and
+// copy the next tile's operands to shared memory (cp.async) while they convert
+// the present one.  16-byte chunks are swizzled by the rows that one
+// instruction reads together, 4 apart.
+struct BwdSmem {
+  uint4 gate[2][kRows][8];   // chunk c of row r at c ^ ((r / 4) % 4) * 2
+  uint4 up[2][kRows][8];
+  uint4 da[2][kRows][16];    // chunk c of row r at c ^ ((r / 4) % 2) * 4
+  Scales sg[2], su[2];       // of the gradient
+  uint8_t exps[2][8][kRows];  // of the operands: four blocks of gate, four of up
+};
+constexpr int kBwdCtasPerSm = 2;
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdCtasPerSm)
     swiglu_bwd_kernel(const uint16_t* __restrict__ da, const uint8_t* __restrict__ hq, const uint8_t* __restrict__ he,
-                      int64_t R, int64_t F, uint8_t* __restrict__ dq, uint8_t* __restrict__ de,
-                      uint8_t* __restrict__ dqT, uint8_t* __restrict__ deT, int mode) {
-  __shared__ Scales sg, su;
+                      int64_t R, int64_t F, uint32_t stripes, uint32_t tiles, uint8_t* __restrict__ dq,
+                      uint8_t* __restrict__ de, uint8_t* __restrict__ dqT, uint8_t* __restrict__ deT, int mode) {
+  extern __shared__ __align__(128) uint8_t bwd_smem[];
+  BwdSmem& sm = *reinterpret_cast<BwdSmem*>(bwd_smem);
   const Lane l = lane_of();
-  const int64_t tr = static_cast<int64_t>(blockIdx.x) * kRows, tc = static_cast<int64_t>(blockIdx.y) * kCols;
-  const int64_t r0 = tr + l.rt, c0 = tc + l.ct;
-  const bool live = r0 < R && c0 < F;
   const uint32_t round = mx_round_f32(mode);
-  uint4 d[4];
-  uint2 gc[4], uc[4];
-  uint8_t ge[4], ue[4];
-  const uint8_t* hp = hq + (live ? r0 * 2 * F + c0 : 0);
-  const uint8_t* ep = he + (live ? r0 * (F / 16) + c0 / 32 : 0);
-  const uint16_t* dp = da + (live ? r0 * F + c0 : 0);
+  const int tid = threadIdx.x;
+
+  struct Origin {
+    int64_t r, c;
+  };
+  auto origin = [&](uint32_t tile) {
+    const uint32_t band = tile / stripes;
+    return Origin{static_cast<int64_t>(band) * kRows, static_cast<int64_t>(tile - band * stripes) * kCols};
+  };
+  auto fetch = [&](int s, Origin o) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    gc[i] = ld_codes8(hp + i * 2 * F, live);
-    uc[i] = ld_codes8(hp + i * 2 * F + F, live);
-    d[i] = ld_once_v4(dp + i * F, live);
-    ge[i] = live ? ep[i * (F / 16)] : 0;
-    ue[i] = live ? ep[i * (F / 16) + F / 32] : 0;
-  }
-  float2 dg[4][4], du[4][4];
+    for (int j = 0; j < 4; ++j) {  // 64 rows x 8 chunks of gate, then of up
+      const int r = (tid >> 3) + 32 * (j & 1), c = tid & 7;
+      const bool live = o.r + r < R && o.c + 16 * c < F;
+      const uint8_t* from = hq + (live ? (o.r + r) * 2 * F + (j >> 1) * F + o.c + 16 * c : 0);
+      copy16(&(j >> 1 ? sm.up : sm.gate)[s][r][c ^ ((r >> 2) & 3) << 1], from, live);
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 g[4], u[4];
-    decode8(gc[i], e8m0_value(ge[i]), g);
-    decode8(uc[i], e8m0_value(ue[i]), u);
+    for (int j = 0; j < 4; ++j) {
+      const int r = (tid >> 4) + 16 * j, c = tid & 15;
+      const bool live = o.r + r < R && o.c + 8 * c < F;
+      copy16(&sm.da[s][r][c ^ ((r >> 2) & 1) << 2], da + (live ? (o.r + r) * F + o.c + 8 * c : 0), live);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // Scale bytes of the operands: thread i < 128 has the four blocks of row i / 2 of gate (i even) or up.
+  auto exps_of = [&](Origin o) {
+    uint32_t e = 0;
+    const int64_t r = o.r + (tid >> 1);
+    if (tid < 128 && r < R) {
+      const uint8_t* from = he + r * (F / 16) + (tid & 1) * (F / 32) + o.c / 32;
+      if ((reinterpret_cast<uintptr_t>(from) & 3) == 0 && o.c + kCols <= F) {
+        e = *reinterpret_cast<const uint32_t*>(from);
+      } else {
+        for (int b = 0; b < 4 && o.c + 32 * b < F; ++b) e |= uint32_t{from[b]} << 8 * b;
+      }
+    }
+    return e;
+  };
+  auto note_exps = [&](int s, uint32_t e) {
+    if (tid >= 128) return;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = bf16x2_to_f32(word_of(d[i], k));
-      const float2 s = sigmoid2(g[k]), one = make_float2(1.f, 1.f);
-      const float2 p = __fmul2_rn(x, s), rest = __fadd2_rn(one, make_float2(-s.x, -s.y));
-      du[i][k] = __fmul2_rn(p, g[k]);
-      dg[i][k] = __fmul2_rn(__fmul2_rn(p, u[k]), __ffma2_rn(g[k], rest, one));
+    for (int b = 0; b < 4; ++b) sm.exps[s][(tid & 1) * 4 + b][tid >> 1] = static_cast<uint8_t>(e >> 8 * b);
+  };
+  auto flush = [&](int s, Origin o) {
+    flush_rows(sm.sg[s], o.r, R, de, o.c / 32, F / 32, F / 16);
+    flush_rows(sm.su[s], o.r, R, de, F / 32 + o.c / 32, F / 16, F / 16);
+    flush_cols(sm.sg[s], o.c, F, deT, o.r / 32, R / 32);
+    flush_cols(sm.su[s], F + o.c, 2 * F, deT, o.r / 32, R / 32);
+  };
+
+  uint32_t tile = blockIdx.x;
+  Origin now = origin(tile), last{};
+  fetch(0, now);
+  note_exps(0, exps_of(now));
+  for (int n = 0;; ++n) {
+    const int s = n & 1;
+    const uint32_t ahead = tile + gridDim.x;
+    const bool more = ahead < tiles;
+    const Origin next = origin(more ? ahead : tile);
+    // This tile has landed; everyone has left the one before and its buffers.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    uint32_t exps = 0;
+    if (more) {
+      fetch(s ^ 1, next);
+      exps = exps_of(next);
+    }
+    if (n > 0) flush(s ^ 1, last);
+
+    const int64_t r0 = now.r + l.rt, c0 = now.c + l.ct;
+    const bool live = r0 < R && c0 < F;
+    const uint32_t ge = *reinterpret_cast<const uint32_t*>(&sm.exps[s][l.ct / 32][l.rt]);
+    const uint32_t ue = *reinterpret_cast<const uint32_t*>(&sm.exps[s][4 + l.ct / 32][l.rt]);
+    const int hc = (l.ct >> 4) ^ ((l.rt >> 2) & 3) << 1, dc = (l.ct >> 3) ^ ((l.rt >> 2) & 1) << 2;
+    float2 dg[4][4], du[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 g[4], u[4];
+      decode8(reinterpret_cast<const uint2*>(&sm.gate[s][l.rt + i][hc])[(l.ct >> 3) & 1], e8m0_value(ge >> 8 * i & 0xFF), g);
+      decode8(reinterpret_cast<const uint2*>(&sm.up[s][l.rt + i][hc])[(l.ct >> 3) & 1], e8m0_value(ue >> 8 * i & 0xFF), u);
+      const uint4 d = sm.da[s][l.rt + i][dc];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = bf16x2_to_f32(word_of(d, k));
+        const float2 sig = sigmoid2(g[k]), one = make_float2(1.f, 1.f);
+        const float2 p = __fmul2_rn(x, sig), rest = __fadd2_rn(one, make_float2(-sig.x, -sig.y));
+        du[i][k] = __fmul2_rn(p, g[k]);
+        dg[i][k] = __fmul2_rn(__fmul2_rn(p, u[k]), __ffma2_rn(g[k], rest, one));
+      }
+    }
+    quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sm.sg[s]);
+    quant_4x8(du, l, live, round, dq + r0 * 2 * F + F + c0, 2 * F, dqT + (F + c0) * R + r0, R, sm.su[s]);
+    if (more) note_exps(s ^ 1, exps);
+    last = now;
+    now = next;
+    tile = ahead;
+    if (!more) {
+      __syncthreads();
+      flush(s, last);
+      return;
     }
   }
-  quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sg);
-  quant_4x8(du, l, live, round, dq + r0 * 2 * F + F + c0, 2 * F, dqT + (F + c0) * R + r0, R, su);
-  __syncthreads();
-  flush_rows(sg, tr, R, de, tc / 32, F / 32, F / 16);
-  flush_rows(su, tr, R, de, F / 32 + tc / 32, F / 16, F / 16);
-  flush_cols(sg, tc, F, deT, tr / 32, R / 32);
-  flush_cols(su, F + tc, 2 * F, deT, tr / 32, R / 32);
 }
 
-dim3 grid_of(int64_t R, int64_t F) {
-  return dim3(static_cast<unsigned>((R + kRows - 1) / kRows), static_cast<unsigned>((F + kCols - 1) / kCols));
+struct Tiles {
+  int64_t stripes, count;
+};
+Tiles tiles_of(int64_t R, int64_t F) {
+  const int64_t stripes = (F + kCols - 1) / kCols;
+  return Tiles{stripes, stripes * ((R + kRows - 1) / kRows)};
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t st) {
-  swiglu_kernel<<<grid_of(a.R, a.F), kThreads, 0, st>>>(a.h, a.R, a.F, a.aq, a.ae, a.aqT, a.aeT, a.hq, a.he, a.mode);
+  const Tiles t = tiles_of(a.R, a.F);
+  if (t.count > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  swiglu_kernel<<<dim3(static_cast<unsigned>(t.count)), kThreads, 0, st>>>(
+      a.h, a.R, a.F, static_cast<uint32_t>(t.stripes), a.aq, a.ae, a.aqT, a.aeT, a.hq, a.he, a.mode);
   return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t st) {
-  swiglu_bwd_kernel<<<grid_of(a.R, a.F), kThreads, 0, st>>>(a.da, a.hq, a.he, a.R, a.F, a.dq, a.de, a.dqT, a.deT, a.mode);
+  const Tiles t = tiles_of(a.R, a.F);
+  if (t.count > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const cudaError_t e =
+      cudaFuncSetAttribute(swiglu_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(BwdSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t cap = static_cast<int64_t>(a.num_sms) * kBwdCtasPerSm;
+  swiglu_bwd_kernel<<<dim3(static_cast<unsigned>(t.count < cap ? t.count : cap)), kThreads, sizeof(BwdSmem), st>>>(
+      a.da, a.hq, a.he, a.R, a.F, static_cast<uint32_t>(t.stripes), static_cast<uint32_t>(t.count), a.dq, a.de, a.dqT,
+      a.deT, a.mode);
   return cudaGetLastError();
 }
 

@@ -33,13 +33,16 @@ __device__ __forceinline__ uint4 ld_once_v4(const void* p, bool live = true) {
       : "l"(p), "r"(static_cast<int>(live)));
   return r;
 }
+// Codes go out with the streaming hint: nothing here reads them again, and
+// without it they push what is still to be read out of L2 (130048 x 1024
+// activations forward: 210 us without, 176 with).
 __device__ __forceinline__ void st_codes8(uint8_t* p, uint2 v, bool live) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.global.v2.u32 [%0], {%1, %2};\n\t}" ::"l"(p),
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.global.cs.v2.u32 [%0], {%1, %2};\n\t}" ::"l"(p),
                "r"(v.x), "r"(v.y), "r"(static_cast<int>(live))
                : "memory");
 }
 __device__ __forceinline__ void st_codes4(uint8_t* p, uint32_t v, bool live) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.u32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.cs.u32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
                "r"(static_cast<int>(live))
                : "memory");
 }
