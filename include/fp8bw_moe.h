@@ -92,8 +92,8 @@ int fp8bw_moe_route_bwd(const float* dweights, const void* logits, int logits_ty
  * Host-only. */
 int64_t fp8bw_moe_plan_rows(int64_t M, int64_t E, int64_t top_k);
 
-/* Bytes of workspace fp8bw_moe_plan needs for these dims (0 if they are
- * invalid).  Host-only. */
+/* Bytes of workspace fp8bw_moe_plan needs for these dims: 0 for few entries
+ * (and for invalid dims).  Host-only. */
 size_t fp8bw_moe_plan_workspace_bytes(int64_t M, int64_t E, int64_t top_k);
 
 /* Sorts the entries (token t, choice j), numbered t * top_k + j, by expert.
@@ -108,7 +108,8 @@ size_t fp8bw_moe_plan_workspace_bytes(int64_t M, int64_t E, int64_t top_k);
  *   src_of    : int32 [P], the row's entry or -1 (an empty row)
  * P: a multiple of 32, at least fp8bw_moe_plan_rows(M, E, top_k).
  * workspace: caller-owned DEVICE scratch of at least
- * fp8bw_moe_plan_workspace_bytes bytes; concurrent calls need one each. */
+ * fp8bw_moe_plan_workspace_bytes bytes, NULL where that is 0; concurrent calls
+ * need one each. */
 int fp8bw_moe_plan(const int32_t* experts, int64_t M, int64_t E, int64_t top_k, int64_t P, int32_t* group_end,
                    int32_t* counts, int32_t* row_of, int32_t* src_of, void* workspace, size_t workspace_bytes,
                    void* stream);

@@ -147,8 +147,8 @@ FP8BW_API int fp8bw_moe_plan(const int32_t* experts, int64_t M, int64_t E, int64
                              int32_t* group_end, int32_t* counts, int32_t* row_of, int32_t* src_of, void* workspace,
                              size_t workspace_bytes, void* stream) {
   const char* name = "fp8bw_moe_plan";
-  if (!experts || !group_end || !counts || !row_of || !src_of || !workspace)
-    return fail(FP8BW_ERR_NULL, "%s: every pointer must be non-NULL", name);
+  if (!experts || !group_end || !counts || !row_of || !src_of)
+    return fail(FP8BW_ERR_NULL, "%s: experts, group_end, counts, row_of and src_of must be non-NULL", name);
   if (!plan_dims_ok(M, E, top_k))
     return fail(FP8BW_ERR_SHAPE,
                 "%s: need 0 < M, 0 < E <= 1024, 0 < top_k <= min(E, 32) and M * top_k < 2^31 - 2^15; got M=%lld E=%lld "
@@ -160,6 +160,8 @@ FP8BW_API int fp8bw_moe_plan(const int32_t* experts, int64_t M, int64_t E, int64
   if (!all_aligned({experts, group_end, counts, row_of, src_of, workspace}))
     return fail(FP8BW_ERR_ALIGN, "%s: pointers must be 16-byte aligned", name);
   const size_t need = moe_plan_workspace_bytes(M, E, top_k);
+  if (need > 0 && !workspace)
+    return fail(FP8BW_ERR_NULL, "%s: these dims need a workspace of %zu bytes", name, need);
   if (workspace_bytes < need)
     return fail(FP8BW_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu bytes these dims need", name,
                 workspace_bytes, need);

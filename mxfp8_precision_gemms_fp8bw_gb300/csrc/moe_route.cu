@@ -30,12 +30,31 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float((u >> 31) ? u & 0x7FFFFFFFu : ~u);
 }
 
-// The scores of one row; a lane holds experts v * 32 + lane.  Divisions and
-// exponentials are the correctly rounded or library forms and the sum runs by
-// halves (first over v, then over lanes), because the choice has to come out
-// the same however the row is split.
-template <int V>
-__device__ __forceinline__ void scores_of(const float (&x)[V], int E, int lane, int score, float (&s)[V]) {
+// A row belongs to L lanes (8, or 32 where a row is long), 32 / L rows to a
+// warp, and lane l of the row holds experts v * L + l, v < V.  Everything but
+// the reductions is then work of V registers per lane, which with L = 8 is
+// shared by four rows; and the reductions are three shuffles.  (A whole warp
+// per row, with warp-wide reductions, took 104 us for 127999 rows of 160
+// experts, 4 of them chosen, against ROUTE_LONG_US.)
+template <int L, typename F>
+__device__ __forceinline__ float lanes_reduce(float v, F&& f) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+
+__host__ __device__ constexpr int pow2_from(int n) { return n <= 1 ? 1 : 2 * pow2_from((n + 1) / 2); }
+
+// The scores of a row.  Divisions and exponentials are the correctly rounded
+// or library forms and the sum runs by halves (first over v, then over the
+// lanes, zeros past the last expert), because the choice has to come out the
+// same however the row is split.
+template <int L, int V>
+__device__ __forceinline__ void scores_of(const float (&x)[V], int score, float (&s)[V]) {
   if (score != 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = 1.f / (1.f + expf(-x[v]));
@@ -44,7 +63,7 @@ __device__ __forceinline__ void scores_of(const float (&x)[V], int E, int lane, 
   float top = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  top = lanes_reduce<L>(top, [](float a, float b) { return fmaxf(a, b); });
   const bool empty = top == -INFINITY;
   // NaN in the row makes every score NaN through the sum; an empty row has none.
   float part[V];
@@ -53,14 +72,36 @@ __device__ __forceinline__ void scores_of(const float (&x)[V], int E, int lane, 
     s[v] = empty ? (x[v] != x[v] ? x[v] : 0.f) : expf(x[v] - top);
     part[v] = s[v];
   }
+  constexpr int kHalf = pow2_from(V) / 2;
 #pragma unroll
-  for (int h = V / 2; h > 0; h /= 2)
+  for (int h = kHalf; h > 0; h /= 2)
 #pragma unroll
-    for (int v = 0; v < h; ++v) part[v] += part[v + h];
-  float total = part[0];
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    for (int v = 0; v < h; ++v)
+      if (v + h < V) part[v] += part[v + h];
+  const float total = lanes_sum<L>(part[0]);
 #pragma unroll
   for (int v = 0; v < V; ++v) s[v] = empty ? s[v] + total : s[v] / total;
+}
+
+// The largest key of the row and where it is, the lowest place of equal ones;
+// key 0 where nothing is left.
+struct Best {
+  uint32_t key;
+  int at;
+};
+template <int L, int V>
+__device__ __forceinline__ Best best_of(const uint32_t (&key)[V], int l) {
+  Best b{key[0], 0};
+#pragma unroll
+  for (int v = 1; v < V; ++v)
+    if (key[v] > b.key) b = Best{key[v], v};
+  b.at = b.at * L + l;
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const Best c{__shfl_xor_sync(kAll, b.key, o), __shfl_xor_sync(kAll, b.at, o)};
+    if (c.key > b.key || (c.key == b.key && c.at < b.at)) b = c;
+  }
+  return b;
 }
 
 struct RouteShape {
@@ -71,157 +112,180 @@ struct RouteShape {
 
 constexpr int kRouteWarps = 4;
 
-template <typename T, int V>
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __restrict__ logits,
                                                                  const float* __restrict__ bias, RouteShape p,
                                                                  int32_t* __restrict__ experts,
                                                                  float* __restrict__ weights) {
+  constexpr int kRowsPerWarp = 32 / L;
   extern __shared__ uint32_t staged[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (row >= p.M) return;
+  const int l = threadIdx.x & (L - 1), mine = threadIdx.x / L;  // the lane in its row, the row in the block
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRowsPerWarp) + mine;
+  const bool live = row < p.M;  // all lanes go through the shuffles
   float x[V], s[V];
   uint32_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    x[v] = e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
+    const int e = v * L + l;
+    x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
   }
-  scores_of<V>(x, p.E, lane, p.score, s);
+  scores_of<L, V>(x, p.score, s);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
+    const int e = v * L + l;
     const float b = bias != nullptr && e < p.E ? bias[e] : 0.f;
     const bool masked = e >= p.E || x[v] == -INFINITY || b == -INFINITY;
     key[v] = masked ? 0u : ordered(s[v] + b);
   }
 
   if (p.groups > 1) {
-    // Lane g scores group g from the keys in shared memory.
-    uint32_t* mine = staged + warp * p.E;
+    // Lane l scores groups l, l + L, ... from the keys in shared memory; each
+    // starts at another place of its group, so that lanes hit other banks.
+    constexpr int G = (32 + L - 1) / L;
+    uint32_t* keys = staged + mine * (p.E | 8);
     const int size = p.E / p.groups;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v * 32 + lane < p.E) mine[v * 32 + lane] = key[v];
+      if (v * L + l < p.E) keys[v * L + l] = key[v];
     __syncwarp();
-    uint32_t best = 0, second = 0;
-    if (lane < p.groups) {
-      for (int i = 0; i < size; ++i) {
-        const uint32_t u = mine[lane * size + i];
-        second = max(second, min(best, u));
-        best = max(best, u);
+    uint32_t total[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int g = j * L + l;
+      uint32_t best = 0, second = 0;
+      if (g < p.groups) {
+        int at = g % size;
+        for (int i = 0; i < size; ++i) {
+          const uint32_t u = keys[g * size + at];
+          second = max(second, min(best, u));
+          best = max(best, u);
+          at = at + 1 == size ? 0 : at + 1;
+        }
       }
-    }
-    uint32_t total = best;
-    if (p.group_top == 2 && second != 0 && best != 0) {
-      const float sum = unordered(best) + unordered(second);
-      total = ordered(sum < kLowest ? kLowest : sum);
+      total[j] = best;
+      if (p.group_top == 2 && second != 0) {
+        const float sum = unordered(best) + unordered(second);
+        total[j] = ordered(sum < kLowest ? kLowest : sum);
+      }
     }
     uint32_t kept = 0;
     for (int i = 0; i < p.kept; ++i) {
-      const uint32_t m = __reduce_max_sync(kAll, total);
-      if (m == 0) break;
-      const int g = __ffs(__ballot_sync(kAll, total == m)) - 1;
-      kept |= 1u << g;
-      if (lane == g) total = 0;
+      const Best b = best_of<L, G>(total, l);
+      if (b.key != 0) kept |= 1u << b.at;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (j * L + l == b.at) total[j] = 0;
     }
+    const uint32_t per = (0xffffffffu / static_cast<uint32_t>(size)) + 1;  // e / size = (e * per) >> 32 for e, size <= 1024
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 32 + lane;
-      if (e < p.E && !((kept >> (e / size)) & 1u)) key[v] = 0;
+      const uint32_t g = size == 1 ? v * L + l : __umulhi(v * L + l, per);
+      if (v * L + l < p.E && !((kept >> g) & 1u)) key[v] = 0;
     }
   }
 
-  int chosen = -1;
-  float cs = 0.f;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t local = 0;
+  // Choice j is kept by lane j % L.
+  constexpr int K = (32 + L - 1) / L;
+  int chosen[K];
+  float cs[K], sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) local = max(local, key[v]);
-    const uint32_t m = __reduce_max_sync(kAll, local);
-    if (m == 0) break;
-    uint32_t e = 0xffffffffu;
-    float sv = 0.f;
+  for (int j = 0; j < K; ++j) {
+    chosen[j] = -1;
+    cs[j] = 0.f;
+    if (j * L < p.k) {
+      for (int i = 0; i < L && j * L + i < p.k; ++i) {
+        const Best b = best_of<L, V>(key, l);
+        float sv = 0.f;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == m) {
-        e = v * 32 + lane;
-        sv = s[v];
+        for (int v = 0; v < V; ++v)
+          if (v * L + l == b.at) {
+            sv = s[v];
+            key[v] = 0;
+          }
+        sv = __shfl_sync(kAll, sv, b.at, L);  // from the expert's lane
+        if (b.key != 0 && l == i) {
+          chosen[j] = b.at;
+          cs[j] = sv;
+        }
       }
-    const uint32_t win = __reduce_min_sync(kAll, e);
-    sv = __shfl_sync(kAll, sv, win & 31);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 32 + lane == static_cast<int>(win)) key[v] = 0;
-    if (lane == j) {
-      chosen = static_cast<int>(win);
-      cs = sv;
+      sum += lanes_sum<L>(cs[j]);
     }
   }
-  float w = cs * p.scale;
-  if (p.renorm) {
-    float total = cs;
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    w = cs / (total + 1e-20f) * p.scale;
-  }
-  if (lane < p.k) {
-    experts[row * p.k + lane] = chosen;
-    weights[row * p.k + lane] = w;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int c = j * L + l;
+    if (live && c < p.k) {
+      experts[row * p.k + c] = chosen[j];
+      weights[row * p.k + c] = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
+    }
   }
 }
 
-template <typename T, int V>
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_bwd_kernel(const float* __restrict__ dw, const T* __restrict__ logits, const int32_t* __restrict__ experts,
                      RouteShape p, T* __restrict__ dlogits, int* status) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (row >= p.M) return;
-  float x[V], s[V], g[V];
+  constexpr int kRowsPerWarp = 32 / L;
+  constexpr int K = (32 + L - 1) / L;
+  extern __shared__ uint32_t staged[];
+  const int l = threadIdx.x & (L - 1), mine = threadIdx.x / L;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRowsPerWarp) + mine;
+  const bool live = row < p.M;
+  float x[V], s[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    x[v] = e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
-    g[v] = 0.f;
+    const int e = v * L + l;
+    x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
   }
-  scores_of<V>(x, p.E, lane, p.score, s);
-  int mine = lane < p.k ? experts[row * p.k + lane] : -1;
-  if (mine < -1 || mine >= p.E) {
-    atomicExch(status, kStatusShape);
-    mine = -1;
-  }
-  // Lane j holds choice j: its score and the gradient of its score.
-  float cs = 0.f;
+  int at[K];
+  float ds[K];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float t = __shfl_sync(kAll, s[v], mine & 31);
-    if (mine >= 0 && (mine >> 5) == v) cs = t;
-  }
-  float ds = mine >= 0 ? dw[row * p.k + lane] * p.scale : 0.f;
-  if (p.renorm) {
-    float total = cs, dot = mine >= 0 ? ds * cs : 0.f;
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(kAll, total, o);
-      dot += __shfl_xor_sync(kAll, dot, o);
+  for (int j = 0; j < K; ++j) {
+    const int c = j * L + l;
+    at[j] = live && c < p.k ? experts[row * p.k + c] : -1;
+    if (at[j] < -1 || at[j] >= p.E) {
+      atomicExch(status, kStatusShape);
+      at[j] = -1;
     }
-    total += 1e-20f;
-    ds = mine >= 0 ? (ds - dot / total) / total : 0.f;
+    ds[j] = at[j] >= 0 ? dw[row * p.k + c] * p.scale : 0.f;
   }
-  for (int j = 0; j < p.k; ++j) {
-    const int e = __shfl_sync(kAll, mine, j);
-    const float d = __shfl_sync(kAll, ds, j);
+  scores_of<L, V>(x, p.score, s);
+  // The chosen scores come by way of shared memory.
+  float* scores = reinterpret_cast<float*>(staged) + mine * (p.E | 8);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 32 + lane == e) g[v] = d;
+  for (int v = 0; v < V; ++v)
+    if (v * L + l < p.E) scores[v * L + l] = s[v];
+  __syncwarp();
+  float cs[K], sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    cs[j] = at[j] >= 0 ? scores[at[j]] : 0.f;
+    sum += cs[j];
+    dot += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
   }
-  float dot = mine >= 0 ? ds * cs : 0.f;
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+  if (p.renorm) {
+    sum = lanes_sum<L>(sum) + 1e-20f;
+    dot = lanes_sum<L>(dot);
+    float rest = 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      ds[j] = at[j] >= 0 ? (ds[j] - dot / sum) / sum : 0.f;
+      rest += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
+    }
+    dot = rest;
+  }
+  dot = lanes_sum<L>(dot);
+  // What every expert gets, then, behind the barrier, what the chosen ones get in its place.
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    const float d = p.score != 0 ? g[v] * s[v] * (1.f - s[v]) : s[v] * (g[v] - dot);
-    if (e < p.E) put_logit(dlogits, row * p.E + e, d);
+    const int e = v * L + l;
+    if (live && e < p.E) put_logit(dlogits, row * p.E + e, p.score != 0 ? 0.f * s[v] : s[v] * (0.f - dot));
   }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (at[j] >= 0)
+      put_logit(dlogits, row * p.E + at[j], p.score != 0 ? ds[j] * cs[j] * (1.f - cs[j]) : cs[j] * (ds[j] - dot));
 }
 
 // ---------------------------------------------------------------- plan
@@ -398,25 +462,36 @@ cudaError_t route_of(const MoeRouteArgs& a, cudaStream_t st) {
                      a.score,
                      a.renorm,
                      a.scale};
-  const dim3 grid(static_cast<unsigned>((a.M + kRouteWarps - 1) / kRouteWarps));
   const T* logits = static_cast<const T*>(a.logits);
-  auto go = [&](auto W) {
-    constexpr int V = decltype(W)::value;
+  auto go = [&](auto lanes, auto width) {
+    constexpr int L = decltype(lanes)::value, V = decltype(width)::value;
+    constexpr int kRows = kRouteWarps * 32 / L;
+    const dim3 grid(static_cast<unsigned>((a.M + kRows - 1) / kRows));
+    const size_t smem = kRows * (a.E | 8) * sizeof(uint32_t);
     if (a.dlogits != nullptr) {
-      route_bwd_kernel<T, V><<<grid, kRouteWarps * 32, 0, st>>>(a.dweights, logits, a.experts_in, p,
-                                                               static_cast<T*>(a.dlogits), a.status);
+      route_bwd_kernel<T, L, V><<<grid, kRouteWarps * 32, smem, st>>>(a.dweights, logits, a.experts_in, p,
+                                                                     static_cast<T*>(a.dlogits), a.status);
     } else {
-      const size_t smem = a.groups > 1 ? kRouteWarps * a.E * sizeof(uint32_t) : 0;
-      route_kernel<T, V><<<grid, kRouteWarps * 32, smem, st>>>(logits, a.bias, p, a.experts, a.weights);
+      route_kernel<T, L, V><<<grid, kRouteWarps * 32, a.groups > 1 ? smem : 0, st>>>(logits, a.bias, p, a.experts,
+                                                                                     a.weights);
     }
     return cudaGetLastError();
   };
-  if (a.E <= 32) return go(std::integral_constant<int, 1>{});
-  if (a.E <= 64) return go(std::integral_constant<int, 2>{});
-  if (a.E <= 128) return go(std::integral_constant<int, 4>{});
-  if (a.E <= 256) return go(std::integral_constant<int, 8>{});
-  if (a.E <= 512) return go(std::integral_constant<int, 16>{});
-  return go(std::integral_constant<int, 32>{});
+  // Registers per lane: the next of these widths, a quarter more than needed at most beyond 8.
+  using std::integral_constant;
+  const integral_constant<int, 8> eight;
+  const integral_constant<int, 32> all;
+  if (a.E <= 8) return go(eight, integral_constant<int, 1>{});
+  if (a.E <= 16) return go(eight, integral_constant<int, 2>{});
+  if (a.E <= 32) return go(eight, integral_constant<int, 4>{});
+  if (a.E <= 64) return go(eight, integral_constant<int, 8>{});
+  if (a.E <= 96) return go(eight, integral_constant<int, 12>{});
+  if (a.E <= 128) return go(eight, integral_constant<int, 16>{});
+  if (a.E <= 160) return go(eight, integral_constant<int, 20>{});
+  if (a.E <= 192) return go(eight, integral_constant<int, 24>{});
+  if (a.E <= 256) return go(eight, integral_constant<int, 32>{});
+  if (a.E <= 512) return go(all, integral_constant<int, 16>{});
+  return go(all, integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -427,8 +502,7 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t st) {
 
 size_t moe_plan_workspace_bytes(int64_t M, int64_t E, int64_t top_k) {
   const PlanShape s = plan_shape(M, E, top_k, 0);
-  const size_t n = s.blocks > 1 ? static_cast<size_t>(s.blocks) * s.E * sizeof(int32_t) : 0;
-  return n < 16 ? 16 : n;
+  return s.blocks > 1 ? static_cast<size_t>(s.blocks) * s.E * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_moe_plan(const MoePlanArgs& a, cudaStream_t st) {

@@ -15,6 +15,7 @@ and each has its ``..._backward``.  ``MxMoEFFN`` is the layer.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -92,14 +93,21 @@ def plan(experts: torch.Tensor, num_experts: int) -> Plan:
     groups of whole 32-row blocks, without the host learning the counts."""
     M, top_k = experts.shape
     dev = experts.device
-    P = MB.fp8bw_moe_plan_rows(M, num_experts, top_k)
-    if P == 0:
-        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid plan dims: experts {tuple(experts.shape)} of {num_experts}")
+    P, ws_bytes = _plan_sizes(M, num_experts, top_k)
     e = lambda *shape: torch.empty(shape, dtype=_I32, device=dev)  # noqa: E731
     p = Plan(e(num_experts), e(num_experts), e(M, top_k), e(P))
-    ws = torch.empty(MB.fp8bw_moe_plan_workspace_bytes(M, num_experts, top_k), dtype=_U8, device=dev)
+    ws = torch.empty(ws_bytes, dtype=_U8, device=dev) if ws_bytes else None
     MB.fp8bw_moe_plan(experts, num_experts, p.group_end, p.counts, p.row_of, p.src_of, ws)
     return p
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_sizes(M: int, num_experts: int, top_k: int) -> tuple[int, int]:
+    """Rows and workspace bytes of a plan: functions of the dims alone."""
+    P = MB.fp8bw_moe_plan_rows(M, num_experts, top_k)
+    if P == 0:
+        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid plan dims: {M} tokens, {num_experts} experts, top_k {top_k}")
+    return P, MB.fp8bw_moe_plan_workspace_bytes(M, num_experts, top_k)
 
 
 def dispatch(x: torch.Tensor, p: Plan, colwise: bool = True, mode: int = B.MX_RCEIL) -> MxRows:

@@ -97,13 +97,14 @@ def fp8bw_moe_plan_workspace_bytes(M: int, E: int, top_k: int) -> int:
     return int(lib().fp8bw_moe_plan_workspace_bytes(M, E, top_k))
 
 
-def fp8bw_moe_plan(experts, E, group_end, counts, row_of, src_of, workspace, stream=None) -> None:
+def fp8bw_moe_plan(experts, E, group_end, counts, row_of, src_of, workspace=None, stream=None) -> None:
     M, top_k = experts.shape
     P = src_of.shape[0]
+    n = 0 if workspace is None else workspace.numel()
     B._check(lib().fp8bw_moe_plan(_arg(experts, _I32, "experts", M, top_k), M, E, top_k, P,
                                   _arg(group_end, _I32, "group_end", E), _arg(counts, _I32, "counts", E),
                                   _arg(row_of, _I32, "row_of", M, top_k), _arg(src_of, _I32, "src_of", P),
-                                  _arg(workspace, _U8, "workspace", workspace.numel()), workspace.numel(),
+                                  _arg(workspace, _U8, "workspace", n), n,
                                   _stream(stream, experts)))
 
 

@@ -62,19 +62,20 @@ def test_plan_rows_and_workspace(L):
     assert rows(1, 1, 1) == 32 and rows(17, 64, 4) == 2048 and rows(8192, 8, 2) == 16608
     assert rows(1, 64, 4) == 128          # 4 entries over at most 4 experts: a block each
     assert rows(0, 8, 2) == rows(8, 0, 2) == rows(8, 8, 9) == rows(1 << 30, 8, 4) == 0
-    assert MB.fp8bw_moe_plan_workspace_bytes(16, 8, 2) > 0
+    assert MB.fp8bw_moe_plan_workspace_bytes(16, 8, 2) == 0       # few entries need none
+    assert MB.fp8bw_moe_plan_workspace_bytes(16384, 8, 2) > 0
     assert MB.fp8bw_moe_plan_workspace_bytes(16, 2000, 2) == 0
 
 
 def test_plan_refusals(L):
-    n = MB.fp8bw_moe_plan_workspace_bytes(16, 8, 2)
-    ok = [P, 16, 8, 2, 288, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, n, None]
+    rows, n = MB.fp8bw_moe_plan_rows(16384, 8, 2), MB.fp8bw_moe_plan_workspace_bytes(16384, 8, 2)
+    ok = [P, 16384, 8, 2, rows, 2 * P, 3 * P, 4 * P, 5 * P, 6 * P, n, None]
     f = lambda **kw: L.fp8bw_moe_plan(*[kw.get("a%d" % i, v) for i, v in enumerate(ok)])  # noqa: E731
     for i in (0, 5, 6, 7, 8, 9):
         assert f(**{"a%d" % i: None}) == B.ERR_NULL
         assert f(**{"a%d" % i: ok[i] + 8}) == B.ERR_ALIGN
-    assert f(a4=224) == B.ERR_SHAPE and "plan_rows" in B.last_error()
-    assert f(a4=289) == B.ERR_SHAPE
+    assert f(a4=rows - 32) == B.ERR_SHAPE and "plan_rows" in B.last_error()
+    assert f(a4=rows + 1) == B.ERR_SHAPE
     assert f(a1=0) == B.ERR_SHAPE and f(a2=1) == B.ERR_SHAPE and f(a3=33) == B.ERR_SHAPE
     assert f(a10=n - 1) == B.ERR_ARG
     assert f(a5=P) == B.ERR_LAYOUT and f(a8=4 * P + 64) == B.ERR_LAYOUT
