@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "route_math.cuh"
 
 namespace fp8bw {
 namespace {
@@ -49,29 +50,47 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 __host__ __device__ constexpr int pow2_from(int n) { return n <= 1 ? 1 : 2 * pow2_from((n + 1) / 2); }
 
-// The scores of a row.  Divisions and exponentials are the correctly rounded
-// or library forms and the sum runs by halves (first over v, then over the
-// lanes, zeros past the last expert), because the choice has to come out the
-// same however the row is split.
-template <int L, int V>
-__device__ __forceinline__ void scores_of(const float (&x)[V], int score, float (&s)[V]) {
+// What the softmax scores of a row have in common.
+struct RowScale {
+  float top, total, inv;
+  bool tiny;  // an exponential too small for the short division
+};
+// fl(e / total): one correction step of Markstein's division from the rounded
+// reciprocal (route_math.cuh), and the plain division for the rows in which
+// that could lose bits.
+__device__ __forceinline__ float softmax_of(float e, const RowScale& r) {
+  return r.tiny ? __fdiv_rn(e, r.total) : div_by(e, r.total, r.inv);
+}
+__device__ __forceinline__ float sigmoid_of(float x) { return __frcp_rn(1.f + expf(-x)); }  // rounded as 1 / (...)
+
+// The scores of a row.  For the choice (kExact) quotients are correctly
+// rounded, exponentials the library's, and the sum runs by halves (first over
+// v, then over the lanes, zeros past the last expert), because the choice has
+// to come out the same however the row is split.  A gradient takes the
+// product with the reciprocal, an ulp off.
+template <int L, int V, bool kExact>
+__device__ __forceinline__ RowScale scores_of(const float (&x)[V], int score, float (&s)[V]) {
+  RowScale r{};
   if (score != 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 1.f / (1.f + expf(-x[v]));
-    return;
+    for (int v = 0; v < V; ++v) s[v] = sigmoid_of(x[v]);
+    return r;
   }
   float top = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
   top = lanes_reduce<L>(top, [](float a, float b) { return fmaxf(a, b); });
-  const bool empty = top == -INFINITY;
-  // NaN in the row makes every score NaN through the sum; an empty row has none.
+  // A row of nothing but -inf gets exponentials 0 over a sum of 1: no scores.
+  // NaN makes the sum NaN, and with it every score.
+  r.top = top == -INFINITY ? 0.f : top;
   float part[V];
+  uint32_t least = 0xffffffffu;  // bits of the smallest exponential that is not 0, less one
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = empty ? (x[v] != x[v] ? x[v] : 0.f) : expf(x[v] - top);
-    part[v] = s[v];
+    part[v] = s[v] = expf(x[v] - r.top);
+    if (kExact) least = min(least, __float_as_uint(s[v]) - 1u);
   }
+  if (kExact) r.tiny = __any_sync(kAll, least < __float_as_uint(kShortDivisionMin) - 1u);
   constexpr int kHalf = pow2_from(V) / 2;
 #pragma unroll
   for (int h = kHalf; h > 0; h /= 2)
@@ -79,8 +98,23 @@ __device__ __forceinline__ void scores_of(const float (&x)[V], int score, float 
     for (int v = 0; v < h; ++v)
       if (v + h < V) part[v] += part[v + h];
   const float total = lanes_sum<L>(part[0]);
+  r.total = total == 0.f ? 1.f : total;
+  r.inv = __frcp_rn(r.total);
+  if (!kExact) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = empty ? s[v] + total : s[v] / total;
+    for (int v = 0; v < V; ++v) s[v] *= r.inv;
+  } else if (r.tiny) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = __fdiv_rn(s[v], r.total);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = div_by(s[v], r.total, r.inv);
+  }
+  return r;
+}
+// The score of one logit of a row, the same bits.
+__device__ __forceinline__ float score_at(float x, int score, const RowScale& r) {
+  return score != 0 ? sigmoid_of(x) : softmax_of(expf(x - r.top), r);
 }
 
 // The largest key of the row and where it is, the lowest place of equal ones;
@@ -96,6 +130,19 @@ __device__ __forceinline__ Best best_of(const uint32_t (&key)[V], int l) {
   for (int v = 1; v < V; ++v)
     if (key[v] > b.key) b = Best{key[v], v};
   b.at = b.at * L + l;
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const Best c{__shfl_xor_sync(kAll, b.key, o), __shfl_xor_sync(kAll, b.at, o)};
+    if (c.key > b.key || (c.key == b.key && c.at < b.at)) b = c;
+  }
+  return b;
+}
+
+// The same over two candidates a lane that carry their places.
+template <int L>
+__device__ __forceinline__ Best best_of2(const uint32_t (&key)[2], const int (&at)[2]) {
+  const bool second = key[1] > key[0] || (key[1] == key[0] && at[1] < at[0]);
+  Best b = second ? Best{key[1], at[1]} : Best{key[0], at[0]};
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) {
     const Best c{__shfl_xor_sync(kAll, b.key, o), __shfl_xor_sync(kAll, b.at, o)};
@@ -129,13 +176,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
     const int e = v * L + l;
     x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
   }
-  scores_of<L, V>(x, p.score, s);
+  const RowScale scale = scores_of<L, V, true>(x, p.score, s);
+  if (bias == nullptr) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * L + l;
-    const float b = bias != nullptr && e < p.E ? bias[e] : 0.f;
-    const bool masked = e >= p.E || x[v] == -INFINITY || b == -INFINITY;
-    key[v] = masked ? 0u : ordered(s[v] + b);
+    for (int v = 0; v < V; ++v)  // x is -inf past the last expert
+      key[v] = x[v] == -INFINITY ? 0u : s[v] != s[v] ? 0xffffffffu : __float_as_uint(s[v]) | 0x80000000u;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float b = v * L + l < p.E ? bias[v * L + l] : 0.f;
+      key[v] = x[v] == -INFINITY || b == -INFINITY ? 0u : ordered(s[v] + b);
+    }
   }
 
   if (p.groups > 1) {
@@ -187,34 +238,88 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
   // Choice j is kept by lane j % L.
   constexpr int K = (32 + L - 1) / L;
   int chosen[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) chosen[j] = -1;
+  bool done = false;
+  if constexpr (L == 8 && V > 2) {
+    // Looking through all V keys again for every choice costs more than all
+    // the scores.  At least k experts are not below the k-th largest of the
+    // lanes' maxima, and rarely more than twice as many: those go into a short
+    // list, two to a lane, and the choices are made there.
+    if (p.k <= L) {
+      __shared__ uint2 lists[kRouteWarps * kRowsPerWarp][2 * L];
+      uint32_t most = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) most = max(most, key[v]);
+      int rank = 0;  // of the lane's maximum, the lower lane first among equals
+#pragma unroll
+      for (int o = 1; o < L; ++o) {
+        const uint32_t other = __shfl_xor_sync(kAll, most, o);
+        rank += other > most || (other == most && (l ^ o) < l);
+      }
+      const uint32_t holder = __ballot_sync(kAll, rank == p.k - 1) >> (threadIdx.x & 31 & ~(L - 1)) & ((1u << L) - 1);
+      const uint32_t least = max(__shfl_sync(kAll, most, __ffs(holder) - 1, L), 1u);
+      int count = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) count += key[v] >= least;
+      int up = count;
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) {
+        const int t = __shfl_up_sync(kAll, up, o, L);
+        if (l >= o) up += t;
+      }
+      const int all = __shfl_sync(kAll, up, L - 1, L);
+      if (__all_sync(kAll, all <= 2 * L)) {
+        done = true;
+        uint2* list = lists[mine];
+        uint32_t to = smem_u32(list + up - count);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool in = key[v] >= least;
+          asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.shared.v2.u32 [%0], {%1, %2};\n\t}" ::"r"(to),
+                       "r"(key[v]), "r"(v * L + l), "r"(static_cast<int>(in))
+                       : "memory");
+          to += in ? sizeof(uint2) : 0;
+        }
+        __syncwarp();
+        const uint2 a = l < all ? list[l] : make_uint2(0, 0), b = l + L < all ? list[l + L] : make_uint2(0, 0);
+        uint32_t ck[2] = {a.x, b.x};
+        const int ce[2] = {static_cast<int>(a.y), static_cast<int>(b.y)};
+        for (int j = 0; j < p.k; ++j) {
+          const Best w = best_of2<L>(ck, ce);
+          if (w.key != 0 && l == j) chosen[0] = w.at;
+          if (ce[0] == w.at) ck[0] = 0;
+          if (ce[1] == w.at) ck[1] = 0;
+        }
+      }
+    }
+  }
+  if (!done) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      for (int i = 0; i < L && j * L + i < p.k; ++i) {
+        const Best b = best_of<L, V>(key, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v * L + l == b.at) key[v] = 0;
+        if (b.key != 0 && l == i) chosen[j] = b.at;
+      }
+    }
+  }
+  // Weights from the scores without the bias, computed again for the few chosen.
   float cs[K], sum = 0.f;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    chosen[j] = -1;
     cs[j] = 0.f;
-    if (j * L < p.k) {
-      for (int i = 0; i < L && j * L + i < p.k; ++i) {
-        const Best b = best_of<L, V>(key, l);
-        float sv = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (v * L + l == b.at) {
-            sv = s[v];
-            key[v] = 0;
-          }
-        sv = __shfl_sync(kAll, sv, b.at, L);  // from the expert's lane
-        if (b.key != 0 && l == i) {
-          chosen[j] = b.at;
-          cs[j] = sv;
-        }
-      }
-      sum += lanes_sum<L>(cs[j]);
-    }
+    if (j * L >= p.k) continue;
+    cs[j] = chosen[j] >= 0 ? score_at(logit_at(logits, row * p.E + chosen[j]), p.score, scale) : 0.f;
+    sum += cs[j];
   }
+  sum = lanes_sum<L>(sum);
 #pragma unroll
   for (int j = 0; j < K; ++j) {
     const int c = j * L + l;
-    if (live && c < p.k) {
+    if (j * L < p.k && live && c < p.k) {
       experts[row * p.k + c] = chosen[j];
       weights[row * p.k + c] = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
     }
@@ -242,6 +347,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
   for (int j = 0; j < K; ++j) {
     const int c = j * L + l;
+    at[j] = -1;
+    ds[j] = 0.f;
+    if (j * L >= p.k) continue;
     at[j] = live && c < p.k ? experts[row * p.k + c] : -1;
     if (at[j] < -1 || at[j] >= p.E) {
       atomicExch(status, kStatusShape);
@@ -249,7 +357,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
     ds[j] = at[j] >= 0 ? dw[row * p.k + c] * p.scale : 0.f;
   }
-  scores_of<L, V>(x, p.score, s);
+  scores_of<L, V, false>(x, p.score, s);
   // The chosen scores come by way of shared memory.
   float* scores = reinterpret_cast<float*>(staged) + mine * (p.E | 8);
 #pragma unroll
@@ -259,6 +367,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   float cs[K], sum = 0.f, dot = 0.f;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
+    cs[j] = 0.f;
+    if (j * L >= p.k) continue;
     cs[j] = at[j] >= 0 ? scores[at[j]] : 0.f;
     sum += cs[j];
     dot += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
@@ -269,6 +379,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     float rest = 0.f;
 #pragma unroll
     for (int j = 0; j < K; ++j) {
+      if (j * L >= p.k) continue;
       ds[j] = at[j] >= 0 ? (ds[j] - dot / sum) / sum : 0.f;
       rest += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
     }

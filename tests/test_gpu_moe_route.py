@@ -268,3 +268,32 @@ def test_plan_on_a_reused_workspace_and_in_a_graph():
         B.fp8bw_sync_status()
         for got, want in zip((p.group_end, p.counts, p.row_of, p.src_of), O.moe_plan(new, E, p.rows)):
             assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E,k", [(160, 4), (160, 8), (64, 1), (256, 8), (200, 7), (24, 8)])
+def test_rows_of_every_spread(E, k, dtype):
+    """Rows whose best experts share one lane, many ties at the smallest chosen key, keys spread over all magnitudes down
+    to underflow, and masked experts in between: equal to the oracle where keys tie exactly or lie far apart."""
+    r = np.random.default_rng(E + k)
+    M = 64
+    logits = coarse_logits(M, E, seed=E)
+    logits[0:8] = -4
+    logits[0:8, 0::8] = 1 + np.arange(len(range(0, E, 8))) / 8          # the best are all 8 apart
+    logits[8:16] = 0.5                                                 # everything ties
+    logits[16:24] = np.where(r.uniform(size=(8, E)) < 0.5, 2.0, -1.0)  # half of the experts tie at the top
+    logits[24:32] = -np.arange(E) * 4.0                                # spread down to underflow
+    logits[32:40][r.uniform(size=(8, E)) < 0.9] = NINF                 # few left
+    logits[40, :] = NINF
+    logits[40, E // 2:E // 2 + k + 3] = 3.0
+    logits = logits[r.permutation(M)]
+    ref_e, ref_w = O.moe_route(logits, k)
+    # spread rows: keys that underflow to the same value tie in fp32 and not in 64 bits
+    s = O.moe_scores(logits, "softmax").astype(np.float32)
+    keep = np.array([len(np.unique(s[t][s[t] > 1e-37])) >= k or (s[t] > 1e-37).sum() >= k or np.isneginf(logits[t]).any()
+                     for t in range(M)])
+    x = torch.from_numpy(logits).to(dtype).cuda()
+    experts, weights = moe.route(x, k)
+    B.fp8bw_sync_status()
+    assert keep.sum() > M // 2 and np.array_equal(experts.cpu().numpy()[keep], ref_e[keep])
+    assert np.all(np.abs(weights.cpu().numpy() - ref_w)[keep] <= (weight_bound(logits, k) * ref_w + 1e-37)[keep])
