@@ -78,7 +78,7 @@ int route_common(const char* name, MoeRouteArgs& a, int logits_type, void* strea
   DeviceState* d;
   if (int rc = current_device(&d)) return rc;
   a.status = d->error_word;
-  return launched(launch_moe_route(a, as_stream(stream)), name);
+  return launched(a.dlogits ? launch_moe_route_bwd(a, as_stream(stream)) : launch_moe_route(a, as_stream(stream)), name);
 }
 
 }  // namespace

@@ -99,12 +99,13 @@ struct MoeRouteArgs {
   float scale;
   int32_t* experts;    // forward outputs
   float* weights;
-  const float* dweights;  // backward, when dlogits is set
+  const float* dweights;  // backward
   const int32_t* experts_in;
   void* dlogits;
   int* status;
 };
 cudaError_t launch_moe_route(const MoeRouteArgs& args, cudaStream_t st);
+cudaError_t launch_moe_route_bwd(const MoeRouteArgs& args, cudaStream_t st);
 
 struct MoePlanArgs {
   const int32_t* experts;

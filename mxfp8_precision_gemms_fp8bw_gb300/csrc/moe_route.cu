@@ -1,121 +1,9 @@
-// Routing of a mixture-of-experts layer: scores, the choice of experts and
-// its gradient, and the sort of the choices into expert groups.
-#include <type_traits>
-
-#include "common.cuh"
-#include "launch.h"
-#include "route_math.cuh"
+// Routing of a mixture-of-experts layer: the choice of experts, and the sort of
+// the choices into expert groups.
+#include "route_row.cuh"
 
 namespace fp8bw {
 namespace {
-
-constexpr uint32_t kAll = 0xffffffffu;
-constexpr float kLowest = -3.4028234663852886e38f;
-
-__device__ __forceinline__ float logit_at(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float logit_at(const uint16_t* p, int64_t i) { return __uint_as_float(uint32_t{p[i]} << 16); }
-__device__ __forceinline__ void put_logit(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void put_logit(uint16_t* p, int64_t i, float v) {
-  p[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
-}
-
-// Keys as unsigned integers of the same order: 0 is a masked expert, below
-// the lowest finite key (0x00800000), and NaN is above everything.
-__device__ __forceinline__ uint32_t ordered(float f) {
-  if (f != f) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(f + 0.f);  // -0 becomes +0
-  return (b >> 31) ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  if (u == 0xffffffffu) return __uint_as_float(0x7FFFFFFFu);
-  return __uint_as_float((u >> 31) ? u & 0x7FFFFFFFu : ~u);
-}
-
-// A row belongs to L lanes (8, or 32 where a row is long), 32 / L rows to a
-// warp, and lane l of the row holds experts v * L + l, v < V.  Everything but
-// the reductions is then work of V registers per lane, which with L = 8 is
-// shared by four rows; and the reductions are three shuffles.  (A whole warp
-// per row, with warp-wide reductions, took 104 us for 127999 rows of 160
-// experts, 4 of them chosen, against ROUTE_LONG_US.)
-template <int L, typename F>
-__device__ __forceinline__ float lanes_reduce(float v, F&& f) {
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v) {
-  return lanes_reduce<L>(v, [](float a, float b) { return a + b; });
-}
-
-__host__ __device__ constexpr int pow2_from(int n) { return n <= 1 ? 1 : 2 * pow2_from((n + 1) / 2); }
-
-// What the softmax scores of a row have in common.
-struct RowScale {
-  float top, total, inv;
-  bool tiny;  // an exponential too small for the short division
-};
-// fl(e / total): one correction step of Markstein's division from the rounded
-// reciprocal (route_math.cuh), and the plain division for the rows in which
-// that could lose bits.
-__device__ __forceinline__ float softmax_of(float e, const RowScale& r) {
-  return r.tiny ? __fdiv_rn(e, r.total) : div_by(e, r.total, r.inv);
-}
-__device__ __forceinline__ float sigmoid_of(float x) { return __frcp_rn(1.f + expf(-x)); }  // rounded as 1 / (...)
-
-// The scores of a row.  For the choice (kExact) quotients are correctly
-// rounded, exponentials the library's, and the sum runs by halves (first over
-// v, then over the lanes, zeros past the last expert), because the choice has
-// to come out the same however the row is split.  A gradient takes the
-// product with the reciprocal, an ulp off.
-template <int L, int V, bool kExact>
-__device__ __forceinline__ RowScale scores_of(const float (&x)[V], int score, float (&s)[V]) {
-  RowScale r{};
-  if (score != 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = sigmoid_of(x[v]);
-    return r;
-  }
-  float top = -INFINITY;
-#pragma unroll
-  for (int v = 0; v < V; ++v) top = fmaxf(top, x[v]);
-  top = lanes_reduce<L>(top, [](float a, float b) { return fmaxf(a, b); });
-  // A row of nothing but -inf gets exponentials 0 over a sum of 1: no scores.
-  // NaN makes the sum NaN, and with it every score.
-  r.top = top == -INFINITY ? 0.f : top;
-  float part[V];
-  uint32_t least = 0xffffffffu;  // bits of the smallest exponential that is not 0, less one
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    part[v] = s[v] = expf(x[v] - r.top);
-    if (kExact) least = min(least, __float_as_uint(s[v]) - 1u);
-  }
-  if (kExact) r.tiny = __any_sync(kAll, least < __float_as_uint(kShortDivisionMin) - 1u);
-  constexpr int kHalf = pow2_from(V) / 2;
-#pragma unroll
-  for (int h = kHalf; h > 0; h /= 2)
-#pragma unroll
-    for (int v = 0; v < h; ++v)
-      if (v + h < V) part[v] += part[v + h];
-  const float total = lanes_sum<L>(part[0]);
-  r.total = total == 0.f ? 1.f : total;
-  r.inv = __frcp_rn(r.total);
-  if (!kExact) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] *= r.inv;
-  } else if (r.tiny) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = __fdiv_rn(s[v], r.total);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = div_by(s[v], r.total, r.inv);
-  }
-  return r;
-}
-// The score of one logit of a row, the same bits.
-__device__ __forceinline__ float score_at(float x, int score, const RowScale& r) {
-  return score != 0 ? sigmoid_of(x) : softmax_of(expf(x - r.top), r);
-}
 
 // The largest key of the row and where it is, the lowest place of equal ones;
 // key 0 where nothing is left.
@@ -150,14 +38,6 @@ __device__ __forceinline__ Best best_of2(const uint32_t (&key)[2], const int (&a
   }
   return b;
 }
-
-struct RouteShape {
-  int64_t M;
-  int E, k, groups, kept, group_top, score, renorm;
-  float scale;
-};
-
-constexpr int kRouteWarps = 4;
 
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __restrict__ logits,
@@ -206,6 +86,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
       uint32_t best = 0, second = 0;
       if (g < p.groups) {
         int at = g % size;
+#pragma unroll 4
         for (int i = 0; i < size; ++i) {
           const uint32_t u = keys[g * size + at];
           second = max(second, min(best, u));
@@ -220,6 +101,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
       }
     }
     uint32_t kept = 0;
+#pragma unroll 1
     for (int i = 0; i < p.kept; ++i) {
       const Best b = best_of<L, G>(total, l);
       if (b.key != 0) kept |= 1u << b.at;
@@ -285,6 +167,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
         const uint2 a = l < all ? list[l] : make_uint2(0, 0), b = l + L < all ? list[l + L] : make_uint2(0, 0);
         uint32_t ck[2] = {a.x, b.x};
         const int ce[2] = {static_cast<int>(a.y), static_cast<int>(b.y)};
+#pragma unroll 1
         for (int j = 0; j < p.k; ++j) {
           const Best w = best_of2<L>(ck, ce);
           if (w.key != 0 && l == j) chosen[0] = w.at;
@@ -295,15 +178,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
     }
   }
   if (!done) {
+#pragma unroll 1
+    for (int c = 0; c < p.k; ++c) {
+      const Best b = best_of<L, V>(key, l);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      for (int i = 0; i < L && j * L + i < p.k; ++i) {
-        const Best b = best_of<L, V>(key, l);
+      for (int v = 0; v < V; ++v)
+        if (v * L + l == b.at) key[v] = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (v * L + l == b.at) key[v] = 0;
-        if (b.key != 0 && l == i) chosen[j] = b.at;
-      }
+      for (int j = 0; j < K; ++j)
+        if (c == j * L + l && b.key != 0) chosen[j] = b.at;
     }
   }
   // Weights from the scores without the bias, computed again for the few chosen.
@@ -324,79 +207,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
       weights[row * p.k + c] = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
     }
   }
-}
-
-template <typename T, int L, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32)
-    route_bwd_kernel(const float* __restrict__ dw, const T* __restrict__ logits, const int32_t* __restrict__ experts,
-                     RouteShape p, T* __restrict__ dlogits, int* status) {
-  constexpr int kRowsPerWarp = 32 / L;
-  constexpr int K = (32 + L - 1) / L;
-  extern __shared__ uint32_t staged[];
-  const int l = threadIdx.x & (L - 1), mine = threadIdx.x / L;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRowsPerWarp) + mine;
-  const bool live = row < p.M;
-  float x[V], s[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * L + l;
-    x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
-  }
-  int at[K];
-  float ds[K];
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-    const int c = j * L + l;
-    at[j] = -1;
-    ds[j] = 0.f;
-    if (j * L >= p.k) continue;
-    at[j] = live && c < p.k ? experts[row * p.k + c] : -1;
-    if (at[j] < -1 || at[j] >= p.E) {
-      atomicExch(status, kStatusShape);
-      at[j] = -1;
-    }
-    ds[j] = at[j] >= 0 ? dw[row * p.k + c] * p.scale : 0.f;
-  }
-  scores_of<L, V, false>(x, p.score, s);
-  // The chosen scores come by way of shared memory.
-  float* scores = reinterpret_cast<float*>(staged) + mine * (p.E | 8);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (v * L + l < p.E) scores[v * L + l] = s[v];
-  __syncwarp();
-  float cs[K], sum = 0.f, dot = 0.f;
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-    cs[j] = 0.f;
-    if (j * L >= p.k) continue;
-    cs[j] = at[j] >= 0 ? scores[at[j]] : 0.f;
-    sum += cs[j];
-    dot += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
-  }
-  if (p.renorm) {
-    sum = lanes_sum<L>(sum) + 1e-20f;
-    dot = lanes_sum<L>(dot);
-    float rest = 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      if (j * L >= p.k) continue;
-      ds[j] = at[j] >= 0 ? (ds[j] - dot / sum) / sum : 0.f;
-      rest += at[j] >= 0 ? ds[j] * cs[j] : 0.f;
-    }
-    dot = rest;
-  }
-  dot = lanes_sum<L>(dot);
-  // What every expert gets, then, behind the barrier, what the chosen ones get in its place.
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * L + l;
-    if (live && e < p.E) put_logit(dlogits, row * p.E + e, p.score != 0 ? 0.f * s[v] : s[v] * (0.f - dot));
-  }
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < K; ++j)
-    if (at[j] >= 0)
-      put_logit(dlogits, row * p.E + at[j], p.score != 0 ? ds[j] * cs[j] * (1.f - cs[j]) : cs[j] * (ds[j] - dot));
 }
 
 // ---------------------------------------------------------------- plan
@@ -564,45 +374,13 @@ __global__ void __launch_bounds__(1024)
 
 template <typename T>
 cudaError_t route_of(const MoeRouteArgs& a, cudaStream_t st) {
-  const RouteShape p{a.M,
-                     static_cast<int>(a.E),
-                     static_cast<int>(a.top_k),
-                     static_cast<int>(a.groups),
-                     static_cast<int>(a.groups_kept),
-                     static_cast<int>(a.group_top),
-                     a.score,
-                     a.renorm,
-                     a.scale};
-  const T* logits = static_cast<const T*>(a.logits);
-  auto go = [&](auto lanes, auto width) {
+  return for_experts(a.E, [&](auto lanes, auto width) {
     constexpr int L = decltype(lanes)::value, V = decltype(width)::value;
-    constexpr int kRows = kRouteWarps * 32 / L;
-    const dim3 grid(static_cast<unsigned>((a.M + kRows - 1) / kRows));
-    const size_t smem = kRows * (a.E | 8) * sizeof(uint32_t);
-    if (a.dlogits != nullptr) {
-      route_bwd_kernel<T, L, V><<<grid, kRouteWarps * 32, smem, st>>>(a.dweights, logits, a.experts_in, p,
-                                                                     static_cast<T*>(a.dlogits), a.status);
-    } else {
-      route_kernel<T, L, V><<<grid, kRouteWarps * 32, a.groups > 1 ? smem : 0, st>>>(logits, a.bias, p, a.experts,
-                                                                                     a.weights);
-    }
+    const dim3 grid(static_cast<unsigned>((a.M + kRouteRows<L> - 1) / kRouteRows<L>));
+    route_kernel<T, L, V><<<grid, kRouteWarps * 32, a.groups > 1 ? staged_bytes<L>(a.E) : 0, st>>>(
+        static_cast<const T*>(a.logits), a.bias, shape_of(a), a.experts, a.weights);
     return cudaGetLastError();
-  };
-  // Registers per lane: the next of these widths, a quarter more than needed at most beyond 8.
-  using std::integral_constant;
-  const integral_constant<int, 8> eight;
-  const integral_constant<int, 32> all;
-  if (a.E <= 8) return go(eight, integral_constant<int, 1>{});
-  if (a.E <= 16) return go(eight, integral_constant<int, 2>{});
-  if (a.E <= 32) return go(eight, integral_constant<int, 4>{});
-  if (a.E <= 64) return go(eight, integral_constant<int, 8>{});
-  if (a.E <= 96) return go(eight, integral_constant<int, 12>{});
-  if (a.E <= 128) return go(eight, integral_constant<int, 16>{});
-  if (a.E <= 160) return go(eight, integral_constant<int, 20>{});
-  if (a.E <= 192) return go(eight, integral_constant<int, 24>{});
-  if (a.E <= 256) return go(eight, integral_constant<int, 32>{});
-  if (a.E <= 512) return go(all, integral_constant<int, 16>{});
-  return go(all, integral_constant<int, 32>{});
+  });
 }
 
 }  // namespace
