@@ -2,12 +2,14 @@
 // kept in 8 bits, and its gradient from those 8 bits.
 //
 // Both kernels read each element once and write only codes (8.1 bytes per
-// element of a forward, 8.2 backward), with some twenty instructions per
-// element between; they are bound by memory where enough warps overlap the
-// two.  A thread has 4 rows x 8 columns, a warp 32 x 32: lane 4 i + j has
+// element of a forward, 8.2 backward).  The forward pass is bound by memory:
+// 90 us for 16640 x 4096 (0.91 of the measured copy bandwidth), 168 us for
+// 130048 x 1024 (0.95).  The backward pass has twice the results to convert,
+// some forty instructions per element, and is bound by them as much as by
+// memory: 114 us (0.72) and 213 us (0.76).  A thread has 4 rows x 8 columns, a warp 32 x 32: lane 4 i + j has
 // rows 4 i + [0, 4) and columns 8 j + [0, 8), so that a row block is four
 // neighbouring lanes and a column block the eight lanes 4 apart.  (8 x 8 per
-// thread, as in the gather, needs twice the registers here, where two
+// thread, as in moe_rows.cu, needs twice the registers here, where two
 // operands and one or two results are live at once.)  A block has 64 x 128.
 #include "common.cuh"
 #include "launch.h"
@@ -230,19 +232,26 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm)
     const uint32_t band = tile / stripes;
     return Origin{static_cast<int64_t>(band) * kRows, static_cast<int64_t>(tile - band * stripes) * kCols};
   };
+  // The thread's chunks of a tile: rows tid / 8 + {0, 32} of gate and of up, rows tid / 16 + {0, 16, 32, 48} of da.
+  const int hr = tid >> 3, hc = tid & 7, dr = tid >> 4, dc = tid & 15;
+  const uint8_t* h0 = hq + hr * 2 * F + 16 * hc;
+  const uint16_t* d0 = da + dr * F + 8 * dc;
   auto fetch = [&](int s, Origin o) {
+    const bool whole = o.r + kRows <= R && o.c + kCols <= F;
+    const uint8_t* hp = h0 + o.r * 2 * F + o.c;
+    const uint16_t* dp = d0 + o.r * F + o.c;
+    const int64_t h_rows = 64 * F, d_rows = 16 * F;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // 64 rows x 8 chunks of gate, then of up
-      const int r = (tid >> 3) + 32 * (j & 1), c = tid & 7;
-      const bool live = o.r + r < R && o.c + 16 * c < F;
-      const uint8_t* from = hq + (live ? (o.r + r) * 2 * F + (j >> 1) * F + o.c + 16 * c : 0);
-      copy16(&(j >> 1 ? sm.up : sm.gate)[s][r][c ^ ((r >> 2) & 3) << 1], from, live);
+    for (int j = 0; j < 2; ++j) {
+      const bool live = whole || (o.r + hr + 32 * j < R && o.c + 16 * hc < F);
+      const int chunk = hc ^ ((hr >> 2) & 3) << 1;
+      copy16(&sm.gate[s][hr + 32 * j][chunk], live ? hp + j * h_rows : hq, live);
+      copy16(&sm.up[s][hr + 32 * j][chunk], live ? hp + j * h_rows + F : hq, live);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = (tid >> 4) + 16 * j, c = tid & 15;
-      const bool live = o.r + r < R && o.c + 8 * c < F;
-      copy16(&sm.da[s][r][c ^ ((r >> 2) & 1) << 2], da + (live ? (o.r + r) * F + o.c + 8 * c : 0), live);
+      const bool live = whole || (o.r + dr + 16 * j < R && o.c + 8 * dc < F);
+      copy16(&sm.da[s][dr + 16 * j][dc ^ ((dr >> 2) & 1) << 2], live ? dp + j * d_rows : da, live);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -295,14 +304,14 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm)
     const bool live = r0 < R && c0 < F;
     const uint32_t ge = *reinterpret_cast<const uint32_t*>(&sm.exps[s][l.ct / 32][l.rt]);
     const uint32_t ue = *reinterpret_cast<const uint32_t*>(&sm.exps[s][4 + l.ct / 32][l.rt]);
-    const int hc = (l.ct >> 4) ^ ((l.rt >> 2) & 3) << 1, dc = (l.ct >> 3) ^ ((l.rt >> 2) & 1) << 2;
+    const int gu = (l.ct >> 4) ^ ((l.rt >> 2) & 3) << 1, dd = (l.ct >> 3) ^ ((l.rt >> 2) & 1) << 2;
     float2 dg[4][4], du[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 g[4], u[4];
-      decode8(reinterpret_cast<const uint2*>(&sm.gate[s][l.rt + i][hc])[(l.ct >> 3) & 1], e8m0_value(ge >> 8 * i & 0xFF), g);
-      decode8(reinterpret_cast<const uint2*>(&sm.up[s][l.rt + i][hc])[(l.ct >> 3) & 1], e8m0_value(ue >> 8 * i & 0xFF), u);
-      const uint4 d = sm.da[s][l.rt + i][dc];
+      decode8(reinterpret_cast<const uint2*>(&sm.gate[s][l.rt + i][gu])[(l.ct >> 3) & 1], e8m0_value(ge >> 8 * i & 0xFF), g);
+      decode8(reinterpret_cast<const uint2*>(&sm.up[s][l.rt + i][gu])[(l.ct >> 3) & 1], e8m0_value(ue >> 8 * i & 0xFF), u);
+      const uint4 d = sm.da[s][l.rt + i][dd];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 x = bf16x2_to_f32(word_of(d, k));
@@ -312,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm)
         dg[i][k] = __fmul2_rn(__fmul2_rn(p, u[k]), __ffma2_rn(g[k], rest, one));
       }
     }
-    quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sm.sg[s]);
     quant_4x8(du, l, live, round, dq + r0 * 2 * F + F + c0, 2 * F, dqT + (F + c0) * R + r0, R, sm.su[s]);
+    quant_4x8(dg, l, live, round, dq + r0 * 2 * F + c0, 2 * F, dqT + c0 * R + r0, R, sm.sg[s]);
     if (more) note_exps(s ^ 1, exps);
     last = now;
     now = next;

@@ -15,14 +15,8 @@ namespace fp8bw {
 // clamp E >= -127 is t >= 8.  The largest t of a finite amax is 255, to which
 // infinities and NaN (256 with some payloads) are clamped.  The E8M0 byte is
 // t - 8, and 2^-E has the biased exponent 262 - t, in [7, 254]: a normal
-// number.
+// number.  mx_tile.cuh has the rule for two blocks at a time.
 __device__ __forceinline__ uint32_t mx_round_f32(int mode) { return mode == 0 ? 0x1FFFFFu : 0u; }
-__device__ __forceinline__ uint32_t mx_t(uint32_t abs_bits, uint32_t round) {
-  return min(max((abs_bits + round) >> 23, 8u), 255u);
-}
-__device__ __forceinline__ float mx_mul_of(uint32_t t) { return __uint_as_float((262u - t) << 23); }
-__device__ __forceinline__ uint8_t mx_e8_of(uint32_t t) { return static_cast<uint8_t>(t - 8u); }
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 // 2^E of an E8M0 byte (0 is 2^-127, a subnormal).
 __device__ __forceinline__ float e8m0_value(uint32_t e8) {

@@ -1,12 +1,15 @@
-// Register tiles of the kernels that quantize what they compute to MX codes.
+// What the kernels that quantize gathered or computed values to MX codes share:
+// loads and stores of 16 and 8 bytes, block maxima, and the scale rule and the
+// conversion for several values at a time.
 //
-// A warp owns 32 rows x 64 columns, a thread 8 rows x 8 columns of them: lane
-// 8 i + j has rows 8 i + [0, 8) and columns 8 j + [0, 8).  A row block (32
-// columns) is then four neighbouring lanes and a column block (32 rows) the
-// four lanes 8 apart, so both block maxima are two shuffles, the tile is read
-// once, and nothing goes through shared memory.  Every access is whole
-// sectors: a row of bf16 is 128 contiguous bytes over its eight lanes, a row
-// of codes 64, a column of codes 32.
+// The tile of moe_rows.cu: a warp owns 32 rows x 64 columns, a thread 8 rows x
+// 8 columns of them: lane 8 i + j has rows 8 i + [0, 8) and columns 8 j + [0,
+// 8).  A row block (32 columns) is then four neighbouring lanes and a column
+// block (32 rows) the four lanes 8 apart, so both block maxima are two
+// shuffles and the values are read once for both layouts.  Every access is
+// whole sectors: a row of codes is 64 contiguous bytes over its eight lanes, a
+// column of codes 32.  (moe_swiglu.cu has more values live per element and
+// half the tile per thread.)
 #pragma once
 
 #include "common.cuh"
@@ -87,8 +90,9 @@ __device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float m) {
   const float2 a = __fmul2_rn(v[0], mm), b = __fmul2_rn(v[1], mm), c = __fmul2_rn(v[2], mm), d = __fmul2_rn(v[3], mm);
   return make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y));
 }
+
 // Two blocks' exponents in the halves of one word.  `raw` is (bits(amax) +
-// round) >> 23 of mx_t before its clamp: it grows with the max, so the lanes
+// round) >> 23 of mx_fp32.cuh before its clamp: it grows with the max, so the lanes
 // of a block reduce it (__vmaxu2) and clamp once.
 __device__ __forceinline__ uint32_t mx_raw2(float amax_lo, float amax_hi, uint32_t round) {  // both >= 0 or NaN
   return (__float_as_uint(amax_lo) + round) >> 23 | (((__float_as_uint(amax_hi) + round) >> 7) & 0xFFFF0000u);

@@ -209,23 +209,24 @@ class _Experts(torch.autograd.Function):
         a, kept = swiglu(h, keep=train, colwise=train, mode=mode)
         y = _grouped(B.GROUPED_FWD, a.q, a.e8, q2.q_row, q2.e8_row, p, C, F, bf(p.rows, C))
         if train:
-            ctx.plan, ctx.mode, ctx.weights, ctx.y, ctx.kept = p, mode, weights, y, kept
-            ctx.xT, ctx.aT = (rows.qT, rows.e8T), (a.qT, a.e8T)
-            ctx.w13T, ctx.w2T = (q13.qT_col, q13.e8_col), (q2.qT_col, q2.e8_col)
+            ctx.mode = mode
+            ctx.save_for_backward(weights, y, kept.q, kept.e8, rows.qT, rows.e8T, a.qT, a.e8T, q13.qT_col, q13.e8_col,
+                                  q2.qT_col, q2.e8_col, p.group_end, p.counts, p.row_of, p.src_of)
         return combine(y, weights, p)
 
     @staticmethod
     def backward(ctx, dout):
-        p, mode = ctx.plan, ctx.mode
-        E, C, F2 = ctx.w13T[0].shape
+        weights, y, hq, he, xT, xeT, aT, aeT, w13T, w13e, w2T, w2e, *tables = ctx.saved_tensors
+        p, mode = Plan(*tables), ctx.mode
+        E, C, F2 = w13T.shape
         F = F2 // 2
         bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=dout.device)  # noqa: E731
-        dy, dweights = combine_backward(dout.contiguous(), ctx.y, ctx.weights, p, mode=mode)
-        da = _grouped(B.GROUPED_DGRAD, dy.q, dy.e8, *ctx.w2T, p, C, F, bf(p.rows, F))
-        dw2 = _grouped(B.GROUPED_WGRAD, dy.qT, dy.e8T, *ctx.aT, p, C, F, bf(E, C, F))
-        dh = swiglu_backward(da, ctx.kept, mode=mode)
-        drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, *ctx.w13T, p, F2, C, bf(p.rows, C))
-        dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, *ctx.xT, p, F2, C, bf(E, F2, C))
+        dy, dweights = combine_backward(dout.contiguous(), y, weights, p, mode=mode)
+        da = _grouped(B.GROUPED_DGRAD, dy.q, dy.e8, w2T, w2e, p, C, F, bf(p.rows, F))
+        dw2 = _grouped(B.GROUPED_WGRAD, dy.qT, dy.e8T, aT, aeT, p, C, F, bf(E, C, F))
+        dh = swiglu_backward(da, MxRows(hq, he), mode=mode)
+        drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, w13T, w13e, p, F2, C, bf(p.rows, C))
+        dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, xT, xeT, p, F2, C, bf(E, F2, C))
         return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None
 
 
