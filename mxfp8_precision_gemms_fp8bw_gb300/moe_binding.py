@@ -53,9 +53,11 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, *shape: int):
     """The tensor's address, once its dtype, device, layout and shape are what the call reads or writes."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    return B._ptr(t, dtype, name)
+    return B._ptr(t, dtype, name)  # raises with what is wrong
 
 
 def _stream(stream, t: torch.Tensor):
