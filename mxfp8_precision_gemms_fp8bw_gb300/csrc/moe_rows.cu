@@ -1,5 +1,7 @@
 // Rows of the experts: gathering tokens into them as MX codes, and summing
 // them back into the tokens.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "mx_tile.cuh"
@@ -10,16 +12,15 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 
 constexpr int kGatherWarps = 8;
-// Blocks per SM: three without weights; the products that the weighted form
-// keeps leave registers for two (three spill: 76 us against 70 on 8192 x 2
-// rows of 5120).
-constexpr int gather_ctas_per_sm(bool weighted) { return weighted ? 2 : 3; }
 
 // Where a block has its copies: two tiles of x, and of four tiles in turn the
 // rows' tokens (-1: none) and weights, because the tokens are needed two
-// tiles before the weights are done with.
+// tiles before the weights are done with; and two tiles of column codes on
+// their way out.
+template <bool kCol>
 struct GatherSmem {
   uint4 x[2][128][16];
+  alignas(kCol ? 1024 : 16) uint8_t qT[kCol ? 2 : 1][kCol ? 128 * 128 : 16];
   ScaleTile scales[2];
   int32_t token[4][16][8];  // row r at [r % 16][r / 16]: the eight that a thread copies are contiguous
   float weight[4][128];
@@ -29,6 +30,30 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool liv
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
                : "memory");
 }
+
+// Column codes leave through shared memory by a tensor store of 128 rows x 128
+// columns: straight from the lanes they are 32-byte pieces, and the requests
+// for those, more than the bytes, were what the two-layout kernel waited for
+// (7.1 million write requests for 170 MB, L1 to crossbar 58 % busy).  A
+// column's 128 codes are a 128-byte line of shared memory under the 128-byte
+// swizzle; lines are ordered by (column % 8, column / 8), which the tensor map
+// undoes, so that the eight columns that lanes write together are lines with
+// different swizzles and hit different banks.
+__device__ __forceinline__ void put_column(uint8_t* cols, int rt, int ct, int j, uint2 codes) {
+  const int line = j * 16 + ct / 8;
+  *reinterpret_cast<uint2*>(cols + line * 128 + (((rt >> 4) ^ (line & 7)) << 4) + (rt & 8)) = codes;
+}
+__device__ __forceinline__ void store_columns(const CUtensorMap* map, const uint8_t* cols, int row, int group) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(smem_u32(cols)), "r"(row), "r"(group), "r"(0)
+      : "memory");
+}
+
+// Blocks per SM: the rows alone leave room for three, the column codes on their
+// way out for two.
+constexpr int gather_ctas_per_sm(bool columns) { return columns ? 2 : 3; }
 
 // MX codes of gathered rows, v_p = w_p * x[src_p / top_k], in both layouts.
 //
@@ -56,14 +81,15 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool liv
 // gathered up to top_k times, and a stripe of x stays in L2 between them
 // (with the columns fastest, 5120 of them and 8192 x 2 entries, x came from
 // DRAM 1.9 times).
-template <bool kWeighted>
-__global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighted))
-    gather_quant_kernel(const uint16_t* __restrict__ x, const float* __restrict__ weights,
-                        const int32_t* __restrict__ src_of, uint32_t entries, uint32_t top_k, int P, int C, int bands,
-                        int tiles, uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ qT,
-                        uint8_t* __restrict__ e8T, int mode, int* status) {
-  extern __shared__ __align__(128) uint8_t gather_smem[];
-  GatherSmem& sm = *reinterpret_cast<GatherSmem*>(gather_smem);
+template <bool kWeighted, bool kCol>
+__global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kCol))
+    gather_quant_kernel(const __grid_constant__ CUtensorMap map, const uint16_t* __restrict__ x,
+                        const float* __restrict__ weights, const int32_t* __restrict__ src_of, uint32_t entries, uint32_t top_k, int P, int C, int bands,
+                        int tiles, uint8_t* __restrict__ q, uint8_t* __restrict__ e8, uint8_t* __restrict__ e8T,
+                        int mode, int* status) {
+  extern __shared__ uint8_t gather_smem[];
+  GatherSmem<kCol>& sm = *reinterpret_cast<GatherSmem<kCol>*>(
+      (reinterpret_cast<uintptr_t>(gather_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   const TileLane t = tile_lane();
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t round = mx_round_f32(mode);
@@ -113,9 +139,10 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto finish_scales = [&](int n, Tile w) {  // of tile n, once every thread has written its bytes
+  auto finish = [&](int n, Tile w) {  // of tile n, once every thread has written its part
+    if (kCol && tid == 0) store_columns(&map, sm.qT[n & 1], w.band * 128, w.stripe * 16);
     put_scales(sm.scales[n & 1].row, tid, static_cast<int64_t>(w.band) * 128, P, e8, w.stripe * 4, C / 32);
-    if (qT != nullptr)
+    if (kCol)
       put_scales(sm.scales[n & 1].col, tid - 128, static_cast<int64_t>(w.stripe) * 128, C, e8T, w.band * 4, P / 32);
   };
 
@@ -126,13 +153,14 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
   fetch(0, now);
   int n = 0;
   for (; now.band >= 0; ++n) {
-    // Tile n has landed; everyone has left tile n - 1 and its buffers.
+    // Tile n has landed, the column codes of tile n - 2 have left; everyone has left tile n - 1 and its buffers.
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (kCol && tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncthreads();
     fetch(n + 1, next);
     const Tile after = tile_at(n + 2);
     const uint32_t src = look_up(after);
-    if (n > 0) finish_scales(n - 1, last);
+    if (n > 0) finish(n - 1, last);
 
     const int rt = (warp >> 1) * 32 + t.rg * 8, ct = (warp & 1) * 64 + t.cg * 8;  // the thread's part of the tile
     const int c0 = now.stripe * 128 + ct;
@@ -142,14 +170,14 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = sm.x[n & 1][rt + i][ct / 8];
     uint8_t* qrow = q + r0 * C + c0;
-    uint8_t* qcol = qT + static_cast<int64_t>(c0) * P + r0;
+    uint8_t* cols = sm.qT[n & 1];
 
     uint32_t m[4];  // of rows 2 p and 2 p + 1
 #pragma unroll
     for (int p = 0; p < 4; ++p) m[p] = block_absmax2<1>(fold2(absmax2_of8(v[2 * p]), absmax2_of8(v[2 * p + 1])));
 
     uint32_t cm[4];  // of columns 2 k and 2 k + 1
-    if (!kWeighted && qT != nullptr) {  // before the conversions, which hide the shuffles
+    if (!kWeighted && kCol) {  // before the conversions, which hide the shuffles
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         cm[k] = word_of(v[0], k);
@@ -169,14 +197,13 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
         qrow += 2 * static_cast<int64_t>(C);
         rb[p] = mx_bytes2(e);
       }
-      if (qT != nullptr) {
+      if (kCol) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // columns c0 + 2k and c0 + 2k + 1
           const uint32_t e = mx_t2(cm[k], round);
           const CodePair codes = codes8_cols(v, k, mx_mul2(e));
-          st_codes8(qcol, codes.lo, live);
-          st_codes8(qcol + P, codes.hi, live);
-          qcol += 2 * static_cast<int64_t>(P);
+          put_column(cols, rt, ct, 2 * k, codes.lo);
+          put_column(cols, rt, ct, 2 * k + 1, codes.hi);
           cb[k] = mx_bytes2(e);
         }
       }
@@ -199,7 +226,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
         qrow += 2 * static_cast<int64_t>(C);
         rb[p] = mx_bytes2(e);
       }
-      if (qT != nullptr) {
+      if (kCol) {
         uint32_t e[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -221,21 +248,22 @@ __global__ void __launch_bounds__(kGatherWarps * 32, gather_ctas_per_sm(kWeighte
 #pragma unroll
           for (int i = 0; i < 8; ++i) p[i] = __fmul2_rn(f[i][k], mul);
           const CodePair codes = pair_of_columns(p);
-          st_codes8(qcol, codes.lo, live);
-          st_codes8(qcol + P, codes.hi, live);
-          qcol += 2 * static_cast<int64_t>(P);
+          put_column(cols, rt, ct, 2 * k, codes.lo);
+          put_column(cols, rt, ct, 2 * k + 1, codes.hi);
           cb[k] = mx_bytes2(e[k]);
         }
       }
     }
     put_bytes(sm.scales[n & 1], rt, ct, rb, cb);
+    if (kCol) fence_proxy_async_smem();  // the column codes, for the bulk store behind the barrier
     note(n + 2, src);
     last = now;
     now = next;
     next = after;
   }
   __syncthreads();
-  finish_scales(n - 1, last);
+  finish(n - 1, last);
+  if (kCol && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ int64_t checked_row(const int32_t* row_of, int64_t i, int64_t P, int* status) {
@@ -339,20 +367,42 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
+// qT [C][P] as (row, column / 8, column % 8), in boxes of 128 x 16 x 8.
+static bool column_map(CUtensorMap* map, uint8_t* qT, int64_t C, int64_t P) {
+  typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(P), static_cast<cuuint64_t>(C / 8), 8};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(8 * P), static_cast<cuuint64_t>(P)};
+  const cuuint32_t box[3] = {128, 16, 8}, each[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, qT, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_moe_gather_quant(const MoeGatherArgs& a, cudaStream_t st) {
   const int64_t bands = (a.P + 127) / 128, tiles = bands * ((a.C + 127) / 128);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const int64_t cap = static_cast<int64_t>(a.num_sms) * gather_ctas_per_sm(a.weights != nullptr);
-  auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(GatherSmem));
+  CUtensorMap map{};
+  if (a.qT != nullptr && !column_map(&map, a.qT, a.C, a.P)) return cudaErrorInvalidValue;
+  auto go = [&](auto weighted, auto columns) {
+    constexpr bool kWeighted = decltype(weighted)::value, kCol = decltype(columns)::value;
+    const auto kernel = gather_quant_kernel<kWeighted, kCol>;
+    constexpr int smem = sizeof(GatherSmem<kCol>) + 1024;  // for its alignment
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), kGatherWarps * 32, sizeof(GatherSmem), st>>>(
-        a.x, a.weights, a.src_of, static_cast<uint32_t>(a.M * a.top_k), static_cast<uint32_t>(a.top_k),
-        static_cast<int>(a.P), static_cast<int>(a.C), static_cast<int>(bands), static_cast<int>(tiles), a.q, a.e8, a.qT,
-        a.e8T, a.mode, a.status);
+    const int64_t cap = static_cast<int64_t>(a.num_sms) * gather_ctas_per_sm(kCol);
+    kernel<<<dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), kGatherWarps * 32, smem, st>>>(
+        map, a.x, a.weights, a.src_of, static_cast<uint32_t>(a.M * a.top_k), static_cast<uint32_t>(a.top_k),
+        static_cast<int>(a.P), static_cast<int>(a.C), static_cast<int>(bands), static_cast<int>(tiles), a.q, a.e8, a.e8T,
+        a.mode, a.status);
     return cudaGetLastError();
   };
-  return a.weights != nullptr ? go(gather_quant_kernel<true>) : go(gather_quant_kernel<false>);
+  const std::true_type yes;
+  const std::false_type no;
+  if (a.weights != nullptr) return a.qT != nullptr ? go(yes, yes) : go(yes, no);
+  return a.qT != nullptr ? go(no, yes) : go(no, no);
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs& a, cudaStream_t st) {

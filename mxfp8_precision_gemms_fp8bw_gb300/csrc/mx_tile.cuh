@@ -158,19 +158,27 @@ __device__ __forceinline__ void put_bytes(ScaleTile& s, int rt, int ct, const ui
         make_uint2(__byte_perm(cols[0], cols[1], 0x6420), __byte_perm(cols[2], cols[3], 0x6420));
 }
 
-// Line `i` (0 to 127; others do nothing) of one side: entries b0 .. b0 + 3 of
-// line first + i of out [lines][per_line].
+// One side by 128 threads, i = 0 to 127 (others do nothing): entries b0 .. b0 +
+// 3 of lines first .. first + 127 of out [lines][per_line].  A word per line
+// where lines are words; else four neighbouring lanes have a line's four
+// bytes, which then still are one request (a thread per line, byte by byte,
+// is four: 62 us for the two-layout kernel at 519 bytes per line against
+// 54).
 __device__ __forceinline__ void put_scales(const uint8_t (&side)[4][128], int i, int64_t first, int64_t lines,
                                            uint8_t* __restrict__ out, int b0, int per_line) {
-  if (i < 0 || i >= 128 || first + i >= lines) return;
-  uint8_t* to = out + (first + i) * per_line + b0;
+  if (i < 0 || i >= 128) return;
   if ((per_line & 3) == 0) {
-    *reinterpret_cast<uint32_t*>(to) =
-        side[0][i] | side[1][i] << 8 | side[2][i] << 16 | static_cast<uint32_t>(side[3][i]) << 24;
+    if (first + i < lines)
+      *reinterpret_cast<uint32_t*>(out + (first + i) * per_line + b0) =
+          side[0][i] | side[1][i] << 8 | side[2][i] << 16 | static_cast<uint32_t>(side[3][i]) << 24;
   } else {
+    const int b = i & 3;
+    if (b0 + b >= per_line) return;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (b0 + b < per_line) to[b] = side[b][i];
+    for (int j = 0; j < 4; ++j) {
+      const int line = j * 32 + i / 4;
+      if (first + line < lines) out[(first + line) * per_line + b0 + b] = side[b][line];
+    }
   }
 }
 
