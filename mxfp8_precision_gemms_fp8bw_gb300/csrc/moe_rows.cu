@@ -57,25 +57,25 @@ constexpr int gather_ctas_per_sm(bool columns) { return columns ? 2 : 3; }
 
 // MX codes of gathered rows, v_p = w_p * x[src_p / top_k], in both layouts.
 //
-// Both layouts are bound by instructions (two conversions per element, some 14
-// instructions with what belongs to them, issued in half of the cycles), the
-// rows alone by memory.  Blocks are persistent, two or three to an SM, and
-// walk 128 x 128 tiles whose rows of x are on their way (cp.async, one 16-byte
-// chunk at a time, zeros where there is no row) while the tile before is
-// converted, and whose tokens were looked up one tile earlier still.  A
-// thread takes its 8 x 8 part into registers (mx_tile.cuh) and reads nothing
-// twice; 128 x 128 because the codes of a tile's rows and of its columns
-// then fill whole 128-byte lines.  Without weights the maxima and products are
-// taken on packed bf16 pairs.  With them the max of a row block is still the
-// bf16 max, times |w| (rounding is monotonic, so the product of the max is the
-// max of the products); a column block mixes weights and takes the max of the
-// fp32 products.
+// Blocks are persistent, two or three to an SM, and walk 128 x 128 tiles whose
+// rows of x are on their way (cp.async, one 16-byte chunk at a time, zeros
+// where there is no row) while the tile before is converted, and whose tokens
+// were looked up one tile earlier still.  A thread takes its 8 x 8 part into
+// registers (mx_tile.cuh) and reads nothing twice; 128 x 128 because the codes
+// of a tile's rows and of its columns then fill whole 128-byte lines.  Without
+// weights the maxima and products are taken on packed bf16 pairs.  With them
+// the max of a row block is still the bf16 max, times |w| (rounding is
+// monotonic, so the product of the max is the max of the products); a column
+// block mixes weights and takes the max of the fp32 products.
 //
-// 8192 tokens x 2, 5120 columns: 66 us for both layouts (0.58 of the measured
-// copy bandwidth, counting x once), 33 us for the rows alone (0.76), 70 us
-// weighted.  Not persistent, with the loads straight into registers, it took
-// 70, 43 and 80; with 4 x 8 values per thread and twice the warps 72, 42 and
-// 80; with a 256-byte bulk copy per row in place of the cp.async 67, 39 and 71.
+// 8192 tokens x 2, 5120 columns: 54 us for both layouts (0.70 of the measured
+// copy bandwidth, counting x once), 34 us for the rows alone (0.75), 60 us
+// weighted.  No unit is full: leaving out the scale bytes, the column store,
+// the copies or the row stores saves 4, 8, 8 and 4 us, and what is left, the
+// conversion alone, takes 37.  Not persistent, with the loads straight into
+// registers, and with the column codes stored by the lanes it took 70, 43 and
+// 80; with 4 x 8 values per thread and twice the warps 72, 42 and 80; with a
+// 256-byte bulk copy per row in place of the cp.async 67, 39 and 71.
 //
 // The tiles of one 128-column stripe come one after another: a token is
 // gathered up to top_k times, and a stripe of x stays in L2 between them
