@@ -384,14 +384,16 @@ static bool column_map(CUtensorMap* map, uint8_t* qT, int64_t C, int64_t P) {
 cudaError_t launch_moe_gather_quant(const MoeGatherArgs& a, cudaStream_t st) {
   const int64_t bands = (a.P + 127) / 128, tiles = bands * ((a.C + 127) / 128);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  CUtensorMap map{};
-  if (a.qT != nullptr && !column_map(&map, a.qT, a.C, a.P)) return cudaErrorInvalidValue;
   auto go = [&](auto weighted, auto columns) {
     constexpr bool kWeighted = decltype(weighted)::value, kCol = decltype(columns)::value;
     const auto kernel = gather_quant_kernel<kWeighted, kCol>;
     constexpr int smem = sizeof(GatherSmem<kCol>) + 1024;  // for its alignment
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // Behind a runtime call, which binds the device's context to a thread that has made none yet (a backward
+    // pass runs in one); the driver's encoder does not.
+    CUtensorMap map{};
+    if (kCol && !column_map(&map, a.qT, a.C, a.P)) return cudaErrorInvalidValue;
     const int64_t cap = static_cast<int64_t>(a.num_sms) * gather_ctas_per_sm(kCol);
     kernel<<<dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), kGatherWarps * 32, smem, st>>>(
         map, a.x, a.weights, a.src_of, static_cast<uint32_t>(a.M * a.top_k), static_cast<uint32_t>(a.top_k),

@@ -1,7 +1,7 @@
 """A mixture-of-experts layer in MXFP8: the operators around the experts' products and the layer they make.
 
 Each function allocates its outputs, runs on the current stream and returns
-without waiting; the work is in libfp8bw's kernels (``include/fp8bw_moe.h`` has
+without waiting; a batch may have no tokens.  The work is in libfp8bw's kernels (``include/fp8bw_moe.h`` has
 the formulas).  For ``linear``'s grouped GEMMs, ``Plan.group_end`` is the group
 table and ``MxRows`` holds their operands.
 
@@ -46,6 +46,8 @@ def route(logits: torch.Tensor, top_k: int, *, bias: torch.Tensor | None = None,
     M = logits.shape[0]
     experts = torch.empty((M, top_k), dtype=_I32, device=logits.device)
     weights = torch.empty((M, top_k), dtype=_F32, device=logits.device)
+    if M == 0:
+        return experts, weights
     MB.fp8bw_moe_route(logits, bias, top_k, experts, weights, groups, groups_kept, group_top, _score(score),
                        renormalize, scale)
     return experts, weights
@@ -55,6 +57,8 @@ def route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.
                    renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
     """Gradient of the logits (their dtype) from that of ``route``'s weights."""
     dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    if logits.shape[0] == 0:
+        return dlogits
     MB.fp8bw_moe_route_bwd(dweights, logits, experts, dlogits, _score(score), renormalize, scale)
     return dlogits
 
@@ -93,8 +97,12 @@ def plan(experts: torch.Tensor, num_experts: int) -> Plan:
     groups of whole 32-row blocks, without the host learning the counts."""
     M, top_k = experts.shape
     dev = experts.device
-    P, ws_bytes = _plan_sizes(M, num_experts, top_k)
+    P, ws_bytes = _plan_sizes(max(M, 1), num_experts, top_k)
     e = lambda *shape: torch.empty(shape, dtype=_I32, device=dev)  # noqa: E731
+    if M == 0:  # no entries: every row is empty
+        p = Plan(e(num_experts).zero_(), e(num_experts).zero_(), e(0, top_k), e(P).fill_(-1))
+        p.group_end[-1:] = P
+        return p
     p = Plan(e(num_experts), e(num_experts), e(M, top_k), e(P))
     ws = torch.empty(ws_bytes, dtype=_U8, device=dev) if ws_bytes else None
     MB.fp8bw_moe_plan(experts, num_experts, p.group_end, p.counts, p.row_of, p.src_of, ws)
@@ -110,12 +118,20 @@ def _plan_sizes(M: int, num_experts: int, top_k: int) -> tuple[int, int]:
     return P, MB.fp8bw_moe_plan_workspace_bytes(M, num_experts, top_k)
 
 
+def _gathered(x: torch.Tensor, weights: torch.Tensor | None, p: Plan, colwise: bool, mode: int) -> MxRows:
+    out = _mx_rows(p.rows, x.shape[1], x.device, colwise)
+    if x.shape[0] == 0:  # rows of zeros are codes and scales of 0
+        for t in (out.q, out.e8, *((out.qT, out.e8T) if colwise else ())):
+            t.zero_()
+        return out
+    MB.mxfp8_moe_gather_quant(x, weights, p.src_of, p.row_of.shape[1], out.q, out.e8, out.qT, out.e8T, mode)
+    return out
+
+
 def dispatch(x: torch.Tensor, p: Plan, colwise: bool = True, mode: int = B.MX_RCEIL) -> MxRows:
     """MX codes of the experts' rows of x (bf16 [M, C]); ``colwise`` adds the
     layout the weight gradient reads."""
-    out = _mx_rows(p.rows, x.shape[1], x.device, colwise)
-    MB.mxfp8_moe_gather_quant(x, None, p.src_of, p.row_of.shape[1], out.q, out.e8, out.qT, out.e8T, mode)
-    return out
+    return _gathered(x, None, p, colwise, mode)
 
 
 def dispatch_backward(drows: torch.Tensor, p: Plan) -> torch.Tensor:
@@ -127,6 +143,8 @@ def combine(y: torch.Tensor, weights: torch.Tensor | None, p: Plan, base: torch.
     """out[t] = base[t] + the sum of token t's rows of y (bf16 [P, C]) times
     their weights (fp32 [M, top_k]; None: one each)."""
     out = torch.empty((p.row_of.shape[0], y.shape[1]), dtype=_BF16, device=y.device)
+    if out.shape[0] == 0:
+        return out
     MB.fp8bw_moe_combine(y, weights, p.row_of, base, out)
     return out
 
@@ -134,10 +152,10 @@ def combine(y: torch.Tensor, weights: torch.Tensor | None, p: Plan, base: torch.
 def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, p: Plan, mode: int = B.MX_RCEIL):
     """Gradients of ``combine``: that of y as MX codes in both layouts, and
     that of the weights."""
-    dy = _mx_rows(p.rows, dout.shape[1], dout.device)
-    MB.mxfp8_moe_gather_quant(dout, weights, p.src_of, p.row_of.shape[1], dy.q, dy.e8, dy.qT, dy.e8T, mode)
+    dy = _gathered(dout, weights, p, True, mode)
     dweights = torch.empty_like(weights, memory_format=torch.contiguous_format)
-    MB.fp8bw_moe_combine_dweights(dout, y, p.row_of, dweights)
+    if dout.shape[0] > 0:
+        MB.fp8bw_moe_combine_dweights(dout, y, p.row_of, dweights)
     return dy, dweights
 
 

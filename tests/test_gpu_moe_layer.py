@@ -76,6 +76,32 @@ def test_inference_keeps_nothing_and_agrees():
         assert torch.equal(layer(x), out)
 
 
+def test_a_batch_without_tokens():
+    """Outputs of no rows, empty groups, and gradients of zero."""
+    logits = torch.empty(0, 8, device="cuda")
+    experts, weights = moe.route(logits, 2)
+    assert experts.shape == weights.shape == (0, 2)
+    assert moe.route_backward(weights, logits, experts).shape == (0, 8)
+    p = moe.plan(experts, 8)
+    assert p.group_end.tolist() == [0] * 7 + [p.rows] and p.rows % 32 == 0
+    assert not p.counts.any() and bool((p.src_of == -1).all()) and p.row_of.shape == (0, 2)
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    rows = moe.dispatch(x, p)
+    assert rows.qT.shape == (64, p.rows) and not any(t.any() for t in (rows.q, rows.e8, rows.qT, rows.e8T))
+    y = torch.ones(p.rows, 64, dtype=torch.bfloat16, device="cuda")
+    assert moe.combine(y, weights, p).shape == (0, 64)
+    dy, dw = moe.combine_backward(x, y, weights, p)
+    assert not dy.qT.any() and dw.shape == (0, 2)
+
+    layer = moe.MxMoEFFN(256, 256, 4, 2, device="cuda")
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    out = layer(x)
+    out.backward(torch.empty_like(out))
+    B.fp8bw_sync_status()
+    assert out.shape == x.grad.shape == (0, 256)
+    assert not layer.w13.grad.any() and not layer.w2.grad.any() and not layer.router.grad.any()
+
+
 def test_update_balance_moves_against_the_load():
     layer = moe.MxMoEFFN(256, 256, 4, 1, device="cuda")
     with pytest.raises(RuntimeError):

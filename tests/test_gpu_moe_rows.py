@@ -211,6 +211,28 @@ def test_calls_follow_their_stream_and_replay_in_graphs():
     assert torch.equal(d, ref[1])
 
 
+def test_first_call_of_a_thread():
+    """A thread that has not used the GPU yet, as autograd's backward thread may be, on a stream it is handed."""
+    import threading
+
+    r, p, w = setup(200, 4, 2, seed=8)
+    x = normal(r, 200, 160)
+    ref = moe.dispatch(x, p)
+    out, stream, errors = moe._mx_rows(p.rows, 160, x.device), torch.cuda.current_stream().cuda_stream, []
+
+    def work():
+        try:
+            MB.mxfp8_moe_gather_quant(x, None, p.src_of, 2, out.q, out.e8, out.qT, out.e8T, stream=stream)
+        except Exception as e:
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    B.fp8bw_sync_status()
+    assert not errors and torch.equal(out.q, ref.q) and torch.equal(out.qT, ref.qT) and torch.equal(out.e8T, ref.e8T)
+
+
 def test_outputs_stay_in_bounds():
     """Canaries on both sides of every output."""
     r, p, w = setup(45, 8, 2, seed=6)

@@ -139,5 +139,5 @@ def test_binding_refuses_wrong_types_shapes_and_devices():
     with pytest.raises(ValueError):       # an odd width is no [gate | up]
         moe.swiglu(z(32, 65, dtype=torch.bfloat16))
     with pytest.raises(B.Fp8bwError) as e:
-        moe.plan(z(0, 2, dtype=torch.int32), 8)
+        moe.plan(z(5, 2, dtype=torch.int32), 0)
     assert e.value.code == B.ERR_SHAPE
