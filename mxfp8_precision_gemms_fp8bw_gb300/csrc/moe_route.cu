@@ -26,19 +26,6 @@ __device__ __forceinline__ Best best_of(const uint32_t (&key)[V], int l) {
   return b;
 }
 
-// The same over two candidates a lane that carry their places.
-template <int L>
-__device__ __forceinline__ Best best_of2(const uint32_t (&key)[2], const int (&at)[2]) {
-  const bool second = key[1] > key[0] || (key[1] == key[0] && at[1] < at[0]);
-  Best b = second ? Best{key[1], at[1]} : Best{key[0], at[0]};
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const Best c{__shfl_xor_sync(kAll, b.key, o), __shfl_xor_sync(kAll, b.at, o)};
-    if (c.key > b.key || (c.key == b.key && c.at < b.at)) b = c;
-  }
-  return b;
-}
-
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __restrict__ logits,
                                                                  const float* __restrict__ bias, RouteShape p,
@@ -57,14 +44,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
     x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
   }
   const RowScale scale = scores_of<L, V, true>(x, p.score, s);
-  if (bias == nullptr) {
+  if (bias == nullptr && p.groups == 1) {
+    // Scores are not negative, and NaN comes as 0x7fffffff: their bits order them.
 #pragma unroll
     for (int v = 0; v < V; ++v)  // x is -inf past the last expert
-      key[v] = x[v] == -INFINITY ? 0u : s[v] != s[v] ? 0xffffffffu : __float_as_uint(s[v]) | 0x80000000u;
+      key[v] = x[v] == -INFINITY ? 0u : __float_as_uint(s[v]) + 1u;
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float b = v * L + l < p.E ? bias[v * L + l] : 0.f;
+      const float b = bias != nullptr && v * L + l < p.E ? bias[v * L + l] : 0.f;
       key[v] = x[v] == -INFINITY || b == -INFINITY ? 0u : ordered(s[v] + b);
     }
   }
@@ -127,9 +115,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
     // Looking through all V keys again for every choice costs more than all
     // the scores.  At least k experts are not below the k-th largest of the
     // lanes' maxima, and rarely more than twice as many: those go into a short
-    // list, two to a lane, and the choices are made there.
+    // list, whose members then rank each other.
     if (p.k <= L) {
       __shared__ uint2 lists[kRouteWarps * kRowsPerWarp][2 * L];
+      __shared__ int16_t orders[kRouteWarps * kRowsPerWarp][L];
       uint32_t most = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) most = max(most, key[v]);
@@ -164,16 +153,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
           to += in ? sizeof(uint2) : 0;
         }
         __syncwarp();
-        const uint2 a = l < all ? list[l] : make_uint2(0, 0), b = l + L < all ? list[l + L] : make_uint2(0, 0);
-        uint32_t ck[2] = {a.x, b.x};
-        const int ce[2] = {static_cast<int>(a.y), static_cast<int>(b.y)};
-#pragma unroll 1
-        for (int j = 0; j < p.k; ++j) {
-          const Best w = best_of2<L>(ck, ce);
-          if (w.key != 0 && l == j) chosen[0] = w.at;
-          if (ce[0] == w.at) ck[0] = 0;
-          if (ce[1] == w.at) ck[1] = 0;
+        // Every candidate's rank among them, by reading the list.
+        int16_t* order = orders[mine];
+        for (int i = l; i < all; i += L) {
+          const uint2 c = list[i];
+          int before = 0;
+#pragma unroll
+          for (int j = 0; j < 2 * L; ++j) {
+            const uint2 o = j < all ? list[j] : make_uint2(0, 0);
+            before += o.x > c.x || (o.x == c.x && o.y < c.y);
+          }
+          if (before < p.k) order[before] = static_cast<int16_t>(c.y);
         }
+        __syncwarp();
+        if (l < p.k && l < all) chosen[0] = order[l];
       }
     }
   }

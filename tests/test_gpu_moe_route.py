@@ -297,3 +297,23 @@ def test_rows_of_every_spread(E, k, dtype):
     B.fp8bw_sync_status()
     assert keep.sum() > M // 2 and np.array_equal(experts.cpu().numpy()[keep], ref_e[keep])
     assert np.all(np.abs(weights.cpu().numpy() - ref_w)[keep] <= (weight_bound(logits, k) * ref_w + 1e-37)[keep])
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E", [16, 64, 160, 600])
+def test_nan_is_chosen_first_at_every_width(E, biased, groups):
+    """A NaN logit comes before every number, masked experts never, whatever path the width takes."""
+    x = torch.randn(9, E, device="cuda")
+    at = [0, 1, 7, 8, E // 2, E - 2, E - 1, 3, 5]
+    for t, e in enumerate(at):
+        x[t, e] = float("nan")
+        x[t, (e + 2) % E] = float("-inf")
+    bias = torch.randn(E, device="cuda") * 0.01 if biased else None
+    how = dict(bias=bias, groups=groups, groups_kept=min(groups, 2), group_top=1)
+    experts, weights = moe.route(x, 3, score="sigmoid", **how)
+    assert experts[:, 0].tolist() == at and bool(weights[:, 0].isnan().all())
+    experts, weights = moe.route(x, 3, **how)       # a softmax row with a NaN has nothing else
+    assert bool(weights.isnan().all())
+    assert not bool((experts == torch.tensor([(e + 2) % E for e in at], device="cuda")[:, None]).any())
+    B.fp8bw_sync_status()
