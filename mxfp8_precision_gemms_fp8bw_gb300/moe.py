@@ -1,8 +1,8 @@
 """A mixture-of-experts layer in MXFP8: the operators around the experts' products and the layer they make.
 
 Each function allocates its outputs, runs on the current stream and returns
-without waiting; a batch may have no tokens.  The work is in libfp8bw's kernels (``include/fp8bw_moe.h`` has
-the formulas).  For ``linear``'s grouped GEMMs, ``Plan.group_end`` is the group
+without waiting; a batch may have no tokens.  The work is in libfp8bw's
+kernels (``include/fp8bw_moe.h`` has the formulas).  For ``linear``'s grouped GEMMs, ``Plan.group_end`` is the group
 table and ``MxRows`` holds their operands.
 
     experts, weights = route(logits, top_k)          x -> experts of each token

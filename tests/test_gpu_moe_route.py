@@ -317,3 +317,32 @@ def test_nan_is_chosen_first_at_every_width(E, biased, groups):
     assert bool(weights.isnan().all())
     assert not bool((experts == torch.tensor([(e + 2) % E for e in at], device="cuda")[:, None]).any())
     B.fp8bw_sync_status()
+
+
+@pytest.mark.parametrize("bits", [0x7FC00000, -0x400000, -1, 0x7F800001])
+@pytest.mark.parametrize("E", [8, 16, 64, 160, 600])
+def test_a_nan_counts_whatever_its_sign_and_payload(E, bits):
+    x = torch.randn(5, E, device="cuda")
+    at = [0, 7, E // 2, E - 1, 3]
+    for t, e in enumerate(at):
+        x[t].view(torch.int32)[e] = bits
+    assert int(x.isnan().sum()) == 5
+    experts, weights = moe.route(x, 2, score="sigmoid")
+    assert experts[:, 0].tolist() == at and bool(weights.isnan().all())
+    experts, weights = moe.route(x, 2)       # every score is NaN: the lowest places
+    assert experts.tolist() == [[0, 1]] * 5 and bool(weights.isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [8, 16, 64, 160, 600])
+def test_infinite_logits(E, dtype):
+    x = torch.randn(4, E, device="cuda").to(dtype)
+    x[:, E - 3] = float("inf")
+    x[1, 2] = float("-inf")
+    x[2] = float("-inf")
+    experts, weights = moe.route(x, 2, score="sigmoid", renormalize=False)
+    assert experts[:, 0].tolist() == [E - 3, E - 3, -1, E - 3]
+    assert weights[:, 0].tolist() == [1, 1, 0, 1] and experts[2].tolist() == [-1, -1]
+    experts, weights = moe.route(x, 2, renormalize=False)  # inf - inf: the softmax of the row is NaN
+    assert bool(weights[[0, 1, 3]].isnan().all()) and weights[2].tolist() == [0, 0]
+    assert experts.tolist() == [[0, 1], [0, 1], [-1, -1], [0, 1]]
