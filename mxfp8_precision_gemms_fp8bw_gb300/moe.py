@@ -214,10 +214,9 @@ class _Experts(torch.autograd.Function):
     one (the weights' gradient reads it)."""
 
     @staticmethod
-    def forward(ctx, x, weights, experts, w13, w2, mode, counts):
+    def forward(ctx, x, weights, experts, w13, w2, mode, train, counts):
         E, F2, C = w13.shape
         F = F2 // 2
-        train = any(ctx.needs_input_grad)
         p = plan(experts, E)
         counts.append(p.counts)
         rows = dispatch(x, p, colwise=train, mode=mode)
@@ -245,7 +244,7 @@ class _Experts(torch.autograd.Function):
         dh = swiglu_backward(da, MxRows(hq, he), mode=mode)
         drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, w13T, w13e, p, F2, C, bf(p.rows, C))
         dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, xT, xeT, p, F2, C, bf(E, F2, C))
-        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None
+        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None, None
 
 
 class MxMoEFFN(torch.nn.Module):
@@ -275,8 +274,10 @@ class MxMoEFFN(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         logits = torch.nn.functional.linear(x.float(), self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
+        # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
+        train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, self.w13, self.w2))
         counts = []
-        out = _Experts.apply(x, weights, experts, self.w13, self.w2, self.mode, counts)
+        out = _Experts.apply(x, weights, experts, self.w13, self.w2, self.mode, train, counts)
         self.counts = counts[0]
         return out
 

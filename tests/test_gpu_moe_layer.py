@@ -76,6 +76,19 @@ def test_inference_keeps_nothing_and_agrees():
         assert torch.equal(layer(x), out)
 
 
+@pytest.mark.parametrize("how", ["no_grad", "frozen"])
+def test_inference_makes_nothing_for_backward(how, monkeypatch):
+    layer = moe.MxMoEFFN(256, 256, 8, 2, device="cuda").requires_grad_(how != "frozen")
+    x = torch.randn(50, 256, device="cuda").bfloat16()
+    made = []
+    quantized, activation = moe.MB.mxfp8_moe_gather_quant, moe.MB.mxfp8_swiglu
+    monkeypatch.setattr(moe.MB, "mxfp8_moe_gather_quant", lambda *a: (made.append(a[6:8]), quantized(*a)))
+    monkeypatch.setattr(moe.MB, "mxfp8_swiglu", lambda *a, **k: (made.append(a[3:7]), activation(*a, **k)))
+    with torch.set_grad_enabled(how == "frozen"):
+        layer(x)
+    assert made == [(None, None), (None,) * 4]
+
+
 def test_a_batch_without_tokens():
     """Outputs of no rows, empty groups, and gradients of zero."""
     logits = torch.empty(0, 8, device="cuda")
