@@ -214,13 +214,13 @@ class _Experts(torch.autograd.Function):
     one (the weights' gradient reads it)."""
 
     @staticmethod
-    def forward(ctx, x, weights, experts, w13, w2, mode, train, counts):
+    def forward(ctx, x, weights, experts, w13, w2, codes, mode, train, counts):
         E, F2, C = w13.shape
         F = F2 // 2
         p = plan(experts, E)
         counts.append(p.counts)
         rows = dispatch(x, p, colwise=train, mode=mode)
-        q13, q2 = L.mx_quantize_experts(w13, mode), L.mx_quantize_experts(w2, mode)
+        q13, q2 = codes
         bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
         h = _grouped(B.GROUPED_FWD, rows.q, rows.e8, q13.q_row, q13.e8_row, p, F2, C, bf(p.rows, F2))
         a, kept = swiglu(h, keep=train, colwise=train, mode=mode)
@@ -244,7 +244,7 @@ class _Experts(torch.autograd.Function):
         dh = swiglu_backward(da, MxRows(hq, he), mode=mode)
         drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, w13T, w13e, p, F2, C, bf(p.rows, C))
         dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, xT, xeT, p, F2, C, bf(E, F2, C))
-        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None, None
+        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None, None, None
 
 
 class MxMoEFFN(torch.nn.Module):
@@ -271,13 +271,20 @@ class MxMoEFFN(torch.nn.Module):
         self.mode = mode
         self.counts = None
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def weight_codes(self) -> tuple[L.MxExpertWeights, L.MxExpertWeights]:
+        """MX codes of w13 and w2 as they are now, for calls between two changes of the weights."""
+        return tuple(L.mx_quantize_experts(w.detach(), self.mode) for w in (self.w13, self.w2))
+
+    def forward(self, x: torch.Tensor, codes: tuple[L.MxExpertWeights, L.MxExpertWeights] | None = None) -> torch.Tensor:
+        """``codes``: ``weight_codes()`` kept by the caller (a decoder, or the micro-batches of a step); by default
+        the weights are quantized in every call."""
         logits = torch.nn.functional.linear(x.float(), self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
         train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, self.w13, self.w2))
         counts = []
-        out = _Experts.apply(x, weights, experts, self.w13, self.w2, self.mode, train, counts)
+        out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes or self.weight_codes(), self.mode,
+                             train, counts)
         self.counts = counts[0]
         return out
 

@@ -89,6 +89,22 @@ def test_inference_makes_nothing_for_backward(how, monkeypatch):
     assert made == [(None, None), (None,) * 4]
 
 
+def test_kept_weight_codes_change_nothing():
+    torch.manual_seed(2)
+    layer = moe.MxMoEFFN(256, 512, 4, 2, device="cuda")
+    codes = layer.weight_codes()
+    grads = []
+    for kept in (None, codes):
+        x = torch.randn(70, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16().requires_grad_(True)
+        layer.zero_grad()
+        out = layer(x) if kept is None else layer(x, kept)
+        out.backward(torch.ones_like(out))
+        grads.append((out, x.grad, layer.w13.grad, layer.w2.grad, layer.router.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    with torch.no_grad():
+        assert torch.equal(layer(x, codes), grads[0][0])
+
+
 def test_a_batch_without_tokens():
     """Outputs of no rows, empty groups, and gradients of zero."""
     logits = torch.empty(0, 8, device="cuda")
