@@ -1,8 +1,9 @@
 """ctypes binding of libfp8bw.so: the C ABI's calls under the same names.
 
-Argument marshalling only: each function takes torch CUDA tensors, checks
-their dtype/device/contiguity, passes ``data_ptr()`` and the current CUDA
-stream to the library, and raises ``Fp8bwError`` on a nonzero status.  Every
+Argument marshalling only: each function takes torch CUDA tensors of the
+current device, checks their dtype/device/contiguity, passes ``data_ptr()`` and
+the current CUDA stream to the library, and raises ``Fp8bwError`` on a nonzero
+status.  Every
 step of the computation runs in the library's kernels; there is no fallback.
 ``alloc_*`` helpers create output tensors of the shapes the ABI documents.
 """
@@ -98,6 +99,11 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _current_device() -> int:
+    """The device that the library's calls launch on."""
+    return torch._C._cuda_getDevice()
+
+
 def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str):
     if t is None:
         return None
@@ -105,6 +111,9 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name}: is on cuda:{t.get_device()}, and the call would run on the current device, "
+                         f"cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous (row-major); the library never copies into a layout")
     return t.data_ptr()

@@ -53,7 +53,8 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, *shape: int):
     """The tensor's address, once its dtype, device, layout and shape are what the call reads or writes."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+            and t.get_device() == B._current_device()):
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
@@ -61,7 +62,7 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, *shape: int):
 
 
 def _stream(stream, t: torch.Tensor):
-    """The stream's handle; None is the current stream of the tensor's device."""
+    """The stream's handle; None is the current stream of the tensor's device, the current one (``_arg`` checks)."""
     # torch.cuda.current_stream() builds a Stream object: 2.9 us a call on a Grace core, the raw handle 0.1 us
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else B._stream(stream)
 
