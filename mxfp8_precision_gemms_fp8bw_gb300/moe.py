@@ -190,6 +190,16 @@ def _grouped(kind: int, a, a_e8, b, b_e8, p: Plan, N: int, K: int, out: torch.Te
     return out
 
 
+def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
+    """The grouped GEMMs take sizes from the layer and read the codes by address."""
+    E, N, K = w.shape
+    for name, shape in (("q_row", (E, N, K)), ("e8_row", (E * N, K // 32)), ("qT_col", (E, K, N)),
+                        ("e8_col", (E, K, N // 32))):
+        got = tuple(getattr(codes, name).shape)
+        if got != shape:
+            raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {got}")
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, bias, top_k, score, renormalize, scale, groups, groups_kept, group_top):
@@ -278,6 +288,8 @@ class MxMoEFFN(torch.nn.Module):
     def forward(self, x: torch.Tensor, codes: tuple[L.MxExpertWeights, L.MxExpertWeights] | None = None) -> torch.Tensor:
         """``codes``: ``weight_codes()`` kept by the caller (a decoder, or the micro-batches of a step); by default
         the weights are quantized in every call."""
+        for got, w in zip(codes or (), (self.w13, self.w2)):
+            _check_codes(got, w)
         logits = torch.nn.functional.linear(x.float(), self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
