@@ -200,6 +200,18 @@ def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
             raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {got}")
 
 
+def _differentiable_once(backward):
+    """For a backward made of kernel calls, whose results have no graph: a second derivative would leave out their part and
+    say nothing, so ``create_graph`` is refused.  (torch's ``once_differentiable`` marks what depends on the incoming
+    gradient; these results depend on the forward's inputs too.)"""
+    @functools.wraps(backward)
+    def wrapper(ctx, *douts):
+        if torch.is_grad_enabled():  # in a backward: create_graph
+            raise RuntimeError("the mixture-of-experts operators have no second derivative (create_graph=True)")
+        return backward(ctx, *douts)
+    return wrapper
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, bias, top_k, score, renormalize, scale, groups, groups_kept, group_top):
@@ -211,6 +223,7 @@ class _Route(torch.autograd.Function):
         return experts, weights
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, _, dweights):
         logits, experts = ctx.saved_tensors
         return (route_backward(dweights.contiguous(), logits, experts, **ctx.how),) + (None,) * 8
@@ -242,6 +255,7 @@ class _Experts(torch.autograd.Function):
         return combine(y, weights, p)
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dout):
         weights, y, hq, he, xT, xeT, aT, aeT, w13T, w13e, w2T, w2e, *tables = ctx.saved_tensors
         p, mode = Plan(*tables), ctx.mode

@@ -1,0 +1,33 @@
+"""The mixture-of-experts layer in a training program: what it refuses, what it keeps and what it computes for partly frozen
+or cast modules."""
+import pytest
+import torch
+
+from gpu_util import lib
+from mxfp8_precision_gemms_fp8bw_gb300 import binding as B
+from mxfp8_precision_gemms_fp8bw_gb300 import moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    lib()
+
+
+def layer_and_tokens(tokens=70, dim=256, hidden=512, experts=4, top_k=2, **how):
+    torch.manual_seed(5)
+    layer = moe.MxMoEFFN(dim, hidden, experts, top_k, device="cuda", **how)
+    return layer, torch.randn(tokens, dim, device="cuda").bfloat16().requires_grad_(True)
+
+
+@pytest.mark.parametrize("linear", [True, False])
+def test_a_second_derivative_is_an_error(linear):
+    layer, x = layer_and_tokens()
+    out = layer(x)
+    loss = out.float().sum() if linear else out.float().square().sum()
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        dx, dw = torch.autograd.grad(loss, (x, layer.w13), create_graph=True)
+        torch.autograd.grad(dx.float().square().sum() + dw.float().square().sum(), layer.router)
+    loss.backward()
+    assert x.grad is not None and layer.router.grad is not None

@@ -28,3 +28,53 @@ def test_codes_of_other_weights_are_refused(which, name):
     setattr(codes[which], name, getattr(codes[which], name)[1:])
     with pytest.raises(ValueError, match=name):
         layer(x, codes)
+
+
+# ------------------------------------------------------------------ second derivatives
+
+def plain_route(logits, top_k, *, bias=None, score="softmax", renormalize=True, scale=1.0, groups=1, groups_kept=1,
+                group_top=1):
+    s = torch.softmax(logits.detach(), 1)
+    w, experts = s.topk(top_k, dim=1)
+    return experts.to(torch.int32), scale * (w / w.sum(1, keepdim=True) if renormalize else w)
+
+
+def plain_route_backward(dweights, logits, experts, *, score="softmax", renormalize=True, scale=1.0):
+    with torch.enable_grad():
+        leaf = logits.detach().requires_grad_(True)
+        w = torch.softmax(leaf, 1).gather(1, experts.long())
+        w = scale * (w / w.sum(1, keepdim=True) if renormalize else w)
+        return torch.autograd.grad(w, leaf, dweights.detach())[0]
+
+
+def routed(monkeypatch):
+    """Weights of tokens through the router product and _Route, whose kernels are these formulas in torch."""
+    monkeypatch.setattr(moe, "route", plain_route)
+    monkeypatch.setattr(moe, "route_backward", plain_route_backward)
+    torch.manual_seed(0)
+    x = torch.randn(6, 16, requires_grad=True)
+    router = torch.randn(8, 16, requires_grad=True)
+    logits = torch.nn.functional.linear(x, router)
+    _, weights = moe._Route.apply(logits, None, 2, "softmax", True, 1.0, 1, 1, 1)
+    return x, router, logits, weights
+
+
+def test_the_first_derivative_is_autograds(monkeypatch):
+    x, router, logits, weights = routed(monkeypatch)
+    dw = torch.randn(6, 2)
+    s = torch.softmax(logits, 1).topk(2, dim=1)[0]
+    want = torch.autograd.grad(s / s.sum(1, keepdim=True), (x, router), dw, retain_graph=True)
+    for a, b in zip(torch.autograd.grad(weights, (x, router), dw), want):
+        assert torch.allclose(a, b, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("linear", [True, False])
+def test_a_second_derivative_is_an_error(monkeypatch, linear):
+    """The kernels' gradients have no graph: what autograd would make of the products around them is part of an answer.
+    Whether the loss is linear in the weights or not, so that the incoming gradient does or does not have one."""
+    x, router, _, weights = routed(monkeypatch)
+    dw = torch.randn(6, 2)
+    loss = (weights * dw).sum() if linear else weights.square().sum()
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        (dx,) = torch.autograd.grad(loss, x, create_graph=True)
+        torch.autograd.grad(dx.square().sum(), router)
