@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
     const int c = j * L + l;
     if (j * L < p.k && live && c < p.k) {
       experts[row * p.k + c] = chosen[j];
-      weights[row * p.k + c] = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
+      const float w = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
+      weights[row * p.k + c] = chosen[j] >= 0 ? w : 0.f;  // also beside a NaN, which makes the sum NaN
     }
   }
 }
