@@ -118,7 +118,13 @@ def _plan_sizes(M: int, num_experts: int, top_k: int) -> tuple[int, int]:
     return P, MB.fp8bw_moe_plan_workspace_bytes(M, num_experts, top_k)
 
 
+def _tokens(t: torch.Tensor, p: Plan, name: str) -> None:
+    if t.shape[0] != p.row_of.shape[0]:
+        raise ValueError(f"{name}: the plan has {p.row_of.shape[0]} tokens, got {t.shape[0]}")
+
+
 def _gathered(x: torch.Tensor, weights: torch.Tensor | None, p: Plan, colwise: bool, mode: int) -> MxRows:
+    _tokens(x, p, "x" if weights is None else "dout")
     out = _mx_rows(p.rows, x.shape[1], x.device, colwise)
     if x.shape[0] == 0:  # rows of zeros are codes and scales of 0
         for t in (out.q, out.e8, *((out.qT, out.e8T) if colwise else ())):
@@ -152,6 +158,7 @@ def combine(y: torch.Tensor, weights: torch.Tensor | None, p: Plan, base: torch.
 def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, p: Plan, mode: int = B.MX_RCEIL):
     """Gradients of ``combine``: that of y as MX codes in both layouts, and
     that of the weights."""
+    _tokens(weights, p, "weights")
     dy = _gathered(dout, weights, p, True, mode)
     dweights = torch.empty_like(weights, memory_format=torch.contiguous_format)
     if dout.shape[0] > 0:
