@@ -197,16 +197,6 @@ def _grouped(kind: int, a, a_e8, b, b_e8, p: Plan, N: int, K: int, out: torch.Te
     return out
 
 
-def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
-    """The grouped GEMMs take sizes from the layer and read the codes by address."""
-    E, N, K = w.shape
-    for name, shape in (("q_row", (E, N, K)), ("e8_row", (E * N, K // 32)), ("qT_col", (E, K, N)),
-                        ("e8_col", (E, K, N // 32))):
-        got = tuple(getattr(codes, name).shape)
-        if got != shape:
-            raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {got}")
-
-
 def _differentiable_once(backward):
     """For a backward made of kernel calls, whose results have no graph: a second derivative would leave out their part and
     say nothing, so ``create_graph`` is refused.  (torch's ``once_differentiable`` marks what depends on the incoming
@@ -217,6 +207,38 @@ def _differentiable_once(backward):
             raise RuntimeError("the mixture-of-experts operators have no second derivative (create_graph=True)")
         return backward(ctx, *douts)
     return wrapper
+
+
+class _RouterLogits(torch.autograd.Function):
+    """x router^T in fp32 whatever autocast says, forward and backward: logits rounded to bf16 choose other experts."""
+
+    @staticmethod
+    def forward(ctx, x, router):
+        ctx.save_for_backward(x, router)
+        with torch.autocast(x.device.type, enabled=False):
+            return torch.nn.functional.linear(x, router)
+
+    @staticmethod
+    @_differentiable_once
+    def backward(ctx, dlogits):
+        x, router = ctx.saved_tensors
+        with torch.autocast(x.device.type, enabled=False):
+            return (dlogits @ router if ctx.needs_input_grad[0] else None,
+                    dlogits.t() @ x if ctx.needs_input_grad[1] else None)
+
+
+def _router_logits(x: torch.Tensor, router: torch.Tensor) -> torch.Tensor:
+    return _RouterLogits.apply(x.float(), router)
+
+
+def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
+    """The grouped GEMMs take sizes from the layer and read the codes by address."""
+    E, N, K = w.shape
+    for name, shape in (("q_row", (E, N, K)), ("e8_row", (E * N, K // 32)), ("qT_col", (E, K, N)),
+                        ("e8_col", (E, K, N // 32))):
+        got = tuple(getattr(codes, name).shape)
+        if got != shape:
+            raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {got}")
 
 
 class _Route(torch.autograd.Function):
@@ -283,7 +305,8 @@ class MxMoEFFN(torch.nn.Module):
 
     Inputs are 2D bf16 CUDA tensors [tokens, dim]; dim and hidden must be
     multiples of 256, the token count is free.  The router's logits are a
-    plain fp32 product.  ``balance`` (a buffer, not a parameter) is the bias
+    plain fp32 product, under autocast too (and in TF32 only where the program
+    has turned that on for fp32 products).  ``balance`` (a buffer, not a parameter) is the bias
     that shifts the choice of experts; ``update_balance`` moves it against the
     loads of the last forward.  ``route``'s keyword arguments are taken too.
     """
@@ -311,7 +334,7 @@ class MxMoEFFN(torch.nn.Module):
         the weights are quantized in every call."""
         for got, w in zip(codes or (), (self.w13, self.w2)):
             _check_codes(got, w)
-        logits = torch.nn.functional.linear(x.float(), self.router)
+        logits = _router_logits(x, self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
         train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, self.w13, self.w2))

@@ -31,3 +31,20 @@ def test_a_second_derivative_is_an_error(linear):
         torch.autograd.grad(dx.float().square().sum() + dw.float().square().sum(), layer.router)
     loss.backward()
     assert x.grad is not None and layer.router.grad is not None
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_autocast_changes_nothing(dtype, score):
+    """Neither in the forward pass nor in a backward pass under it."""
+    layer, x = layer_and_tokens(tokens=300, experts=8, score=score)
+    made = []
+    for on in (False, True):
+        layer.zero_grad()
+        x.grad = None
+        with torch.autocast("cuda", dtype=dtype, enabled=on):
+            out = layer(x)
+            out.backward(torch.ones_like(out))
+        made.append((layer.counts, out, x.grad, layer.router.grad, layer.w13.grad, layer.w2.grad))
+    B.fp8bw_sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(*made))

@@ -78,3 +78,21 @@ def test_a_second_derivative_is_an_error(monkeypatch, linear):
     with pytest.raises(RuntimeError, match="no second derivative"):
         (dx,) = torch.autograd.grad(loss, x, create_graph=True)
         torch.autograd.grad(dx.square().sum(), router)
+
+
+# ------------------------------------------------------------------ the router product
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_router_product_stays_fp32_under_autocast(dtype):
+    torch.manual_seed(1)
+    x = torch.randn(9, 32).bfloat16().requires_grad_(True)
+    router = torch.randn(8, 32, requires_grad=True)
+    d = torch.randn(9, 8)
+    want = torch.nn.functional.linear(x.float(), router)
+    wants = torch.autograd.grad(want, (x, router), d)
+    with torch.autocast("cpu", dtype=dtype):
+        got = moe._router_logits(x, router)
+        gots = torch.autograd.grad(got, (x, router), d)
+    assert got.dtype == torch.float32 and torch.equal(got, want)
+    for a, b in zip(gots, wants):
+        assert a.dtype == b.dtype and torch.allclose(a, b, rtol=1e-5, atol=1e-6)
