@@ -210,25 +210,23 @@ def _differentiable_once(backward):
 
 
 class _RouterLogits(torch.autograd.Function):
-    """x router^T in fp32 whatever autocast says, forward and backward: logits rounded to bf16 choose other experts."""
+    """x router^T in fp32 whatever autocast says, forward and backward: logits rounded to bf16 choose other experts.  Keeps
+    x as it came, and makes its fp32 copy again for the gradient."""
 
     @staticmethod
     def forward(ctx, x, router):
-        ctx.save_for_backward(x, router)
+        ctx.dtype, (need_dx, need_drouter) = x.dtype, ctx.needs_input_grad
+        ctx.save_for_backward(x if need_drouter else None, router if need_dx else None)
         with torch.autocast(x.device.type, enabled=False):
-            return torch.nn.functional.linear(x, router)
+            return torch.nn.functional.linear(x.float(), router)
 
     @staticmethod
     @_differentiable_once
     def backward(ctx, dlogits):
         x, router = ctx.saved_tensors
-        with torch.autocast(x.device.type, enabled=False):
-            return (dlogits @ router if ctx.needs_input_grad[0] else None,
-                    dlogits.t() @ x if ctx.needs_input_grad[1] else None)
-
-
-def _router_logits(x: torch.Tensor, router: torch.Tensor) -> torch.Tensor:
-    return _RouterLogits.apply(x.float(), router)
+        with torch.autocast(dlogits.device.type, enabled=False):
+            return (None if router is None else (dlogits @ router).to(ctx.dtype),
+                    None if x is None else dlogits.t() @ x.float())
 
 
 def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
@@ -306,7 +304,8 @@ class MxMoEFFN(torch.nn.Module):
     Inputs are 2D bf16 CUDA tensors [tokens, dim]; dim and hidden must be
     multiples of 256, the token count is free.  The router's logits are a
     plain fp32 product, under autocast too (and in TF32 only where the program
-    has turned that on for fp32 products).  ``balance`` (a buffer, not a parameter) is the bias
+    has turned that on for fp32 products); its gradient reads x again, so that
+    x is not to be changed in place before the backward pass.  ``balance`` (a buffer, not a parameter) is the bias
     that shifts the choice of experts; ``update_balance`` moves it against the
     loads of the last forward.  ``route``'s keyword arguments are taken too.
     """
@@ -334,7 +333,7 @@ class MxMoEFFN(torch.nn.Module):
         the weights are quantized in every call."""
         for got, w in zip(codes or (), (self.w13, self.w2)):
             _check_codes(got, w)
-        logits = _router_logits(x, self.router)
+        logits = _RouterLogits.apply(x, self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
         train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, self.w13, self.w2))

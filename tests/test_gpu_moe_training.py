@@ -48,3 +48,16 @@ def test_autocast_changes_nothing(dtype, score):
         made.append((layer.counts, out, x.grad, layer.router.grad, layer.w13.grad, layer.w2.grad))
     B.fp8bw_sync_status()
     assert all(torch.equal(a, b) for a, b in zip(*made))
+
+
+def test_no_fp32_copy_of_the_tokens_is_kept():
+    layer, x = layer_and_tokens(tokens=96)
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (kept.append(t), t)[1], lambda t: t):
+        out = layer(x)
+    assert not [t for t in kept if t.dtype == torch.float32 and t.numel() >= x.numel() and t.shape != layer.router.shape]
+    # what is kept in bf16: the experts' output, and the caller's own tokens
+    assert {t.data_ptr() for t in kept if t.dtype == torch.bfloat16 and t.shape == x.shape} <= {x.data_ptr()}
+    assert len([t for t in kept if t.dtype == torch.bfloat16 and t.shape != x.shape]) == 1
+    out.backward(torch.ones_like(out))
+    assert x.grad.shape == x.shape

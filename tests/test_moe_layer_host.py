@@ -91,8 +91,25 @@ def test_router_product_stays_fp32_under_autocast(dtype):
     want = torch.nn.functional.linear(x.float(), router)
     wants = torch.autograd.grad(want, (x, router), d)
     with torch.autocast("cpu", dtype=dtype):
-        got = moe._router_logits(x, router)
+        got = moe._RouterLogits.apply(x, router)
         gots = torch.autograd.grad(got, (x, router), d)
     assert got.dtype == torch.float32 and torch.equal(got, want)
     for a, b in zip(gots, wants):
         assert a.dtype == b.dtype and torch.allclose(a, b, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("frozen", ["x", "router"])
+def test_router_product_keeps_what_its_gradients_read(frozen):
+    torch.manual_seed(2)
+    x = torch.randn(9, 32).bfloat16().requires_grad_(frozen != "x")
+    router = torch.randn(8, 32, requires_grad=frozen != "router")
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (kept.append(t), t)[1], lambda t: t):
+        out = moe._RouterLogits.apply(x, router)
+    assert [t.data_ptr() for t in kept] == [(x if frozen == "x" else router).data_ptr()]
+    out.sum().backward()
+    want = torch.ones(9, 8)
+    if frozen == "x":
+        assert x.grad is None and torch.allclose(router.grad, want.t() @ x.float(), rtol=1e-5, atol=1e-6)
+    else:
+        assert router.grad is None and torch.equal(x.grad, (want @ router).bfloat16())
