@@ -308,6 +308,8 @@ class MxMoEFFN(torch.nn.Module):
     x is not to be changed in place before the backward pass.  ``balance`` (a buffer, not a parameter) is the bias
     that shifts the choice of experts; ``update_balance`` moves it against the
     loads of the last forward.  ``route``'s keyword arguments are taken too.
+    Casting the module (``bfloat16()``, ``to(dtype)``) leaves the router and
+    ``balance`` in fp32: a bias in bf16 would lose its steps.
     """
 
     def __init__(self, dim: int, hidden: int, num_experts: int, top_k: int, *, score: str = "softmax",
@@ -323,6 +325,15 @@ class MxMoEFFN(torch.nn.Module):
         self.how = (top_k, score, renormalize, scale, groups, groups_kept, group_top)
         self.mode = mode
         self.counts = None
+
+    def _apply(self, fn, recurse=True):
+        fp32 = [t for t in (self.router, self.router.grad, self.balance) if t is not None]
+
+        def but_keep_fp32(t):
+            new = fn(t)
+            return t.to(new.device) if new.dtype != t.dtype and any(t is k for k in fp32) else new
+
+        return super()._apply(but_keep_fp32, recurse)
 
     def weight_codes(self) -> tuple[L.MxExpertWeights, L.MxExpertWeights]:
         """MX codes of w13 and w2 as they are now, for calls between two changes of the weights."""

@@ -61,3 +61,15 @@ def test_no_fp32_copy_of_the_tokens_is_kept():
     assert len([t for t in kept if t.dtype == torch.bfloat16 and t.shape != x.shape]) == 1
     out.backward(torch.ones_like(out))
     assert x.grad.shape == x.shape
+
+
+def test_a_layer_cast_to_bf16_runs_as_before():
+    layer, x = layer_and_tokens(score="sigmoid")
+    layer.balance.copy_(torch.randn(4, device="cuda") * 1e-2)
+    want = layer(x)
+    got = layer.bfloat16()(x)
+    assert torch.equal(got, want)
+    got.backward(torch.ones_like(got))
+    layer.update_balance()
+    B.fp8bw_sync_status()
+    assert layer.router.grad.dtype == layer.balance.dtype == torch.float32

@@ -113,3 +113,26 @@ def test_router_product_keeps_what_its_gradients_read(frozen):
         assert x.grad is None and torch.allclose(router.grad, want.t() @ x.float(), rtol=1e-5, atol=1e-6)
     else:
         assert router.grad is None and torch.equal(x.grad, (want @ router).bfloat16())
+
+
+# ------------------------------------------------------------------ casts
+
+@pytest.mark.parametrize("cast", [lambda m: m.bfloat16(), lambda m: m.to(torch.bfloat16), lambda m: m.half().bfloat16(),
+                                  lambda m: torch.nn.Sequential(m).to("cpu", torch.bfloat16)[0]])
+def test_a_cast_module_keeps_its_router_in_fp32(cast):
+    layer = moe.MxMoEFFN(256, 512, 4, 2)
+    layer.balance += 0.501
+    layer.router.grad = torch.randn_like(layer.router)
+    router, grad, balance = layer.router.detach().clone(), layer.router.grad.clone(), layer.balance.clone()
+    layer = cast(layer)
+    assert torch.equal(layer.router.detach(), router) and torch.equal(layer.router.grad, grad)
+    assert torch.equal(layer.balance, balance)
+    assert layer.w13.dtype == layer.w2.dtype == torch.bfloat16
+    x = torch.randn(3, 256).bfloat16()
+    assert moe._RouterLogits.apply(x, layer.router).dtype == torch.float32
+
+
+def test_a_module_still_moves():
+    layer = moe.MxMoEFFN(256, 512, 4, 2).to("meta", torch.bfloat16)
+    assert layer.router.is_meta and layer.balance.is_meta and layer.w2.is_meta
+    assert layer.router.dtype == torch.float32 and isinstance(layer.router, torch.nn.Parameter)
