@@ -154,6 +154,7 @@ int fp8bw_moe_combine_dweights(const fp8bw_bf16* dout, const fp8bw_bf16* y, cons
 /* a = gate * sigmoid(gate) * up of h = [gate | up], in fp32, held as MX codes;
  * and h itself as rowwise MX codes, which are all that the backward pass needs
  * of it (33/32 bytes per element instead of the 2 of bf16).
+ * Where 1 + exp(-gate) is over fp32 (gates below -88.7) the sigmoid is 0.
  *   h  : bf16 [R, 2F]
  *   aq : e4m3 [R, F]   ae : E8M0 [R][F/32]
  *   aqT: e4m3 [F, R]   aeT: E8M0 [F][R/32]    (both or neither NULL)

@@ -6,8 +6,10 @@
 // 90 us for 16640 x 4096 (0.91 of the measured copy bandwidth), 168 us for
 // 130048 x 1024 (0.95).  The backward pass has twice the results to convert,
 // some forty instructions per element, and is bound by them as much as by
-// memory: 114 us (0.72) and 213 us (0.76).  A thread has 4 rows x 8 columns, a warp 32 x 32: lane 4 i + j has
-// rows 4 i + [0, 4) and columns 8 j + [0, 8), so that a row block is four
+// memory: 115 us (0.71) and 216 us (0.75).
+//
+// A thread has 4 rows x 8 columns, a warp 32 x 32: lane 4 i + j has rows
+// 4 i + [0, 4) and columns 8 j + [0, 8), so that a row block is four
 // neighbouring lanes and a column block the eight lanes 4 apart.  (8 x 8 per
 // thread, as in moe_rows.cu, needs twice the registers here, where two
 // operands and one or two results are live at once.)  A block has 64 x 128.
@@ -21,19 +23,26 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 64, kCols = 128, kThreads = 256;
 
-// 1 / (1 + 2^(-x log2 e)) of two values: a few ulp, against the 2^-4 of the
-// codes it goes into; exactly 0 and 1 far out, NaN for NaN.
+// 1 / (1 + 2^(-x log2 e)) of two values.  The exponent's argument is rounded
+// to fp32 before ex2, which costs up to |x log2 e| / 2 units of 2^-24 (29 at
+// -30, 64 at -88) beside the few of ex2 and rcp: far below the 2^-4 of the
+// codes that it goes into (with the argument in two parts the backward pass
+// takes 121 and 227 us in place of 115 and 216).  rcp flushes what lies below
+// 2^-126, so it gets a quarter of the sum (1 % of the backward pass): the
+// result then reaches as far down as 1 + exp(-x) fits fp32, x >= -88.7, and is
+// 0 beyond.  Exactly 1 far out on the other side, NaN for NaN.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   constexpr float kMinusLog2e = -1.4426950408889634f;
+  const float2 quarter = make_float2(0.25f, 0.25f);
   const float2 t = __fmul2_rn(x, make_float2(kMinusLog2e, kMinusLog2e));
   float2 e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  e = __ffma2_rn(e, quarter, quarter);
   float2 s;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
-  return s;
+  return __fmul2_rn(s, quarter);
 }
 
 struct Lane {
