@@ -99,9 +99,21 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+_one_device = None  # whether the machine has one device only, known once a CUDA tensor has been seen
+
+
 def _current_device() -> int:
     """The device that the library's calls launch on."""
     return torch._C._cuda_getDevice()
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether a CUDA tensor is on another device than the current one.  Where there is one device there is nothing to ask
+    (0.3 us a tensor on a Grace core)."""
+    global _one_device
+    if _one_device is None:
+        _one_device = torch._C._cuda_getDeviceCount() == 1
+    return not _one_device and t.get_device() != _current_device()
 
 
 def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str):
@@ -111,7 +123,7 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.get_device() != _current_device():
+    if _elsewhere(t):
         raise ValueError(f"{name}: is on cuda:{t.get_device()}, and the call would run on the current device, "
                          f"cuda:{_current_device()}")
     if not t.is_contiguous():

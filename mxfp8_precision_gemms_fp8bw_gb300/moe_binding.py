@@ -54,7 +54,7 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, *shape: int):
     if t is None:
         return None
     if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
-            and t.get_device() == B._current_device()):
+            and (B._one_device or not B._elsewhere(t))):
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")

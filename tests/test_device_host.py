@@ -62,8 +62,9 @@ TENSORS = {"route": 4, "plan": 5, "gather": 4, "combine": 3, "swiglu": 3, "row q
 
 @pytest.fixture(autouse=True)
 def _no_launch(monkeypatch):
-    """Device 0 is current, and a call that reaches the library ends there."""
+    """Device 0 of several is current, and a call that reaches the library ends there."""
     build.build()
+    monkeypatch.setattr(B, "_one_device", False, raising=False)
     monkeypatch.setattr(B, "_current_device", lambda: 0, raising=False)
 
     class Library:
@@ -87,3 +88,24 @@ def test_refused(name):
 def test_let_through_on_the_current_device(name):
     with pytest.raises(AssertionError, match="was called"):
         calls(lambda i: 0)[name]()
+
+
+def test_one_device_is_never_asked(monkeypatch):
+    monkeypatch.setattr(B, "_one_device", None)
+    monkeypatch.setattr(torch._C, "_cuda_getDeviceCount", lambda: 1, raising=False)
+    monkeypatch.setattr(B, "_current_device", lambda: pytest.fail("asked"))
+    for name in TENSORS:
+        with pytest.raises(AssertionError, match="was called"):
+            calls(lambda i: 0)[name]()
+    assert B._one_device is True
+
+
+def test_several_devices_are_counted_once(monkeypatch):
+    counted = []
+    monkeypatch.setattr(B, "_one_device", None)
+    monkeypatch.setattr(torch._C, "_cuda_getDeviceCount", lambda: counted.append(1) or 2, raising=False)
+    with pytest.raises(ValueError, match="cuda:1"):
+        calls(lambda i: 1)["route"]()
+    with pytest.raises(AssertionError, match="was called"):
+        calls(lambda i: 0)["route"]()
+    assert counted == [1] and B._one_device is False
