@@ -34,7 +34,7 @@ def main(steps: int = 30, tokens: int = 1000, dim: int = 256, hidden: int = 512,
         if step % 10 == 0 or step + 1 == steps:
             print(f"step {step:3d}  mean square error {float(losses[-1]):.4f}  loads {layer.counts.tolist()}")
     with torch.no_grad():
-        codes = layer.weight_codes()  # the weights stay as they are from here on
+        codes = layer.weight_codes(colwise=False)  # the weights stay as they are from here on
         together = layer(x[:4], codes)
         alone = torch.cat([layer(x[i:i + 1], codes) for i in range(4)])
     B.fp8bw_sync_status()

@@ -113,17 +113,27 @@ class Float8BlockwiseLinear(torch.nn.Module):
 
 @dataclass
 class MxExpertWeights:
-    q_row: torch.Tensor    # e4m3 [G, N, K], 1x32 along K (forward)
-    e8_row: torch.Tensor   # [G*N, K/32]
-    qT_col: torch.Tensor   # e4m3 [G, K, N], 1x32 along N (dgrad, 3D colwise)
-    e8_col: torch.Tensor   # [G, K, N/32]
+    q_row: torch.Tensor            # e4m3 [G, N, K], 1x32 along K (forward)
+    e8_row: torch.Tensor           # [G*N, K/32]
+    qT_col: torch.Tensor | None    # e4m3 [G, K, N], 1x32 along N (dgrad, 3D colwise), or None
+    e8_col: torch.Tensor | None    # [G, K, N/32]
 
 
-def mx_quantize_experts(w: torch.Tensor, mode: int = B.MX_RCEIL, stream=None) -> MxExpertWeights:
+MX_ROWS_PER_CALL = 65535 * 32  # of mxfp8_quant_1x32_row
+
+
+def mx_quantize_experts(w: torch.Tensor, mode: int = B.MX_RCEIL, stream=None, colwise: bool = True) -> MxExpertWeights:
     """Rowwise (forward) and 3D colwise (dgrad) MX codes of the expert
-    weights w [G, N, K], both from one read of w."""
+    weights w [G, N, K], both from one read of w; without ``colwise`` the
+    rowwise ones alone, which are all that a forward pass reads."""
     G, N, K = w.shape
-    q, e8 = B.alloc_mx_row(w.view(G * N, K))
+    rows = w.view(G * N, K)
+    q, e8 = B.alloc_mx_row(rows)
+    if not colwise:
+        for r in range(0, G * N, MX_ROWS_PER_CALL):
+            part = slice(r, r + MX_ROWS_PER_CALL)
+            B.mxfp8_quant_1x32_row(rows[part], q[part], e8[part], mode, stream)
+        return MxExpertWeights(q.view(G, N, K), e8, None, None)
     qT, e8c = B.alloc_mx_3d_col(w)
     B.mxfp8_quant_1x32_rowcol(w, q, e8, qT, e8c, mode, stream)
     return MxExpertWeights(q.view(G, N, K), e8, qT, e8c)

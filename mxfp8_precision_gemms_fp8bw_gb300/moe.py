@@ -229,14 +229,17 @@ class _RouterLogits(torch.autograd.Function):
                     None if x is None else dlogits.t() @ x.float())
 
 
-def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor) -> None:
-    """The grouped GEMMs take sizes from the layer and read the codes by address."""
+def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor, colwise: bool) -> None:
+    """The grouped GEMMs take sizes from the layer and read the codes by address; a gradient reads the colwise ones."""
     E, N, K = w.shape
     for name, shape in (("q_row", (E, N, K)), ("e8_row", (E * N, K // 32)), ("qT_col", (E, K, N)),
                         ("e8_col", (E, K, N // 32))):
-        got = tuple(getattr(codes, name).shape)
-        if got != shape:
-            raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {got}")
+        t = getattr(codes, name)
+        if t is None and name.endswith("col"):
+            if colwise:
+                raise ValueError(f"codes: gradients read {name}, which weight_codes(colwise=False) leaves out")
+        elif tuple(t.shape) != shape:
+            raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, got {tuple(t.shape)}")
 
 
 class _Route(torch.autograd.Function):
@@ -335,22 +338,23 @@ class MxMoEFFN(torch.nn.Module):
 
         return super()._apply(but_keep_fp32, recurse)
 
-    def weight_codes(self) -> tuple[L.MxExpertWeights, L.MxExpertWeights]:
-        """MX codes of w13 and w2 as they are now, for calls between two changes of the weights."""
-        return tuple(L.mx_quantize_experts(w.detach(), self.mode) for w in (self.w13, self.w2))
+    def weight_codes(self, colwise: bool = True) -> tuple[L.MxExpertWeights, L.MxExpertWeights]:
+        """MX codes of w13 and w2 as they are now, for calls between two changes of the weights.  Without ``colwise`` those
+        that a forward pass reads, half of the bytes: for calls without gradients."""
+        return tuple(L.mx_quantize_experts(w.detach(), self.mode, colwise=colwise) for w in (self.w13, self.w2))
 
     def forward(self, x: torch.Tensor, codes: tuple[L.MxExpertWeights, L.MxExpertWeights] | None = None) -> torch.Tensor:
         """``codes``: ``weight_codes()`` kept by the caller (a decoder, or the micro-batches of a step); by default
         the weights are quantized in every call."""
+        # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
+        train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, self.router, self.w13, self.w2))
         for got, w in zip(codes or (), (self.w13, self.w2)):
-            _check_codes(got, w)
+            _check_codes(got, w, colwise=train)
         logits = _RouterLogits.apply(x, self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
-        # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
-        train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, self.w13, self.w2))
         counts = []
-        out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes or self.weight_codes(), self.mode,
-                             train, counts)
+        out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes or self.weight_codes(colwise=train),
+                             self.mode, train, counts)
         self.counts = counts[0]
         return out
 

@@ -5,6 +5,7 @@ import torch
 
 from gpu_util import lib
 from mxfp8_precision_gemms_fp8bw_gb300 import binding as B
+from mxfp8_precision_gemms_fp8bw_gb300 import linear as L
 from mxfp8_precision_gemms_fp8bw_gb300 import moe
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +74,37 @@ def test_a_layer_cast_to_bf16_runs_as_before():
     layer.update_balance()
     B.fp8bw_sync_status()
     assert layer.router.grad.dtype == layer.balance.dtype == torch.float32
+
+
+@pytest.mark.parametrize("how", ["no_grad", "frozen"])
+def test_without_gradients_no_column_codes_of_the_weights(how, monkeypatch):
+    layer, x = layer_and_tokens()
+    want = layer(x).detach()
+    x = x.detach()
+    layer.requires_grad_(how != "frozen")
+    monkeypatch.setattr(L.B, "alloc_mx_3d_col", lambda w: pytest.fail("column codes of the weights"))
+    monkeypatch.setattr(L.B, "mxfp8_quant_1x32_rowcol", lambda *a: pytest.fail("column codes of the weights"))
+    with torch.set_grad_enabled(how == "frozen"):
+        assert torch.equal(layer(x), want)
+        codes = layer.weight_codes(colwise=False)
+        assert all(c.qT_col is None and c.e8_col is None for c in codes)
+        assert torch.equal(layer(x, codes), want)
+    B.fp8bw_sync_status()
+
+
+@pytest.mark.parametrize("mode", [B.MX_RCEIL, B.MX_FLOOR])
+@pytest.mark.parametrize("rows", [65535 * 32, 256, 160])
+def test_rowwise_expert_codes_are_those_of_both_layouts(rows, mode, monkeypatch):
+    monkeypatch.setattr(L, "MX_ROWS_PER_CALL", rows)
+    w = torch.randn(5, 96, 128, device="cuda").bfloat16()
+    a, b = L.mx_quantize_experts(w, mode), L.mx_quantize_experts(w, mode, colwise=False)
+    B.fp8bw_sync_status()
+    assert torch.equal(a.q_row, b.q_row) and torch.equal(a.e8_row, b.e8_row)
+
+
+def test_more_expert_rows_than_one_call_takes():
+    w = torch.randn(66, 32768, 32, device="cuda").bfloat16()
+    assert w.shape[0] * w.shape[1] > 65535 * 32
+    a, b = L.mx_quantize_experts(w), L.mx_quantize_experts(w, colwise=False)
+    B.fp8bw_sync_status()
+    assert torch.equal(a.q_row, b.q_row) and torch.equal(a.e8_row, b.e8_row)

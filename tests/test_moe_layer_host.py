@@ -30,6 +30,26 @@ def test_codes_of_other_weights_are_refused(which, name):
         layer(x, codes)
 
 
+def test_rowwise_codes_are_refused_where_a_gradient_reads_the_others(monkeypatch):
+    layer = moe.MxMoEFFN(256, 512, 4, 2)
+    codes = tuple(dataclasses.replace(c, qT_col=None, e8_col=None) for c in codes_like(layer))
+    x = torch.zeros(5, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="colwise"):
+        layer(x, codes)
+
+    class Reached(Exception):
+        pass
+
+    def route(*a, **k):
+        raise Reached
+
+    monkeypatch.setattr(moe, "route", route)
+    with torch.no_grad(), pytest.raises(Reached):
+        layer(x, codes)
+    with pytest.raises(Reached):
+        layer.requires_grad_(False)(x, codes)
+
+
 # ------------------------------------------------------------------ second derivatives
 
 def plain_route(logits, top_k, *, bias=None, score="softmax", renormalize=True, scale=1.0, groups=1, groups_kept=1,
