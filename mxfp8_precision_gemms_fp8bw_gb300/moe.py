@@ -159,11 +159,14 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor,
     """Gradients of ``combine``: that of y as MX codes in both layouts, and
     that of the weights."""
     _tokens(weights, p, "weights")
-    dy = _gathered(dout, weights, p, True, mode)
-    dweights = torch.empty_like(weights, memory_format=torch.contiguous_format)
+    return _gathered(dout, weights, p, True, mode), _dweights(dout, y, p)
+
+
+def _dweights(dout: torch.Tensor, y: torch.Tensor, p: Plan) -> torch.Tensor:
+    dweights = torch.empty(p.row_of.shape, dtype=_F32, device=dout.device)
     if dout.shape[0] > 0:
         MB.fp8bw_moe_combine_dweights(dout, y, p.row_of, dweights)
-    return dy, dweights
+    return dweights
 
 
 # ------------------------------------------------------------------ gated activation
@@ -262,43 +265,58 @@ class _Route(torch.autograd.Function):
 class _Experts(torch.autograd.Function):
     """sum over a token's experts of weight * W2 (silu(Wg x) * Wu x), with [Wg; Wu] = w13.
 
-    Kept for backward: the colwise MX codes of the gathered tokens and of the
-    activation, h as rowwise codes, the weights' codes and y, the only bf16
-    one (the weights' gradient reads it)."""
+    Kept for backward, each only where a gradient that is asked for reads it:
+    the colwise MX codes of the gathered tokens (dw13) and of the activation
+    (dw2), h as rowwise codes and the weights' column codes (what goes on to
+    dw13 and dx), and y, the only bf16 one (the gradient of the choices'
+    weights)."""
 
     @staticmethod
     def forward(ctx, x, weights, experts, w13, w2, codes, mode, train, counts):
         E, F2, C = w13.shape
         F = F2 // 2
+        need_x, need_weights, _, need_13, need_2 = (train and n for n in ctx.needs_input_grad[:5])
+        through = need_x or need_13  # the gradient goes on through the activation
         p = plan(experts, E)
         counts.append(p.counts)
-        rows = dispatch(x, p, colwise=train, mode=mode)
+        rows = dispatch(x, p, colwise=need_13, mode=mode)
         q13, q2 = codes
         bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
         h = _grouped(B.GROUPED_FWD, rows.q, rows.e8, q13.q_row, q13.e8_row, p, F2, C, bf(p.rows, F2))
-        a, kept = swiglu(h, keep=train, colwise=train, mode=mode)
+        a, kept = swiglu(h, keep=through, colwise=need_2, mode=mode)
         y = _grouped(B.GROUPED_FWD, a.q, a.e8, q2.q_row, q2.e8_row, p, C, F, bf(p.rows, C))
         if train:
-            ctx.mode = mode
-            ctx.save_for_backward(weights, y, kept.q, kept.e8, rows.qT, rows.e8T, a.qT, a.e8T, q13.qT_col, q13.e8_col,
-                                  q2.qT_col, q2.e8_col, p.group_end, p.counts, p.row_of, p.src_of)
+            ctx.mode, ctx.dims, ctx.need = mode, (E, C, F), (need_x, need_weights, need_13, need_2)
+            kept = kept or MxRows(None, None)
+            ctx.save_for_backward(weights if through or need_2 else None, y if need_weights else None, kept.q, kept.e8,
+                                  *((q2.qT_col, q2.e8_col) if through else (None, None)),
+                                  *((q13.qT_col, q13.e8_col) if need_x else (None, None)),
+                                  rows.qT, rows.e8T, a.qT, a.e8T, p.group_end, p.counts, p.row_of, p.src_of)
         return combine(y, weights, p)
 
     @staticmethod
     @_differentiable_once
     def backward(ctx, dout):
-        weights, y, hq, he, xT, xeT, aT, aeT, w13T, w13e, w2T, w2e, *tables = ctx.saved_tensors
-        p, mode = Plan(*tables), ctx.mode
-        E, C, F2 = w13T.shape
-        F = F2 // 2
+        weights, y, hq, he, w2T, w2e, w13T, w13e, xT, xeT, aT, aeT, *tables = ctx.saved_tensors
+        p, mode, (E, C, F) = Plan(*tables), ctx.mode, ctx.dims
+        need_x, need_weights, need_13, need_2 = ctx.need
+        dout = dout.contiguous()
         bf = lambda *shape: torch.empty(shape, dtype=_BF16, device=dout.device)  # noqa: E731
-        dy, dweights = combine_backward(dout.contiguous(), y, weights, p, mode=mode)
-        da = _grouped(B.GROUPED_DGRAD, dy.q, dy.e8, w2T, w2e, p, C, F, bf(p.rows, F))
-        dw2 = _grouped(B.GROUPED_WGRAD, dy.qT, dy.e8T, aT, aeT, p, C, F, bf(E, C, F))
-        dh = swiglu_backward(da, MxRows(hq, he), mode=mode)
-        drows = _grouped(B.GROUPED_DGRAD, dh.q, dh.e8, w13T, w13e, p, F2, C, bf(p.rows, C))
-        dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, xT, xeT, p, F2, C, bf(E, F2, C))
-        return dispatch_backward(drows, p), dweights, None, dw13, dw2, None, None, None, None
+        dx = dweights = dw13 = dw2 = None
+        if need_weights:
+            dweights = _dweights(dout, y, p)
+        if need_x or need_13 or need_2:
+            dy = _gathered(dout, weights, p, need_2, mode)
+        if need_2:
+            dw2 = _grouped(B.GROUPED_WGRAD, dy.qT, dy.e8T, aT, aeT, p, C, F, bf(E, C, F))
+        if need_x or need_13:
+            da = _grouped(B.GROUPED_DGRAD, dy.q, dy.e8, w2T, w2e, p, C, F, bf(p.rows, F))
+            dh = swiglu_backward(da, MxRows(hq, he), mode=mode)
+        if need_x:
+            dx = dispatch_backward(_grouped(B.GROUPED_DGRAD, dh.q, dh.e8, w13T, w13e, p, 2 * F, C, bf(p.rows, C)), p)
+        if need_13:
+            dw13 = _grouped(B.GROUPED_WGRAD, dh.qT, dh.e8T, xT, xeT, p, 2 * F, C, bf(E, 2 * F, C))
+        return dx, dweights, None, dw13, dw2, None, None, None, None
 
 
 class MxMoEFFN(torch.nn.Module):
@@ -347,14 +365,19 @@ class MxMoEFFN(torch.nn.Module):
         """``codes``: ``weight_codes()`` kept by the caller (a decoder, or the micro-batches of a step); by default
         the weights are quantized in every call."""
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
-        train = torch.is_grad_enabled() and any(t.requires_grad for t in (x, self.router, self.w13, self.w2))
-        for got, w in zip(codes or (), (self.w13, self.w2)):
-            _check_codes(got, w, colwise=train)
+        grad = torch.is_grad_enabled()
+        train = grad and any(t.requires_grad for t in (x, self.router, self.w13, self.w2))
+        need_x = grad and x.requires_grad
+        weights13, weights2 = (self.w13, need_x), (self.w2, need_x or grad and self.w13.requires_grad)
+        if codes is None:
+            codes = tuple(L.mx_quantize_experts(w.detach(), self.mode, colwise=c) for w, c in (weights13, weights2))
+        else:
+            for got, (w, colwise) in zip(codes, (weights13, weights2)):
+                _check_codes(got, w, colwise)
         logits = _RouterLogits.apply(x, self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         counts = []
-        out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes or self.weight_codes(colwise=train),
-                             self.mode, train, counts)
+        out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes, self.mode, train, counts)
         self.counts = counts[0]
         return out
 

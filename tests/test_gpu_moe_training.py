@@ -108,3 +108,41 @@ def test_more_expert_rows_than_one_call_takes():
     a, b = L.mx_quantize_experts(w), L.mx_quantize_experts(w, colwise=False)
     B.fp8bw_sync_status()
     assert torch.equal(a.q_row, b.q_row) and torch.equal(a.e8_row, b.e8_row)
+
+
+NAMES = ("x", "router", "w13", "w2")
+
+
+@pytest.mark.parametrize("wanted", [[n for i, n in enumerate(NAMES) if bits >> i & 1] for bits in range(1, 16)],
+                         ids="+".join)
+def test_what_no_gradient_asks_for_is_not_computed(wanted, monkeypatch):
+    """Partly frozen layers: the same gradients to the bit, from no more products than they need."""
+    layer, x = layer_and_tokens()
+    leaves = {"x": x, "router": layer.router, "w13": layer.w13, "w2": layer.w2}
+    dout = torch.randn(x.shape, device="cuda").bfloat16()
+    layer(x).backward(dout)
+    full = {n: t.grad.clone() for n, t in leaves.items()}
+    for n, t in leaves.items():
+        t.grad = None
+        t.requires_grad_(n in wanted)
+    kinds, grouped = [], moe._grouped
+    monkeypatch.setattr(moe, "_grouped", lambda kind, *a: (kinds.append(kind), grouped(kind, *a))[1])
+    layer(x).backward(dout)
+    B.fp8bw_sync_status()
+    for n, t in leaves.items():
+        assert t.grad is None if n not in wanted else torch.equal(t.grad, full[n])
+    through = "x" in wanted or "w13" in wanted
+    assert kinds.count(B.GROUPED_FWD) == 2
+    assert kinds.count(B.GROUPED_DGRAD) == through + ("x" in wanted)
+    assert kinds.count(B.GROUPED_WGRAD) == ("w13" in wanted) + ("w2" in wanted)
+
+
+def test_rowwise_codes_serve_where_only_the_router_or_w2_trains():
+    layer, x = layer_and_tokens()
+    x = x.detach()
+    layer.w13.requires_grad_(False)
+    layer(x).backward(torch.ones_like(x))
+    want = layer.router.grad.clone(), layer.w2.grad.clone()
+    layer.zero_grad()
+    layer(x, layer.weight_codes(colwise=False)).backward(torch.ones_like(x))
+    assert torch.equal(layer.router.grad, want[0]) and torch.equal(layer.w2.grad, want[1])
