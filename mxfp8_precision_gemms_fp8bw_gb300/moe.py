@@ -326,9 +326,10 @@ class MxMoEFFN(torch.nn.Module):
     multiples of 256, the token count is free.  The router's logits are a
     plain fp32 product, under autocast too (and in TF32 only where the program
     has turned that on for fp32 products); its gradient reads x again, so that
-    x is not to be changed in place before the backward pass.  ``balance`` (a buffer, not a parameter) is the bias
-    that shifts the choice of experts; ``update_balance`` moves it against the
-    loads of the last forward.  ``route``'s keyword arguments are taken too.
+    x is not to be changed in place before the backward pass.  ``balance`` (a
+    buffer, not a parameter) is the bias that shifts the choice of experts;
+    ``update_balance`` moves it against ``counts``, the loads of the last
+    forward in training mode.  ``route``'s keyword arguments are taken too.
     Casting the module (``bfloat16()``, ``to(dtype)``) leaves the router and
     ``balance`` in fp32: a bias in bf16 would lose its steps.
     """
@@ -378,13 +379,14 @@ class MxMoEFFN(torch.nn.Module):
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         counts = []
         out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes, self.mode, train, counts)
-        self.counts = counts[0]
+        if self.training:
+            self.counts = counts[0]
         return out
 
     @torch.no_grad()
     def update_balance(self, rate: float = 1e-3) -> None:
         """Moves each expert's bias one step up where its last load was below the mean, down where above."""
         if self.counts is None:
-            raise RuntimeError("update_balance needs a forward pass first")
+            raise RuntimeError("update_balance needs a forward pass in training mode first")
         load = self.counts.float()
         self.balance += rate * torch.sign(load.mean() - load)

@@ -146,3 +146,21 @@ def test_rowwise_codes_serve_where_only_the_router_or_w2_trains():
     layer.zero_grad()
     layer(x, layer.weight_codes(colwise=False)).backward(torch.ones_like(x))
     assert torch.equal(layer.router.grad, want[0]) and torch.equal(layer.w2.grad, want[1])
+
+
+def test_an_evaluation_does_not_move_the_balance():
+    layer, x = layer_and_tokens(tokens=400, experts=8, score="sigmoid")
+    layer.eval()
+    with torch.no_grad():
+        layer(x)
+    with pytest.raises(RuntimeError):
+        layer.update_balance()
+    layer.train()
+    layer(x)
+    counts = layer.counts
+    layer.eval()
+    with torch.no_grad():
+        layer(x[:7])
+    assert layer.counts is counts and int(counts.sum()) == 800
+    layer.update_balance(0.5)
+    assert torch.equal(layer.balance, 0.5 * torch.sign(100 - counts.float()))
