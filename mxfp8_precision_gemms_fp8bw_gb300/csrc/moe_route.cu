@@ -111,12 +111,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __rest
 #pragma unroll
   for (int j = 0; j < K; ++j) chosen[j] = -1;
   bool done = false;
-  if constexpr (L == 8 && V > 2) {
+  if constexpr (L == 8 && V > 4) {
     // Looking through all V keys again for every choice costs more than all
     // the scores.  At least k experts are not below the k-th largest of the
-    // lanes' maxima, and rarely more than twice as many: those go into a short
-    // list, whose members then rank each other.
-    if (p.k <= L) {
+    // lanes' maxima, and for a k well below the lanes rarely more than twice
+    // as many: those go into a short list, whose members then rank each other.
+    // The list costs about three choices of the loop below; the eighth of eight
+    // lanes' maxima is so low that most warps hold a row with too many
+    // candidates, and pay for both, and with more keys to a lane so is the
+    // seventh.  127999 rows, list against loop:
+    // 160 experts 41.3 us against 39.3 for k = 2, 41.3 and 45.4 (3), 49.5 and
+    // 61.8 (6), 65.9 and 68.0 (7), 81 and 74 (8); 64 experts 24.9 and 23.7
+    // (3), 24.9 and 27.0 (4), 29.4 and 33.1 (6), 43 and 39 (8); 256 experts
+    // 62 and 58 (2), 62 and 66 (3), 78 and 93 (6), 111 and 103 (7); 32 experts
+    // 20.8 and 18.7 (3), 24.9 and 22.9 (6).
+    if (p.k >= 3 && p.k <= (V > 24 ? 6 : 7)) {
       __shared__ uint2 lists[kRouteWarps * kRowsPerWarp][2 * L];
       __shared__ int16_t orders[kRouteWarps * kRowsPerWarp][L];
       uint32_t most = 0;
