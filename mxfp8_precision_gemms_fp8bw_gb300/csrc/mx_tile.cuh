@@ -6,10 +6,10 @@
 // 8 columns of them: lane 8 i + j has rows 8 i + [0, 8) and columns 8 j + [0,
 // 8).  A row block (32 columns) is then four neighbouring lanes and a column
 // block (32 rows) the four lanes 8 apart, so both block maxima are two
-// shuffles and the values are read once for both layouts.  Every access is
-// whole sectors: a row of codes is 64 contiguous bytes over its eight lanes, a
-// column of codes 32.  (moe_swiglu.cu has more values live per element and
-// half the tile per thread.)
+// shuffles and the values are read once for both layouts.  A row of codes is
+// 64 contiguous bytes over its eight lanes; column codes leave through shared
+// memory.  (moe_swiglu.cu has more values live per element and half the tile
+// per thread.)
 #pragma once
 
 #include "common.cuh"

@@ -149,7 +149,9 @@ size_t staged_bytes(int64_t E) {
 }
 
 // Calls go(lanes per row, registers per lane) for E experts: the next of these
-// widths, a quarter more than needed at most beyond 8.
+// widths.  A row holds up to a third more registers than it fills, 60 % more
+// at 33 experts, and with a warp per row 78 % more at 257 and 88 % at 513
+// (forward, 384 experts, 8 of them chosen, 127999 rows: 238 us).
 template <typename Go>
 cudaError_t for_experts(int64_t E, Go&& go) {
   using std::integral_constant;
