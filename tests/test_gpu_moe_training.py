@@ -164,3 +164,43 @@ def test_an_evaluation_does_not_move_the_balance():
     assert layer.counts is counts and int(counts.sum()) == 800
     layer.update_balance(0.5)
     assert torch.equal(layer.balance, 0.5 * torch.sign(100 - counts.float()))
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_under_activation_checkpointing(reentrant):
+    """The forward pass run again in the backward pass: the same gradients, and no refusal of it as a second derivative."""
+    from torch.utils.checkpoint import checkpoint
+
+    layer, x = layer_and_tokens()
+    made = []
+    for run in (layer, lambda t: checkpoint(layer, t, use_reentrant=reentrant)):
+        layer.zero_grad()
+        x.grad = None
+        out = run(x)
+        out.backward(torch.ones_like(out))
+        made.append((out, x.grad, layer.router.grad, layer.w13.grad, layer.w2.grad))
+    B.fp8bw_sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(*made))
+
+
+def test_kept_tensors_may_wait_on_the_host():
+    layer, x = layer_and_tokens()
+    layer(x).backward(torch.ones_like(x))
+    want = [t.grad.clone() for t in (x, layer.router, layer.w13, layer.w2)]
+    layer.zero_grad()
+    x.grad = None
+    with torch.autograd.graph.save_on_cpu():
+        out = layer(x)
+    out.backward(torch.ones_like(x))
+    B.fp8bw_sync_status()
+    assert all(torch.equal(t.grad, w) for t, w in zip((x, layer.router, layer.w13, layer.w2), want))
+
+
+def test_rowwise_codes_are_refused_by_the_grouped_backward():
+    w = torch.randn(2, 256, 256, device="cuda").bfloat16()
+    x, dy = (torch.randn(64, 256, device="cuda").bfloat16() for _ in range(2))
+    end = torch.tensor([32, 64], dtype=torch.int32, device="cuda")
+    with pytest.raises(B.Fp8bwError) as e:
+        L.mx_moe_backward(dy, x, L.mx_quantize_experts(w, colwise=False), end)
+    assert e.value.code == B.ERR_NULL
+    B.fp8bw_sync_status()
