@@ -212,24 +212,29 @@ def _differentiable_once(backward):
     return wrapper
 
 
+def _without_autocast(product, a: torch.Tensor, b: torch.Tensor) -> torch.Tensor:
+    if not torch.is_autocast_enabled(a.device.type):
+        return product(a, b)
+    with torch.autocast(a.device.type, enabled=False):
+        return product(a, b)
+
+
 class _RouterLogits(torch.autograd.Function):
-    """x router^T in fp32 whatever autocast says, forward and backward: logits rounded to bf16 choose other experts.  Keeps
-    x as it came, and makes its fp32 copy again for the gradient."""
+    """x router^T of fp32 x, in fp32 whatever autocast says, forward and backward: logits rounded to bf16 choose other
+    experts."""
 
     @staticmethod
     def forward(ctx, x, router):
-        ctx.dtype, (need_dx, need_drouter) = x.dtype, ctx.needs_input_grad
+        need_dx, need_drouter = ctx.needs_input_grad
         ctx.save_for_backward(x if need_drouter else None, router if need_dx else None)
-        with torch.autocast(x.device.type, enabled=False):
-            return torch.nn.functional.linear(x.float(), router)
+        return _without_autocast(torch.nn.functional.linear, x, router)
 
     @staticmethod
     @_differentiable_once
     def backward(ctx, dlogits):
         x, router = ctx.saved_tensors
-        with torch.autocast(dlogits.device.type, enabled=False):
-            return (None if router is None else (dlogits @ router).to(ctx.dtype),
-                    None if x is None else dlogits.t() @ x.float())
+        return (None if router is None else _without_autocast(torch.matmul, dlogits, router),
+                None if x is None else _without_autocast(torch.matmul, dlogits.t(), x))
 
 
 def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor, colwise: bool) -> None:
@@ -325,11 +330,11 @@ class MxMoEFFN(torch.nn.Module):
     Inputs are 2D bf16 CUDA tensors [tokens, dim]; dim and hidden must be
     multiples of 256, the token count is free.  The router's logits are a
     plain fp32 product, under autocast too (and in TF32 only where the program
-    has turned that on for fp32 products); its gradient reads x again, so that
-    x is not to be changed in place before the backward pass.  ``balance`` (a
-    buffer, not a parameter) is the bias that shifts the choice of experts;
-    ``update_balance`` moves it against ``counts``, the loads of the last
-    forward in training mode.  ``route``'s keyword arguments are taken too.
+    has turned that on for fp32 products); its gradient keeps x in fp32.
+    ``balance`` (a buffer, not a parameter) is the bias that shifts the choice
+    of experts; ``update_balance`` moves it against ``counts``, the loads of
+    the last forward in training mode.  ``route``'s keyword arguments are taken
+    too.
     Casting the module (``bfloat16()``, ``to(dtype)``) leaves the router and
     ``balance`` in fp32: a bias in bf16 would lose its steps.
     """
@@ -375,7 +380,10 @@ class MxMoEFFN(torch.nn.Module):
         else:
             for got, (w, colwise) in zip(codes, (weights13, weights2)):
                 _check_codes(got, w, colwise)
-        logits = _RouterLogits.apply(x, self.router)
+        if train:
+            logits = _RouterLogits.apply(x.float(), self.router)
+        else:
+            logits = _without_autocast(torch.nn.functional.linear, x.float(), self.router)
         experts, weights = _Route.apply(logits, self.balance, *self.how)
         counts = []
         out = _Experts.apply(x, weights, experts, self.w13, self.w2, codes, self.mode, train, counts)
