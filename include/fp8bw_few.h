@@ -1,0 +1,71 @@
+/*
+ * fp8bw_few.h -- C ABI of libfp8bw.so, third part: answering a few tokens with
+ * weights held in MX codes, 4 or 8 bits (fp8bw.h has the conventions, status
+ * codes and MX modes that hold here too, fp8bw_moe.h the routing).
+ *
+ * An MX weight matrix W[R, C] is its codes and E8M0 bytes e8[R][C/32]:
+ *   W[r, c] = value(code[r, c]) * 2^(e8[r][c / 32] - 127)
+ * with, for bits = 8, e4m3 codes [R, C] (as mxfp8_quant_1x32_row writes them),
+ * and, for bits = 4, e2m1 codes [R, C/2], two to a byte, the lower nibble
+ * first: bit 3 the sign, codes 0 to 7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4
+ * and 6.  An E8M0 byte of 255 makes its block NaN.
+ *
+ * Products here round nothing on the way in: tokens stay bf16, weights are
+ * what their codes stand for, sums run in fp32, and the result is rounded once
+ * to bf16.  (The grouped GEMM of fp8bw.h quantizes its tokens to MXFP8.)  No
+ * result depends on the order in which blocks run.
+ */
+#ifndef FP8BW_FEW_H
+#define FP8BW_FEW_H
+
+#include "fp8bw.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define FP8BW_FEW_TOKENS 32
+
+/* MXFP4 codes of w, blocks of 32 along C: E is the smallest with
+ * 6 * 2^E >= amax (FP8BW_MX_RCEIL), or floor(log2 amax) - 2 (FP8BW_MX_FLOOR),
+ * clamped to [-127, 127]; codes are e2m1 of w * 2^-E, to the nearest, ties to
+ * even, saturating at 6.  A block with an infinity or a NaN gets byte 255.
+ *   w : bf16 [R, C]    q : e2m1 [R, C/2]    e8 : E8M0 [R][C/32]
+ * C a positive multiple of 32. */
+int mxfp4_quant_1x32_row(const fp8bw_bf16* w, int64_t R, int64_t C, uint8_t* q, uint8_t* e8, int mode, void* stream);
+
+/* The same values as e4m3 codes, which with the same E8M0 bytes are an MXFP8
+ * matrix: every e2m1 value is an e4m3 value.
+ *   q4 : e2m1 [R, C/2]    q8 : e4m3 [R, C]      C a positive multiple of 32. */
+int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q8, void* stream);
+
+/* y = x W^T.
+ *   x : bf16 [M, K]    w : codes of W[N, K]    e8 : E8M0 [N][K/32]    y : bf16 [M, N]
+ * 1 <= M <= 32, N positive, K a positive multiple of 32, bits 4 or 8. */
+int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N, int64_t K,
+                  fp8bw_bf16* y, void* stream);
+
+/* Bytes of workspace mx_few_moe needs; 0 for invalid dims.  Host-only. */
+size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F);
+
+/* A mixture-of-experts layer of gated feed-forward experts on M tokens:
+ *   logits = x router^T (fp32);  experts e_j, weights w_j: fp8bw_moe_route's of them
+ *   [gate; up] = W13[e_j] x;  a_j = gate * sigmoid(gate) * up;  y = sum_j w_j W2[e_j] a_j
+ * A choice without an expert adds nothing.  h = [gate; up] stays fp32.  The activation is held
+ * between the two products with 11 significant bits, its 32 blocks' largest elements alike.
+ *   x   : bf16 [M, C]           router : fp32 [E, C]      bias : fp32 [E] or NULL
+ *   w13 : codes of [E, 2F, C]   e13    : E8M0 [E][2F][C/32]
+ *   w2  : codes of [E, C, F]    e2     : E8M0 [E][C][F/32]     y : bf16 [M, C]
+ * 1 <= M <= 32, C and F positive multiples of 32, bits 4 or 8, and the routing's arguments as in fp8bw_moe.h.
+ * workspace: caller-owned DEVICE scratch of at least mx_few_moe_workspace_bytes bytes, in any state; concurrent calls
+ * need one each. */
+int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13, const uint8_t* e13,
+               const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F,
+               int64_t groups, int64_t groups_kept, int64_t group_top, int score, int renorm, float scale, fp8bw_bf16* y,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8BW_FEW_H */

@@ -21,7 +21,7 @@ LIB_NAME = "libfp8bw.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["quant.cu", "gemm_blockwise.cu", "gemm_mx.cu", "moe_route.cu", "moe_route_bwd.cu", "moe_rows.cu", "moe_swiglu.cu",
-           "api.cu", "api_moe.cu"]
+           "mx4.cu", "few.cu", "api.cu", "api_moe.cu", "api_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I" + INCLUDE]
 
@@ -38,7 +38,7 @@ def _stamp() -> str:
     for name in sorted(os.listdir(CSRC)):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
-    for name in ("fp8bw.h", "fp8bw_moe.h"):
+    for name in ("fp8bw.h", "fp8bw_moe.h", "fp8bw_few.h"):
         with open(os.path.join(INCLUDE, name), "rb") as f:
             h.update(f.read())
     h.update(" ".join(ARCH + CFLAGS).encode())

@@ -1,43 +1,11 @@
 // C ABI of libfp8bw, second part (declared in include/fp8bw_moe.h): argument
 // validation and dispatch of the operators around the experts' products.
-#include <initializer_list>
-
 #include "api_common.h"
 #include "fp8bw_moe.h"
 
 using namespace fp8bw;
 
 namespace {
-
-// A memory range of a call: outputs may overlap nothing.
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-  for (const Range* a = outs.begin(); a != outs.end(); ++a) {
-    if (a->p == nullptr) continue;
-    for (const Range& b : ins)
-      if (b.p != nullptr && overlaps(a->p, a->bytes, b.p, b.bytes)) return true;
-    for (const Range* b = a + 1; b != outs.end(); ++b)
-      if (b->p != nullptr && overlaps(a->p, a->bytes, b->p, b->bytes)) return true;
-  }
-  return false;
-}
-
-bool all_aligned(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return false;
-  return true;
-}
-
-bool mode_ok(int mode) { return mode == FP8BW_MX_RCEIL || mode == FP8BW_MX_FLOOR; }
-
-bool choices_ok(int64_t M, int64_t E, int64_t top_k) {
-  return dim_ok(M, 1) && dim_ok(E, 1) && E <= FP8BW_MOE_MAX_EXPERTS && dim_ok(top_k, 1) &&
-         top_k <= FP8BW_MOE_MAX_TOP_K && top_k <= E;
-}
 
 // Entries and their padded rows are numbered in int32.
 bool plan_dims_ok(int64_t M, int64_t E, int64_t top_k) {
@@ -57,8 +25,7 @@ int route_common(const char* name, MoeRouteArgs& a, int logits_type, void* strea
   if (!choices_ok(a.M, a.E, a.top_k))
     return fail(FP8BW_ERR_SHAPE, "%s: need 0 < M, 0 < E <= 1024 and 0 < top_k <= min(E, 32); got M=%lld E=%lld top_k=%lld",
                 name, (long long)a.M, (long long)a.E, (long long)a.top_k);
-  if (a.groups < 1 || a.groups > FP8BW_MOE_MAX_GROUPS || a.E % a.groups != 0 || a.groups_kept < 1 ||
-      a.groups_kept > a.groups || a.top_k > a.groups_kept * (a.E / a.groups))
+  if (!groups_ok(a.E, a.top_k, a.groups, a.groups_kept))
     return fail(FP8BW_ERR_SHAPE,
                 "%s: groups (%lld) must be 1 to 32 and divide E, groups_kept (%lld) 1 to groups, and top_k at most the "
                 "experts of the kept groups",

@@ -177,6 +177,40 @@ struct SwigluBwdArgs {
 };
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& args, cudaStream_t st);
 
+// ---- a few tokens on MX weights (mx4.cu, few_*.cu)
+
+cudaError_t launch_mxfp4_quant_row(const uint16_t* w, int64_t n, uint8_t* q, uint8_t* e8, int mode, int num_sms,
+                                   cudaStream_t st);  // n weights, whole blocks of 32
+cudaError_t launch_mxfp4_to_mxfp8(const uint8_t* q4, int64_t n, uint8_t* q8, int num_sms, cudaStream_t st);
+
+struct FewLinearArgs {
+  const uint16_t* x;
+  const uint8_t* w;
+  const uint8_t* e8;
+  int bits;
+  int64_t M, N, K;
+  uint16_t* y;
+  int num_sms;
+};
+cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st);
+
+struct FewMoeArgs {
+  const uint16_t* x;
+  const float* router;
+  const uint8_t* w13;
+  const uint8_t* e13;
+  const uint8_t* w2;
+  const uint8_t* e2;
+  int bits;
+  int64_t C, F;
+  MoeRouteArgs route;  // dims, bias and how to choose; no outputs
+  uint16_t* y;
+  void* workspace;
+  int num_sms;
+};
+size_t few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F);
+cudaError_t launch_few_moe(const FewMoeArgs& args, cudaStream_t st);
+
 cudaError_t launch_selftest_bounded_wait(uint32_t timeout_us, int* status, cudaStream_t st);
 
 // cuTensorMapEncodeTiled, resolved once through the runtime's driver entry

@@ -21,6 +21,7 @@ from dataclasses import dataclass
 import torch
 
 from . import binding as B
+from . import few_binding as FB
 
 
 @dataclass
@@ -168,6 +169,59 @@ def mx_moe_backward(dy: torch.Tensor, x: torch.Tensor, wq: MxExpertWeights, grou
     ws = B.alloc_grouped_workspace(B.GROUPED_WGRAD, G, M, N, K, dy.device)
     B.mxfp8_grouped_gemm(B.GROUPED_WGRAD, dyqT, dyeT, xqT, xeT, group_end, G, M, N, K, dW, ws, stream)
     return dx, dW
+
+
+# ------------------------------------------------------------------ weights in 4 bits, and a few tokens
+
+@dataclass
+class Mx4Weights:
+    """MXFP4 codes of W [N, K], or of stacked matrices [G, N, K]."""
+    q: torch.Tensor                # e2m1 [..., N, K/2], two codes to a byte, the lower nibble first
+    e8: torch.Tensor               # E8M0 [G*N, K/32], blocks of 32 along K
+
+
+def mx4_quantize(w: torch.Tensor, mode: int = B.MX_RCEIL, stream=None) -> Mx4Weights:
+    """MXFP4 codes of bf16 w [N, K] or [G, N, K], blocks of 32 along K."""
+    K = w.shape[-1]
+    rows = w.view(-1, K)
+    q = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
+    e8 = torch.empty((rows.shape[0], K // 32), dtype=torch.uint8, device=w.device)
+    FB.mxfp4_quant_1x32_row(rows, q.view(-1, K // 2), e8, mode, stream)
+    return Mx4Weights(q, e8)
+
+
+def mx4_widen(w: Mx4Weights, stream=None) -> MxExpertWeights:
+    """The same weights as rowwise MXFP8 codes, exactly: for the products of a
+    prompt (``mx_moe_forward``, ``MxMoEFFN``).  The scales are shared."""
+    K = 2 * w.q.shape[-1]
+    q = torch.empty((*w.q.shape[:-1], K), dtype=torch.uint8, device=w.q.device)
+    FB.mxfp4_to_mxfp8(w.q.view(-1, K // 2), q.view(-1, K), stream)
+    return MxExpertWeights(q, w.e8, None, None)
+
+
+def _held(w: Mx4Weights | MxExpertWeights) -> tuple[torch.Tensor, torch.Tensor, int]:
+    """Codes, scales and bits of MX weights."""
+    return (w.q, w.e8, 4) if isinstance(w, Mx4Weights) else (w.q_row, w.e8_row, 8)
+
+
+def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad()")
+
+
+def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None) -> torch.Tensor:
+    """y = x W^T in bf16 for 0 to 32 tokens x (bf16 [M, K]) and one matrix W
+    [N, K] in MX codes, 4 bits (``mx4_quantize``) or 8 (the rowwise codes of
+    ``mx_quantize_experts``).  x is not quantized, and sums are fp32: a product
+    for decoding, bound by the bytes of W.  It has no gradient."""
+    _refuse_grad("mx_linear_few", x)
+    q, e8, bits = _held(w)
+    if q.dim() == 3 and q.shape[0] == 1:
+        q = q[0]
+    y = torch.empty((x.shape[0], q.shape[0]), dtype=torch.bfloat16, device=x.device)
+    if x.shape[0] > 0:
+        FB.mx_few_linear(x, q, e8, bits, y, stream)
+    return y
 
 
 # ------------------------------------------------------------------ preallocated step

@@ -11,7 +11,8 @@ table and ``MxRows`` holds their operands.
     a, kept = swiglu(h)                              h = [gate | up] of the first product
     out = combine(y, weights, p)                     y the second product
 
-and each has its ``..._backward``.  ``MxMoEFFN`` is the layer.
+and each has its ``..._backward``.  ``MxMoEFFN`` is the layer, and ``ffn_few``
+all of it at once for a few tokens and no gradients.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ from dataclasses import dataclass
 import torch
 
 from . import binding as B
+from . import few_binding as FB
 from . import linear as L
 from . import moe_binding as MB
 
@@ -191,6 +193,45 @@ def swiglu_backward(da: torch.Tensor, kept: MxRows, mode: int = B.MX_RCEIL) -> M
     return dh
 
 
+# ------------------------------------------------------------------ a few tokens
+
+def ffn_few(x: torch.Tensor, router: torch.Tensor, w13: L.Mx4Weights | L.MxExpertWeights,
+            w2: L.Mx4Weights | L.MxExpertWeights, top_k: int, *, bias: torch.Tensor | None = None, score: str = "softmax",
+            renormalize: bool = True, scale: float = 1.0, groups: int = 1, groups_kept: int = 1,
+            group_top: int = 1) -> torch.Tensor:
+    """The whole layer for 0 to 32 tokens x (bf16 [M, C]): router (fp32 [E, C])
+    and ``route``, the gated experts W13 [E, 2F, C] and W2 [E, C, F] in MX codes,
+    both in 4 bits or both in 8, and the weighted sum, bf16 [M, C].
+
+    Nothing is quantized on the way: tokens stay bf16, h fp32, the activation
+    keeps 11 bits, sums are fp32 and the result is rounded once.  So it is
+    closer to the weights' own product than ``MxMoEFFN.forward``, which holds
+    tokens and activations in MXFP8.  C and F are multiples of 32.  It has no
+    gradient."""
+    L._refuse_grad("ffn_few", x, router, bias)
+    (q13, e13, bits), (q2, e2, bits2) = L._held(w13), L._held(w2)
+    if bits != bits2:
+        raise ValueError(f"w13 is held in {bits} bits and w2 in {bits2}")
+    M, C = x.shape
+    E, F2 = q13.shape[:2]
+    y = torch.empty((M, C), dtype=_BF16, device=x.device)
+    if M == 0:
+        return y
+    ws = torch.empty(_few_workspace(M, E, top_k, C, F2 // 2), dtype=_U8, device=x.device)
+    FB.mx_few_moe(x, router, bias, q13, e13, q2, e2, bits, top_k, y, ws, groups, groups_kept, group_top, _score(score),
+                  renormalize, scale)
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def _few_workspace(M: int, E: int, top_k: int, C: int, F: int) -> int:
+    n = FB.mx_few_moe_workspace_bytes(M, E, top_k, C, F)
+    if n == 0:
+        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid dims of ffn_few: {M} tokens (at most {FB.FEW_TOKENS}), {E} experts, top_k "
+                                        f"{top_k}, {C} and {F} features")
+    return n
+
+
 # ------------------------------------------------------------------ the layer
 
 def _grouped(kind: int, a, a_e8, b, b_e8, p: Plan, N: int, K: int, out: torch.Tensor) -> torch.Tensor:
@@ -237,9 +278,17 @@ class _RouterLogits(torch.autograd.Function):
                 None if x is None else _without_autocast(torch.matmul, dlogits.t(), x))
 
 
-def _check_codes(codes: L.MxExpertWeights, w: torch.Tensor, colwise: bool) -> None:
-    """The grouped GEMMs take sizes from the layer and read the codes by address; a gradient reads the colwise ones."""
+def _check_codes(codes: L.MxExpertWeights | L.Mx4Weights, w: torch.Tensor, colwise: bool) -> None:
+    """The kernels take sizes from the layer and read the codes by address; a gradient reads the colwise ones."""
     E, N, K = w.shape
+    if isinstance(codes, L.Mx4Weights):
+        if colwise:
+            raise ValueError("codes: gradients read colwise codes, which weights in 4 bits do not have")
+        for name, shape in (("q", (E, N, K // 2)), ("e8", (E * N, K // 32))):
+            if tuple(getattr(codes, name).shape) != shape:
+                raise ValueError(f"codes: {name} of weights {tuple(w.shape)} is {shape}, "
+                                 f"got {tuple(getattr(codes, name).shape)}")
+        return
     for name, shape in (("q_row", (E, N, K)), ("e8_row", (E * N, K // 32)), ("qT_col", (E, K, N)),
                         ("e8_col", (E, K, N // 32))):
         t = getattr(codes, name)
@@ -362,14 +411,31 @@ class MxMoEFFN(torch.nn.Module):
 
         return super()._apply(but_keep_fp32, recurse)
 
-    def weight_codes(self, colwise: bool = True) -> tuple[L.MxExpertWeights, L.MxExpertWeights]:
+    def weight_codes(self, colwise: bool = True, bits: int = 8) -> tuple:
         """MX codes of w13 and w2 as they are now, for calls between two changes of the weights.  Without ``colwise`` those
-        that a forward pass reads, half of the bytes: for calls without gradients."""
+        that a forward pass reads, half of the bytes: for calls without gradients.  ``bits=4``: MXFP4 codes (rowwise alone),
+        again half of the bytes, for ``decode`` and for forward passes without gradients."""
+        if bits == 4:
+            return tuple(L.mx4_quantize(w.detach(), self.mode) for w in (self.w13, self.w2))
+        if bits != 8:
+            raise ValueError(f"bits: expected 4 or 8, got {bits!r}")
         return tuple(L.mx_quantize_experts(w.detach(), self.mode, colwise=colwise) for w in (self.w13, self.w2))
 
-    def forward(self, x: torch.Tensor, codes: tuple[L.MxExpertWeights, L.MxExpertWeights] | None = None) -> torch.Tensor:
+    def decode(self, x: torch.Tensor, codes: tuple) -> torch.Tensor:
+        """The layer for 0 to 32 tokens without gradients, with ``weight_codes()`` of either width: ``ffn_few``.  Tokens
+        and activations are not quantized, so results are not bit for bit ``forward``'s."""
+        L._refuse_grad("decode", x)
+        for got, w in zip(codes, (self.w13, self.w2)):
+            _check_codes(got, w, False)
+        top_k, score, renormalize, scale, groups, groups_kept, group_top = self.how
+        with torch.no_grad():
+            return ffn_few(x, self.router, *codes, top_k, bias=self.balance, score=score, renormalize=renormalize, scale=scale,
+                           groups=groups, groups_kept=groups_kept, group_top=group_top)
+
+    def forward(self, x: torch.Tensor, codes: tuple | None = None) -> torch.Tensor:
         """``codes``: ``weight_codes()`` kept by the caller (a decoder, or the micro-batches of a step); by default
-        the weights are quantized in every call."""
+        the weights are quantized in every call.  Codes of 4 bits are widened to 8 in every call: for prompts, with
+        ``decode`` for the tokens after them."""
         # needs_input_grad does not know of no_grad, where the layouts and codes for backward would be for nothing
         grad = torch.is_grad_enabled()
         train = grad and any(t.requires_grad for t in (x, self.router, self.w13, self.w2))
@@ -380,6 +446,7 @@ class MxMoEFFN(torch.nn.Module):
         else:
             for got, (w, colwise) in zip(codes, (weights13, weights2)):
                 _check_codes(got, w, colwise)
+            codes = tuple(L.mx4_widen(c) if isinstance(c, L.Mx4Weights) else c for c in codes)
         if train:
             logits = _RouterLogits.apply(x.float(), self.router)
         else:
