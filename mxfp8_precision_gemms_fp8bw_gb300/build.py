@@ -21,7 +21,7 @@ LIB_NAME = "libfp8bw.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["quant.cu", "gemm_blockwise.cu", "gemm_mx.cu", "moe_route.cu", "moe_route_bwd.cu", "moe_rows.cu", "moe_swiglu.cu",
-           "mx4.cu", "few.cu", "api.cu", "api_moe.cu", "api_few.cu"]
+           "mx4.cu", "few.cu", "few_route.cu", "api.cu", "api_moe.cu", "api_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I" + INCLUDE]
 
