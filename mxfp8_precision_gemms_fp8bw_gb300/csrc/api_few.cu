@@ -11,6 +11,10 @@ constexpr int64_t kMaxWidth = int64_t{1} << 22;  // contraction lengths and rows
 
 bool bits_ok(int bits) { return bits == 4 || bits == 8; }
 
+bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
+  return dim_ok(M, 1) && M <= FP8BW_FEW_TOKENS && dim_ok(N, 1) && dim_ok(K, 32) && K <= kMaxWidth;
+}
+
 bool layer_dims_ok(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {
   return M <= FP8BW_FEW_TOKENS && choices_ok(M, E, top_k) && dim_ok(C, 32) && dim_ok(F, 32) && C <= kMaxWidth &&
          F <= kMaxWidth;
@@ -49,22 +53,34 @@ FP8BW_API int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q
   return launched(launch_mxfp4_to_mxfp8(q4, R * C, q8, d->num_sms, as_stream(stream)), name);
 }
 
+FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K) {
+  return linear_dims_ok(M, 1, K) ? few_linear_workspace_bytes(M, K) : 0;
+}
+
 FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
-                            int64_t K, fp8bw_bf16* y, void* stream) {
+                            int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream) {
   const char* name = "mx_few_linear";
   if (!x || !w || !e8 || !y) return fail(FP8BW_ERR_NULL, "%s: x, w, e8 and y must be non-NULL", name);
-  if (!dim_ok(M, 1) || M > FP8BW_FEW_TOKENS || !dim_ok(N, 1) || !dim_ok(K, 32) || K > kMaxWidth)
+  if (!linear_dims_ok(M, N, K))
     return fail(FP8BW_ERR_SHAPE,
                 "%s: need 0 < M <= 32, 0 < N < 2^31 and K a positive multiple of 32 up to 2^22; got M=%lld N=%lld "
                 "K=%lld",
                 name, (long long)M, (long long)N, (long long)K);
-  if (!all_aligned({x, w, e8, y})) return fail(FP8BW_ERR_ALIGN, "%s: pointers must be 16-byte aligned", name);
+  if (!all_aligned({x, w, e8, y, workspace})) return fail(FP8BW_ERR_ALIGN, "%s: pointers must be 16-byte aligned", name);
   if (!bits_ok(bits)) return fail(FP8BW_ERR_ARG, "%s: bits %d is neither 4 nor 8", name, bits);
-  if (any_overlap({{y, M * N * 2}}, {{x, M * K * 2}, {w, N * K / 8 * bits}, {e8, N * (K / 32)}}))
-    return fail(FP8BW_ERR_LAYOUT, "%s: y overlaps an input", name);
+  const size_t need = few_linear_workspace_bytes(M, K);
+  if (need > 0 && !workspace)
+    return fail(FP8BW_ERR_NULL, "%s: these dims need a workspace of %zu bytes", name, need);
+  if (workspace_bytes < need)
+    return fail(FP8BW_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu bytes these dims need", name,
+                workspace_bytes, need);
+  if (any_overlap({{y, M * N * 2}, {need > 0 ? workspace : nullptr, static_cast<int64_t>(need)}},
+                  {{x, M * K * 2}, {w, N * (K / 8) * bits}, {e8, N * (K / 32)}}))
+    return fail(FP8BW_ERR_LAYOUT, "%s: y or the workspace overlaps an input or each other", name);
   DeviceState* d;
   if (int rc = current_device(&d)) return rc;
-  return launched(launch_few_linear(FewLinearArgs{x, w, e8, bits, M, N, K, y, d->num_sms}, as_stream(stream)), name);
+  return launched(launch_few_linear(FewLinearArgs{x, w, e8, bits, M, N, K, y, workspace, d->num_sms}, as_stream(stream)),
+                  name);
 }
 
 FP8BW_API size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {

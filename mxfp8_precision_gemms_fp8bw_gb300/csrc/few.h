@@ -50,6 +50,18 @@ __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i
 // Where the activation's records of a slot begin: a record of n tokens is at most 80 n bytes.
 __host__ __device__ inline int64_t few_act_at(int64_t start, int64_t F) { return start * 80 * (F / 32); }
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, cudaStream_t st);
+// Tokens as the products read them: f16 [M, K] under a power of two for each token, the elements of each 32 in the order
+// of few::place_of.
+struct FewTokens {
+  uint8_t* rows;
+  float* scales;
+};
+inline int64_t few_tokens_bytes(int64_t M, int64_t K) { return (M * K * 2 + 255) / 256 * 256 + 256; }
+inline FewTokens few_tokens_at(void* p, int64_t M, int64_t K) {
+  uint8_t* at = static_cast<uint8_t*>(p);
+  return FewTokens{at + 256, reinterpret_cast<float*>(at)};
+}
+
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewTokens& tokens, cudaStream_t st);
 
 }  // namespace fp8bw

@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 
 #include "few.h"
+#include "few_product.cuh"
 #include "route_row.cuh"
 
 namespace fp8bw {
@@ -12,14 +13,15 @@ namespace cg = cooperative_groups;
 
 // One cluster.  Each block takes a share of the features: its warps, four
 // experts and eight tokens at a time, multiply fp32 router rows with tokens in
-// shared memory, so that the router is read once, by all blocks together.  The
-// shares of a token's logits then meet in one block (distributed shared
+// shared memory, so that the router is read once, by all blocks together.
+// (Where that is fewer than 16 pieces of work, warps share the features too.)
+// The shares of a token's logits then meet in one block (distributed shared
 // memory, in the order of the blocks), which makes the choice as fp8bw_moe_route
 // does; and the first block sorts the choices.  An expert's tokens are a
 // 32-bit mask, whose bits below a token give its place.
 constexpr int kBlocks = 8, kWarps = 16, kThreads = kWarps * 32;
+static_assert(kWarps == 4 * (kFewTokens / kBlocks));
 constexpr int kMostRows = kFewTokens / kBlocks;  // tokens whose choice a block makes
-constexpr int kTokenBytes = 32 * 1024;           // of tokens in shared memory at a time
 
 struct RouteFew {
   const uint16_t* x;
@@ -28,8 +30,9 @@ struct RouteFew {
   RouteShape how;  // M rows
   int C, share;    // features, and of a block: a multiple of 8
   int width;       // features in shared memory at a time: a multiple of 128
-  int slices;      // warps that share a quartet of experts
+  int slices;      // warps that share four experts and eight tokens
   FewPlan* plan;
+  FewTokens held;  // the tokens as the first product reads them
 };
 
 struct Layout {  // floats of shared memory
@@ -38,7 +41,7 @@ struct Layout {  // floats of shared memory
 __host__ __device__ inline Layout layout_of(int M, int E, int k, int width, int slices) {
   Layout l{};
   l.tokens = 0;
-  l.partial = M * width;
+  l.partial = M * width / 2;  // bf16
   l.logits = l.partial + slices * M * E;
   l.staged = l.logits + kMostRows * E;
   l.experts = l.staged + kMostRows * (E | 8);
@@ -66,67 +69,80 @@ __device__ __forceinline__ float sum_each(float (&v)[32]) {
   return v[0];
 }
 
-template <int L, int V>
+template <int L, int V, int kBits>
 __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_constant__ RouteFew p) {
   extern __shared__ __align__(16) float smem[];
+  __shared__ uint32_t s_top[kMostRows];
   cg::cluster_group cluster = cg::this_cluster();
   const int M = static_cast<int>(p.how.M), E = p.how.E, k = p.how.k;
   const int rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Layout at = layout_of(M, E, k, p.width, p.slices);
   asm volatile("griddepcontrol.launch_dependents;");  // they wait for this kernel's end before they read the plan
 
+  // Tokens rank, rank + kBlocks, ... are this block's: it makes their choice, and brings them into f16.  Four warps look for
+  // the largest element of each.
+  const int rows = rank < M ? (M - rank + kBlocks - 1) / kBlocks : 0;
+  const auto row_of = [&](int r) {
+    return reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(rank + r * kBlocks) * p.C);
+  };
+  if (tid < kMostRows) s_top[tid] = 0;
+  __syncthreads();
+  if (warp / 4 < rows) {
+    const uint4* row = row_of(warp / 4);
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int i = warp % 4 * 32 + lane; i < p.C / 8; i += 128) m = __vmaxu2(m, few::largest(__ldg(row + i)));
+    m = __reduce_max_sync(kAll, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0) atomicMax(s_top + warp / 4, m);  // a maximum does not depend on the order
+  }
+
   // Logits of this block's features.
-  float* const tokens = smem + at.tokens;
+  uint2* const tokens = reinterpret_cast<uint2*>(smem + at.tokens);  // four bf16 each
   float* const partial = smem + at.partial;
   const int first = rank * p.share, last = min(first + p.share, p.C);
-  const int quartets = kWarps / p.slices, slice = warp / quartets;
+  const int tiles = (M + 7) / 8, work = (E + 3) / 4 * tiles * p.slices;
   const int steps = max((last - first + p.width - 1) / p.width, 1);
   for (int s = 0; s < steps; ++s) {
     const int c0 = first + s * p.width, n = min(p.width, max(last - c0, 0));  // n: a multiple of 8
     if (s > 0) __syncthreads();
-    for (int i = tid; i < M * (p.width / 8); i += kThreads) {
-      const int t = i / (p.width / 8), c = i % (p.width / 8) * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c < n) v = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.C + c0 + c));
-      float4* to = reinterpret_cast<float4*>(tokens + t * p.width + c);
-      to[0] = make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
-      to[1] = make_float4(bf16lo_to_f32(v.z), bf16hi_to_f32(v.z), bf16lo_to_f32(v.w), bf16hi_to_f32(v.w));
-    }
+    for (int t = warp; t < M; t += kWarps)
+      for (int c = lane * 8; c < n; c += 256)
+        *reinterpret_cast<uint4*>(tokens + (t * p.width + c) / 4) =
+            __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.C + c0 + c));
     __syncthreads();
-    for (int e0 = warp % quartets * 4; e0 < E; e0 += quartets * 4) {
-      for (int t0 = 0; t0 < M; t0 += 8) {
-        float v[32];
+    for (int w = warp; w < work; w += kWarps) {
+      const int slice = w % p.slices, t0 = w / p.slices % tiles * 8, e0 = w / p.slices / tiles * 4;
+      float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 2
-        for (int c = slice * 128 + lane * 4; c < n; c += p.slices * 128) {
-          float4 r[4];
+      for (int c = slice * 128 + lane * 4; c < n; c += p.slices * 128) {
+        float4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          r[i] = e0 + i < E ? __ldg(reinterpret_cast<const float4*>(p.router + static_cast<int64_t>(e0 + i) * p.C + c0 + c))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (t0 + j >= M) break;
+          const uint2 x = tokens[((t0 + j) * p.width + c) / 4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            r[i] = e0 + i < E ? __ldg(reinterpret_cast<const float4*>(p.router + static_cast<int64_t>(e0 + i) * p.C + c0 + c))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (t0 + j >= M) break;
-            const float4 x = *reinterpret_cast<const float4*>(tokens + (t0 + j) * p.width + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[i * 8 + j] = fmaf(r[i].x, x.x, fmaf(r[i].y, x.y, fmaf(r[i].z, x.z, fmaf(r[i].w, x.w, v[i * 8 + j]))));
-          }
+            v[i * 8 + j] = fmaf(r[i].x, bf16lo_to_f32(x.x),
+                                fmaf(r[i].y, bf16hi_to_f32(x.x),
+                                     fmaf(r[i].z, bf16lo_to_f32(x.y), fmaf(r[i].w, bf16hi_to_f32(x.y), v[i * 8 + j]))));
         }
-        const float sum = sum_each(v);
-        const int e = e0 + lane / 8, t = t0 + lane % 8;
-        if (e < E && t < M) {
-          float* to = partial + (slice * M + t) * E + e;
-          *to = s > 0 ? *to + sum : sum;
-        }
+      }
+      const float sum = sum_each(v);
+      const int e = e0 + lane / 8, t = t0 + lane % 8;
+      if (e < E && t < M) {
+        float* to = partial + (slice * M + t) * E + e;
+        *to = s > 0 ? *to + sum : sum;
       }
     }
   }
   cluster.sync();
 
-  // The choice for tokens rank, rank + kBlocks, ...
-  const int rows = rank < M ? (M - rank + kBlocks - 1) / kBlocks : 0;
   float* const logits = smem + at.logits;
   for (int i = tid; i < rows * E; i += kThreads) {
     const int row = i / E, e = i - row * E;
@@ -140,7 +156,19 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
   __syncthreads();
   int32_t* const experts = reinterpret_cast<int32_t*>(smem + at.experts);
   float* const weights = smem + at.weights;
-  if (warp * (32 / L) < rows) {
+  constexpr int kChoosers = L == 8 ? 1 : kMostRows;  // warps that choose; the others convert
+  if (warp >= kChoosers) {
+    for (int w = warp - kChoosers; w < rows * 4; w += kWarps - kChoosers) {
+      const int r = w / 4, t = rank + r * kBlocks;
+      const uint4* row = row_of(r);
+      uint8_t* to = p.held.rows + static_cast<int64_t>(t) * p.C * 2;
+      const uint32_t field = few::factor_field(s_top[r] >> 7);
+      if (w % 4 == 0 && lane == 0) p.held.scales[t] = few::of_field(254u - field);
+#pragma unroll 4
+      for (int i = w % 4 * 32 + lane; i < p.C / 8; i += 128)
+        few::store_f16<kBits>(to + i / 4 * 64, i & 3, few::to_f16(__ldg(row + i), few::of_field(field)));
+    }
+  } else if (warp * (32 / L) < rows) {
     const int row = tid / L;
     route_row<float, L, V>(logits, p.bias, p.how, row, row < rows, row, reinterpret_cast<uint32_t*>(smem + at.staged), experts,
                            weights);
@@ -205,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
 
 }  // namespace
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, cudaStream_t st) {
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewTokens& tokens, cudaStream_t st) {
   RouteFew p{};
   p.x = a.x;
   p.router = a.router;
@@ -214,16 +242,18 @@ cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, cudaStream_t st
   p.C = static_cast<int>(a.C);
   p.share = (p.C + 8 * kBlocks - 1) / (8 * kBlocks) * 8;
   const int M = static_cast<int>(a.route.M), E = p.how.E;
-  const int most = kTokenBytes / (4 * M) / 128 * 128, want = (p.share + 127) / 128 * 128;
+  // Tokens in shared memory: 64 KB, or 32 beside the logits of very many experts.
+  const int most = (M * E <= 16384 ? 32768 : 16384) / M / 128 * 128, want = (p.share + 127) / 128 * 128;
   p.width = want < most ? want : most;
-  int quartets = 1;
-  while (quartets < kWarps && quartets * 4 < E) quartets *= 2;
-  p.slices = kWarps / quartets;
+  const int work = (E + 3) / 4 * ((M + 7) / 8);
+  p.slices = 1;
+  while (2 * p.slices * work <= kWarps && 2 * p.slices * 128 <= p.width) p.slices *= 2;
   p.plan = plan;
+  p.held = tokens;
   const int smem = layout_of(M, E, p.how.k, p.width, p.slices).total * 4;
   return for_experts(E, [&](auto lanes, auto width) {
     constexpr int L = decltype(lanes)::value, V = decltype(width)::value;
-    auto* kernel = few_route_kernel<L, V>;
+    auto* kernel = a.bits == 4 ? few_route_kernel<L, V, 4> : few_route_kernel<L, V, 8>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;

@@ -190,8 +190,10 @@ struct FewLinearArgs {
   int bits;
   int64_t M, N, K;
   uint16_t* y;
+  void* workspace;  // few_linear_workspace_bytes
   int num_sms;
 };
+size_t few_linear_workspace_bytes(int64_t M, int64_t K);
 cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st);
 
 struct FewMoeArgs {

@@ -16,7 +16,8 @@ FEW_TOKENS = 32
 _SIGNATURES = {
     "mxfp4_quant_1x32_row": [_P, _I64, _I64, _P, _P, _INT, _P],
     "mxfp4_to_mxfp8": [_P, _I64, _I64, _P, _P],
-    "mx_few_linear": [_P, _P, _P, _INT, _I64, _I64, _I64, _P, _P],
+    "mx_few_linear_workspace_bytes": [_I64, _I64],
+    "mx_few_linear": [_P, _P, _P, _INT, _I64, _I64, _I64, _P, _P, _SIZE, _P],
     "mx_few_moe_workspace_bytes": [_I64, _I64, _I64, _I64, _I64],
     "mx_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C, _P,
                    _P, _SIZE, _P],
@@ -33,7 +34,7 @@ def lib() -> ctypes.CDLL:
         for name, args in _SIGNATURES.items():
             fn = getattr(handle, name)
             fn.argtypes = args
-            fn.restype = _SIZE if name == "mx_few_moe_workspace_bytes" else _INT
+            fn.restype = _SIZE if name.endswith("_workspace_bytes") else _INT
         _LIB = handle
     return _LIB
 
@@ -49,12 +50,17 @@ def mxfp4_to_mxfp8(q4, q8, stream=None) -> None:
     B._check(lib().mxfp4_to_mxfp8(_arg(q4, _U8, "q4", R, C // 2), R, C, _arg(q8, _U8, "q8", R, C), _stream(stream, q4)))
 
 
-def mx_few_linear(x, w, e8, bits, y, stream=None) -> None:
+def mx_few_linear_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().mx_few_linear_workspace_bytes(M, K))
+
+
+def mx_few_linear(x, w, e8, bits, y, workspace=None, stream=None) -> None:
     M, K = x.shape
     N = w.shape[0]
+    n = 0 if workspace is None else workspace.shape[0]
     B._check(lib().mx_few_linear(_arg(x, _BF16, "x", M, K), _arg(w, _U8, "w", N, K * bits // 8),
                                  _arg(e8, _U8, "e8", N, K // 32), bits, M, N, K, _arg(y, _BF16, "y", M, N),
-                                 _stream(stream, x)))
+                                 _arg(workspace, _U8, "workspace", n), n, _stream(stream, x)))
 
 
 def mx_few_moe_workspace_bytes(M: int, E: int, top_k: int, C: int, F: int) -> int:

@@ -16,6 +16,7 @@ Backward  : dy -> 1x128 rowwise and colwise in one pass;
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -218,10 +219,15 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     q, e8, bits = _held(w)
     if q.dim() == 3 and q.shape[0] == 1:
         q = q[0]
-    y = torch.empty((x.shape[0], q.shape[0]), dtype=torch.bfloat16, device=x.device)
-    if x.shape[0] > 0:
-        FB.mx_few_linear(x, q, e8, bits, y, stream)
+    M, K = x.shape
+    y = torch.empty((M, q.shape[0]), dtype=torch.bfloat16, device=x.device)
+    if M > 0:
+        n = _few_linear_workspace(M, K)
+        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(n, dtype=torch.uint8, device=x.device) if n else None, stream)
     return y
+
+
+_few_linear_workspace = functools.lru_cache(maxsize=256)(FB.mx_few_linear_workspace_bytes)  # by the dims alone
 
 
 # ------------------------------------------------------------------ preallocated step

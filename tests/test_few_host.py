@@ -49,14 +49,23 @@ def test_widen_refusals(lib, code, kw):
 
 
 @pytest.mark.parametrize("code,kw", [
-    ("NULL", dict(a0=None)), ("NULL", dict(a1=None)), ("NULL", dict(a2=None)), ("NULL", dict(a7=None)),
+    ("NULL", dict(a0=None)), ("NULL", dict(a1=None)), ("NULL", dict(a2=None)), ("NULL", dict(a7=None)), ("NULL", dict(a8=None)),
     ("SHAPE", dict(a4=0)), ("SHAPE", dict(a4=33)), ("SHAPE", dict(a5=0)), ("SHAPE", dict(a6=40)), ("SHAPE", dict(a6=0)),
     ("SHAPE", dict(a6=(1 << 22) + 32)), ("ALIGN", dict(a0=P + 2)), ("ALIGN", dict(a2=3 * P + 4)), ("ALIGN", dict(a7=4 * P + 2)),
-    ("ARG", dict(a3=6)), ("ARG", dict(a3=16)), ("LAYOUT", dict(a7=P + 16)), ("LAYOUT", dict(a7=2 * P)), ("LAYOUT", dict(a7=3 * P)),
+    ("ALIGN", dict(a8=50 * P + 8)), ("ARG", dict(a3=6)), ("ARG", dict(a3=16)), ("ARG", dict(a9=100)),
+    ("LAYOUT", dict(a7=P + 16)), ("LAYOUT", dict(a7=2 * P)), ("LAYOUT", dict(a7=30 * P)), ("LAYOUT", dict(a8=2 * P + 4096)),
+    ("LAYOUT", dict(a8=40 * P)),
 ])
 def test_linear_refusals(lib, code, kw):
-    ok = [P, 2 * P, 3 * P, 4, 3, 65, 64, 4 * P, None]
+    M, N, K = 32, 65, 2048
+    ok = [P, 2 * P, 30 * P, 4, M, N, K, 40 * P, 50 * P, lib.mx_few_linear_workspace_bytes(M, K), None]
     assert lib.mx_few_linear(*[kw.get(f"a{i}", v) for i, v in enumerate(ok)]) == getattr(B, "ERR_" + code)
+
+
+def test_linear_workspace(lib):
+    size = lib.mx_few_linear_workspace_bytes
+    assert size(1, 5120) == 0 and size(32, 5120) >= 32 * 5120 * 2
+    assert size(0, 5120) == size(33, 5120) == size(32, 5100) == size(32, (1 << 22) + 32) == 0
 
 
 def test_layer_workspace(lib):
