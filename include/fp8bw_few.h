@@ -10,10 +10,13 @@
  * first: bit 3 the sign, codes 0 to 7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4
  * and 6.  An E8M0 byte of 255 makes its block NaN.
  *
- * Products here round nothing on the way in: tokens stay bf16, weights are
- * what their codes stand for, sums run in fp32, and the result is rounded once
- * to bf16.  (The grouped GEMM of fp8bw.h quantizes its tokens to MXFP8.)  No
- * result depends on the order in which blocks run.
+ * Products here round nothing that matters on the way in: a token is read as
+ * the sum of two MXFP8 numbers, which is the bf16 value itself down to 2^-12 of
+ * the largest element of its block of 32, and off by at most 2^-21 of that
+ * below; weights are what their codes stand for, sums run in fp32, and the
+ * result is rounded once to bf16.  (The grouped GEMM of fp8bw.h reads tokens
+ * that are rounded to MXFP8 once.)  A token with an infinity or a NaN gives
+ * NaN.  No result depends on the order in which blocks run.
  */
 #ifndef FP8BW_FEW_H
 #define FP8BW_FEW_H
@@ -39,16 +42,15 @@ int mxfp4_quant_1x32_row(const fp8bw_bf16* w, int64_t R, int64_t C, uint8_t* q, 
  *   q4 : e2m1 [R, C/2]    q8 : e4m3 [R, C]      C a positive multiple of 32. */
 int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q8, void* stream);
 
-/* Bytes of workspace mx_few_linear needs: 0 for few elements of x, and for
- * invalid dims.  Host-only. */
+/* Bytes of workspace mx_few_linear needs; 0 for invalid dims.  Host-only. */
 size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K);
 
 /* y = x W^T.
  *   x : bf16 [M, K]    w : codes of W[N, K]    e8 : E8M0 [N][K/32]    y : bf16 [M, N]
  * 1 <= M <= 32, N positive, K a positive multiple of 32, bits 4 or 8.
  * workspace: caller-owned DEVICE scratch of at least
- * mx_few_linear_workspace_bytes bytes, in any state, NULL where that is 0;
- * concurrent calls need one each. */
+ * mx_few_linear_workspace_bytes bytes, in any state; concurrent calls need one
+ * each. */
 int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N, int64_t K,
                   fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -58,8 +60,9 @@ size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C
 /* A mixture-of-experts layer of gated feed-forward experts on M tokens:
  *   logits = x router^T (fp32);  experts e_j, weights w_j: fp8bw_moe_route's of them
  *   [gate; up] = W13[e_j] x;  a_j = gate * sigmoid(gate) * up;  y = sum_j w_j W2[e_j] a_j
- * A choice without an expert adds nothing.  h = [gate; up] stays fp32.  The activation is held
- * between the two products with 11 significant bits, its 32 blocks' largest elements alike.
+ * A choice without an expert adds nothing.  h = [gate; up] stays fp32; the
+ * activation is held between the two products with 12 significant bits (2^-25
+ * of the largest of its block of 32 where that is more).
  *   x   : bf16 [M, C]           router : fp32 [E, C]      bias : fp32 [E] or NULL
  *   w13 : codes of [E, 2F, C]   e13    : E8M0 [E][2F][C/32]
  *   w2  : codes of [E, C, F]    e2     : E8M0 [E][C][F/32]     y : bf16 [M, C]

@@ -47,21 +47,24 @@ __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i
   return FewSlot{v.x, v.y, static_cast<uint32_t>(v.z), v.w};
 }
 
-// Where the activation's records of a slot begin: a record of n tokens is at most 80 n bytes.
-__host__ __device__ inline int64_t few_act_at(int64_t start, int64_t F) { return start * 80 * (F / 32); }
-
-// Tokens as the products read them: f16 [M, K] under a power of two for each token, the elements of each 32 in the order
-// of few::place_of.
-struct FewTokens {
-  uint8_t* rows;
-  float* scales;
+// Values as the products read them (few_tokens.cuh): for every row, `parts` rows of e4m3 codes and as many of E8M0 bytes,
+// both padded to whole chunks of 128.  Tokens come in two parts, activations (a row for every choice, by slot and column) in
+// three.
+constexpr int kTokenParts = 2, kActParts = 3;
+struct FewRows {
+  uint8_t* codes;   // [rows * parts][pitch]
+  uint8_t* scales;  // [rows * parts][pitch / 32]
+  int64_t pitch;
 };
-inline int64_t few_tokens_bytes(int64_t M, int64_t K) { return (M * K * 2 + 255) / 256 * 256 + 256; }
-inline FewTokens few_tokens_at(void* p, int64_t M, int64_t K) {
+__host__ __device__ inline int64_t few_pitch(int64_t K) { return (K + 127) / 128 * 128; }
+inline int64_t few_rows_bytes(int64_t rows, int parts, int64_t K) {
+  return (rows * parts * (few_pitch(K) / 32) * 33 + 255) / 256 * 256;
+}
+inline FewRows few_rows_at(void* p, int64_t rows, int parts, int64_t K) {
   uint8_t* at = static_cast<uint8_t*>(p);
-  return FewTokens{at + 256, reinterpret_cast<float*>(at)};
+  return FewRows{at, at + rows * parts * few_pitch(K), few_pitch(K)};
 }
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewTokens& tokens, cudaStream_t st);
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewRows& tokens, cudaStream_t st);
 
 }  // namespace fp8bw

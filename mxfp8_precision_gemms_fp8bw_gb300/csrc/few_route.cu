@@ -3,7 +3,7 @@
 #include <cooperative_groups.h>
 
 #include "few.h"
-#include "few_product.cuh"
+#include "few_tokens.cuh"
 #include "route_row.cuh"
 
 namespace fp8bw {
@@ -20,7 +20,6 @@ namespace cg = cooperative_groups;
 // does; and the first block sorts the choices.  An expert's tokens are a
 // 32-bit mask, whose bits below a token give its place.
 constexpr int kBlocks = 8, kWarps = 16, kThreads = kWarps * 32;
-static_assert(kWarps == 4 * (kFewTokens / kBlocks));
 constexpr int kMostRows = kFewTokens / kBlocks;  // tokens whose choice a block makes
 
 struct RouteFew {
@@ -32,7 +31,7 @@ struct RouteFew {
   int width;       // features in shared memory at a time: a multiple of 128
   int slices;      // warps that share four experts and eight tokens
   FewPlan* plan;
-  FewTokens held;  // the tokens as the first product reads them
+  FewRows held;    // the tokens as the first product reads them
 };
 
 struct Layout {  // floats of shared memory
@@ -69,32 +68,14 @@ __device__ __forceinline__ float sum_each(float (&v)[32]) {
   return v[0];
 }
 
-template <int L, int V, int kBits>
+template <int L, int V>
 __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_constant__ RouteFew p) {
   extern __shared__ __align__(16) float smem[];
-  __shared__ uint32_t s_top[kMostRows];
   cg::cluster_group cluster = cg::this_cluster();
   const int M = static_cast<int>(p.how.M), E = p.how.E, k = p.how.k;
   const int rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Layout at = layout_of(M, E, k, p.width, p.slices);
   asm volatile("griddepcontrol.launch_dependents;");  // they wait for this kernel's end before they read the plan
-
-  // Tokens rank, rank + kBlocks, ... are this block's: it makes their choice, and brings them into f16.  Four warps look for
-  // the largest element of each.
-  const int rows = rank < M ? (M - rank + kBlocks - 1) / kBlocks : 0;
-  const auto row_of = [&](int r) {
-    return reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(rank + r * kBlocks) * p.C);
-  };
-  if (tid < kMostRows) s_top[tid] = 0;
-  __syncthreads();
-  if (warp / 4 < rows) {
-    const uint4* row = row_of(warp / 4);
-    uint32_t m = 0;
-#pragma unroll 4
-    for (int i = warp % 4 * 32 + lane; i < p.C / 8; i += 128) m = __vmaxu2(m, few::largest(__ldg(row + i)));
-    m = __reduce_max_sync(kAll, max(m & 0xFFFFu, m >> 16));
-    if (lane == 0) atomicMax(s_top + warp / 4, m);  // a maximum does not depend on the order
-  }
 
   // Logits of this block's features.
   uint2* const tokens = reinterpret_cast<uint2*>(smem + at.tokens);  // four bf16 each
@@ -143,6 +124,8 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
   }
   cluster.sync();
 
+  // The choice for tokens rank, rank + kBlocks, ...
+  const int rows = rank < M ? (M - rank + kBlocks - 1) / kBlocks : 0;
   float* const logits = smem + at.logits;
   for (int i = tid; i < rows * E; i += kThreads) {
     const int row = i / E, e = i - row * E;
@@ -156,17 +139,19 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
   __syncthreads();
   int32_t* const experts = reinterpret_cast<int32_t*>(smem + at.experts);
   float* const weights = smem + at.weights;
-  constexpr int kChoosers = L == 8 ? 1 : kMostRows;  // warps that choose; the others convert
+  constexpr int kChoosers = L == 8 ? 1 : kMostRows;  // warps that choose; the others bring the tokens into e4m3
   if (warp >= kChoosers) {
-    for (int w = warp - kChoosers; w < rows * 4; w += kWarps - kChoosers) {
-      const int r = w / 4, t = rank + r * kBlocks;
-      const uint4* row = row_of(r);
-      uint8_t* to = p.held.rows + static_cast<int64_t>(t) * p.C * 2;
-      const uint32_t field = few::factor_field(s_top[r] >> 7);
-      if (w % 4 == 0 && lane == 0) p.held.scales[t] = few::of_field(254u - field);
-#pragma unroll 4
-      for (int i = w % 4 * 32 + lane; i < p.C / 8; i += 128)
-        few::store_f16<kBits>(to + i / 4 * 64, i & 3, few::to_f16(__ldg(row + i), few::of_field(field)));
+    const int pieces = p.C / 8;  // of 8 values
+    for (int r = 0; r < rows; ++r) {
+      const int64_t t = rank + r * kBlocks;
+      const uint4* row = reinterpret_cast<const uint4*>(p.x + t * p.C);
+      uint8_t* to = p.held.codes + t * kTokenParts * p.held.pitch;
+      uint8_t* scales = p.held.scales + t * kTokenParts * (p.held.pitch / 32);
+#pragma unroll 2
+      for (int i0 = (warp - kChoosers) * 32; i0 < pieces; i0 += (kWarps - kChoosers) * 32) {
+        const int i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
+        few::split8(__ldg(row + i), to + i * 8, scales + i / 4, p.held.pitch);
+      }
     }
   } else if (warp * (32 / L) < rows) {
     const int row = tid / L;
@@ -233,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
 
 }  // namespace
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewTokens& tokens, cudaStream_t st) {
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewRows& tokens, cudaStream_t st) {
   RouteFew p{};
   p.x = a.x;
   p.router = a.router;
@@ -253,7 +238,7 @@ cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewTokens
   const int smem = layout_of(M, E, p.how.k, p.width, p.slices).total * 4;
   return for_experts(E, [&](auto lanes, auto width) {
     constexpr int L = decltype(lanes)::value, V = decltype(width)::value;
-    auto* kernel = a.bits == 4 ? few_route_kernel<L, V, 4> : few_route_kernel<L, V, 8>;
+    auto* kernel = few_route_kernel<L, V>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;

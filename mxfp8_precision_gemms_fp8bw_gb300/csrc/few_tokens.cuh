@@ -1,0 +1,73 @@
+// Tokens as the products of a few of them read them: e4m3 codes in parts.
+#pragma once
+
+#include "few.h"
+#include "mx_fp32.cuh"
+
+namespace fp8bw {
+namespace few {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+// A block of 32 values is the sum of parts, each a block of MXFP8 codes under a
+// power of two of its own: the codes of the values, the codes of what those
+// leave, and so on.  e4m3 has 4 significant bits, so two parts hold the 8 bits
+// of bf16 exactly down to 2^-12 of the block's largest value, and to 2^-21 of
+// it below that; three hold 12 bits of fp32.  An infinity becomes a NaN, which
+// e4m3 has.
+__device__ __forceinline__ float without_infinity(float v) {
+  return fabsf(v) == INFINITY ? __uint_as_float(0x7FFFFFFFu) : v;
+}
+
+// E8M0 byte of a block's largest magnitude (as bits).
+__device__ __forceinline__ uint32_t part_byte(uint32_t top) { return min(max((top + 0x1FFFFFu) >> 23, 8u), 255u) - 8u; }
+__device__ __forceinline__ float part_factor(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }  // 2^-E
+
+// Eight consecutive bf16 values of a block that four neighbouring lanes hold, in kTokenParts parts: codes to to[part * pitch],
+// the block's bytes to scales[part * pitch / 32] (by the first of the four).
+__device__ __forceinline__ void split8(uint4 v, uint8_t* to, uint8_t* scales, int64_t pitch) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = without_infinity(bf16lo_to_f32(w[i]));
+    f[2 * i + 1] = without_infinity(bf16hi_to_f32(w[i]));
+  }
+#pragma unroll
+  for (int part = 0; part < kTokenParts; ++part) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(kAll, top, 1));
+    top = max(top, __shfl_xor_sync(kAll, top, 2));
+    const uint32_t byte = part_byte(top);
+    const float down = part_factor(byte), up = e8m0_value(byte);
+    uint2 q;
+    q.x = e4m3x4(f[0] * down, f[1] * down, f[2] * down, f[3] * down);
+    q.y = e4m3x4(f[4] * down, f[5] * down, f[6] * down, f[7] * down);
+    *reinterpret_cast<uint2*>(to + part * pitch) = q;
+    if ((threadIdx.x & 3) == 0) scales[part * (pitch / 32)] = static_cast<uint8_t>(byte);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 g = e4m3x2_to_f32((i < 2 ? q.x : q.y) >> (i & 1) * 16);
+      f[2 * i] -= g.x * up;
+      f[2 * i + 1] -= g.y * up;
+    }
+  }
+}
+
+// One fp32 value of a block that the warp holds, in kActParts parts.
+__device__ __forceinline__ void split1(float v, uint8_t* to, uint8_t* scales, int64_t pitch) {
+  v = without_infinity(v);
+#pragma unroll
+  for (int part = 0; part < kActParts; ++part) {
+    const uint32_t byte = part_byte(__reduce_max_sync(kAll, __float_as_uint(v) & 0x7FFFFFFFu));
+    const uint32_t q = cvt_e4m3x2(v * part_factor(byte), 0.f);
+    to[part * pitch] = static_cast<uint8_t>(q);
+    if ((threadIdx.x & 31) == 0) scales[part * (pitch / 32)] = static_cast<uint8_t>(byte);
+    v -= e4m3x2_to_f32(q).x * e8m0_value(byte);
+  }
+}
+
+}  // namespace few
+}  // namespace fp8bw

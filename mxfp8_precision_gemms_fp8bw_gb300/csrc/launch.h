@@ -191,6 +191,7 @@ struct FewLinearArgs {
   int64_t M, N, K;
   uint16_t* y;
   void* workspace;  // few_linear_workspace_bytes
+  int* status;
   int num_sms;
 };
 size_t few_linear_workspace_bytes(int64_t M, int64_t K);

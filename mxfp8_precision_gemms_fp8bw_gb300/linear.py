@@ -213,8 +213,8 @@ def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
 def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None) -> torch.Tensor:
     """y = x W^T in bf16 for 0 to 32 tokens x (bf16 [M, K]) and one matrix W
     [N, K] in MX codes, 4 bits (``mx4_quantize``) or 8 (the rowwise codes of
-    ``mx_quantize_experts``).  x is not quantized, and sums are fp32: a product
-    for decoding, bound by the bytes of W.  It has no gradient."""
+    ``mx_quantize_experts``).  x is not rounded to MXFP8, and sums are fp32: a
+    product for decoding, bound by the bytes of W.  It has no gradient."""
     _refuse_grad("mx_linear_few", x)
     q, e8, bits = _held(w)
     if q.dim() == 3 and q.shape[0] == 1:
@@ -222,12 +222,16 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     M, K = x.shape
     y = torch.empty((M, q.shape[0]), dtype=torch.bfloat16, device=x.device)
     if M > 0:
-        n = _few_linear_workspace(M, K)
-        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(n, dtype=torch.uint8, device=x.device) if n else None, stream)
+        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(_few_workspace(M, K), dtype=torch.uint8, device=x.device), stream)
     return y
 
 
-_few_linear_workspace = functools.lru_cache(maxsize=256)(FB.mx_few_linear_workspace_bytes)  # by the dims alone
+@functools.lru_cache(maxsize=256)
+def _few_workspace(M: int, K: int) -> int:
+    n = FB.mx_few_linear_workspace_bytes(M, K)
+    if n == 0:
+        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid dims of mx_linear_few: {M} tokens (at most {FB.FEW_TOKENS}) of {K} features")
+    return n
 
 
 # ------------------------------------------------------------------ preallocated step

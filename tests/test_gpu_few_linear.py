@@ -1,8 +1,10 @@
 """y = x W^T for a few tokens with MX weights, against the product in 64 bits.
 
 Bound of an element: products are exact in fp32 (8 bits times 4), K of them are summed with at most K roundings (or
-truncations) of 2^-23 of the sum of magnitudes; a token is held with 11 bits under a common exponent, which is exact for bf16
-down to 2^-38 of its largest element; and the result is rounded once to bf16, 2^-8 of it, or, below 2^-126, where bf16 values are
+truncations) of 2^-23 of the sum of magnitudes; a token is held in two parts of e4m3 in
+blocks of 32: the first leaves at most 1/14 of the block's largest element (half a step, 16, of more than 224), the second's
+power of two is thus at most 2^-11 of that element and its smallest step 2^-9 of its power of two, so that what is left of an
+element is nothing, or at most 2^-21 of the largest; and the result is rounded once to bf16, 2^-8 of it, or, below 2^-126, where bf16 values are
 2^-133 apart, 2^-134.
 """
 import numpy as np
@@ -47,8 +49,8 @@ def check(y, x, w, floor=0.0):
     W, xd = values(w), f32(x).astype(np.float64)
     K = xd.shape[1]
     want = xd @ W.T
-    top = np.abs(xd).max(axis=1, keepdims=True) + np.zeros_like(xd)
-    bound = BF16 * np.abs(want) + 2.0 ** -134 + 1.01 * (K * 2.0 ** -23 * (np.abs(xd) @ np.abs(W).T) + 2.0 ** -38 * (top @ np.abs(W).T)) + floor
+    top = np.repeat(np.abs(xd).reshape(len(xd), -1, 32).max(axis=2), 32, axis=1)
+    bound = BF16 * np.abs(want) + 2.0 ** -134 + 1.01 * (K * 2.0 ** -23 * (np.abs(xd) @ np.abs(W).T) + 2.0 ** -21 * (top @ np.abs(W).T)) + floor
     assert (np.abs(f32(y) - want) <= bound).all(), float((np.abs(f32(y) - want) / np.maximum(bound, 1e-300)).max())
 
 
@@ -112,7 +114,7 @@ def test_nan_and_infinity_stay_in_their_rows_and_columns(M, bits):
     want = L.mx_linear_few(x, w)
     x[1, 77], x[2, 300] = float("nan"), float("inf")
     y = L.mx_linear_few(x, w)
-    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[2]).any())
+    assert bool(torch.isnan(y[[1, 2]]).all())
     rest = [t for t in range(M) if t not in (1, 2)]
     assert torch.equal(y[rest], want[rest])
     e8 = L._held(w)[1]
@@ -157,10 +159,9 @@ def test_nothing_is_written_behind_the_result(M, N, K):
     x, w = inputs(M, N, K, 4)
     buf = torch.full((M * N + 512,), 3.0, dtype=torch.bfloat16, device="cuda")
     n = FB.mx_few_linear_workspace_bytes(M, K)
-    assert (n > 0) == (M == 32)
     for fill in (0x00, 0xFF):  # whatever was in the workspace before
         ws = torch.full((n + 256,), fill, dtype=torch.uint8, device="cuda")
-        FB.mx_few_linear(x, w.q, w.e8, 4, buf[:M * N].view(M, N), ws[:n] if n else None)
+        FB.mx_few_linear(x, w.q, w.e8, 4, buf[:M * N].view(M, N), ws[:n])
         assert bool((buf[M * N:] == 3.0).all()) and bool((ws[n:] == fill).all())
         check(buf[:M * N].view(M, N), x, w)
 
