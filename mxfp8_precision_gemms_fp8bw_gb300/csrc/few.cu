@@ -39,7 +39,6 @@ namespace cg = cooperative_groups;
 enum Mode { kLinear, kUp, kDown };
 
 constexpr int kRows = 128, kChunk = 128;
-constexpr int kDepth = 4;  // stages: chunks under way
 constexpr int kDrainWarps = 4, kWeightWarps = 4, kTokenWarps = 2;
 constexpr int kIssuer = kDrainWarps + kWeightWarps + kTokenWarps;
 constexpr int kThreads = (kIssuer + 1) * 32;
@@ -80,28 +79,30 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
-// 4 bytes, of which the last 4 - n become zeros without being read.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives on `bar` once the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Whether a wait came to its end for all lanes: they go on, or unwind, together.
 __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 
+constexpr int kMostDepth = 4;
 struct Shared {
-  uint64_t full[kDepth], empty[kDepth];  // a stage has landed, has been read
+  uint64_t full[kMostDepth], empty[kMostDepth];  // a stage has landed, has been read
   uint64_t sum_full[2], sum_empty[2];    // an accumulator is complete, has been drained
   uint64_t drain;
   uint32_t tmem;
   int abort;
   int list[32];       // kUp: the tokens of the columns
 };
+
+// Barrier 1, for the warps that use tensor memory.
+template <int kCount>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
+}
 
 // x [M, K] in parts.
 __global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restrict__ x, int64_t K, FewRows t) {
@@ -121,7 +122,7 @@ struct Place {
   int slot, c;
 };
 
-template <Mode kMode, int kBits>
+template <Mode kMode, int kBits, int kDepth>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ Product p) {
   constexpr int kParts = kMode == kDown ? kActParts : kTokenParts;
   constexpr int kRowBytes = 16 * kBits;  // of a chunk in memory
@@ -131,26 +132,23 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % p.splits, block = blockIdx.x / p.splits;
   const int K = p.m.K, chunks = (K + kChunk - 1) / kChunk;
-  float* const sums = reinterpret_cast<float*>(smem + kDepth * p.stage);  // [M][128]
+  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind.
+  float* const sums = reinterpret_cast<float*>(kMode == kDown ? smem + kDepth * p.stage : smem);
   FewSlot* const table = reinterpret_cast<FewSlot*>(sums + p.M * kRows);  // kDown
+  const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
 
-  if (warp == kIssuer) {
-    if (lane == 0) {
-      for (int s = 0; s < kDepth; ++s) {
-        mbar_init(&sh.full[s], kWeightWarps + kTokenWarps);
-        mbar_init(&sh.empty[s], 1);
-      }
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.sum_full[b], 1);
-        mbar_init(&sh.sum_empty[b], kDrainWarps);
-      }
-      mbar_init(&sh.drain, 1);
-      sh.abort = 0;
-      fence_mbar_init();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDepth; ++s) {
+      mbar_init(&sh.full[s], (kWeightWarps * (whole_words ? 1 : 2) + kTokenWarps) * 32);
+      mbar_init(&sh.empty[s], 1);
     }
-    __syncwarp();
-    tmem_alloc(&sh.tmem, p.tmem);
-    tmem_relinquish();
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.sum_full[b], 1);
+      mbar_init(&sh.sum_empty[b], kDrainWarps);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
   }
   // What the plan says.  The plan is older than the kernel before this one, which waited for it before it let this one
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
@@ -168,10 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = few_slot(p.plan, p.choices, i);
     for (int i = threadIdx.x; i < p.M * kRows; i += kThreads) sums[i] = 0.f;
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   const AbortFlag ab{&sh.abort};
   const auto slot_at = [&](int i) { return kMode == kDown ? table[i] : one; };
 
@@ -188,8 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int last = static_cast<int>(min((kMode == kUp ? p.m.rows / 2 : p.m.rows) - row0, static_cast<int64_t>(tile))) - 1;
   const uint32_t acc_columns = p.columns, scale_column = kMode == kDown ? 2 * acc_columns : acc_columns;
   const uint32_t stage0 = smem_u32(smem);
-  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128, token_scales_at = scales_at + kScales,
-                 raw_at = token_scales_at + kScales;
+  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128, token_scales_at = scales_at + kScales;
 
   if (warp >= kDrainWarps && warp < kDrainWarps + kWeightWarps) {
     // ------------------------------------------------------------ weights
@@ -206,50 +200,54 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const uint32_t to = (tid / 8) * 128 + ((piece ^ (tid / 8 & 7)) << 4);
     const int64_t scale_from = (row0 + row_of(tid)) * scale_pitch;
     const uint32_t scale_to = scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
-    const bool whole_words = (scale_pitch & 3) == 0;
 
-    const auto copy = [&](int t, uint32_t stage) {
+    // Where no word holds a row's four scale bytes: they come through registers, kDepth chunks ahead.
+    const auto scale_word = [&](int t) {
+      if (t >= t1) return 0u;
       const Place at = place_of(t);
-      const int64_t matrix = slot_at(at.slot).expert * p.m.rows;
-      const uint32_t off = at.c * kRowBytes;
-      const int64_t base = matrix * pitch + off;
-      if (off + piece * kPiece < pitch) {  // the last chunk of a row may be short
+      const int64_t s = slot_at(at.slot).expert * p.m.rows * scale_pitch + scale_from + at.c * 4, word = s & ~int64_t{3};
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
+      uint32_t lo = 0, hi = 0;
+      if (word + 8 <= p.m.scale_end) {
+        lo = __ldg(from), hi = __ldg(from + 1);
+      } else {  // the array's last bytes, one by one
+        for (int i = 0; i < 8 && word + i < p.m.scale_end; ++i)
+          (i < 4 ? lo : hi) |= static_cast<uint32_t>(p.m.e8[word + i]) << (i & 3) * 8;
+      }
+      return __funnelshift_r(lo, hi, (static_cast<uint32_t>(s) & 3) * 8);
+    };
+    uint32_t words[kDepth];
+    if (!whole_words)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) cp_async<kPiece>(stage + to + j * 2048, from[j] + base);
-      }
-      const int64_t s = matrix * scale_pitch + scale_from + at.c * 4;
-      if (whole_words) {
-        cp_async<4>(stage + scale_to, p.m.e8 + s);
-      } else {
-        // The two words that hold the row's four bytes; the last one no further than the array.
-        const int64_t word = s & ~int64_t{3}, left = p.m.scale_end - word;
-        cp_async4(stage + raw_at + tid * 8, p.m.e8 + word, static_cast<uint32_t>(left < 4 ? left : 4));
-        if (left > 4) cp_async4(stage + raw_at + tid * 8 + 4, p.m.e8 + word + 4, static_cast<uint32_t>(left < 8 ? left - 4 : 4));
-      }
-    };
-    const auto hand_over = [&](int t, int s) {
-      if (!whole_words) {
+      for (int s = 0; s < kDepth; ++s) words[s] = scale_word(t0 + s);
+
+    bool alive = true;
+    for (int i = 0; t0 + i < t1 && alive; i += kDepth) {
+#pragma unroll
+      for (int s = 0; s < kDepth; ++s) {
+        const int t = t0 + i + s;
+        if (t >= t1) break;
+        if (i > 0 && !all_of(mbar_wait(&sh.empty[s], (i / kDepth - 1) & 1, ab, p.status))) {
+          alive = false;
+          break;
+        }
         const uint32_t stage = stage0 + s * p.stage;
-        uint32_t lo, hi;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(stage + raw_at + tid * 8));
-        const int64_t at = slot_at(place_of(t).slot).expert * p.m.rows * scale_pitch + scale_from;
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to),
-                     "r"(__funnelshift_r(lo, hi, (static_cast<uint32_t>(at) & 3) * 8))
-                     : "memory");
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[s]);
-    };
-    for (int t = t0, i = 0; t < t1 + kDepth - 1; ++t, ++i) {
-      if (t < t1) {
-        if (i >= kDepth && !all_of(mbar_wait(&sh.empty[i % kDepth], (i / kDepth - 1) & 1, ab, p.status))) break;
-        copy(t, stage0 + i % kDepth * p.stage);
-      }
-      cp_async_commit();
-      if (i >= kDepth - 1) {
-        cp_async_wait<kDepth - 1>();
-        hand_over(t - (kDepth - 1), (i - (kDepth - 1)) % kDepth);
+        const Place at = place_of(t);
+        const int64_t matrix = slot_at(at.slot).expert * p.m.rows;
+        const uint32_t off = at.c * kRowBytes;
+        const int64_t base = matrix * pitch + off;
+        if (off + piece * kPiece < pitch) {  // the last chunk of a row may be short
+#pragma unroll
+          for (int j = 0; j < 8; ++j) cp_async<kPiece>(stage + to + j * 2048, from[j] + base);
+        }
+        if (whole_words) {
+          cp_async<4>(stage + scale_to, p.m.e8 + (matrix * scale_pitch + scale_from + at.c * 4));
+        } else {
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(words[s]) : "memory");
+          mbar_arrive(&sh.full[s]);
+          words[s] = scale_word(t + kDepth);
+        }
+        cp_async_arrive(&sh.full[s]);
       }
     }
     cp_async_wait_all();
@@ -258,36 +256,34 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     if (kMode != kUp) grid_wait();
     const int tid = threadIdx.x - (kDrainWarps + kWeightWarps) * 32;
     const int scale_pitch = static_cast<int>(p.t.pitch / 32);
-    for (int t = t0, i = 0; t < t1 + kDepth - 1; ++t, ++i) {
-      if (t < t1) {
-        if (i >= kDepth && !all_of(mbar_wait(&sh.empty[i % kDepth], (i / kDepth - 1) & 1, ab, p.status))) break;
-        const Place at = place_of(t);
-        const FewSlot s = slot_at(at.slot);
-        const uint32_t stage = stage0 + i % kDepth * p.stage;
-        const int n = s.n * kParts;
-        const auto row_of = [&](int r) {
-          return kMode == kUp ? sh.list[r / kParts] * kParts + r % kParts : s.start * kParts + r;
-        };
-        for (int j = tid; j < n * 8; j += kTokenWarps * 32) {
-          const int r = j >> 3;
-          cp_async<16>(stage + tokens_at + r * 128 + (((j & 7) ^ (r & 7)) << 4),
-                       p.t.codes + row_of(r) * p.t.pitch + at.c * 128 + (j & 7) * 16);
-        }
-        for (int r = tid; r < n; r += kTokenWarps * 32)
-          cp_async<4>(stage + token_scales_at + (r & 31) * 16 + (r >> 5) * 4,
-                      p.t.scales + static_cast<int64_t>(row_of(r)) * scale_pitch + at.c * 4);
+    for (int t = t0, i = 0; t < t1; ++t, ++i) {
+      if (i >= kDepth && !all_of(mbar_wait(&sh.empty[i % kDepth], (i / kDepth - 1) & 1, ab, p.status))) break;
+      const Place at = place_of(t);
+      const FewSlot s = slot_at(at.slot);
+      const uint32_t stage = stage0 + i % kDepth * p.stage;
+      const int n = s.n * kParts;
+      const auto row_of = [&](int r) {
+        return kMode == kUp ? sh.list[r / kParts] * kParts + r % kParts : s.start * kParts + r;
+      };
+      for (int j = tid; j < n * 8; j += kTokenWarps * 32) {
+        const int r = j >> 3;
+        cp_async<16>(stage + tokens_at + r * 128 + (((j & 7) ^ (r & 7)) << 4),
+                     p.t.codes + row_of(r) * p.t.pitch + at.c * 128 + (j & 7) * 16);
       }
-      cp_async_commit();
-      if (i >= kDepth - 1) {
-        cp_async_wait<kDepth - 1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[(i - (kDepth - 1)) % kDepth]);
-      }
+      for (int r = tid; r < n; r += kTokenWarps * 32)
+        cp_async<4>(stage + token_scales_at + (r & 31) * 16 + (r >> 5) * 4,
+                    p.t.scales + static_cast<int64_t>(row_of(r)) * scale_pitch + at.c * 4);
+      cp_async_arrive(&sh.full[i % kDepth]);
     }
     cp_async_wait_all();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
+    tmem_alloc(&sh.tmem, p.tmem);
+    tmem_relinquish();
+    tc_fence_before();
+    named_sync<(kDrainWarps + 1) * 32>();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
     if (lane == 0) {
       bool alive = true;
       int sum = 0;  // accumulators begun
@@ -304,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
           break;
         }
         tc_fence_after();
+        fence_proxy_async_smem();  // cp.async wrote what the tensor core reads
         const uint32_t stage = stage0 + i % kDepth * p.stage;
         const uint32_t sfa = tmem + scale_column + i % kDepth * 8, sfb = sfa + 4;
         tmem_cp_32x128b_warpx4(sfa, sdesc_plain_128b_rows(stage + scales_at));
@@ -328,6 +325,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums
+    named_sync<(kDrainWarps + 1) * 32>();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
     const int row = threadIdx.x;  // warps 0-3
     const float* weights = kMode == kDown ? few_weights(p.plan) : nullptr;
     int sum = 0;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   __syncthreads();
   if (warp == kIssuer) {
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem);
+    tmem_dealloc(sh.tmem, p.tmem);
   }
   if (idle) return;  // with its whole cluster
 
@@ -406,29 +406,25 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
 // ---------------------------------------------------------------- launches
 
-constexpr uint32_t kMostSmem = 227 * 1024 - 1024;
+// Shared memory of a block beside its fixed part, alone on an SM and as one of two: an SM has 228 KB, of which each block takes
+// 1 KB more than it asks for.
+constexpr uint32_t kMostSmem = 226 * 1024, kHalfSmem = 112 * 1024;
 
-// Blocks of a cluster for `tiles` row tiles over `chunks` chunks of contraction.
-int splits_of(int64_t tiles, int64_t chunks, int num_sms) {
-  int splits = 1;
-  while (splits < 8 && tiles * splits < 2 * num_sms && chunks >= 2 * (splits + 1)) ++splits;
-  return splits;
+// Blocks of a cluster for `tiles` row tiles over `chunks` chunks of contraction, with room for `slots` blocks at a time: the
+// fewest rounds of blocks, each of which costs about as much as six chunks besides its own.
+int splits_of(int64_t tiles, int64_t chunks, int64_t slots) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= 8 && s <= (chunks + 1) / 2; ++s) {
+    const int64_t cost = (tiles * s + slots - 1) / slots * ((chunks + s - 1) / s + 6);
+    if (cost < least) best = s, least = cost;
+  }
+  return best;
 }
 
-template <Mode kMode, int kBits>
-cudaError_t launch(Product p, int matrices, int copies, int num_sms, cudaStream_t st) {
-  const int parts = kMode == kDown ? kActParts : kTokenParts;
-  const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
-  const int64_t tiles = (rows + tile - 1) / tile;
-  p.splits = splits_of(tiles * copies, static_cast<int64_t>((p.m.K + kChunk - 1) / kChunk) * matrices, num_sms);
-  p.columns = (p.M + 15) / 16 * 16 * parts;
-  const uint32_t columns = (kMode == kDown ? 2 : 1) * p.columns + kDepth * 8;
-  p.tmem = 32;
-  while (p.tmem < columns) p.tmem *= 2;
-  const bool whole_words = p.m.K % 128 == 0;
-  p.stage = kCodes + p.columns * 128 + 2 * kScales + (whole_words ? 0 : 1024);
-  const uint32_t smem = 1024 + kDepth * p.stage + p.M * kRows * 4 + (kMode == kDown ? matrices * sizeof(FewSlot) : 0);
-  auto* kernel = few_kernel<kMode, kBits>;
+template <Mode kMode, int kBits, int kDepth>
+cudaError_t launch(const Product& p, uint32_t smem, dim3 grid, cudaStream_t st) {
+  auto* kernel = few_kernel<kMode, kBits, kDepth>;
   static thread_local bool allowed[64] = {};  // by device
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -439,7 +435,7 @@ cudaError_t launch(Product p, int matrices, int copies, int num_sms, cudaStream_
   }
   cudaLaunchAttribute attrs[2]{};
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -457,9 +453,31 @@ cudaError_t launch(Product p, int matrices, int copies, int num_sms, cudaStream_
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// matrices: how many lie behind each other along the contraction (kDown), copies: how many share the grid (kUp).
+template <Mode kMode, int kBits>
+cudaError_t launch_sized(Product p, int matrices, int copies, int num_sms, cudaStream_t st) {
+  const int parts = kMode == kDown ? kActParts : kTokenParts;
+  const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
+  const int64_t tiles = (rows + tile - 1) / tile;
+  p.columns = (p.M + 15) / 16 * 16 * parts;
+  const uint32_t columns = (kMode == kDown ? 2 : 1) * p.columns + kMostDepth * 8;
+  p.tmem = 32;
+  while (p.tmem < columns) p.tmem *= 2;
+  p.stage = kCodes + p.columns * 128 + 2 * kScales;
+  const uint32_t behind = kMode == kDown ? p.M * kRows * 4 + matrices * static_cast<uint32_t>(sizeof(FewSlot)) : 0;
+  const auto smem = [&](int depth) { return 1024 + depth * p.stage + behind; };
+  // Two blocks an SM, with three stages where four are too many for that.
+  const int depth = smem(4) > kHalfSmem && smem(3) <= kHalfSmem ? 3 : 4;
+  p.splits = splits_of(tiles * copies, static_cast<int64_t>((p.m.K + kChunk - 1) / kChunk) * matrices,
+                       num_sms * (smem(depth) <= kHalfSmem ? 2 : 1));
+  const dim3 grid(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
+  return depth == 3 ? launch<kMode, kBits, 3>(p, smem(3), grid, st) : launch<kMode, kBits, 4>(p, smem(4), grid, st);
+}
+
 template <Mode kMode>
 cudaError_t launch_product(const Product& p, int bits, int matrices, int copies, int num_sms, cudaStream_t st) {
-  return bits == 4 ? launch<kMode, 4>(p, matrices, copies, num_sms, st) : launch<kMode, 8>(p, matrices, copies, num_sms, st);
+  return bits == 4 ? launch_sized<kMode, 4>(p, matrices, copies, num_sms, st)
+                   : launch_sized<kMode, 8>(p, matrices, copies, num_sms, st);
 }
 
 }  // namespace
