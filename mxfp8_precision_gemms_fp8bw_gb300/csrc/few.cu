@@ -9,8 +9,6 @@
 // two or three parts (few_tokens.cuh) that are columns of their own.  (A
 // version that turned weights into f16 for mma.sync took 55 instructions for
 // 32 weights of 32 rows, 2 to 4 times the time that memory allows.)
-#include <cooperative_groups.h>
-
 #include "few.h"
 #include "few_tokens.cuh"
 #include "launch.h"
@@ -19,7 +17,6 @@ namespace fp8bw {
 namespace {
 
 using few::kAll;
-namespace cg = cooperative_groups;
 
 // A block owns 128 rows and walks through its share of the contraction in
 // chunks of 128; the `splits` blocks of a cluster have a share each, and their
@@ -59,6 +56,8 @@ struct Matrix {
 struct Product {
   Matrix m;
   int M, splits;
+  bool late;            // the cluster's sums meet in the stages
+  int slots;            // kDown: room for as many
   int columns;          // room for token rows in a stage: a multiple of 16
   uint32_t tmem;        // columns of tensor memory
   uint32_t stage;       // bytes
@@ -117,10 +116,23 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restr
               t.scales + row * (t.pitch / 32) + i / 4, t.pitch);
 }
 
-// Where a chunk of the block's list is: chunk `c` of the matrix of slot `slot`.
-struct Place {
-  int slot, c;
+// A stage of the ring, as each role walks through it: which, and the parity of its next completion.
+template <int kDepth>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kDepth) s = 0, phase ^= 1;
+  }
 };
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_remote(float* mine, int rank, float v) {  // to the same place of another block
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
 
 template <Mode kMode, int kBits, int kDepth>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ Product p) {
@@ -132,9 +144,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % p.splits, block = blockIdx.x / p.splits;
   const int K = p.m.K, chunks = (K + kChunk - 1) / kChunk;
-  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind.
+  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind, and behind them its slots.
+  // What the cluster's other blocks send: behind, or, where two blocks an SM need the room, over the stages too, once all of
+  // the cluster's blocks have read theirs.
   float* const sums = reinterpret_cast<float*>(kMode == kDown ? smem + kDepth * p.stage : smem);
-  FewSlot* const table = reinterpret_cast<FewSlot*>(sums + p.M * kRows);  // kDown
+  float* const behind = reinterpret_cast<float*>(smem + kDepth * p.stage) + (kMode == kDown ? p.M * kRows : 0);
+  FewSlot* const table = reinterpret_cast<FewSlot*>(behind);
+  float* const received = p.late ? reinterpret_cast<float*>(smem) + (kMode == kDown ? 0 : p.M * kRows)
+                                 : behind + (kMode == kDown ? p.slots * 4 : 0);
   const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
 
   if (threadIdx.x == 0) {
@@ -159,29 +176,29 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     grid_wait();
     grid_release();
     idle = static_cast<int>(blockIdx.y) >= few_active(p.plan);
-    if (!idle) one = few_slot(p.plan, p.choices, blockIdx.y);
+    one = few_slot(p.plan, p.choices, blockIdx.y);  // of an idle block: not read further
     if (warp == 0 && ((one.mask >> lane) & 1)) sh.list[__popc(one.mask & ((1u << lane) - 1))] = lane;
   } else if constexpr (kMode == kDown) {
     slots = few_active(p.plan);
     for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = few_slot(p.plan, p.choices, i);
     for (int i = threadIdx.x; i < p.M * kRows; i += kThreads) sums[i] = 0.f;
   }
+  if (idle) return;  // with its whole cluster
   __syncthreads();
+  if (p.splits > 1 && !p.late) cluster_arrive();  // the others may write to this block's memory once it runs
   const AbortFlag ab{&sh.abort};
   const auto slot_at = [&](int i) { return kMode == kDown ? table[i] : one; };
 
-  // The block's chunks: t0 .. t1 of all matrices', one behind the other.
-  const int64_t all = idle ? 0 : static_cast<int64_t>(slots) * chunks;
-  const int t0 = static_cast<int>(all * rank / p.splits), t1 = static_cast<int>(all * (rank + 1) / p.splits);
-  const auto place_of = [&](int t) {
-    const int slot = slots == 1 ? 0 : t / chunks;
-    return Place{slot, t - slot * chunks};
-  };
+  // The block's chunks: t0 .. t1 of all matrices', one behind the other; in runs of one matrix.
+  const int all = slots * chunks;
+  const int t0 = static_cast<int>(static_cast<int64_t>(all) * rank / p.splits);
+  const int t1 = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / p.splits);
+  const int slot0 = slots == 1 ? 0 : t0 / chunks, c0 = t0 - slot0 * chunks;
+  const auto run_of = [&](int c, int t) { return min(chunks - c, t1 - t); };  // chunks of the run that begins with chunk c
   // The block's first row in a matrix (kUp: of each half), and its last valid row.
   const int tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t row0 = static_cast<int64_t>(block) * tile;
   const int last = static_cast<int>(min((kMode == kUp ? p.m.rows / 2 : p.m.rows) - row0, static_cast<int64_t>(tile))) - 1;
-  const uint32_t acc_columns = p.columns, scale_column = kMode == kDown ? 2 * acc_columns : acc_columns;
   const uint32_t stage0 = smem_u32(smem);
   const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128, token_scales_at = scales_at + kScales;
 
@@ -191,89 +208,123 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const int tid = threadIdx.x - kDrainWarps * 32, piece = tid & 7;
     constexpr int kPiece = kRowBytes / 8;
     const uint32_t pitch = K / 8 * kBits, scale_pitch = K / 32;
-    const auto row_of = [&](int r) {  // in the block, of its matrix
-      return kMode == kUp ? min(r & 63, last) + (r >= 64 ? p.m.rows / 2 : 0) : static_cast<int64_t>(min(r, last));
-    };
-    const uint8_t* from[8];
+    const int64_t half = kMode == kUp ? p.m.rows / 2 : 0;  // from a row of gate to its row of up
+    uint32_t from[kMode == kUp ? 4 : 8];  // rows j of gate and j + 4 of up have the same offset
 #pragma unroll
-    for (int j = 0; j < 8; ++j) from[j] = p.m.w + (row0 + row_of(tid / 8 + 16 * j)) * pitch + piece * kPiece;
+    for (int j = 0; j < (kMode == kUp ? 4 : 8); ++j) from[j] = min(tid / 8 + 16 * j, last) * pitch + piece * kPiece;
     const uint32_t to = (tid / 8) * 128 + ((piece ^ (tid / 8 & 7)) << 4);
-    const int64_t scale_from = (row0 + row_of(tid)) * scale_pitch;
+    const int64_t scale_row = kMode == kUp ? min(tid & 63, last) + (tid >= 64 ? half : 0) : static_cast<int64_t>(min(tid, last));
     const uint32_t scale_to = scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
 
-    // Where no word holds a row's four scale bytes: they come through registers, kDepth chunks ahead.
-    const auto scale_word = [&](int t) {
-      if (t >= t1) return 0u;
-      const Place at = place_of(t);
-      const int64_t s = slot_at(at.slot).expert * p.m.rows * scale_pitch + scale_from + at.c * 4, word = s & ~int64_t{3};
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
+    // Where no word holds a row's four scale bytes: they come through registers, a chunk ahead.
+    const auto scale_word = [&](int64_t s) {
+      const int64_t word = s & ~int64_t{3};
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
       uint32_t lo = 0, hi = 0;
       if (word + 8 <= p.m.scale_end) {
-        lo = __ldg(from), hi = __ldg(from + 1);
+        lo = __ldg(at), hi = __ldg(at + 1);
       } else {  // the array's last bytes, one by one
+#pragma unroll 1
         for (int i = 0; i < 8 && word + i < p.m.scale_end; ++i)
           (i < 4 ? lo : hi) |= static_cast<uint32_t>(p.m.e8[word + i]) << (i & 3) * 8;
       }
       return __funnelshift_r(lo, hi, (static_cast<uint32_t>(s) & 3) * 8);
     };
-    uint32_t words[kDepth];
-    if (!whole_words)
-#pragma unroll
-      for (int s = 0; s < kDepth; ++s) words[s] = scale_word(t0 + s);
 
-    bool alive = true;
-    for (int i = 0; t0 + i < t1 && alive; i += kDepth) {
-#pragma unroll
-      for (int s = 0; s < kDepth; ++s) {
-        const int t = t0 + i + s;
-        if (t >= t1) break;
-        if (i > 0 && !all_of(mbar_wait(&sh.empty[s], (i / kDepth - 1) & 1, ab, p.status))) {
-          alive = false;
+    Ring<kDepth> ring;
+    bool refill = false;
+    int c = c0, slot = slot0;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++slot, c = 0) {
+      const int64_t first = slot_at(slot).expert * p.m.rows + row0;
+      const uint8_t* w = p.m.w + first * pitch + c * kRowBytes;
+      int64_t scale = (first + scale_row) * scale_pitch + c * 4;
+      uint32_t off = c * kRowBytes + piece * kPiece;
+      const int end = t + run_of(c, t);
+      uint32_t word = whole_words ? 0 : scale_word(scale);
+#pragma unroll 1
+      for (; t < end; ++t) {
+        if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
+          t = t1;
           break;
         }
-        const uint32_t stage = stage0 + s * p.stage;
-        const Place at = place_of(t);
-        const int64_t matrix = slot_at(at.slot).expert * p.m.rows;
-        const uint32_t off = at.c * kRowBytes;
-        const int64_t base = matrix * pitch + off;
-        if (off + piece * kPiece < pitch) {  // the last chunk of a row may be short
+        const uint32_t stage = stage0 + ring.s * p.stage;
+        if (off < pitch) {  // the last chunk of a row may be short
+          if constexpr (kMode == kUp) {
+            const uint8_t* up = w + half * pitch;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) cp_async<kPiece>(stage + to + j * 2048, from[j] + base);
+            for (int j = 0; j < 4; ++j) cp_async<kPiece>(stage + to + j * 2048, w + from[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async<kPiece>(stage + to + (j + 4) * 2048, up + from[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cp_async<kPiece>(stage + to + j * 2048, w + from[j]);
+          }
         }
         if (whole_words) {
-          cp_async<4>(stage + scale_to, p.m.e8 + (matrix * scale_pitch + scale_from + at.c * 4));
+          cp_async<4>(stage + scale_to, p.m.e8 + scale);
         } else {
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(words[s]) : "memory");
-          mbar_arrive(&sh.full[s]);
-          words[s] = scale_word(t + kDepth);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(word) : "memory");
+          mbar_arrive(&sh.full[ring.s]);
+          if (t + 1 < end) word = scale_word(scale + 4);
         }
-        cp_async_arrive(&sh.full[s]);
+        cp_async_arrive(&sh.full[ring.s]);
+        w += kRowBytes, off += kRowBytes, scale += 4;
+        ring.next();
+        refill |= ring.s == 0;
       }
     }
     cp_async_wait_all();
   } else if (warp >= kDrainWarps + kWeightWarps && warp < kIssuer) {
     // ------------------------------------------------------------ tokens
+    // Of a chunk a thread copies piece tid % 8 of rows tid / 8 + 8 j, and the scales of rows tid and tid + 64.
     if (kMode != kUp) grid_wait();
-    const int tid = threadIdx.x - (kDrainWarps + kWeightWarps) * 32;
-    const int scale_pitch = static_cast<int>(p.t.pitch / 32);
-    for (int t = t0, i = 0; t < t1; ++t, ++i) {
-      if (i >= kDepth && !all_of(mbar_wait(&sh.empty[i % kDepth], (i / kDepth - 1) & 1, ab, p.status))) break;
-      const Place at = place_of(t);
-      const FewSlot s = slot_at(at.slot);
-      const uint32_t stage = stage0 + i % kDepth * p.stage;
+    constexpr int kMostCopies = kFewTokens * kParts / 8;
+    const int tid = threadIdx.x - (kDrainWarps + kWeightWarps) * 32, piece = tid & 7;
+    const uint32_t pitch = static_cast<uint32_t>(p.t.pitch), scale_pitch = pitch / 32;
+    const uint32_t to = tokens_at + (tid >> 3) * 128 + ((piece ^ (tid >> 3)) << 4);
+    const uint32_t scale_to = token_scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
+    Ring<kDepth> ring;
+    bool refill = false;
+    int c = c0, slot = slot0;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++slot, c = 0) {
+      const FewSlot s = slot_at(slot);
       const int n = s.n * kParts;
       const auto row_of = [&](int r) {
-        return kMode == kUp ? sh.list[r / kParts] * kParts + r % kParts : s.start * kParts + r;
+        return static_cast<uint32_t>(kMode == kUp ? sh.list[r / kParts] * kParts + r % kParts : r);
       };
-      for (int j = tid; j < n * 8; j += kTokenWarps * 32) {
-        const int r = j >> 3;
-        cp_async<16>(stage + tokens_at + r * 128 + (((j & 7) ^ (r & 7)) << 4),
-                     p.t.codes + row_of(r) * p.t.pitch + at.c * 128 + (j & 7) * 16);
+      const int64_t start = static_cast<int64_t>(kMode == kDown ? s.start : 0) * kParts;
+      const uint8_t* codes = p.t.codes + start * pitch + c * 128 + piece * 16;
+      const uint8_t* scales = p.t.scales + start * scale_pitch + c * 4;
+      uint64_t from[kMode == kUp ? kMostCopies : 1];
+      if constexpr (kMode == kUp)
+#pragma unroll
+        for (int j = 0; j < kMostCopies; ++j) {
+          const int r = (tid >> 3) + 8 * j;
+          from[j] = r < n ? static_cast<uint64_t>(row_of(r)) * pitch : 0;
+        }
+      const int end = t + run_of(c, t);
+#pragma unroll 1
+      for (; t < end; ++t) {
+        if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
+          t = t1;
+          break;
+        }
+        const uint32_t stage = stage0 + ring.s * p.stage;
+#pragma unroll
+        for (int j = 0; j < kMostCopies; ++j) {
+          const int r = (tid >> 3) + 8 * j;
+          if (8 * j >= n) break;
+          if (r < n) cp_async<16>(stage + to + j * 1024, codes + (kMode == kUp ? from[j] : static_cast<uint64_t>(r) * pitch));
+        }
+        for (int r = tid, j = 0; r < n; r += 64, ++j)
+          cp_async<4>(stage + scale_to + j * 8, scales + static_cast<uint64_t>(row_of(r)) * scale_pitch);
+        cp_async_arrive(&sh.full[ring.s]);
+        codes += 128, scales += 4;
+        ring.next();
+        refill |= ring.s == 0;
       }
-      for (int r = tid; r < n; r += kTokenWarps * 32)
-        cp_async<4>(stage + token_scales_at + (r & 31) * 16 + (r >> 5) * 4,
-                    p.t.scales + static_cast<int64_t>(row_of(r)) * scale_pitch + at.c * 4);
-      cp_async_arrive(&sh.full[i % kDepth]);
     }
     cp_async_wait_all();
   } else if (warp == kIssuer) {
@@ -286,41 +337,51 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const uint32_t tmem = sh.tmem;
     if (lane == 0) {
       bool alive = true;
-      int sum = 0;  // accumulators begun
-      for (int t = t0, i = 0; t < t1; ++t, ++i) {
-        const Place at = place_of(t);
-        const bool first = t == t0 || at.c == 0, end = t + 1 == t1 || at.c + 1 == chunks;
+      Ring<kDepth> ring;
+      const uint32_t acc_columns = p.columns, sf0 = tmem + (kMode == kDown ? 2 : 1) * acc_columns;
+      const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(stage0 + tokens_at);
+      const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + token_scales_at);
+      int c = c0, slot = slot0, sum = 0;
+#pragma unroll 1
+      for (int t = t0; t < t1 && alive; ++slot, c = 0, ++sum) {
         const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * acc_columns : 0);
-        if (kMode == kDown && first && sum >= 2 && !mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status)) {
+        if (kMode == kDown && sum >= 2 && !mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status)) {
           alive = false;
           break;
         }
-        if (!mbar_wait(&sh.full[i % kDepth], (i / kDepth) & 1, ab, p.status)) {
-          alive = false;
-          break;
-        }
-        tc_fence_after();
-        fence_proxy_async_smem();  // cp.async wrote what the tensor core reads
-        const uint32_t stage = stage0 + i % kDepth * p.stage;
-        const uint32_t sfa = tmem + scale_column + i % kDepth * 8, sfb = sfa + 4;
-        tmem_cp_32x128b_warpx4(sfa, sdesc_plain_128b_rows(stage + scales_at));
-        tmem_cp_32x128b_warpx4(sfb, sdesc_plain_128b_rows(stage + token_scales_at));
-        const uint64_t a = sdesc_kmajor_sw128(stage), b = sdesc_kmajor_sw128(stage + tokens_at);
-        const int N = (slot_at(at.slot).n * kParts + 15) & ~15;
+        const uint32_t N = (slot_at(slot).n * kParts + 15) & ~15;
         const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
-        const int blocks = min(4, K / 32 - at.c * 4);
-        for (int j = 0; j < blocks; ++j)
-          mma_mx_e4m3(acc, a + 2 * j, b + 2 * j, kind | idesc_mx_e4m3(0, 0, j, j), sfa, sfb, !first || j > 0);
-        mma_commit(&sh.empty[i % kDepth]);
-        if (end) {
-          mma_commit(&sh.sum_full[sum & 1]);
-          ++sum;
+        const int end = t + run_of(c, t);
+        int left = K / 32 - c * 4;  // blocks of 32
+        uint32_t first = 1;
+#pragma unroll 1
+        for (; t < end; ++t, left -= 4) {
+          if (!mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          fence_proxy_async_smem();  // cp.async wrote what the tensor core reads
+          const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+          const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
+          tmem_cp_32x128b_warpx4(sfa, sa0 + stage);
+          tmem_cp_32x128b_warpx4(sfb, sb0 + stage);
+          const uint64_t a = a0 + stage, b = b0 + stage;
+          mma_mx_e4m3(acc, a, b, kind, sfa, sfb, first ^ 1);
+          first = 0;
+          if (left > 1) mma_mx_e4m3(acc, a + 2, b + 2, kind | idesc_mx_e4m3(0, 0, 1, 1), sfa, sfb, 1);
+          if (left > 2) mma_mx_e4m3(acc, a + 4, b + 4, kind | idesc_mx_e4m3(0, 0, 2, 2), sfa, sfb, 1);
+          if (left > 3) mma_mx_e4m3(acc, a + 6, b + 6, kind | idesc_mx_e4m3(0, 0, 3, 3), sfa, sfb, 1);
+          mma_commit(&sh.empty[ring.s]);
+          ring.next();
         }
+        mma_commit(&sh.sum_full[sum & 1]);
       }
-      // Nothing may be under way when tensor memory is given back.
-      mma_commit(&sh.drain);
-      int none = 0;
-      mbar_wait(&sh.drain, 0, AbortFlag{&none}, p.status, alive ? kWaitLimitNs : 1000000ull);
+      if (!alive) {  // nothing may be under way when tensor memory is given back
+        mma_commit(&sh.drain);
+        int none = 0;
+        mbar_wait(&sh.drain, 0, AbortFlag{&none}, p.status, 1000000ull);
+      }
     }
     __syncwarp();
   } else {
@@ -330,15 +391,16 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const uint32_t tmem = sh.tmem;
     const int row = threadIdx.x;  // warps 0-3
     const float* weights = kMode == kDown ? few_weights(p.plan) : nullptr;
-    int sum = 0;
-    for (int t = t0; t < t1; ++sum) {
-      const Place at = place_of(t);
-      const FewSlot s = slot_at(at.slot);
-      t += min(chunks - at.c, t1 - t);
+    int c = c0, slot = slot0, sum = 0;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++slot, c = 0, ++sum) {
+      const FewSlot s = slot_at(slot);
+      t += run_of(c, t);
       if (!all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * acc_columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
+      const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
       uint32_t mask = s.mask;
+#pragma unroll 1
       for (int n0 = 0; n0 < s.n; n0 += 16) {  // 16 tokens at a time
         uint32_t v[kParts][16];
 #pragma unroll
@@ -362,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sum_empty[sum & 1]);
     }
-    if (kMode != kDown && t0 == t1 && !idle)  // no share of a short contraction
+    if (kMode != kDown && t0 == t1)  // no share of a short contraction
       for (int i = 0; i < one.n; ++i) sums[i * kRows + row] = 0.f;
   }
   tc_fence_before();
@@ -371,37 +433,50 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     tc_fence_after();
     tmem_dealloc(sh.tmem, p.tmem);
   }
-  if (idle) return;  // with its whole cluster
 
-  // The sums of the cluster's blocks.
-  const int n = kMode == kUp ? one.n : p.M;
-  cg::cluster_group cluster = cg::this_cluster();
-  if (p.splits > 1) cluster.sync();
-  const auto total = [&](int token, int row) {
-    if (p.splits == 1) return sums[token * kRows + row];
-    float v = 0.f;
-    for (int r = 0; r < p.splits; ++r) v += cluster.map_shared_rank(sums, r)[token * kRows + row];
-    return v;
+  // The sums of the cluster's blocks.  Block r of them brings home items r, r + splits, ...: for each the others send theirs,
+  // item i of block q to received[i / splits * splits + q].  An item: 32 rows of a token (kUp: of gate and of up).
+  constexpr int kItemRows = kMode == kUp ? 64 : 32, kItems = kRows / kItemRows;  // of a token
+  const int items = (kMode == kUp ? one.n : p.M) * kItems;
+  const auto value_of = [&](int item, int h) {  // row `lane` of its half h
+    const int token = item / kItems, i = item % kItems;
+    return sums[token * kRows + i * 32 + h * 64 + lane];
   };
-  if constexpr (kMode == kUp) {
-    // A warp per token and block of 32 of the activation.
-    for (int i = rank * (kIssuer + 1) + warp; i < n * 2; i += p.splits * (kIssuer + 1)) {
-      const int token = i >> 1, half = i & 1;
-      const int64_t f = row0 + half * 32;
-      if (f >= p.m.rows / 2) continue;
-      const float gate = total(token, half * 32 + lane), up = total(token, 64 + half * 32 + lane);
-      const int64_t r = static_cast<int64_t>(one.start + token) * kActParts;
-      few::split1(gate / (1.f + expf(-gate)) * up, p.act.codes + r * p.act.pitch + f + lane,
-                  p.act.scales + r * (p.act.pitch / 32) + f / 32, p.act.pitch);
+  constexpr int kHalves = kItemRows / 32;
+  if (p.splits > 1) {
+    if (p.late) cluster_arrive();
+    cluster_wait();
+    for (int item = warp; item < items; item += kIssuer + 1) {
+      const int home = item % p.splits;
+      if (home == rank) continue;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        store_remote(received + ((item / p.splits * p.splits + rank) * kHalves + h) * 32 + lane, home, value_of(item, h));
     }
-  } else {
-    for (int i = rank * kThreads + threadIdx.x; i < n * kRows; i += p.splits * kThreads) {
-      const int token = i / kRows, row = i % kRows;
-      if (row <= last)
-        p.y[token * p.m.rows + row0 + row] = static_cast<uint16_t>(pack_bf16x2(total(token, row), 0.f) & 0xFFFFu);
+    cluster_arrive();
+    cluster_wait();
+  }
+  for (int item = rank + warp * p.splits; item < items; item += (kIssuer + 1) * p.splits) {
+    float v[kHalves];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      v[h] = p.splits == 1 ? value_of(item, h) : 0.f;
+      if (p.splits > 1)
+        for (int q = 0; q < p.splits; ++q)
+          v[h] += q == rank ? value_of(item, h) : received[((item / p.splits * p.splits + q) * kHalves + h) * 32 + lane];
+    }
+    const int token = item / kItems, i = item % kItems;
+    if constexpr (kMode == kUp) {
+      const int64_t f = row0 + i * 32;
+      if (f >= p.m.rows / 2) continue;
+      const int64_t r = static_cast<int64_t>(one.start + token) * kActParts;
+      few::split1(v[0] / (1.f + expf(-v[0])) * v[1], p.act.codes + r * p.act.pitch + f + lane,
+                  p.act.scales + r * (p.act.pitch / 32) + f / 32, p.act.pitch);
+    } else {
+      const int row = i * 32 + lane;
+      if (row <= last) p.y[token * p.m.rows + row0 + row] = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
     }
   }
-  if (p.splits > 1) cluster.sync();  // a block's shared memory is read until then
 }
 
 // ---------------------------------------------------------------- launches
@@ -464,7 +539,12 @@ cudaError_t launch_sized(Product p, int matrices, int copies, int num_sms, cudaS
   p.tmem = 32;
   while (p.tmem < columns) p.tmem *= 2;
   p.stage = kCodes + p.columns * 128 + 2 * kScales;
-  const uint32_t behind = kMode == kDown ? p.M * kRows * 4 + matrices * static_cast<uint32_t>(sizeof(FewSlot)) : 0;
+  // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
+  const uint32_t received = (p.M * kRows + 7 * 64) * 4;
+  p.late = p.M > 16;
+  p.slots = matrices;
+  const uint32_t behind = (p.late ? 0 : received) +
+                          (kMode == kDown ? p.M * kRows * 4 + matrices * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
   const auto smem = [&](int depth) { return 1024 + depth * p.stage + behind; };
   // Two blocks an SM, with three stages where four are too many for that.
   const int depth = smem(4) > kHalfSmem && smem(3) <= kHalfSmem ? 3 : 4;

@@ -1,7 +1,5 @@
 // The first kernel of the mixture-of-experts layer for a few tokens: router
 // logits, the choice of experts, and the plan of the products.
-#include <cooperative_groups.h>
-
 #include "few.h"
 #include "few_tokens.cuh"
 #include "route_row.cuh"
@@ -9,18 +7,21 @@
 namespace fp8bw {
 namespace {
 
-namespace cg = cooperative_groups;
-
-// One cluster.  Each block takes a share of the features: its warps, four
-// experts and eight tokens at a time, multiply fp32 router rows with tokens in
-// shared memory, so that the router is read once, by all blocks together.
-// (Where that is fewer than 16 pieces of work, warps share the features too.)
-// The shares of a token's logits then meet in one block (distributed shared
-// memory, in the order of the blocks), which makes the choice as fp8bw_moe_route
-// does; and the first block sorts the choices.  An expert's tokens are a
-// 32-bit mask, whose bits below a token give its place.
+// One cluster of eight blocks, a few microseconds of latencies: the kernel runs
+// once through its code, which is kept short (instructions come from memory
+// too), and blocks send each other what they have rather than fetch it.
+//
+//   1. Each block takes an eighth of the features.  A warp takes four experts
+//      and eight tokens at a time (where that is fewer than 16 pieces of work,
+//      warps share the features as well), and sends each logit's share to the
+//      block that makes the token's choice.
+//   2. Block r adds up the shares of tokens r, r + 8, .. in the order of the
+//      blocks, and a warp chooses for each, as fp8bw_moe_route does, while the
+//      others bring the tokens into e4m3 for the first product.
+//   3. The first block sorts the choices.  An expert's tokens are a 32-bit mask,
+//      whose bits below a token give its place.
 constexpr int kBlocks = 8, kWarps = 16, kThreads = kWarps * 32;
-constexpr int kMostRows = kFewTokens / kBlocks;  // tokens whose choice a block makes
+constexpr int kMostRows = kFewTokens / kBlocks;  // tokens of a block
 
 struct RouteFew {
   const uint16_t* x;
@@ -28,28 +29,32 @@ struct RouteFew {
   const float* bias;
   RouteShape how;  // M rows
   int C, share;    // features, and of a block: a multiple of 8
-  int width;       // features in shared memory at a time: a multiple of 128
   int slices;      // warps that share four experts and eight tokens
   FewPlan* plan;
   FewRows held;    // the tokens as the first product reads them
 };
 
-struct Layout {  // floats of shared memory
-  int tokens, partial, logits, staged, experts, weights, all_experts, all_weights, masks, starts, total;
+// A power of two, at least 32, that E is not above.
+__host__ __device__ inline int padded(int E) {
+  int P = 32;
+  while (P < E) P *= 2;
+  return P;
+}
+
+struct Layout {  // words of shared memory
+  int partial, received, scores, keys, experts, weights, masks, starts, total;
 };
-__host__ __device__ inline Layout layout_of(int M, int E, int k, int width, int slices) {
+__host__ __device__ inline Layout layout_of(int M, int E, int k, int slices) {
   Layout l{};
-  l.tokens = 0;
-  l.partial = M * width / 2;  // bf16
-  l.logits = l.partial + slices * M * E;
-  l.staged = l.logits + kMostRows * E;
-  l.experts = l.staged + kMostRows * (E | 8);
-  l.weights = l.experts + kMostRows * k;
-  l.all_experts = l.weights + kMostRows * k;
-  l.all_weights = l.all_experts + M * k;
-  l.masks = l.all_weights + M * k;
+  l.partial = 0;
+  l.received = slices > 1 ? slices * M * E : 0;  // [rows][blocks][E]
+  l.scores = l.received + kMostRows * kBlocks * E;
+  l.keys = l.scores + kMostRows * E;
+  l.experts = l.keys + kMostRows * padded(E);    // first the exponentials that are summed up
+  l.weights = l.experts + M * k;
+  l.masks = l.weights + M * k;
   l.starts = l.masks + E;
-  l.total = l.starts + E + 32;
+  l.total = l.starts + E;
   return l;
 }
 
@@ -68,151 +73,238 @@ __device__ __forceinline__ float sum_each(float (&v)[32]) {
   return v[0];
 }
 
-template <int L, int V>
+__device__ __forceinline__ void store_remote(uint32_t mine, int rank, uint32_t v) {  // to the same place of another block
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The choice of one row by a warp: the rule, the keys and the scores of
+// route_row, bit for bit (the softmax's sum by halves of the row's indexes),
+// with the row in shared memory.  s: logits, then scores; key: P words.
+// Lane c < k returns choice c and the sum over all choices' scores.
+struct Choice {
+  int expert;
+  float score, sum;
+};
+__device__ Choice choose_row(float* s, uint32_t* key, const float* __restrict__ bias, const RouteShape& p) {
+  const int lane = threadIdx.x & 31, E = p.E;
+  float top = -INFINITY;
+  for (int e = lane; e < E; e += 32) top = fmaxf(top, s[e]);
+  uint32_t masked = 0;  // of the lane's experts, those whose logit is -inf
+  for (int e = lane, i = 0; e < E; e += 32, ++i) masked |= s[e] == -INFINITY ? 1u << i : 0u;
+  if (p.score == 0) {
+    top = lanes_reduce<32>(top, [](float a, float b) { return fmaxf(a, b); });
+    if (top == -INFINITY) top = 0.f;
+    float* part = reinterpret_cast<float*>(key);
+    const int P = padded(E);
+    for (int e = lane; e < P; e += 32) part[e] = e < E ? expf(s[e] - top) : 0.f;
+    for (int e = lane; e < E; e += 32) s[e] = part[e];
+    for (int h = P / 2; h >= 32; h /= 2)  // a lane adds what it wrote itself
+      for (int e = lane; e < h; e += 32) part[e] += part[e + h];
+    float total = lanes_sum<32>(part[lane]);
+    if (total == 0.f) total = 1.f;
+    for (int e = lane; e < E; e += 32) s[e] = __fdiv_rn(s[e], total);
+  } else {
+    for (int e = lane; e < E; e += 32) s[e] = sigmoid_of(s[e]);
+  }
+  for (int e = lane, i = 0; e < E; e += 32, ++i) {
+    const float b = bias != nullptr ? bias[e] : 0.f;
+    key[e] = ((masked >> i) & 1) || b == -INFINITY ? 0u : ordered(s[e] + b);
+  }
+  __syncwarp();
+  if (p.groups > 1) {
+    const int size = E / p.groups;
+    uint32_t total = 0;
+    if (lane < p.groups) {
+      uint32_t best = 0, second = 0;
+      for (int i = 0; i < size; ++i) {
+        const uint32_t u = key[lane * size + i];
+        second = max(second, min(best, u));
+        best = max(best, u);
+      }
+      total = best;
+      if (p.group_top == 2 && second != 0) {
+        const float sum = unordered(best) + unordered(second);
+        total = ordered(sum < kLowest ? kLowest : sum);
+      }
+    }
+    int before = 0;  // groups that come first
+    for (int g = 0; g < p.groups; ++g) {
+      const uint32_t other = __shfl_sync(kAll, total, g);
+      before += other > total || (other == total && g < lane);
+    }
+    const uint32_t kept = __ballot_sync(kAll, lane < p.groups && total != 0 && before < p.kept);
+    for (int e = lane; e < E; e += 32)
+      if (!((kept >> (e / size)) & 1)) key[e] = 0;
+  }
+  Choice mine{-1, 0.f, 0.f};
+  uint32_t best = 0;  // of the lane's keys
+  int at = 0;
+  for (int e = lane; e < E; e += 32)
+    if (key[e] > best) best = key[e], at = e;
+#pragma unroll 1
+  for (int c = 0; c < p.k; ++c) {
+    const uint32_t most = __reduce_max_sync(kAll, best);
+    if (most == 0) break;
+    const int e = __reduce_min_sync(kAll, best == most ? at : E);
+    if (lane == c) mine.expert = e;
+    if (best == most && at == e) {
+      key[e] = 0;
+      best = 0;
+      for (int i = lane; i < E; i += 32)
+        if (key[i] > best) best = key[i], at = i;
+    }
+  }
+  __syncwarp();
+  mine.score = mine.expert >= 0 ? s[mine.expert] : 0.f;
+  mine.sum = lanes_sum<32>(mine.score);
+  return mine;
+}
+
 __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_constant__ RouteFew p) {
   extern __shared__ __align__(16) float smem[];
-  cg::cluster_group cluster = cg::this_cluster();
   const int M = static_cast<int>(p.how.M), E = p.how.E, k = p.how.k;
   const int rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout at = layout_of(M, E, k, p.width, p.slices);
+  const Layout at = layout_of(M, E, k, p.slices);
   asm volatile("griddepcontrol.launch_dependents;");  // they wait for this kernel's end before they read the plan
+  cluster_arrive();  // blocks may write to each other's memory once they run
 
-  // Logits of this block's features.
-  uint2* const tokens = reinterpret_cast<uint2*>(smem + at.tokens);  // four bf16 each
-  float* const partial = smem + at.partial;
+  // 1. Logits.
+  uint32_t* const received = reinterpret_cast<uint32_t*>(smem + at.received);
+  const auto send = [&](int t, int e, float v) {
+    store_remote(smem_u32(received + (t / kBlocks * kBlocks + rank) * E + e), t % kBlocks, __float_as_uint(v));
+  };
   const int first = rank * p.share, last = min(first + p.share, p.C);
   const int tiles = (M + 7) / 8, work = (E + 3) / 4 * tiles * p.slices;
-  const int steps = max((last - first + p.width - 1) / p.width, 1);
-  for (int s = 0; s < steps; ++s) {
-    const int c0 = first + s * p.width, n = min(p.width, max(last - c0, 0));  // n: a multiple of 8
-    if (s > 0) __syncthreads();
-    for (int t = warp; t < M; t += kWarps)
-      for (int c = lane * 8; c < n; c += 256)
-        *reinterpret_cast<uint4*>(tokens + (t * p.width + c) / 4) =
-            __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.C + c0 + c));
-    __syncthreads();
-    for (int w = warp; w < work; w += kWarps) {
-      const int slice = w % p.slices, t0 = w / p.slices % tiles * 8, e0 = w / p.slices / tiles * 4;
-      float v[32];
+  bool together = false;
+#pragma unroll 1
+  for (int w = warp; w < work; w += kWarps) {
+    const int slice = w % p.slices, t0 = w / p.slices % tiles * 8, e0 = w / p.slices / tiles * 4;
+    float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 2
-      for (int c = slice * 128 + lane * 4; c < n; c += p.slices * 128) {
-        float4 r[4];
+    for (int c = first + slice * 128 + lane * 4; c < last; c += p.slices * 128) {
+      float4 r[4];
+      uint2 x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = __ldg(reinterpret_cast<const float4*>(p.router + static_cast<int64_t>(min(e0 + i, E - 1)) * p.C + c));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (t0 + j < M) x[j] = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t0 + j) * p.C + c));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (t0 + j >= M) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          r[i] = e0 + i < E ? __ldg(reinterpret_cast<const float4*>(p.router + static_cast<int64_t>(e0 + i) * p.C + c0 + c))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (t0 + j >= M) break;
-          const uint2 x = tokens[((t0 + j) * p.width + c) / 4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i * 8 + j] = fmaf(r[i].x, bf16lo_to_f32(x.x),
-                                fmaf(r[i].y, bf16hi_to_f32(x.x),
-                                     fmaf(r[i].z, bf16lo_to_f32(x.y), fmaf(r[i].w, bf16hi_to_f32(x.y), v[i * 8 + j]))));
-        }
-      }
-      const float sum = sum_each(v);
-      const int e = e0 + lane / 8, t = t0 + lane % 8;
-      if (e < E && t < M) {
-        float* to = partial + (slice * M + t) * E + e;
-        *to = s > 0 ? *to + sum : sum;
+          v[i * 8 + j] = fmaf(r[i].x, bf16lo_to_f32(x[j].x),
+                              fmaf(r[i].y, bf16hi_to_f32(x[j].x),
+                                   fmaf(r[i].z, bf16lo_to_f32(x[j].y), fmaf(r[i].w, bf16hi_to_f32(x[j].y), v[i * 8 + j]))));
       }
     }
+    const float sum = sum_each(v);
+    const int e = e0 + lane / 8, t = t0 + lane % 8;
+    if (p.slices > 1) {
+      if (e < E && t < M) smem[at.partial + (slice * M + t) * E + e] = sum;
+      continue;
+    }
+    if (!together) cluster_wait();  // all blocks run
+    together = true;
+    if (e < E && t < M) send(t, e, sum);
+    __syncwarp();
   }
-  cluster.sync();
+  if (!together) cluster_wait();
+  if (p.slices > 1) {
+    __syncthreads();
+    for (int i = tid; i < M * E; i += kThreads) {
+      float sum = 0.f;
+      for (int s = 0; s < p.slices; ++s) sum += smem[at.partial + s * M * E + i];
+      send(i / E, i % E, sum);
+    }
+    __syncwarp();
+  }
+  cluster_arrive();
+  cluster_wait();
 
-  // The choice for tokens rank, rank + kBlocks, ...
+  // 2. The choice for tokens rank, rank + kBlocks, ..: a warp each.
   const int rows = rank < M ? (M - rank + kBlocks - 1) / kBlocks : 0;
-  float* const logits = smem + at.logits;
-  for (int i = tid; i < rows * E; i += kThreads) {
-    const int row = i / E, e = i - row * E;
-    float sum = 0.f;
-    for (int b = 0; b < kBlocks; ++b) {
-      const float* from = cluster.map_shared_rank(partial, b) + (rank + row * kBlocks) * E + e;
-      for (int s = 0; s < p.slices; ++s) sum += from[s * M * E];
+  uint32_t* const experts = reinterpret_cast<uint32_t*>(smem + at.experts);
+  uint32_t* const weights = reinterpret_cast<uint32_t*>(smem + at.weights);
+  if (warp < rows) {
+    float* const s = smem + at.scores + warp * E;
+    for (int e = lane; e < E; e += 32) {
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) sum += __uint_as_float(received[(warp * kBlocks + b) * E + e]);
+      s[e] = sum;
     }
-    logits[i] = sum;
-  }
-  __syncthreads();
-  int32_t* const experts = reinterpret_cast<int32_t*>(smem + at.experts);
-  float* const weights = smem + at.weights;
-  constexpr int kChoosers = L == 8 ? 1 : kMostRows;  // warps that choose; the others bring the tokens into e4m3
-  if (warp >= kChoosers) {
+    const Choice c = choose_row(s, reinterpret_cast<uint32_t*>(smem + at.keys) + warp * padded(E), p.bias, p.how);
+    if (lane < k) {
+      const float w = (p.how.renorm ? c.score / (c.sum + 1e-20f) : c.score) * p.how.scale;
+      const int entry = (rank + warp * kBlocks) * k + lane;
+      store_remote(smem_u32(experts + entry), 0, static_cast<uint32_t>(c.expert));
+      store_remote(smem_u32(weights + entry), 0, __float_as_uint(c.expert >= 0 ? w : 0.f));
+    }
+  } else if (warp >= kMostRows) {
     const int pieces = p.C / 8;  // of 8 values
+#pragma unroll 1
     for (int r = 0; r < rows; ++r) {
       const int64_t t = rank + r * kBlocks;
       const uint4* row = reinterpret_cast<const uint4*>(p.x + t * p.C);
       uint8_t* to = p.held.codes + t * kTokenParts * p.held.pitch;
       uint8_t* scales = p.held.scales + t * kTokenParts * (p.held.pitch / 32);
-#pragma unroll 2
-      for (int i0 = (warp - kChoosers) * 32; i0 < pieces; i0 += (kWarps - kChoosers) * 32) {
+#pragma unroll 1
+      for (int i0 = (warp - kMostRows) * 32; i0 < pieces; i0 += (kWarps - kMostRows) * 32) {
         const int i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
         few::split8(__ldg(row + i), to + i * 8, scales + i / 4, p.held.pitch);
       }
     }
-  } else if (warp * (32 / L) < rows) {
-    const int row = tid / L;
-    route_row<float, L, V>(logits, p.bias, p.how, row, row < rows, row, reinterpret_cast<uint32_t*>(smem + at.staged), experts,
-                           weights);
   }
-  __syncthreads();
-  {
-    int32_t* to = cluster.map_shared_rank(reinterpret_cast<int32_t*>(smem + at.all_experts), 0);
-    float* tow = cluster.map_shared_rank(smem + at.all_weights, 0);
-    for (int i = tid; i < rows * k; i += kThreads) {
-      const int entry = (rank + i / k * kBlocks) * k + i % k;
-      to[entry] = experts[i];
-      tow[entry] = weights[i];
-    }
-  }
-  cluster.sync();
+  __syncwarp();
+  cluster_arrive();
   if (rank != 0) return;
-
-  // The plan.
   uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + at.masks);
-  int* const starts = reinterpret_cast<int*>(smem + at.starts);
-  int* const sums = starts + E;
-  const int32_t* chosen = reinterpret_cast<const int32_t*>(smem + at.all_experts);
-  const float* given = smem + at.all_weights;
   for (int e = tid; e < E; e += kThreads) masks[e] = 0;
+  cluster_wait();
   __syncthreads();
+
+  // 3. The plan.
+  int* const starts = reinterpret_cast<int*>(smem + at.starts);
   for (int i = tid; i < M * k; i += kThreads)
-    if (chosen[i] >= 0) atomicOr(masks + chosen[i], 1u << (i / k));
+    if (static_cast<int>(experts[i]) >= 0) atomicOr(masks + experts[i], 1u << (i / k));
   __syncthreads();
-  int before = 0;  // slots in the upper half word, choices in the lower
-  FewSlot* slots = few_slots(p.plan, M * k);
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const int e = e0 + tid;
-    const uint32_t mask = e < E ? masks[e] : 0;
-    const int mine = mask != 0 ? (1 << 16) | __popc(mask) : 0;
-    int up = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(kAll, up, o);
-      if (lane >= o) up += t;
+  if (warp == 0) {
+    FewSlot* slots = few_slots(p.plan, M * k);
+    int before = 0;  // slots in the upper half word, choices in the lower
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const uint32_t mask = e < E ? masks[e] : 0;
+      const int mine = mask != 0 ? (1 << 16) | __popc(mask) : 0;
+      int up = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(kAll, up, o);
+        if (lane >= o) up += t;
+      }
+      const int earlier = before + up - mine;
+      if (mask != 0) {
+        slots[earlier >> 16] = FewSlot{e, earlier & 0xFFFF, mask, __popc(mask)};
+        starts[e] = earlier & 0xFFFF;
+      }
+      before += __shfl_sync(kAll, up, 31);
     }
-    if (lane == 31) sums[warp] = up;
-    __syncthreads();
-    int all = 0, earlier = before;
-    for (int w = 0; w < kWarps; ++w) {
-      earlier += w < warp ? sums[w] : 0;
-      all += sums[w];
-    }
-    earlier += up - mine;
-    if (mask != 0) {
-      slots[earlier >> 16] = FewSlot{e, earlier & 0xFFFF, mask, __popc(mask)};
-      starts[e] = earlier & 0xFFFF;
-    }
-    before += all;
-    __syncthreads();
+    if (lane == 0) p.plan->active = before >> 16;
   }
-  if (tid == 0) p.plan->active = before >> 16;
+  __syncthreads();
   float* const out = few_weights(p.plan);
   for (int i = tid; i < M * k; i += kThreads) {
-    const int e = chosen[i];
-    if (e >= 0) out[starts[e] + __popc(masks[e] & ((1u << (i / k)) - 1))] = given[i];
+    const int e = static_cast<int>(experts[i]);
+    if (e >= 0) out[starts[e] + __popc(masks[e] & ((1u << (i / k)) - 1))] = __uint_as_float(weights[i]);
   }
 }
 
@@ -227,36 +319,33 @@ cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewRows& 
   p.C = static_cast<int>(a.C);
   p.share = (p.C + 8 * kBlocks - 1) / (8 * kBlocks) * 8;
   const int M = static_cast<int>(a.route.M), E = p.how.E;
-  // Tokens in shared memory: 64 KB, or 32 beside the logits of very many experts.
-  const int most = (M * E <= 16384 ? 32768 : 16384) / M / 128 * 128, want = (p.share + 127) / 128 * 128;
-  p.width = want < most ? want : most;
   const int work = (E + 3) / 4 * ((M + 7) / 8);
   p.slices = 1;
-  while (2 * p.slices * work <= kWarps && 2 * p.slices * 128 <= p.width) p.slices *= 2;
+  while (2 * p.slices * work <= kWarps && 2 * p.slices * 128 <= p.share + 127) p.slices *= 2;
   p.plan = plan;
   p.held = tokens;
-  const int smem = layout_of(M, E, p.how.k, p.width, p.slices).total * 4;
-  return for_experts(E, [&](auto lanes, auto width) {
-    constexpr int L = decltype(lanes)::value, V = decltype(width)::value;
-    auto* kernel = few_route_kernel<L, V>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-    }
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kBlocks;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kBlocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-  });
+  const int smem = layout_of(M, E, p.how.k, p.slices).total * 4;
+  static thread_local bool allowed[64] = {};  // by device
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (dev >= 64 || !allowed[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(few_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed[dev] = true;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kBlocks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_route_kernel, p);
 }
 
 }  // namespace fp8bw

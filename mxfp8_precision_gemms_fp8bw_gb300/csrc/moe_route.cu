@@ -5,16 +5,211 @@
 namespace fp8bw {
 namespace {
 
+// The largest key of the row and where it is, the lowest place of equal ones;
+// key 0 where nothing is left.
+struct Best {
+  uint32_t key;
+  int at;
+};
+template <int L, int V>
+__device__ __forceinline__ Best best_of(const uint32_t (&key)[V], int l) {
+  Best b{key[0], 0};
+#pragma unroll
+  for (int v = 1; v < V; ++v)
+    if (key[v] > b.key) b = Best{key[v], v};
+  b.at = b.at * L + l;
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const Best c{__shfl_xor_sync(kAll, b.key, o), __shfl_xor_sync(kAll, b.at, o)};
+    if (c.key > b.key || (c.key == b.key && c.at < b.at)) b = c;
+  }
+  return b;
+}
+
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const T* __restrict__ logits,
                                                                  const float* __restrict__ bias, RouteShape p,
                                                                  int32_t* __restrict__ experts,
                                                                  float* __restrict__ weights) {
+  constexpr int kRowsPerWarp = 32 / L;
   extern __shared__ uint32_t staged[];
-  const int mine = threadIdx.x / L;  // the row in the block
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteRows<L> + mine;
-  // all lanes go through the shuffles
-  route_row<T, L, V>(logits, bias, p, row, row < p.M, mine, staged, experts, weights);
+  const int l = threadIdx.x & (L - 1), mine = threadIdx.x / L;  // the lane in its row, the row in the block
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRowsPerWarp) + mine;
+  const bool live = row < p.M;  // all lanes go through the shuffles
+  float x[V], s[V];
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = v * L + l;
+    x[v] = live && e < p.E ? logit_at(logits, row * p.E + e) : -INFINITY;
+  }
+  const RowScale scale = scores_of<L, V, true>(x, p.score, s);
+  if (bias == nullptr && p.groups == 1) {
+    // Scores are not negative, and NaN comes as 0x7fffffff: their bits order them.
+#pragma unroll
+    for (int v = 0; v < V; ++v)  // x is -inf past the last expert
+      key[v] = x[v] == -INFINITY ? 0u : __float_as_uint(s[v]) + 1u;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float b = bias != nullptr && v * L + l < p.E ? bias[v * L + l] : 0.f;
+      key[v] = x[v] == -INFINITY || b == -INFINITY ? 0u : ordered(s[v] + b);
+    }
+  }
+
+  if (p.groups > 1) {
+    // Lane l scores groups l, l + L, ... from the keys in shared memory; each
+    // starts at another place of its group, so that lanes hit other banks.
+    constexpr int G = (32 + L - 1) / L;
+    uint32_t* keys = staged + mine * (p.E | 8);
+    const int size = p.E / p.groups;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v * L + l < p.E) keys[v * L + l] = key[v];
+    __syncwarp();
+    uint32_t total[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int g = j * L + l;
+      uint32_t best = 0, second = 0;
+      if (g < p.groups) {
+        int at = g % size;
+#pragma unroll 4
+        for (int i = 0; i < size; ++i) {
+          const uint32_t u = keys[g * size + at];
+          second = max(second, min(best, u));
+          best = max(best, u);
+          at = at + 1 == size ? 0 : at + 1;
+        }
+      }
+      total[j] = best;
+      if (p.group_top == 2 && second != 0) {
+        const float sum = unordered(best) + unordered(second);
+        total[j] = ordered(sum < kLowest ? kLowest : sum);
+      }
+    }
+    uint32_t kept = 0;
+#pragma unroll 1
+    for (int i = 0; i < p.kept; ++i) {
+      const Best b = best_of<L, G>(total, l);
+      if (b.key != 0) kept |= 1u << b.at;
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (j * L + l == b.at) total[j] = 0;
+    }
+    const uint32_t per = (0xffffffffu / static_cast<uint32_t>(size)) + 1;  // e / size = (e * per) >> 32 for e, size <= 1024
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t g = size == 1 ? v * L + l : __umulhi(v * L + l, per);
+      if (v * L + l < p.E && !((kept >> g) & 1u)) key[v] = 0;
+    }
+  }
+
+  // Choice j is kept by lane j % L.
+  constexpr int K = (32 + L - 1) / L;
+  int chosen[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) chosen[j] = -1;
+  bool done = false;
+  if constexpr (L == 8 && V > 4) {
+    // Looking through all V keys again for every choice costs more than all
+    // the scores.  At least k experts are not below the k-th largest of the
+    // lanes' maxima, and for a k well below the lanes rarely more than twice
+    // as many: those go into a short list, whose members then rank each other.
+    // The list costs about three choices of the loop below; the eighth of eight
+    // lanes' maxima is so low that most warps hold a row with too many
+    // candidates, and pay for both, and with more keys to a lane so is the
+    // seventh.  127999 rows, list against loop:
+    // 160 experts 41.3 us against 39.3 for k = 2, 41.3 and 45.4 (3), 49.5 and
+    // 61.8 (6), 65.9 and 68.0 (7), 81 and 74 (8); 64 experts 24.9 and 23.7
+    // (3), 24.9 and 27.0 (4), 29.4 and 33.1 (6), 43 and 39 (8); 256 experts
+    // 62 and 58 (2), 62 and 66 (3), 78 and 93 (6), 111 and 103 (7); 32 experts
+    // 20.8 and 18.7 (3), 24.9 and 22.9 (6).
+    if (p.k >= 3 && p.k <= (V > 24 ? 6 : 7)) {
+      __shared__ uint2 lists[kRouteWarps * kRowsPerWarp][2 * L];
+      __shared__ int16_t orders[kRouteWarps * kRowsPerWarp][L];
+      uint32_t most = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) most = max(most, key[v]);
+      int rank = 0;  // of the lane's maximum, the lower lane first among equals
+#pragma unroll
+      for (int o = 1; o < L; ++o) {
+        const uint32_t other = __shfl_xor_sync(kAll, most, o);
+        rank += other > most || (other == most && (l ^ o) < l);
+      }
+      const uint32_t holder = __ballot_sync(kAll, rank == p.k - 1) >> (threadIdx.x & 31 & ~(L - 1)) & ((1u << L) - 1);
+      const uint32_t least = max(__shfl_sync(kAll, most, __ffs(holder) - 1, L), 1u);
+      int count = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) count += key[v] >= least;
+      int up = count;
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) {
+        const int t = __shfl_up_sync(kAll, up, o, L);
+        if (l >= o) up += t;
+      }
+      const int all = __shfl_sync(kAll, up, L - 1, L);
+      if (__all_sync(kAll, all <= 2 * L)) {
+        done = true;
+        uint2* list = lists[mine];
+        uint32_t to = smem_u32(list + up - count);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool in = key[v] >= least;
+          asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.shared.v2.u32 [%0], {%1, %2};\n\t}" ::"r"(to),
+                       "r"(key[v]), "r"(v * L + l), "r"(static_cast<int>(in))
+                       : "memory");
+          to += in ? sizeof(uint2) : 0;
+        }
+        __syncwarp();
+        // Every candidate's rank among them, by reading the list.
+        int16_t* order = orders[mine];
+        for (int i = l; i < all; i += L) {
+          const uint2 c = list[i];
+          int before = 0;
+#pragma unroll
+          for (int j = 0; j < 2 * L; ++j) {
+            const uint2 o = j < all ? list[j] : make_uint2(0, 0);
+            before += o.x > c.x || (o.x == c.x && o.y < c.y);
+          }
+          if (before < p.k) order[before] = static_cast<int16_t>(c.y);
+        }
+        __syncwarp();
+        if (l < p.k && l < all) chosen[0] = order[l];
+      }
+    }
+  }
+  if (!done) {
+#pragma unroll 1
+    for (int c = 0; c < p.k; ++c) {
+      const Best b = best_of<L, V>(key, l);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v * L + l == b.at) key[v] = 0;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (c == j * L + l && b.key != 0) chosen[j] = b.at;
+    }
+  }
+  // Weights from the scores without the bias, computed again for the few chosen.
+  float cs[K], sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    cs[j] = 0.f;
+    if (j * L >= p.k) continue;
+    cs[j] = chosen[j] >= 0 ? score_at(logit_at(logits, row * p.E + chosen[j]), p.score, scale) : 0.f;
+    sum += cs[j];
+  }
+  sum = lanes_sum<L>(sum);
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int c = j * L + l;
+    if (j * L < p.k && live && c < p.k) {
+      experts[row * p.k + c] = chosen[j];
+      const float w = (p.renorm ? cs[j] / (sum + 1e-20f) : cs[j]) * p.scale;
+      weights[row * p.k + c] = chosen[j] >= 0 ? w : 0.f;  // also beside a NaN, which makes the sum NaN
+    }
+  }
 }
 
 // ---------------------------------------------------------------- plan
