@@ -32,12 +32,13 @@ using few::kAll;
 // Warps 0-3   drain the accumulators (warp w: rows 32 w ..)
 // Warps 4-7   copy weights and their scales, by cp.async
 // Warps 8, 9  copy tokens and their scales, likewise
-// Warp  10    owns tensor memory and issues the products
+// Warp  10    brings the scales of a stage that has landed into tensor memory
+// Warp  11    owns tensor memory and issues the products
 enum Mode { kLinear, kUp, kDown };
 
 constexpr int kRows = 128, kChunk = 128;
 constexpr int kDrainWarps = 4, kWeightWarps = 4, kTokenWarps = 2;
-constexpr int kIssuer = kDrainWarps + kWeightWarps + kTokenWarps;
+constexpr int kScaler = kDrainWarps + kWeightWarps + kTokenWarps, kIssuer = kScaler + 1;
 constexpr int kThreads = (kIssuer + 1) * 32;
 
 // A stage of shared memory: codes of 128 rows, 128 bytes each with 128-byte swizzling (4-bit codes of 16 weights in the first
@@ -89,9 +90,10 @@ __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 
 constexpr int kMostDepth = 4;
 struct Shared {
-  uint64_t full[kMostDepth], empty[kMostDepth];  // a stage has landed, has been read
+  // Of a stage: it has landed, its scales are in tensor memory, it has been read.
+  uint64_t full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
   uint64_t sum_full[2], sum_empty[2];    // an accumulator is complete, has been drained
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
   int list[32];       // kUp: the tokens of the columns
@@ -101,6 +103,12 @@ struct Shared {
 template <int kCount>
 __device__ __forceinline__ void named_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 
 // x [M, K] in parts.
@@ -157,13 +165,15 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDepth; ++s) {
       mbar_init(&sh.full[s], (kWeightWarps * (whole_words ? 1 : 2) + kTokenWarps) * 32);
+      mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.sum_full[b], 1);
       mbar_init(&sh.sum_empty[b], kDrainWarps);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -275,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       }
     }
     cp_async_wait_all();
-  } else if (warp >= kDrainWarps + kWeightWarps && warp < kIssuer) {
+  } else if (warp >= kDrainWarps + kWeightWarps && warp < kScaler) {
     // ------------------------------------------------------------ tokens
     // Of a chunk a thread copies piece tid % 8 of rows tid / 8 + 8 j, and the scales of rows tid and tid + 64.
     if (kMode != kUp) grid_wait();
@@ -327,66 +337,93 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       }
     }
     cp_async_wait_all();
+  } else if (warp == kScaler) {
+    // ------------------------------------------------------------ scales
+    // cp.async wrote what the tensor core reads: the fence between the two, and the copies, stay off the thread that issues
+    // the products (together 250 to 800 cycles a chunk).
+    named_sync<(kDrainWarps + 2) * 32>();
+    tc_fence_after();
+    const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (kMode == kDown ? 2 : 1) * p.columns;
+    const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + token_scales_at);
+    const bool elected = elect_one();
+    Ring<kDepth> ring;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+      if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+      if (elected) {
+        // The columns were last read by products that were complete before the stage was filled again.
+        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
+        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb0 + stage);
+        mma_commit(&sh.ready[ring.s]);
+      }
+      __syncwarp();
+      ring.next();
+    }
+    if (elected) {  // nothing may be under way when tensor memory is given back
+      mma_commit(&sh.drain[0]);
+      int none = 0;
+      mbar_wait(&sh.drain[0], 0, AbortFlag{&none}, p.status, 1000000ull);
+    }
+    __syncwarp();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
     tmem_alloc(&sh.tmem, p.tmem);
     tmem_relinquish();
     tc_fence_before();
-    named_sync<(kDrainWarps + 1) * 32>();
+    named_sync<(kDrainWarps + 2) * 32>();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    if (lane == 0) {
-      bool alive = true;
-      Ring<kDepth> ring;
-      const uint32_t acc_columns = p.columns, sf0 = tmem + (kMode == kDown ? 2 : 1) * acc_columns;
-      const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(stage0 + tokens_at);
-      const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + token_scales_at);
-      int c = c0, slot = slot0, sum = 0;
+    // All lanes walk through the loop, so that what the products take stays in uniform registers; one issues them.
+    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + (kMode == kDown ? 2 : 1) * p.columns;
+    const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(stage0 + tokens_at);
+    const bool elected = elect_one();
+    bool alive = true;
+    Ring<kDepth> ring;
+    int c = c0, slot = slot0, sum = 0;
 #pragma unroll 1
-      for (int t = t0; t < t1 && alive; ++slot, c = 0, ++sum) {
-        const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * acc_columns : 0);
-        if (kMode == kDown && sum >= 2 && !mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status)) {
+    for (int t = t0; t < t1 && alive; ++slot, c = 0, ++sum) {
+      const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0);
+      if (kMode == kDown && sum >= 2 && !all_of(mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status))) break;
+      const uint32_t N = (__shfl_sync(kAll, slot_at(slot).n, 0) * kParts + 15) & ~15;
+      const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
+      const int end = t + run_of(c, t);
+      int left = K / 32 - c * 4;  // blocks of 32
+      uint32_t more = 0;          // whether there is something in the accumulator
+#pragma unroll 1
+      for (; t < end; ++t, left -= 4) {
+        if (!all_of(mbar_wait(&sh.ready[ring.s], ring.phase, ab, p.status))) {
           alive = false;
           break;
         }
-        const uint32_t N = (slot_at(slot).n * kParts + 15) & ~15;
-        const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
-        const int end = t + run_of(c, t);
-        int left = K / 32 - c * 4;  // blocks of 32
-        uint32_t first = 1;
-#pragma unroll 1
-        for (; t < end; ++t, left -= 4) {
-          if (!mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
-          fence_proxy_async_smem();  // cp.async wrote what the tensor core reads
-          const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
-          const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
-          tmem_cp_32x128b_warpx4(sfa, sa0 + stage);
-          tmem_cp_32x128b_warpx4(sfb, sb0 + stage);
-          const uint64_t a = a0 + stage, b = b0 + stage;
-          mma_mx_e4m3(acc, a, b, kind, sfa, sfb, first ^ 1);
-          first = 0;
-          if (left > 1) mma_mx_e4m3(acc, a + 2, b + 2, kind | idesc_mx_e4m3(0, 0, 1, 1), sfa, sfb, 1);
-          if (left > 2) mma_mx_e4m3(acc, a + 4, b + 4, kind | idesc_mx_e4m3(0, 0, 2, 2), sfa, sfb, 1);
-          if (left > 3) mma_mx_e4m3(acc, a + 6, b + 6, kind | idesc_mx_e4m3(0, 0, 3, 3), sfa, sfb, 1);
+        tc_fence_after();
+        const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+        const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
+        const uint64_t a = a0 + stage, b = b0 + stage;
+        if (elected) {
+          mma_mx_e4m3(acc, a, b, kind, sfa, sfb, more);
+          if (left > 1) mma_mx_e4m3_k<true>(acc, a + 2, b + 2, kind | idesc_mx_e4m3(0, 0, 1, 1), sfa, sfb);
+          if (left > 2) mma_mx_e4m3_k<true>(acc, a + 4, b + 4, kind | idesc_mx_e4m3(0, 0, 2, 2), sfa, sfb);
+          if (left > 3) mma_mx_e4m3_k<true>(acc, a + 6, b + 6, kind | idesc_mx_e4m3(0, 0, 3, 3), sfa, sfb);
           mma_commit(&sh.empty[ring.s]);
-          ring.next();
         }
-        mma_commit(&sh.sum_full[sum & 1]);
+        __syncwarp();
+        more = 1;
+        ring.next();
       }
-      if (!alive) {  // nothing may be under way when tensor memory is given back
-        mma_commit(&sh.drain);
-        int none = 0;
-        mbar_wait(&sh.drain, 0, AbortFlag{&none}, p.status, 1000000ull);
-      }
+      if (elected) mma_commit(&sh.sum_full[sum & 1]);
+      __syncwarp();
+    }
+    if (elected) {
+      mma_commit(&sh.drain[1]);
+      int none = 0;
+      mbar_wait(&sh.drain[1], 0, AbortFlag{&none}, p.status, 1000000ull);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums
-    named_sync<(kDrainWarps + 1) * 32>();
+    named_sync<(kDrainWarps + 2) * 32>();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int row = threadIdx.x;  // warps 0-3
