@@ -17,7 +17,7 @@ bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
 
 bool layer_dims_ok(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {
   return M <= FP8BW_FEW_TOKENS && choices_ok(M, E, top_k) && dim_ok(C, 32) && dim_ok(F, 32) && C <= kMaxWidth &&
-         F <= kMaxWidth;
+         F <= kMaxWidth && E * 2 * F <= kMaxDim && E * C <= kMaxDim;  // rows are numbered in int32
 }
 
 }  // namespace
@@ -97,7 +97,7 @@ FP8BW_API int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* 
   if (!layer_dims_ok(M, E, top_k, C, F))
     return fail(FP8BW_ERR_SHAPE,
                 "%s: need 0 < M <= 32, 0 < E <= 1024, 0 < top_k <= min(E, 32), C and F positive multiples of 32 up to "
-                "2^22; got M=%lld E=%lld top_k=%lld C=%lld F=%lld",
+                "2^22, E * 2F and E * C under 2^31; got M=%lld E=%lld top_k=%lld C=%lld F=%lld",
                 name, (long long)M, (long long)E, (long long)top_k, (long long)C, (long long)F);
   if (!groups_ok(E, top_k, groups, groups_kept))
     return fail(FP8BW_ERR_SHAPE,

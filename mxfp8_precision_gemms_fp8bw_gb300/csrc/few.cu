@@ -9,6 +9,8 @@
 // two or three parts (few_tokens.cuh) that are columns of their own.  (A
 // version that turned weights into f16 for mma.sync took 55 instructions for
 // 32 weights of 32 rows, 2 to 4 times the time that memory allows.)
+#include <cuda.h>
+
 #include "few.h"
 #include "few_tokens.cuh"
 #include "launch.h"
@@ -29,21 +31,26 @@ using few::kAll;
 //            over an expert is drained from tensor memory, weighted and added
 //            to its tokens in shared memory               y
 //
-// Warps 0-3   drain the accumulators (warp w: rows 32 w ..)
-// Warps 4-7   copy weights and their scales, by cp.async
-// Warps 8, 9  copy tokens and their scales, likewise
-// Warp  10    brings the scales of a stage that has landed into tensor memory
-// Warp  11    owns tensor memory and issues the products
+// Warps 0-3  drain the accumulators (warp w: rows 32 w ..)
+// Warps 4-7  copy the weights' scales, by cp.async
+// Warp  8    copies weights, by TMA
+// Warp  9    copies tokens, by bulk copies
+// Warp  10   brings the scales of a stage that has landed into tensor memory
+// Warp  11   owns tensor memory and issues the products
+//
+// Weights and tokens stay off the load and store units: with cp.async those
+// held a block back at 800 to 2000 cycles a chunk, of which 350 to 700 are what
+// the memory takes.
 enum Mode { kLinear, kUp, kDown };
 
 constexpr int kRows = 128, kChunk = 128;
-constexpr int kDrainWarps = 4, kWeightWarps = 4, kTokenWarps = 2;
-constexpr int kScaler = kDrainWarps + kWeightWarps + kTokenWarps, kIssuer = kScaler + 1;
+constexpr int kDrainWarps = 4, kScaleWarps = 4;
+constexpr int kWeights = kDrainWarps + kScaleWarps, kTokens = kWeights + 1, kScaler = kTokens + 1, kIssuer = kScaler + 1;
 constexpr int kThreads = (kIssuer + 1) * 32;
 
 // A stage of shared memory: codes of 128 rows, 128 bytes each with 128-byte swizzling (4-bit codes of 16 weights in the first
-// 8 bytes of 16, which is how the tensor core wants them), codes of up to `columns` token rows likewise, and scales in the
-// layout of tcgen05.cp: row r's four bytes are word (r % 32) * 4 + r / 32.
+// 8 bytes of 16, which is how the tensor core wants them); a record of tokens (few.h); and the weights' scales, row r's four
+// bytes as word (r % 32) * 4 + r / 32.
 constexpr uint32_t kCodes = kRows * 128, kScales = 512;
 
 struct Matrix {
@@ -59,13 +66,14 @@ struct Product {
   int M, splits;
   bool late;            // the cluster's sums meet in the stages
   int slots;            // kDown: room for as many
+  bool tiled;           // weights come by TMA
   int columns;          // room for token rows in a stage: a multiple of 16
   uint32_t tmem;        // columns of tensor memory
   uint32_t stage;       // bytes
-  FewRows t;            // tokens; kDown: activations
+  const uint8_t* t;     // records of tokens; kDown: of activations
   const FewPlan* plan;  // kUp, kDown
   int choices;          // of the plan
-  FewRows act;          // kUp: activations
+  uint8_t* act;         // kUp: records of activations
   uint16_t* y;          // bf16 [M, rows]
   int* status;
 };
@@ -96,8 +104,9 @@ struct Shared {
   uint64_t drain[2];
   uint32_t tmem;
   int abort;
-  int list[32];       // kUp: the tokens of the columns
 };
+
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // Barrier 1, for the warps that use tensor memory.
 template <int kCount>
@@ -112,16 +121,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // x [M, K] in parts.
-__global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restrict__ x, int64_t K, FewRows t) {
+__global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restrict__ x, int64_t K, uint8_t* t) {
   grid_release();
   const int64_t pieces = K / 8;  // of 8 values, of a token
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~31);
   if (i0 >= pieces) return;
   const int lane = threadIdx.x & 31;
   const int64_t i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
-  const int64_t row = static_cast<int64_t>(blockIdx.y) * kTokenParts;
-  few::split8(__ldg(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i), t.codes + row * t.pitch + i * 8,
-              t.scales + row * (t.pitch / 32) + i / 4, t.pitch);
+  few::split8(__ldg(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i), t, static_cast<int>(gridDim.y), i * 8,
+              static_cast<int>(blockIdx.y));
 }
 
 // A stage of the ring, as each role walks through it: which, and the parity of its next completion.
@@ -142,8 +150,24 @@ __device__ __forceinline__ void store_remote(float* mine, int rank, float v) {  
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x2(uint32_t taddr, uint32_t (&r)[2]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+}
+
 template <Mode kMode, int kBits, int kDepth>
-__global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ Product p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    few_kernel(const __grid_constant__ CUtensorMap weights_map, const __grid_constant__ Product p) {
   constexpr int kParts = kMode == kDown ? kActParts : kTokenParts;
   constexpr int kRowBytes = 16 * kBits;  // of a chunk in memory
   extern __shared__ uint8_t smem_raw[];
@@ -164,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDepth; ++s) {
-      mbar_init(&sh.full[s], (kWeightWarps * (whole_words ? 1 : 2) + kTokenWarps) * 32);
+      mbar_init(&sh.full[s], kScaleWarps * (whole_words ? 32 : 64) + 1 + p.tiled);
       mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
@@ -180,14 +204,13 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   // What the plan says.  The plan is older than the kernel before this one, which waited for it before it let this one
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
   int slots = 1;
-  FewSlot one{0, 0, 0, p.M};
+  FewSlot one{0, 0, 0xffffffffu >> (32 - p.M), p.M};
   bool idle = false;
   if constexpr (kMode == kUp) {
     grid_wait();
     grid_release();
     idle = static_cast<int>(blockIdx.y) >= few_active(p.plan);
     one = few_slot(p.plan, p.choices, blockIdx.y);  // of an idle block: not read further
-    if (warp == 0 && ((one.mask >> lane) & 1)) sh.list[__popc(one.mask & ((1u << lane) - 1))] = lane;
   } else if constexpr (kMode == kDown) {
     slots = few_active(p.plan);
     for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = few_slot(p.plan, p.choices, i);
@@ -210,23 +233,22 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int64_t row0 = static_cast<int64_t>(block) * tile;
   const int last = static_cast<int>(min((kMode == kUp ? p.m.rows / 2 : p.m.rows) - row0, static_cast<int64_t>(tile))) - 1;
   const uint32_t stage0 = smem_u32(smem);
-  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128, token_scales_at = scales_at + kScales;
+  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128 + kScales;
+  // Rows of the tokens of a slot: kDown has those of its columns, the others every token's for every expert.
+  const auto rows_of = [&](const FewSlot& s) { return (kMode == kDown ? s.n : p.M) * kParts; };
 
-  if (warp >= kDrainWarps && warp < kDrainWarps + kWeightWarps) {
-    // ------------------------------------------------------------ weights
-    // Of a chunk a thread copies piece tid % 8 of rows tid / 8 + 16 j, and the scales of row tid.
+  if (warp >= kDrainWarps && warp < kWeights) {
+    // ------------------------------------------------------------ scales of the weights
+    // Of a chunk a thread copies the four bytes of row tid.  4-bit codes that TMA does not take (rows of no whole chunks) are
+    // copied here as well: piece tid % 8 of rows tid / 8 + 16 j.
     const int tid = threadIdx.x - kDrainWarps * 32, piece = tid & 7;
-    constexpr int kPiece = kRowBytes / 8;
     const uint32_t pitch = K / 8 * kBits, scale_pitch = K / 32;
     const int64_t half = kMode == kUp ? p.m.rows / 2 : 0;  // from a row of gate to its row of up
-    uint32_t from[kMode == kUp ? 4 : 8];  // rows j of gate and j + 4 of up have the same offset
-#pragma unroll
-    for (int j = 0; j < (kMode == kUp ? 4 : 8); ++j) from[j] = min(tid / 8 + 16 * j, last) * pitch + piece * kPiece;
     const uint32_t to = (tid / 8) * 128 + ((piece ^ (tid / 8 & 7)) << 4);
     const int64_t scale_row = kMode == kUp ? min(tid & 63, last) + (tid >= 64 ? half : 0) : static_cast<int64_t>(min(tid, last));
     const uint32_t scale_to = scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
 
-    // Where no word holds a row's four scale bytes: they come through registers, a chunk ahead.
+    // Where no word holds a row's four bytes: they come through registers, a chunk ahead.
     const auto scale_word = [&](int64_t s) {
       const int64_t word = s & ~int64_t{3};
       const uint32_t* at = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
@@ -247,9 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 #pragma unroll 1
     for (int t = t0; t < t1; ++slot, c = 0) {
       const int64_t first = slot_at(slot).expert * p.m.rows + row0;
-      const uint8_t* w = p.m.w + first * pitch + c * kRowBytes;
       int64_t scale = (first + scale_row) * scale_pitch + c * 4;
-      uint32_t off = c * kRowBytes + piece * kPiece;
+      uint32_t off = c * kRowBytes + piece * 8;
       const int end = t + run_of(c, t);
       uint32_t word = whole_words ? 0 : scale_word(scale);
 #pragma unroll 1
@@ -259,16 +280,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
           break;
         }
         const uint32_t stage = stage0 + ring.s * p.stage;
-        if (off < pitch) {  // the last chunk of a row may be short
-          if constexpr (kMode == kUp) {
-            const uint8_t* up = w + half * pitch;
+        if (kBits == 4 && !p.tiled && off < pitch) {  // the last chunk of a row may be short
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cp_async<kPiece>(stage + to + j * 2048, w + from[j]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cp_async<kPiece>(stage + to + (j + 4) * 2048, up + from[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) cp_async<kPiece>(stage + to + j * 2048, w + from[j]);
+          for (int j = 0; j < 8; ++j) {
+            const int r = tid / 8 + 16 * j;
+            const int64_t row = kMode == kUp ? min(r & 63, last) + (r >= 64 ? half : 0) : static_cast<int64_t>(min(r, last));
+            cp_async<8>(stage + to + j * 2048, p.m.w + (first + row) * pitch + off);
           }
         }
         if (whole_words) {
@@ -279,64 +296,60 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
           if (t + 1 < end) word = scale_word(scale + 4);
         }
         cp_async_arrive(&sh.full[ring.s]);
-        w += kRowBytes, off += kRowBytes, scale += 4;
+        off += kRowBytes, scale += 4;
         ring.next();
         refill |= ring.s == 0;
       }
     }
     cp_async_wait_all();
-  } else if (warp >= kDrainWarps + kWeightWarps && warp < kScaler) {
-    // ------------------------------------------------------------ tokens
-    // Of a chunk a thread copies piece tid % 8 of rows tid / 8 + 8 j, and the scales of rows tid and tid + 64.
-    if (kMode != kUp) grid_wait();
-    constexpr int kMostCopies = kFewTokens * kParts / 8;
-    const int tid = threadIdx.x - (kDrainWarps + kWeightWarps) * 32, piece = tid & 7;
-    const uint32_t pitch = static_cast<uint32_t>(p.t.pitch), scale_pitch = pitch / 32;
-    const uint32_t to = tokens_at + (tid >> 3) * 128 + ((piece ^ (tid >> 3)) << 4);
-    const uint32_t scale_to = token_scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
-    Ring<kDepth> ring;
-    bool refill = false;
-    int c = c0, slot = slot0;
+  } else if (warp == kWeights || warp == kTokens) {
+    // ------------------------------------------------------------ weights, tokens
+    const bool tokens = warp == kTokens;
+    if (lane == 0 && (tokens || p.tiled)) {
+      if (tokens && kMode != kUp) grid_wait();
+      if (tokens) fence_proxy_async_global();  // the kernel before wrote what the bulk copies read
+      Ring<kDepth> ring;
+      bool refill = false, alive = true;
+      int c = c0, slot = slot0, issued = 0;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++slot, c = 0) {
-      const FewSlot s = slot_at(slot);
-      const int n = s.n * kParts;
-      const auto row_of = [&](int r) {
-        return static_cast<uint32_t>(kMode == kUp ? sh.list[r / kParts] * kParts + r % kParts : r);
-      };
-      const int64_t start = static_cast<int64_t>(kMode == kDown ? s.start : 0) * kParts;
-      const uint8_t* codes = p.t.codes + start * pitch + c * 128 + piece * 16;
-      const uint8_t* scales = p.t.scales + start * scale_pitch + c * 4;
-      uint64_t from[kMode == kUp ? kMostCopies : 1];
-      if constexpr (kMode == kUp)
-#pragma unroll
-        for (int j = 0; j < kMostCopies; ++j) {
-          const int r = (tid >> 3) + 8 * j;
-          from[j] = r < n ? static_cast<uint64_t>(row_of(r)) * pitch : 0;
-        }
-      const int end = t + run_of(c, t);
+      for (int t = t0; t < t1 && alive; ++slot, c = 0) {
+        const FewSlot s = slot_at(slot);
+        const uint32_t record = static_cast<uint32_t>(few_record(rows_of(s)));
+        const uint8_t* from = p.t + (kMode == kDown ? few_act_at(slot, s.start, chunks) : 0) + static_cast<int64_t>(c) * record;
+        const int32_t row = static_cast<int32_t>(s.expert * p.m.rows + row0);
+        const int end = t + run_of(c, t);
 #pragma unroll 1
-      for (; t < end; ++t) {
-        if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
-          t = t1;
-          break;
+        for (; t < end; ++t, ++c, ++issued) {
+          if (refill && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+            alive = false;
+            break;
+          }
+          const uint32_t stage = stage0 + ring.s * p.stage;
+          uint64_t* full = &sh.full[ring.s];
+          if (tokens) {
+            mbar_arrive_expect_tx(full, record);
+            bulk_load(stage + tokens_at, from, record, full);
+            from += record;
+          } else {
+            // Codes that TMA spreads out count as they are in memory.
+            mbar_arrive_expect_tx(full, kRows * kRowBytes);
+            tile_load(stage, &weights_map, c * kChunk, row, full);
+            if (kMode == kUp)
+              tile_load(stage + kCodes / 2, &weights_map, c * kChunk, row + static_cast<int32_t>(p.m.rows / 2), full);
+          }
+          ring.next();
+          refill |= ring.s == 0;
         }
-        const uint32_t stage = stage0 + ring.s * p.stage;
-#pragma unroll
-        for (int j = 0; j < kMostCopies; ++j) {
-          const int r = (tid >> 3) + 8 * j;
-          if (8 * j >= n) break;
-          if (r < n) cp_async<16>(stage + to + j * 1024, codes + (kMode == kUp ? from[j] : static_cast<uint64_t>(r) * pitch));
+      }
+      if (!alive) {  // what is under way lands before the block ends, or never will
+        int none = 0;
+        for (int i = min(issued, kDepth); i > 0; --i) {
+          if (--ring.s < 0) ring.s = kDepth - 1, ring.phase ^= 1;
+          mbar_wait(&sh.full[ring.s], ring.phase, AbortFlag{&none}, p.status, 1000000ull);
         }
-        for (int r = tid, j = 0; r < n; r += 64, ++j)
-          cp_async<4>(stage + scale_to + j * 8, scales + static_cast<uint64_t>(row_of(r)) * scale_pitch);
-        cp_async_arrive(&sh.full[ring.s]);
-        codes += 128, scales += 4;
-        ring.next();
-        refill |= ring.s == 0;
       }
     }
-    cp_async_wait_all();
+    __syncwarp();
   } else if (warp == kScaler) {
     // ------------------------------------------------------------ scales
     // cp.async wrote what the tensor core reads: the fence between the two, and the copies, stay off the thread that issues
@@ -344,23 +357,25 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     named_sync<(kDrainWarps + 2) * 32>();
     tc_fence_after();
     const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (kMode == kDown ? 2 : 1) * p.columns;
-    const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + token_scales_at);
+    const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + tokens_at);
     const bool elected = elect_one();
     Ring<kDepth> ring;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0, c = c0, slot = slot0; t < t1; ++t) {
       if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) break;
       fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+      const uint64_t rows = static_cast<uint64_t>(rows_of(slot_at(slot)));
       if (elected) {
         // The columns were last read by products that were complete before the stage was filled again.
         tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
-        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb0 + stage);
+        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb0 + stage + rows * (128 >> 4));
         mma_commit(&sh.ready[ring.s]);
       }
       __syncwarp();
       ring.next();
+      if (++c == chunks) c = 0, ++slot;
     }
     if (elected) {  // nothing may be under way when tensor memory is given back
       mma_commit(&sh.drain[0]);
@@ -386,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     for (int t = t0; t < t1 && alive; ++slot, c = 0, ++sum) {
       const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0);
       if (kMode == kDown && sum >= 2 && !all_of(mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status))) break;
-      const uint32_t N = (__shfl_sync(kAll, slot_at(slot).n, 0) * kParts + 15) & ~15;
+      const uint32_t N = (__shfl_sync(kAll, rows_of(slot_at(slot)), 0) + 15) & ~15;
       const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
       const int end = t + run_of(c, t);
       int left = K / 32 - c * 4;  // blocks of 32
@@ -437,24 +452,37 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       tc_fence_after();
       const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
       uint32_t mask = s.mask;
+      if constexpr (kMode == kDown) {
 #pragma unroll 1
-      for (int n0 = 0; n0 < s.n; n0 += 16) {  // 16 tokens at a time
-        uint32_t v[kParts][16];
+        for (int n0 = 0; n0 < s.n; n0 += 16) {  // 16 columns' parts at a time
+          uint32_t v[kParts][16];
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x16(acc + (n0 * kParts + q * 16), v[q]);
-        tmem_ld_wait();
+          for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x16(acc + (n0 * kParts + q * 16), v[q]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (n0 + i >= s.n) break;
-          float f = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            if (n0 + i >= s.n) break;
+            float f = 0.f;
 #pragma unroll
-          for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[(i * kParts + q) / 16][(i * kParts + q) % 16]);
-          if constexpr (kMode == kDown) {
+            for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[(i * kParts + q) / 16][(i * kParts + q) % 16]);
             sums[(__ffs(mask) - 1) * kRows + row] += f * __ldcg(weights + s.start + n0 + i);
             mask &= mask - 1;
-          } else {
-            sums[(n0 + i) * kRows + row] = f;
           }
+        }
+      } else {
+        // The tokens of the mask, four at a time (past the last one that one again).
+#pragma unroll 1
+        for (int n0 = 0; n0 < s.n; n0 += 4) {
+          uint32_t v[4][kParts];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tmem_ld_32x32b_x2(acc + (__ffs(mask) - 1) * kParts, v[i]);
+            if (n0 + i + 1 < s.n) mask &= mask - 1;
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n0 + i < s.n) sums[(n0 + i) * kRows + row] = __uint_as_float(v[i][0]) + __uint_as_float(v[i][1]);
         }
       }
       tc_fence_before();
@@ -506,9 +534,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     if constexpr (kMode == kUp) {
       const int64_t f = row0 + i * 32;
       if (f >= p.m.rows / 2) continue;
-      const int64_t r = static_cast<int64_t>(one.start + token) * kActParts;
-      few::split1(v[0] / (1.f + expf(-v[0])) * v[1], p.act.codes + r * p.act.pitch + f + lane,
-                  p.act.scales + r * (p.act.pitch / 32) + f / 32, p.act.pitch);
+      few::split1(v[0] / (1.f + expf(-v[0])) * v[1],
+                  p.act + few_act_at(blockIdx.y, one.start, few_chunks(p.m.rows / 2)), one.n, f + lane, token);
     } else {
       const int row = i * 32 + lane;
       if (row <= last) p.y[token * p.m.rows + row0 + row] = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
@@ -534,8 +561,25 @@ int splits_of(int64_t tiles, int64_t chunks, int64_t slots) {
   return best;
 }
 
+// The weights as TMA reads them: boxes of `box` rows by 128.  False where it does not: 4-bit codes are spread out on the way,
+// for which it wants whole chunks of 128 and 32-byte alignment.
+bool weights_map(CUtensorMap* map, const Matrix& m, int64_t rows, int bits, uint32_t box) {
+  typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  if (bits == 4 && (m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(m.w) & 31) != 0)) return false;
+  const auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.K / 8 * bits)};
+  const cuuint32_t boxes[2] = {kChunk, box}, each[2] = {1, 1};
+  return fn(map, bits == 4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<uint8_t*>(m.w), dims, strides, boxes, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <Mode kMode, int kBits, int kDepth>
-cudaError_t launch(const Product& p, uint32_t smem, dim3 grid, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3 grid, cudaStream_t st) {
   auto* kernel = few_kernel<kMode, kBits, kDepth>;
   static thread_local bool allowed[64] = {};  // by device
   int dev = 0;
@@ -562,20 +606,20 @@ cudaError_t launch(const Product& p, uint32_t smem, dim3 grid, cudaStream_t st) 
     attrs[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, map, p);
 }
 
 // matrices: how many lie behind each other along the contraction (kDown), copies: how many share the grid (kUp).
 template <Mode kMode, int kBits>
-cudaError_t launch_sized(Product p, int matrices, int copies, int num_sms, cudaStream_t st) {
+cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st) {
   const int parts = kMode == kDown ? kActParts : kTokenParts;
   const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t tiles = (rows + tile - 1) / tile;
-  p.columns = (p.M + 15) / 16 * 16 * parts;
+  p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
   const uint32_t columns = (kMode == kDown ? 2 : 1) * p.columns + kMostDepth * 8;
   p.tmem = 32;
   while (p.tmem < columns) p.tmem *= 2;
-  p.stage = kCodes + p.columns * 128 + 2 * kScales;
+  p.stage = kCodes + (p.columns * 128 + 2 * kScales);
   // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
   const uint32_t received = (p.M * kRows + 7 * 64) * 4;
   p.late = p.M > 16;
@@ -588,64 +632,81 @@ cudaError_t launch_sized(Product p, int matrices, int copies, int num_sms, cudaS
   p.splits = splits_of(tiles * copies, static_cast<int64_t>((p.m.K + kChunk - 1) / kChunk) * matrices,
                        num_sms * (smem(depth) <= kHalfSmem ? 2 : 1));
   const dim3 grid(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
-  return depth == 3 ? launch<kMode, kBits, 3>(p, smem(3), grid, st) : launch<kMode, kBits, 4>(p, smem(4), grid, st);
+  CUtensorMap map{};
+  p.tiled = weights_map(&map, p.m, experts * p.m.rows, kBits, static_cast<uint32_t>(tile));
+  if (kBits == 8 && !p.tiled) return cudaErrorInvalidValue;
+  return depth == 3 ? launch<kMode, kBits, 3>(map, p, smem(3), grid, st) : launch<kMode, kBits, 4>(map, p, smem(4), grid, st);
 }
 
 template <Mode kMode>
-cudaError_t launch_product(const Product& p, int bits, int matrices, int copies, int num_sms, cudaStream_t st) {
-  return bits == 4 ? launch_sized<kMode, 4>(p, matrices, copies, num_sms, st)
-                   : launch_sized<kMode, 8>(p, matrices, copies, num_sms, st);
+cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st) {
+  // A runtime call binds the device's context to a thread that has made none yet; the driver's encoder does not.
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+  return bits == 4 ? launch_sized<kMode, 4>(p, experts, matrices, copies, num_sms, st)
+                   : launch_sized<kMode, 8>(p, experts, matrices, copies, num_sms, st);
 }
 
 }  // namespace
 
-size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return few_rows_bytes(M, kTokenParts, K); }
+size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return few_tokens_bytes(M, K); }
 
 cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   Product p{};
   p.m = Matrix{a.w, a.e8, a.N * (a.K / 32), a.N, static_cast<int>(a.K)};
   p.M = static_cast<int>(a.M);
-  p.t = few_rows_at(a.workspace, a.M, kTokenParts, a.K);
+  p.t = static_cast<uint8_t*>(a.workspace);
   p.y = a.y;
   p.status = a.status;
   const dim3 grid(static_cast<unsigned>((a.K / 8 + 255) / 256), static_cast<unsigned>(a.M));
-  few_tokens_kernel<<<grid, 256, 0, st>>>(a.x, a.K, p.t);
+  few_tokens_kernel<<<grid, 256, 0, st>>>(a.x, a.K, static_cast<uint8_t*>(a.workspace));
   if (const cudaError_t e = cudaGetLastError()) return e;
-  return launch_product<kLinear>(p, a.bits, 1, 1, a.num_sms, st);
+  return launch_product<kLinear>(p, a.bits, 1, 1, 1, a.num_sms, st);
 }
 
-size_t few_moe_workspace_bytes(int64_t M, int64_t, int64_t top_k, int64_t C, int64_t F) {
-  return few_plan_bytes(M, top_k) + few_rows_bytes(M, kTokenParts, C) + few_rows_bytes(M * top_k, kActParts, F);
+namespace {
+
+struct MoeScratch {
+  FewPlan* plan;
+  uint8_t *tokens, *act;
+  int64_t bytes;
+};
+MoeScratch scratch_of(void* p, int64_t M, int64_t E, int64_t k, int64_t C, int64_t F) {
+  uint8_t* at = static_cast<uint8_t*>(p);
+  const int64_t tokens = few_plan_bytes(M, k), act = tokens + few_tokens_bytes(M, C);
+  return MoeScratch{reinterpret_cast<FewPlan*>(at), at + tokens, at + act,
+                    act + few_act_bytes(M * k, E < M * k ? E : M * k, F)};
+}
+
+}  // namespace
+
+size_t few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {
+  return scratch_of(nullptr, M, E, top_k, C, F).bytes;
 }
 
 cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
   const int64_t E = a.route.E, M = a.route.M, k = a.route.top_k;
   const int active = static_cast<int>(E < M * k ? E : M * k);  // at most
-  uint8_t* at = static_cast<uint8_t*>(a.workspace);
-  FewPlan* plan = reinterpret_cast<FewPlan*>(at);
-  at += few_plan_bytes(M, k);
-  const FewRows tokens = few_rows_at(at, M, kTokenParts, a.C);
-  at += few_rows_bytes(M, kTokenParts, a.C);
-  const FewRows act = few_rows_at(at, M * k, kActParts, a.F);
-  if (const cudaError_t e = launch_few_route(a, plan, tokens, st)) return e;
+  const MoeScratch s = scratch_of(a.workspace, M, E, k, a.C, a.F);
+  if (const cudaError_t e = launch_few_route(a, s.plan, s.tokens, st)) return e;
   Product up{};
   up.m = Matrix{a.w13, a.e13, E * 2 * a.F * (a.C / 32), 2 * a.F, static_cast<int>(a.C)};
   up.M = static_cast<int>(M);
-  up.t = tokens;
-  up.plan = plan;
+  up.t = s.tokens;
+  up.plan = s.plan;
   up.choices = static_cast<int>(M * k);
-  up.act = act;
+  up.act = s.act;
   up.status = a.route.status;
-  if (const cudaError_t e = launch_product<kUp>(up, a.bits, 1, active, a.num_sms, st)) return e;
+  if (const cudaError_t e = launch_product<kUp>(up, a.bits, E, 1, active, a.num_sms, st)) return e;
   Product down{};
   down.m = Matrix{a.w2, a.e2, E * a.C * (a.F / 32), a.C, static_cast<int>(a.F)};
   down.M = static_cast<int>(M);
-  down.t = act;
-  down.plan = plan;
+  down.t = s.act;
+  down.plan = s.plan;
   down.choices = static_cast<int>(M * k);
   down.y = a.y;
   down.status = a.route.status;
-  return launch_product<kDown>(down, a.bits, active, 1, a.num_sms, st);
+  return launch_product<kDown>(down, a.bits, E, active, 1, a.num_sms, st);
 }
 
 }  // namespace fp8bw

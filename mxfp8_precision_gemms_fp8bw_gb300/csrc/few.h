@@ -47,24 +47,21 @@ __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i
   return FewSlot{v.x, v.y, static_cast<uint32_t>(v.z), v.w};
 }
 
-// Values as the products read them (few_tokens.cuh): for every row, `parts` rows of e4m3 codes and as many of E8M0 bytes,
-// both padded to whole chunks of 128.  Tokens come in two parts, activations (a row for every choice, by slot and column) in
-// three.
+// Values as the products read them (few_tokens.cuh): a record for every chunk of 128 of the contraction, of `rows` rows of
+// e4m3 codes, 128 bytes each and already in the order of 128-byte swizzling, and their scales in the layout of tcgen05.cp.  A
+// stage of the products takes a record as it is.
+// Tokens come in two parts, rows 2 t and 2 t + 1 of the batch's records; activations in three, rows 3 i .. of the records of an
+// expert's slot, which has a record for every chunk.
 constexpr int kTokenParts = 2, kActParts = 3;
-struct FewRows {
-  uint8_t* codes;   // [rows * parts][pitch]
-  uint8_t* scales;  // [rows * parts][pitch / 32]
-  int64_t pitch;
-};
-__host__ __device__ inline int64_t few_pitch(int64_t K) { return (K + 127) / 128 * 128; }
-inline int64_t few_rows_bytes(int64_t rows, int parts, int64_t K) {
-  return (rows * parts * (few_pitch(K) / 32) * 33 + 255) / 256 * 256;
+__host__ __device__ inline int64_t few_record(int64_t rows) { return rows * 128 + 512; }
+__host__ __device__ inline int64_t few_chunks(int64_t K) { return (K + 127) / 128; }
+inline int64_t few_tokens_bytes(int64_t M, int64_t K) { return few_chunks(K) * few_record(M * kTokenParts); }
+// Where the records of a slot begin that has `start` choices before it.
+__host__ __device__ inline int64_t few_act_at(int64_t slot, int64_t start, int64_t chunks) {
+  return chunks * (start * kActParts * 128 + slot * 512);
 }
-inline FewRows few_rows_at(void* p, int64_t rows, int parts, int64_t K) {
-  uint8_t* at = static_cast<uint8_t*>(p);
-  return FewRows{at, at + rows * parts * few_pitch(K), few_pitch(K)};
-}
+inline int64_t few_act_bytes(int64_t choices, int64_t slots, int64_t F) { return few_act_at(slots, choices, few_chunks(F)); }
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewRows& tokens, cudaStream_t st);
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, uint8_t* tokens, cudaStream_t st);
 
 }  // namespace fp8bw

@@ -31,7 +31,7 @@ struct RouteFew {
   int C, share;    // features, and of a block: a multiple of 8
   int slices;      // warps that share four experts and eight tokens
   FewPlan* plan;
-  FewRows held;    // the tokens as the first product reads them
+  uint8_t* held;   // the tokens as the first product reads them
 };
 
 // A power of two, at least 32, that E is not above.
@@ -253,14 +253,12 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
     const int pieces = p.C / 8;  // of 8 values
 #pragma unroll 1
     for (int r = 0; r < rows; ++r) {
-      const int64_t t = rank + r * kBlocks;
-      const uint4* row = reinterpret_cast<const uint4*>(p.x + t * p.C);
-      uint8_t* to = p.held.codes + t * kTokenParts * p.held.pitch;
-      uint8_t* scales = p.held.scales + t * kTokenParts * (p.held.pitch / 32);
+      const int t = rank + r * kBlocks;
+      const uint4* row = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.C);
 #pragma unroll 1
       for (int i0 = (warp - kMostRows) * 32; i0 < pieces; i0 += (kWarps - kMostRows) * 32) {
         const int i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
-        few::split8(__ldg(row + i), to + i * 8, scales + i / 4, p.held.pitch);
+        few::split8(__ldg(row + i), p.held, M, i * 8, t);
       }
     }
   }
@@ -310,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
 
 }  // namespace
 
-cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, const FewRows& tokens, cudaStream_t st) {
+cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, uint8_t* tokens, cudaStream_t st) {
   RouteFew p{};
   p.x = a.x;
   p.router = a.router;

@@ -23,9 +23,17 @@ __device__ __forceinline__ float without_infinity(float v) {
 __device__ __forceinline__ uint32_t part_byte(uint32_t top) { return min(max((top + 0x1FFFFFu) >> 23, 8u), 255u) - 8u; }
 __device__ __forceinline__ float part_factor(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }  // 2^-E
 
-// Eight consecutive bf16 values of a block that four neighbouring lanes hold, in kTokenParts parts: codes to to[part * pitch],
-// the block's bytes to scales[part * pitch / 32] (by the first of the four).
-__device__ __forceinline__ void split8(uint4 v, uint8_t* to, uint8_t* scales, int64_t pitch) {
+// Where element k of row r is in records of `rows` rows (few.h), and the scale of its block.
+__device__ __forceinline__ uint8_t* code_at(uint8_t* records, int64_t rows, int64_t k, int r) {
+  const int b = static_cast<int>(k & 127);
+  return records + (k >> 7) * few_record(rows) + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15);
+}
+__device__ __forceinline__ uint8_t* scale_at(uint8_t* records, int64_t rows, int64_t k, int r) {
+  return records + (k >> 7) * few_record(rows) + rows * 128 + (r & 31) * 16 + (r >> 5) * 4 + ((k & 127) >> 5);
+}
+
+// Values k .. k + 7 of token t of M, of a block that four neighbouring lanes hold, in kTokenParts parts.
+__device__ __forceinline__ void split8(uint4 v, uint8_t* records, int M, int64_t k, int t) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float f[8];
 #pragma unroll
@@ -45,8 +53,9 @@ __device__ __forceinline__ void split8(uint4 v, uint8_t* to, uint8_t* scales, in
     uint2 q;
     q.x = e4m3x4(f[0] * down, f[1] * down, f[2] * down, f[3] * down);
     q.y = e4m3x4(f[4] * down, f[5] * down, f[6] * down, f[7] * down);
-    *reinterpret_cast<uint2*>(to + part * pitch) = q;
-    if ((threadIdx.x & 3) == 0) scales[part * (pitch / 32)] = static_cast<uint8_t>(byte);
+    const int r = t * kTokenParts + part;
+    *reinterpret_cast<uint2*>(code_at(records, M * kTokenParts, k, r)) = q;
+    if ((threadIdx.x & 3) == 0) *scale_at(records, M * kTokenParts, k, r) = static_cast<uint8_t>(byte);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 g = e4m3x2_to_f32((i < 2 ? q.x : q.y) >> (i & 1) * 16);
@@ -56,15 +65,16 @@ __device__ __forceinline__ void split8(uint4 v, uint8_t* to, uint8_t* scales, in
   }
 }
 
-// One fp32 value of a block that the warp holds, in kActParts parts.
-__device__ __forceinline__ void split1(float v, uint8_t* to, uint8_t* scales, int64_t pitch) {
+// Value k of column i of n, of a block that the warp holds, in kActParts parts.
+__device__ __forceinline__ void split1(float v, uint8_t* records, int n, int64_t k, int i) {
   v = without_infinity(v);
 #pragma unroll
   for (int part = 0; part < kActParts; ++part) {
     const uint32_t byte = part_byte(__reduce_max_sync(kAll, __float_as_uint(v) & 0x7FFFFFFFu));
     const uint32_t q = cvt_e4m3x2(v * part_factor(byte), 0.f);
-    to[part * pitch] = static_cast<uint8_t>(q);
-    if ((threadIdx.x & 31) == 0) scales[part * (pitch / 32)] = static_cast<uint8_t>(byte);
+    const int r = i * kActParts + part;
+    *code_at(records, n * kActParts, k, r) = static_cast<uint8_t>(q);
+    if ((threadIdx.x & 31) == 0) *scale_at(records, n * kActParts, k, r) = static_cast<uint8_t>(byte);
     v -= e4m3x2_to_f32(q).x * e8m0_value(byte);
   }
 }

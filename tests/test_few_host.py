@@ -73,7 +73,7 @@ def test_layer_workspace(lib):
     assert size(1, 8, 2, 256, 512) > 0
     for bad in ((0, 8, 2, 256, 512), (33, 8, 2, 256, 512), (1, 0, 2, 256, 512), (1, 1025, 2, 256, 512), (1, 8, 9, 256, 512),
                 (1, 8, 0, 256, 512), (1, 64, 33, 256, 512), (1, 8, 2, 250, 512), (1, 8, 2, 256, 0), (1, 8, 2, 256, 520),
-                (1, 8, 2, (1 << 22) + 32, 32)):
+                (1, 8, 2, (1 << 22) + 32, 32), (1, 512, 2, 256, 1 << 22), (1, 1024, 2, 1 << 22, 256)):
         assert size(*bad) == 0, bad
 
 
