@@ -42,15 +42,16 @@ int mxfp4_quant_1x32_row(const fp8bw_bf16* w, int64_t R, int64_t C, uint8_t* q, 
  *   q4 : e2m1 [R, C/2]    q8 : e4m3 [R, C]      C a positive multiple of 32. */
 int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q8, void* stream);
 
-/* Bytes of workspace mx_few_linear needs; 0 for invalid dims.  Host-only. */
+/* Bytes of workspace mx_few_linear needs: 0 for one or two tokens that are not
+ * very long, and for invalid dims.  Host-only. */
 size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K);
 
 /* y = x W^T.
  *   x : bf16 [M, K]    w : codes of W[N, K]    e8 : E8M0 [N][K/32]    y : bf16 [M, N]
  * 1 <= M <= 32, N positive, K a positive multiple of 32, bits 4 or 8.
  * workspace: caller-owned DEVICE scratch of at least
- * mx_few_linear_workspace_bytes bytes, in any state; concurrent calls need one
- * each. */
+ * mx_few_linear_workspace_bytes bytes, in any state, NULL where that is 0;
+ * concurrent calls need one each. */
 int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N, int64_t K,
                   fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream);
 

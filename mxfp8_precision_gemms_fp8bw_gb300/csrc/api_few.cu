@@ -60,8 +60,7 @@ FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K) {
 FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
                             int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream) {
   const char* name = "mx_few_linear";
-  if (!x || !w || !e8 || !y || !workspace)
-    return fail(FP8BW_ERR_NULL, "%s: x, w, e8, y and workspace must be non-NULL", name);
+  if (!x || !w || !e8 || !y) return fail(FP8BW_ERR_NULL, "%s: x, w, e8 and y must be non-NULL", name);
   if (!linear_dims_ok(M, N, K))
     return fail(FP8BW_ERR_SHAPE,
                 "%s: need 0 < M <= 32, 0 < N < 2^31 and K a positive multiple of 32 up to 2^22; got M=%lld N=%lld "
@@ -70,10 +69,12 @@ FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t
   if (!all_aligned({x, w, e8, y, workspace})) return fail(FP8BW_ERR_ALIGN, "%s: pointers must be 16-byte aligned", name);
   if (!bits_ok(bits)) return fail(FP8BW_ERR_ARG, "%s: bits %d is neither 4 nor 8", name, bits);
   const size_t need = few_linear_workspace_bytes(M, K);
+  if (need > 0 && !workspace)
+    return fail(FP8BW_ERR_NULL, "%s: these dims need a workspace of %zu bytes", name, need);
   if (workspace_bytes < need)
     return fail(FP8BW_ERR_ARG, "%s: workspace of %zu bytes is smaller than the %zu bytes these dims need", name,
                 workspace_bytes, need);
-  if (any_overlap({{y, M * N * 2}, {workspace, static_cast<int64_t>(need)}},
+  if (any_overlap({{y, M * N * 2}, {need > 0 ? workspace : nullptr, static_cast<int64_t>(need)}},
                   {{x, M * K * 2}, {w, N * (K / 8) * bits}, {e8, N * (K / 32)}}))
     return fail(FP8BW_ERR_LAYOUT, "%s: y or the workspace overlaps an input or each other", name);
   DeviceState* d;

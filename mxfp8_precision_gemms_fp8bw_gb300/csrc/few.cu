@@ -31,8 +31,10 @@ using few::kAll;
 //            over an expert is drained from tensor memory, weighted and added
 //            to its tokens in shared memory               y
 //
-// Warps 0-3  drain the accumulators (warp w: rows 32 w ..)
-// Warps 4-7  copy the weights' scales, by cp.async
+// Warps 0-3  drain the accumulators (warp w: rows 32 w ..); a linear's one or
+//            two tokens they bring into parts at first
+// Warps 4-7  copy the weights' scales, by cp.async, and spread 4-bit codes
+//            that TMA brings as they are in memory
 // Warp  8    copies weights, by TMA
 // Warp  9    copies tokens, by bulk copies
 // Warp  10   brings the scales of a stage that has landed into tensor memory
@@ -49,9 +51,9 @@ constexpr int kWeights = kDrainWarps + kScaleWarps, kTokens = kWeights + 1, kSca
 constexpr int kThreads = (kIssuer + 1) * 32;
 
 // A stage of shared memory: codes of 128 rows, 128 bytes each with 128-byte swizzling (4-bit codes of 16 weights in the first
-// 8 bytes of 16, which is how the tensor core wants them); a record of tokens (few.h); and the weights' scales, row r's four
-// bytes as word (r % 32) * 4 + r / 32.
-constexpr uint32_t kCodes = kRows * 128, kScales = 512;
+// 8 bytes of 16, which is how the tensor core wants them); a record of tokens (few.h), where they are not in shared memory for
+// good; the weights' scales, row r's four bytes as word (r % 32) * 4 + r / 32; and room for 4-bit codes to be spread.
+constexpr uint32_t kCodes = kRows * 128, kScales = 512, kPacked = kRows * 64;
 
 struct Matrix {
   const uint8_t* w;   // codes
@@ -66,11 +68,15 @@ struct Product {
   int M, splits;
   bool late;            // the cluster's sums meet in the stages
   int slots;            // kDown: room for as many
-  bool tiled;           // weights come by TMA
-  int columns;          // room for token rows in a stage: a multiple of 16
+  bool packed;          // 4-bit weights land as they are in memory, for whole chunks of 128 only TMA can spread them
+  int columns;          // of an accumulator: token rows, a multiple of 16
+  uint32_t tokens;      // bytes of tokens in a stage
   uint32_t tmem;        // columns of tensor memory
   uint32_t stage;       // bytes
-  const uint8_t* t;     // records of tokens; kDown: of activations
+  int share;            // kLinear, one or two tokens: most chunks of a block,
+  uint32_t held_at;     // and where they are, behind the stages
+  const uint16_t* x;    // kLinear, one or two tokens: bf16 [M, K]
+  const uint8_t* t;     // otherwise records of tokens; kDown: of activations
   const FewPlan* plan;  // kUp, kDown
   int choices;          // of the plan
   uint8_t* act;         // kUp: records of activations
@@ -96,10 +102,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Whether a wait came to its end for all lanes: they go on, or unwind, together.
 __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 
+// A chunk of tokens that stay in shared memory, and the most of them: with four stages as much as two blocks an SM have.
+constexpr uint32_t kHeld = 16 * 128;
+constexpr int kMostHeld = 16;
 constexpr int kMostDepth = 4;
 struct Shared {
-  // Of a stage: it has landed, its scales are in tensor memory, it has been read.
-  uint64_t full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
+  // Of a stage: packed codes have landed, all of it has, its scales are in tensor memory, it has been read.
+  uint64_t landed[kMostDepth], full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
+  uint64_t tokens;                       // a linear's tokens are in shared memory
   uint64_t sum_full[2], sum_empty[2];    // an accumulator is complete, has been drained
   uint64_t drain[2];
   uint32_t tmem;
@@ -126,10 +136,12 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restr
   const int64_t pieces = K / 8;  // of 8 values, of a token
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~31);
   if (i0 >= pieces) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, r = static_cast<int>(blockIdx.y) * kTokenParts;
   const int64_t i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
-  few::split8(__ldg(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i), t, static_cast<int>(gridDim.y), i * 8,
-              static_cast<int>(blockIdx.y));
+  const int64_t rows = gridDim.y * kTokenParts;
+  few::split8(__ldg(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i),
+              [&](int part) { return few::code_at(t, rows, i * 8, r + part); },
+              [&](int part) { return few::scale_at(t, rows, i * 8, r + part); });
 }
 
 // A stage of the ring, as each role walks through it: which, and the parity of its next completion.
@@ -165,6 +177,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x2(uint32_t taddr, uint32_t (&r)[
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
 }
 
+// After a wait that expired: the last copies land before the block ends, or never will.
+template <int kDepth>
+__device__ void unwind(Ring<kDepth> ring, uint64_t* bars, int issued, int* status) {
+  int none = 0;
+  for (int i = min(issued, kDepth); i > 0; --i) {
+    if (--ring.s < 0) ring.s = kDepth - 1, ring.phase ^= 1;
+    mbar_wait(bars + ring.s, ring.phase, AbortFlag{&none}, status, 1000000ull);
+  }
+}
+
 template <Mode kMode, int kBits, int kDepth>
 __global__ void __launch_bounds__(kThreads, 2)
     few_kernel(const __grid_constant__ CUtensorMap weights_map, const __grid_constant__ Product p) {
@@ -172,23 +194,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kRowBytes = 16 * kBits;  // of a chunk in memory
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
-  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % p.splits, block = blockIdx.x / p.splits;
-  const int K = p.m.K, chunks = (K + kChunk - 1) / kChunk;
-  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind, and behind them its slots.
-  // What the cluster's other blocks send: behind, or, where two blocks an SM need the room, over the stages too, once all of
-  // the cluster's blocks have read theirs.
-  float* const sums = reinterpret_cast<float*>(kMode == kDown ? smem + kDepth * p.stage : smem);
-  float* const behind = reinterpret_cast<float*>(smem + kDepth * p.stage) + (kMode == kDown ? p.M * kRows : 0);
-  FewSlot* const table = reinterpret_cast<FewSlot*>(behind);
-  float* const received = p.late ? reinterpret_cast<float*>(smem) + (kMode == kDown ? 0 : p.M * kRows)
-                                 : behind + (kMode == kDown ? p.slots * 4 : 0);
-  const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
-
-  if (threadIdx.x == 0) {
+  const bool packed = kBits == 4 && p.packed, held = kMode == kLinear && p.x != nullptr;
+  if (warp == kWeights && lane == 0) {
+    tma_prefetch_desc(&weights_map);
     for (int s = 0; s < kDepth; ++s) {
-      mbar_init(&sh.full[s], kScaleWarps * (whole_words ? 32 : 64) + 1 + p.tiled);
+      if (packed) mbar_init(&sh.landed[s], 1);
+      mbar_init(&sh.full[s], kScaleWarps * 32 + !packed + !held);
       mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
@@ -198,57 +210,70 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
+    mbar_init(&sh.tokens, kDrainWarps);
     sh.abort = 0;
     fence_mbar_init();
   }
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  const uint32_t stage0 = smem_u32(smem);
+  const int rank = blockIdx.x % p.splits, block = blockIdx.x / p.splits;
+  const int K = p.m.K, chunks = (K + kChunk - 1) / kChunk;
+  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind, and behind them its slots.
+  // What the cluster's other blocks send: behind, or, where two blocks an SM need the room, over the stages too, once all of
+  // the cluster's blocks have read theirs.  A linear's tokens last.
+  float* const sums = reinterpret_cast<float*>(kMode == kDown ? smem + kDepth * p.stage : smem);
+  float* const behind = reinterpret_cast<float*>(smem + kDepth * p.stage) + (kMode == kDown ? p.M * kRows : 0);
+  FewSlot* const table = reinterpret_cast<FewSlot*>(behind);
+  float* const received = p.late ? reinterpret_cast<float*>(smem) + (kMode == kDown ? 0 : p.M * kRows)
+                                 : behind + (kMode == kDown ? p.slots * 4 : 0);
+  const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
+
   // What the plan says.  The plan is older than the kernel before this one, which waited for it before it let this one
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
   int slots = 1;
   FewSlot one{0, 0, 0xffffffffu >> (32 - p.M), p.M};
-  bool idle = false;
   if constexpr (kMode == kUp) {
     grid_wait();
     grid_release();
-    idle = static_cast<int>(blockIdx.y) >= few_active(p.plan);
-    one = few_slot(p.plan, p.choices, blockIdx.y);  // of an idle block: not read further
+    const int active = few_active(p.plan);
+    one = few_slot(p.plan, p.choices, blockIdx.y);
+    if (static_cast<int>(blockIdx.y) >= active) return;  // with its whole cluster
   } else if constexpr (kMode == kDown) {
     slots = few_active(p.plan);
-    for (int i = threadIdx.x; i < slots; i += kThreads) table[i] = few_slot(p.plan, p.choices, i);
-    for (int i = threadIdx.x; i < p.M * kRows; i += kThreads) sums[i] = 0.f;
   }
-  if (idle) return;  // with its whole cluster
-  __syncthreads();
-  if (p.splits > 1 && !p.late) cluster_arrive();  // the others may write to this block's memory once it runs
   const AbortFlag ab{&sh.abort};
   const auto slot_at = [&](int i) { return kMode == kDown ? table[i] : one; };
 
   // The block's chunks: t0 .. t1 of all matrices', one behind the other; in runs of one matrix.
-  const int all = slots * chunks;
-  const int t0 = static_cast<int>(static_cast<int64_t>(all) * rank / p.splits);
-  const int t1 = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / p.splits);
+  const uint32_t all = slots * chunks;
+  const int t0 = static_cast<int>(all * rank / p.splits), t1 = static_cast<int>(all * (rank + 1) / p.splits);
   const int slot0 = slots == 1 ? 0 : t0 / chunks, c0 = t0 - slot0 * chunks;
   const auto run_of = [&](int c, int t) { return min(chunks - c, t1 - t); };  // chunks of the run that begins with chunk c
   // The block's first row in a matrix (kUp: of each half), and its last valid row.
   const int tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t row0 = static_cast<int64_t>(block) * tile;
   const int last = static_cast<int>(min((kMode == kUp ? p.m.rows / 2 : p.m.rows) - row0, static_cast<int64_t>(tile))) - 1;
-  const uint32_t stage0 = smem_u32(smem);
-  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.columns * 128 + kScales;
+  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.tokens, packed_at = scales_at + kScales;
   // Rows of the tokens of a slot: kDown has those of its columns, the others every token's for every expert.
   const auto rows_of = [&](const FewSlot& s) { return (kMode == kDown ? s.n : p.M) * kParts; };
 
+  const uint32_t held_codes = stage0 + kDepth * p.stage + p.held_at, held_scales = held_codes + p.share * kHeld;
+
   if (warp >= kDrainWarps && warp < kWeights) {
     // ------------------------------------------------------------ scales of the weights
-    // Of a chunk a thread copies the four bytes of row tid.  4-bit codes that TMA does not take (rows of no whole chunks) are
-    // copied here as well: piece tid % 8 of rows tid / 8 + 16 j.
-    const int tid = threadIdx.x - kDrainWarps * 32, piece = tid & 7;
-    const uint32_t pitch = K / 8 * kBits, scale_pitch = K / 32;
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
+    // Of a chunk a thread copies the four bytes of row tid.
+    const int tid = threadIdx.x - kDrainWarps * 32;
+    const uint32_t scale_pitch = K / 32;
     const int64_t half = kMode == kUp ? p.m.rows / 2 : 0;  // from a row of gate to its row of up
-    const uint32_t to = (tid / 8) * 128 + ((piece ^ (tid / 8 & 7)) << 4);
     const int64_t scale_row = kMode == kUp ? min(tid & 63, last) + (tid >= 64 ? half : 0) : static_cast<int64_t>(min(tid, last));
     const uint32_t scale_to = scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
+    // Spreads the packed codes: pieces of 16 bytes, tid % 4 of rows tid / 4 + 32 j, to twice 8 bytes each.
+    const uint32_t spread_from = packed_at + tid * 16;
+    const uint32_t spread_to = (tid >> 2) * 128 + (((tid & 3) * 2 ^ (tid >> 2 & 7)) << 4);
 
-    // Where no word holds a row's four bytes: they come through registers, a chunk ahead.
+    // Where no word holds a row's four bytes: they come through registers, two chunks ahead.
     const auto scale_word = [&](int64_t s) {
       const int64_t word = s & ~int64_t{3};
       const uint32_t* at = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 8 && word + i < p.m.scale_end; ++i)
           (i < 4 ? lo : hi) |= static_cast<uint32_t>(p.m.e8[word + i]) << (i & 3) * 8;
       }
-      return __funnelshift_r(lo, hi, (static_cast<uint32_t>(s) & 3) * 8);
+      return make_uint2(lo, hi);
     };
 
     Ring<kDepth> ring;
@@ -268,11 +293,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     int c = c0, slot = slot0;
 #pragma unroll 1
     for (int t = t0; t < t1; ++slot, c = 0) {
-      const int64_t first = slot_at(slot).expert * p.m.rows + row0;
-      int64_t scale = (first + scale_row) * scale_pitch + c * 4;
-      uint32_t off = c * kRowBytes + piece * 8;
+      int64_t scale = (slot_at(slot).expert * p.m.rows + row0 + scale_row) * scale_pitch + c * 4;
       const int end = t + run_of(c, t);
-      uint32_t word = whole_words ? 0 : scale_word(scale);
+      const uint32_t shift = (static_cast<uint32_t>(scale) & 3) * 8;
+      uint2 words[2] = {};
+      if (!whole_words) {
+        words[0] = scale_word(scale);
+        if (t + 1 < end) words[1] = scale_word(scale + 4);
+      }
 #pragma unroll 1
       for (; t < end; ++t) {
         if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
@@ -280,97 +308,144 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         const uint32_t stage = stage0 + ring.s * p.stage;
-        if (kBits == 4 && !p.tiled && off < pitch) {  // the last chunk of a row may be short
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = tid / 8 + 16 * j;
-            const int64_t row = kMode == kUp ? min(r & 63, last) + (r >= 64 ? half : 0) : static_cast<int64_t>(min(r, last));
-            cp_async<8>(stage + to + j * 2048, p.m.w + (first + row) * pitch + off);
-          }
-        }
-        if (whole_words) {
+        if (whole_words && !packed) {
           cp_async<4>(stage + scale_to, p.m.e8 + scale);
+          cp_async_arrive(&sh.full[ring.s]);
         } else {
+          uint32_t word;
+          if (whole_words) {
+            word = __ldg(reinterpret_cast<const uint32_t*>(p.m.e8 + scale));
+          } else {
+            word = __funnelshift_r(words[0].x, words[0].y, shift);
+            words[0] = words[1];
+            if (t + 2 < end) words[1] = scale_word(scale + 8);
+          }
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(word) : "memory");
+          if (packed) {
+            if (!all_of(mbar_wait(&sh.landed[ring.s], ring.phase, ab, p.status))) {
+              t = t1;
+              break;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t v[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                           : "r"(stage + spread_from + j * 2048));
+              const uint32_t at = stage + spread_to + j * 4096;
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(v[0]), "r"(v[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at ^ 16), "r"(v[2]), "r"(v[3]) : "memory");
+            }
+          }
           mbar_arrive(&sh.full[ring.s]);
-          if (t + 1 < end) word = scale_word(scale + 4);
         }
-        cp_async_arrive(&sh.full[ring.s]);
-        off += kRowBytes, scale += 4;
+        scale += 4;
         ring.next();
         refill |= ring.s == 0;
       }
     }
     cp_async_wait_all();
-  } else if (warp == kWeights || warp == kTokens) {
-    // ------------------------------------------------------------ weights, tokens
-    const bool tokens = warp == kTokens;
-    if (lane == 0 && (tokens || p.tiled)) {
-      if (tokens && kMode != kUp) grid_wait();
-      if (tokens) fence_proxy_async_global();  // the kernel before wrote what the bulk copies read
+  } else if (warp == kWeights) {
+    // ------------------------------------------------------------ weights
+    Ring<kDepth> ring;
+    int t = t0, c = c0, slot = slot0, end = t0, issued = 0;
+    int32_t row = 0;
+    const auto begin_run = [&](const FewSlot& s) {
+      row = static_cast<int32_t>(s.expert * p.m.rows + row0);
+      end = t + run_of(c, t);
+    };
+    const auto load = [&]() {
+      const uint32_t stage = stage0 + ring.s * p.stage;
+      uint64_t* bar = packed ? &sh.landed[ring.s] : &sh.full[ring.s];
+      // Codes that TMA spreads out count as they are in memory.
+      mbar_arrive_expect_tx(bar, kRows * kRowBytes);
+      const uint32_t to = packed ? stage + packed_at : stage, half = packed ? kPacked / 2 : kCodes / 2;
+      const int x = c * (packed ? kChunk / 2 : kChunk);
+      tile_load(to, &weights_map, x, row, bar);
+      if (kMode == kUp) tile_load(to + half, &weights_map, x, row + static_cast<int32_t>(p.m.rows / 2), bar);
+      ring.next();
+      ++t, ++c, ++issued;
+    };
+    // The first chunks before the others of the block have come together.
+    if (lane == 0 && t0 < t1) {
+      begin_run(kMode == kDown ? few_slot(p.plan, p.choices, slot) : one);
+      while (t < end && issued < kDepth) load();
+    }
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
+    if (lane == 0) {
+      bool alive = true;
+#pragma unroll 1
+      while (t < t1) {
+        if (t == end) {
+          c = 0;
+          begin_run(slot_at(++slot));
+        }
+        if (issued >= kDepth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+          alive = false;
+          break;
+        }
+        load();
+      }
+      if (!alive) unwind(ring, packed ? sh.landed : sh.full, issued, p.status);
+    }
+    __syncwarp();
+  } else if (warp == kTokens) {
+    // ------------------------------------------------------------ tokens
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
+    if (lane == 0 && !held) {
+      if (kMode != kUp) grid_wait();
+      fence_proxy_async_global();  // the kernel before wrote what the bulk copies read
       Ring<kDepth> ring;
-      bool refill = false, alive = true;
+      bool alive = true;
       int c = c0, slot = slot0, issued = 0;
 #pragma unroll 1
       for (int t = t0; t < t1 && alive; ++slot, c = 0) {
         const FewSlot s = slot_at(slot);
         const uint32_t record = static_cast<uint32_t>(few_record(rows_of(s)));
         const uint8_t* from = p.t + (kMode == kDown ? few_act_at(slot, s.start, chunks) : 0) + static_cast<int64_t>(c) * record;
-        const int32_t row = static_cast<int32_t>(s.expert * p.m.rows + row0);
         const int end = t + run_of(c, t);
 #pragma unroll 1
-        for (; t < end; ++t, ++c, ++issued) {
-          if (refill && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+        for (; t < end; ++t, ++issued) {
+          if (issued >= kDepth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
             alive = false;
             break;
           }
-          const uint32_t stage = stage0 + ring.s * p.stage;
-          uint64_t* full = &sh.full[ring.s];
-          if (tokens) {
-            mbar_arrive_expect_tx(full, record);
-            bulk_load(stage + tokens_at, from, record, full);
-            from += record;
-          } else {
-            // Codes that TMA spreads out count as they are in memory.
-            mbar_arrive_expect_tx(full, kRows * kRowBytes);
-            tile_load(stage, &weights_map, c * kChunk, row, full);
-            if (kMode == kUp)
-              tile_load(stage + kCodes / 2, &weights_map, c * kChunk, row + static_cast<int32_t>(p.m.rows / 2), full);
-          }
+          mbar_arrive_expect_tx(&sh.full[ring.s], record);
+          bulk_load(stage0 + ring.s * p.stage + tokens_at, from, record, &sh.full[ring.s]);
+          from += record;
           ring.next();
-          refill |= ring.s == 0;
         }
       }
-      if (!alive) {  // what is under way lands before the block ends, or never will
-        int none = 0;
-        for (int i = min(issued, kDepth); i > 0; --i) {
-          if (--ring.s < 0) ring.s = kDepth - 1, ring.phase ^= 1;
-          mbar_wait(&sh.full[ring.s], ring.phase, AbortFlag{&none}, p.status, 1000000ull);
-        }
-      }
+      if (!alive) unwind(ring, sh.full, issued, p.status);
     }
     __syncwarp();
   } else if (warp == kScaler) {
     // ------------------------------------------------------------ scales
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
     // cp.async wrote what the tensor core reads: the fence between the two, and the copies, stay off the thread that issues
     // the products (together 250 to 800 cycles a chunk).
     named_sync<(kDrainWarps + 2) * 32>();
     tc_fence_after();
     const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (kMode == kDown ? 2 : 1) * p.columns;
-    const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at), sb0 = sdesc_plain_128b_rows(stage0 + tokens_at);
+    const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at);
+    const uint64_t sb0 = sdesc_plain_128b_rows(held ? held_scales : stage0 + tokens_at);
     const bool elected = elect_one();
     Ring<kDepth> ring;
+    if (held && !all_of(mbar_wait(&sh.tokens, 0, ab, p.status))) sh.abort = 1;
 #pragma unroll 1
     for (int t = t0, c = c0, slot = slot0; t < t1; ++t) {
       if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) break;
       fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
-      const uint64_t rows = static_cast<uint64_t>(rows_of(slot_at(slot)));
+      const uint64_t sb = held ? sb0 + (t - t0) * (kScales >> 4) : sb0 + stage + rows_of(slot_at(slot)) * (128 >> 4);
       if (elected) {
         // The columns were last read by products that were complete before the stage was filled again.
         tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
-        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb0 + stage + rows * (128 >> 4));
+        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb);
         mma_commit(&sh.ready[ring.s]);
       }
       __syncwarp();
@@ -385,6 +460,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
     tmem_alloc(&sh.tmem, p.tmem);
     tmem_relinquish();
     tc_fence_before();
@@ -392,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     // All lanes walk through the loop, so that what the products take stays in uniform registers; one issues them.
     const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + (kMode == kDown ? 2 : 1) * p.columns;
-    const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(stage0 + tokens_at);
+    const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(held ? held_codes : stage0 + tokens_at);
     const bool elected = elect_one();
     bool alive = true;
     Ring<kDepth> ring;
@@ -415,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
         const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
-        const uint64_t a = a0 + stage, b = b0 + stage;
+        const uint64_t a = a0 + stage, b = b0 + (held ? static_cast<uint64_t>((t - t0) * (kHeld >> 4)) : stage);
         if (elected) {
           mma_mx_e4m3(acc, a, b, kind, sfa, sfb, more);
           if (left > 1) mma_mx_e4m3_k<true>(acc, a + 2, b + 2, kind | idesc_mx_e4m3(0, 0, 1, 1), sfa, sfb);
@@ -438,6 +515,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums
+    if constexpr (kMode == kDown) {
+      for (int i = threadIdx.x; i < slots; i += kDrainWarps * 32) table[i] = few_slot(p.plan, p.choices, i);
+      for (int i = threadIdx.x; i < p.M * kRows; i += kDrainWarps * 32) sums[i] = 0.f;
+    }
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();
+    if (held) {
+      // One or two tokens: the block's share of them stays in shared memory, in tiles of 16 rows.
+      const int pieces = (min(t1 * kChunk, K) - t0 * kChunk) / 8, work = pieces * p.M;  // of 8 values
+#pragma unroll 1
+      for (int i0 = warp * 32; i0 < work; i0 += kDrainWarps * 32) {
+        const int i = i0 + lane < work ? i0 + lane : i0 + lane % 4;  // past the end the same four again
+        const int token = i >= pieces, k = (i - token * pieces) * 8, r = token * kTokenParts, b = k & 127;
+        uint8_t* codes = smem + (held_codes - stage0) + (k >> 7) * kHeld;
+        uint8_t* scales = smem + (held_scales - stage0) + (k >> 7) * kScales;
+        few::split8(
+            __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * K + t0 * kChunk + k)),
+            [&](int part) { return codes + (r + part) * 128 + (((b >> 4) ^ (r + part)) << 4) + (b & 15); },
+            [&](int part) { return scales + (r + part) * 16 + (b >> 5); });
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.tokens);
+    }
     named_sync<(kDrainWarps + 2) * 32>();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
@@ -561,21 +661,22 @@ int splits_of(int64_t tiles, int64_t chunks, int64_t slots) {
   return best;
 }
 
-// The weights as TMA reads them: boxes of `box` rows by 128.  False where it does not: 4-bit codes are spread out on the way,
-// for which it wants whole chunks of 128 and 32-byte alignment.
-bool weights_map(CUtensorMap* map, const Matrix& m, int64_t rows, int bits, uint32_t box) {
+// The weights as TMA reads them, boxes of `box` rows by a chunk: e4m3 codes as bytes; e2m1 codes spread out, or, where rows are
+// not whole chunks of 128 or not aligned to 32 bytes, which that takes, as bytes.
+bool weights_map(CUtensorMap* map, const Matrix& m, int64_t rows, int bits, bool packed, uint32_t box) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  if (bits == 4 && (m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(m.w) & 31) != 0)) return false;
   const auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(m.K / 8 * bits)};
-  const cuuint32_t boxes[2] = {kChunk, box}, each[2] = {1, 1};
-  return fn(map, bits == 4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-            const_cast<uint8_t*>(m.w), dims, strides, boxes, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const int64_t bytes = m.K / 8 * bits;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(packed ? bytes : m.K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(bytes)};
+  const cuuint32_t boxes[2] = {packed ? kChunk / 2u : kChunk, box}, each[2] = {1, 1};
+  return fn(map, bits == 8 || packed ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2,
+            const_cast<uint8_t*>(m.w), dims, strides, boxes, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            packed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <Mode kMode, int kBits, int kDepth>
@@ -596,15 +697,15 @@ cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attrs;
-  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attrs[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
+  if (p.x == nullptr) {  // there is a kernel before that lets this one start
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   if (p.splits > 1) {
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = p.splits;
-    attrs[1].val.clusterDim.y = 1;
-    attrs[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attrs[cfg.numAttrs].val.clusterDim.x = p.splits;
+    attrs[cfg.numAttrs].val.clusterDim.y = 1;
+    attrs[cfg.numAttrs++].val.clusterDim.z = 1;
   }
   return cudaLaunchKernelEx(&cfg, kernel, map, p);
 }
@@ -619,22 +720,34 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   const uint32_t columns = (kMode == kDown ? 2 : 1) * p.columns + kMostDepth * 8;
   p.tmem = 32;
   while (p.tmem < columns) p.tmem *= 2;
-  p.stage = kCodes + (p.columns * 128 + 2 * kScales);
+  const int chunks = (p.m.K + kChunk - 1) / kChunk;
+  p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
+  p.tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales;
+  p.stage = (kCodes + p.tokens + kScales + (p.packed ? kPacked : 0) + 1023) / 1024 * 1024;
   // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
   const uint32_t received = (p.M * kRows + 7 * 64) * 4;
   p.late = p.M > 16;
   p.slots = matrices;
   const uint32_t behind = (p.late ? 0 : received) +
                           (kMode == kDown ? p.M * kRows * 4 + matrices * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
-  const auto smem = [&](int depth) { return 1024 + depth * p.stage + behind; };
+  const auto splits = [&](int per_sm) {
+    return splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, num_sms * per_sm);
+  };
+  if (p.x != nullptr) {
+    const int least = (chunks + kMostHeld - 1) / kMostHeld;
+    p.splits = splits(2) > least ? splits(2) : least;
+    p.share = (chunks + p.splits - 1) / p.splits;
+    p.held_at = (behind + 1023) / 1024 * 1024;
+  }
+  const uint32_t held = p.held_at + p.share * (kHeld + kScales);
+  const auto smem = [&](int depth) { return 1024 + depth * p.stage + (p.x != nullptr ? held : behind); };
   // Two blocks an SM, with three stages where four are too many for that.
   const int depth = smem(4) > kHalfSmem && smem(3) <= kHalfSmem ? 3 : 4;
-  p.splits = splits_of(tiles * copies, static_cast<int64_t>((p.m.K + kChunk - 1) / kChunk) * matrices,
-                       num_sms * (smem(depth) <= kHalfSmem ? 2 : 1));
+  if (p.x == nullptr) p.splits = splits(smem(depth) <= kHalfSmem ? 2 : 1);
+  if (smem(depth) > kMostSmem) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
   CUtensorMap map{};
-  p.tiled = weights_map(&map, p.m, experts * p.m.rows, kBits, static_cast<uint32_t>(tile));
-  if (kBits == 8 && !p.tiled) return cudaErrorInvalidValue;
+  if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, static_cast<uint32_t>(tile))) return cudaErrorInvalidValue;
   return depth == 3 ? launch<kMode, kBits, 3>(map, p, smem(3), grid, st) : launch<kMode, kBits, 4>(map, p, smem(4), grid, st);
 }
 
@@ -649,18 +762,26 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 
 }  // namespace
 
-size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return few_tokens_bytes(M, K); }
+// One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages.
+static bool held_tokens(int64_t M, int64_t K) { return M <= 2 && K <= 8 * kMostHeld * kChunk; }
+
+size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return held_tokens(M, K) ? 0 : few_tokens_bytes(M, K); }
 
 cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   Product p{};
   p.m = Matrix{a.w, a.e8, a.N * (a.K / 32), a.N, static_cast<int>(a.K)};
   p.M = static_cast<int>(a.M);
-  p.t = static_cast<uint8_t*>(a.workspace);
   p.y = a.y;
   p.status = a.status;
-  const dim3 grid(static_cast<unsigned>((a.K / 8 + 255) / 256), static_cast<unsigned>(a.M));
-  few_tokens_kernel<<<grid, 256, 0, st>>>(a.x, a.K, static_cast<uint8_t*>(a.workspace));
-  if (const cudaError_t e = cudaGetLastError()) return e;
+  if (held_tokens(a.M, a.K)) {
+    p.x = a.x;
+  } else {
+    uint8_t* tokens = static_cast<uint8_t*>(a.workspace);
+    p.t = tokens;
+    const dim3 grid(static_cast<unsigned>((a.K / 8 + 255) / 256), static_cast<unsigned>(a.M));
+    few_tokens_kernel<<<grid, 256, 0, st>>>(a.x, a.K, tokens);
+    if (const cudaError_t e = cudaGetLastError()) return e;
+  }
   return launch_product<kLinear>(p, a.bits, 1, 1, 1, a.num_sms, st);
 }
 

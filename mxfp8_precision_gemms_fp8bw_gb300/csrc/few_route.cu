@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
 #pragma unroll 1
       for (int i0 = (warp - kMostRows) * 32; i0 < pieces; i0 += (kWarps - kMostRows) * 32) {
         const int i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
-        few::split8(__ldg(row + i), p.held, M, i * 8, t);
+        few::split8(
+            __ldg(row + i), [&](int part) { return few::code_at(p.held, M * kTokenParts, i * 8, t * kTokenParts + part); },
+            [&](int part) { return few::scale_at(p.held, M * kTokenParts, i * 8, t * kTokenParts + part); });
       }
     }
   }

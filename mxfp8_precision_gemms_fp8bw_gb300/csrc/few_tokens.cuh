@@ -32,8 +32,10 @@ __device__ __forceinline__ uint8_t* scale_at(uint8_t* records, int64_t rows, int
   return records + (k >> 7) * few_record(rows) + rows * 128 + (r & 31) * 16 + (r >> 5) * 4 + ((k & 127) >> 5);
 }
 
-// Values k .. k + 7 of token t of M, of a block that four neighbouring lanes hold, in kTokenParts parts.
-__device__ __forceinline__ void split8(uint4 v, uint8_t* records, int M, int64_t k, int t) {
+// Eight values of a block that four neighbouring lanes hold, in kTokenParts parts: codes to code(part), and by the first of
+// the four the block's byte to scale(part).
+template <typename Code, typename Scale>
+__device__ __forceinline__ void split8(uint4 v, Code&& code, Scale&& scale) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float f[8];
 #pragma unroll
@@ -53,9 +55,8 @@ __device__ __forceinline__ void split8(uint4 v, uint8_t* records, int M, int64_t
     uint2 q;
     q.x = e4m3x4(f[0] * down, f[1] * down, f[2] * down, f[3] * down);
     q.y = e4m3x4(f[4] * down, f[5] * down, f[6] * down, f[7] * down);
-    const int r = t * kTokenParts + part;
-    *reinterpret_cast<uint2*>(code_at(records, M * kTokenParts, k, r)) = q;
-    if ((threadIdx.x & 3) == 0) *scale_at(records, M * kTokenParts, k, r) = static_cast<uint8_t>(byte);
+    *reinterpret_cast<uint2*>(code(part)) = q;
+    if ((threadIdx.x & 3) == 0) *scale(part) = static_cast<uint8_t>(byte);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 g = e4m3x2_to_f32((i < 2 ? q.x : q.y) >> (i & 1) * 16);

@@ -54,9 +54,9 @@ def mx_few_linear_workspace_bytes(M: int, K: int) -> int:
     return int(lib().mx_few_linear_workspace_bytes(M, K))
 
 
-def mx_few_linear(x, w, e8, bits, y, workspace, stream=None) -> None:
+def mx_few_linear(x, w, e8, bits, y, workspace=None, stream=None) -> None:
     M, K = x.shape
-    N, n = w.shape[0], workspace.shape[0]
+    N, n = w.shape[0], 0 if workspace is None else workspace.shape[0]
     B._check(lib().mx_few_linear(_arg(x, _BF16, "x", M, K), _arg(w, _U8, "w", N, K * bits // 8),
                                  _arg(e8, _U8, "e8", N, K // 32), bits, M, N, K, _arg(y, _BF16, "y", M, N),
                                  _arg(workspace, _U8, "workspace", n), n, _stream(stream, x)))

@@ -222,16 +222,12 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     M, K = x.shape
     y = torch.empty((M, q.shape[0]), dtype=torch.bfloat16, device=x.device)
     if M > 0:
-        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(_few_workspace(M, K), dtype=torch.uint8, device=x.device), stream)
+        n = _few_workspace(M, K)
+        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(n, dtype=torch.uint8, device=x.device) if n else None, stream)
     return y
 
 
-@functools.lru_cache(maxsize=256)
-def _few_workspace(M: int, K: int) -> int:
-    n = FB.mx_few_linear_workspace_bytes(M, K)
-    if n == 0:
-        raise B.Fp8bwError(B.ERR_SHAPE, f"invalid dims of mx_linear_few: {M} tokens (at most {FB.FEW_TOKENS}) of {K} features")
-    return n
+_few_workspace = functools.lru_cache(maxsize=256)(FB.mx_few_linear_workspace_bytes)  # by the dims alone
 
 
 # ------------------------------------------------------------------ preallocated step

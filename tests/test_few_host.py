@@ -64,7 +64,7 @@ def test_linear_refusals(lib, code, kw):
 
 def test_linear_workspace(lib):
     size = lib.mx_few_linear_workspace_bytes
-    assert size(1, 32) > 0 and size(32, 5120) >= 32 * 5120 * 2
+    assert size(2, 5120) == 0 and size(32, 5120) >= 32 * 5120 * 2 and size(1, 1 << 20) >= 2 << 20
     assert size(0, 5120) == size(33, 5120) == size(32, 5100) == size(32, (1 << 22) + 32) == 0
 
 
