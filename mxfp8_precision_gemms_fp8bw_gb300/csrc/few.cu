@@ -20,16 +20,19 @@ namespace {
 
 using few::kAll;
 
-// A block owns 128 rows and walks through its share of the contraction in
-// chunks of 128; the `splits` blocks of a cluster have a share each, and their
-// sums meet in distributed shared memory, in the order of the blocks.
+// A block walks through runs: 128 rows of a matrix by a stretch of its
+// contraction, in chunks of 128.
 //
-//   kLinear  one matrix                                   y
-//   kUp      the matrix of one active expert (grid.y), 64 rows of gate and the
-//            64 of up that go with them                   the activation, in three parts
-//   kDown    the matrices of all active experts, one behind the other; the sum
-//            over an expert is drained from tensor memory, weighted and added
-//            to its tokens in shared memory               y
+//   kLinear  one run of the one matrix                    y
+//   kUp      64 rows of gate and the 64 of up that go with them, of an active
+//            expert: one run, or, where there are many, whole ones of tiles
+//            and experts in turn                          the activation, in three parts
+//   kDown    128 rows of all active experts, one run behind the other; the sum
+//            over each is drained from tensor memory, weighted and added to its
+//            tokens in shared memory                      y
+//
+// The `splits` blocks of a cluster share the contraction, and their sums meet
+// in distributed shared memory, in the order of the blocks.
 //
 // Warps 0-3  drain the accumulators (warp w: rows 32 w ..); a linear's one or
 //            two tokens they bring into parts at first
@@ -65,7 +68,8 @@ struct Matrix {
 
 struct Product {
   Matrix m;
-  int M, splits;
+  int M, splits, depth;  // depth: stages
+  int tiles;            // kUp, in turn: tiles of an expert; else 0
   bool late;            // the cluster's sums meet in the stages
   int slots;            // kDown: room for as many
   bool packed;          // 4-bit weights land as they are in memory, for whole chunks of 128 only TMA can spread them
@@ -105,7 +109,7 @@ __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 // A chunk of tokens that stay in shared memory, and the most of them: with four stages as much as two blocks an SM have.
 constexpr uint32_t kHeld = 16 * 128;
 constexpr int kMostHeld = 16;
-constexpr int kMostDepth = 4;
+constexpr int kMostDepth = 8;
 struct Shared {
   // Of a stage: packed codes have landed, all of it has, its scales are in tensor memory, it has been read.
   uint64_t landed[kMostDepth], full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
@@ -118,10 +122,10 @@ struct Shared {
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
-// Barrier 1, for the warps that use tensor memory.
-template <int kCount>
+// Barrier 1 is for the warps that use tensor memory, 2 for those that drain it.
+template <int kBarrier, int kCount>
 __device__ __forceinline__ void named_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"n"(kBarrier), "n"(kCount) : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -131,27 +135,34 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // x [M, K] in parts.
-__global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* __restrict__ x, int64_t K, uint8_t* t) {
-  grid_release();
+__global__ void __launch_bounds__(256) few_tokens_kernel(const uint16_t* x, int64_t K, uint8_t* t) {
+  grid_wait();
+  grid_release();  // after the wait: the product reads weights that kernels before this one may have written
   const int64_t pieces = K / 8;  // of 8 values, of a token
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~31);
   if (i0 >= pieces) return;
   const int lane = threadIdx.x & 31, r = static_cast<int>(blockIdx.y) * kTokenParts;
   const int64_t i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
   const int64_t rows = gridDim.y * kTokenParts;
-  few::split8(__ldg(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i),
+  few::split8(load_after(reinterpret_cast<const uint4*>(x + blockIdx.y * K) + i),
               [&](int part) { return few::code_at(t, rows, i * 8, r + part); },
               [&](int part) { return few::scale_at(t, rows, i * 8, r + part); });
 }
 
 // A stage of the ring, as each role walks through it: which, and the parity of its next completion.
-template <int kDepth>
 struct Ring {
-  int s = 0;
+  int depth, s = 0;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int n) : depth(n) {}
   __device__ __forceinline__ void next() {
-    if (++s == kDepth) s = 0, phase ^= 1;
+    if (++s == depth) s = 0, phase ^= 1;
   }
+};
+
+// A run of a block: rows of tile `block` of the matrix of slot `at`, chunks c .. c + n.
+struct Run {
+  FewSlot slot;
+  int at, block, c, n;
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -177,17 +188,24 @@ __device__ __forceinline__ void tmem_ld_32x32b_x2(uint32_t taddr, uint32_t (&r)[
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
 }
 
+// kUp: element `lane` of a block of 32 of the activation, of column `column` of the run's slot.
+__device__ void activate(const Product& p, const Run& r, int column, int i, float gate, float up) {
+  const int64_t F = p.m.rows / 2, f = static_cast<int64_t>(r.block) * (kRows / 2) + i * 32;
+  if (f >= F) return;
+  few::split1(gate / (1.f + expf(-gate)) * up, p.act + few_act_at(r.at, r.slot.start, few_chunks(F)), r.slot.n,
+              f + (threadIdx.x & 31), column);
+}
+
 // After a wait that expired: the last copies land before the block ends, or never will.
-template <int kDepth>
-__device__ void unwind(Ring<kDepth> ring, uint64_t* bars, int issued, int* status) {
+__device__ void unwind(Ring ring, uint64_t* bars, int issued, int* status) {
   int none = 0;
-  for (int i = min(issued, kDepth); i > 0; --i) {
-    if (--ring.s < 0) ring.s = kDepth - 1, ring.phase ^= 1;
+  for (int i = min(issued, ring.depth); i > 0; --i) {
+    if (--ring.s < 0) ring.s = ring.depth - 1, ring.phase ^= 1;
     mbar_wait(bars + ring.s, ring.phase, AbortFlag{&none}, status, 1000000ull);
   }
 }
 
-template <Mode kMode, int kBits, int kDepth>
+template <Mode kMode, int kBits>
 __global__ void __launch_bounds__(kThreads, 2)
     few_kernel(const __grid_constant__ CUtensorMap weights_map, const __grid_constant__ Product p) {
   constexpr int kParts = kMode == kDown ? kActParts : kTokenParts;
@@ -195,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool packed = kBits == 4 && p.packed, held = kMode == kLinear && p.x != nullptr;
+  const bool packed = kBits == 4 && p.packed, held = kMode == kLinear && p.x != nullptr, in_turn = kMode == kUp && p.tiles > 0;
   if (warp == kWeights && lane == 0) {
     tma_prefetch_desc(&weights_map);
-    for (int s = 0; s < kDepth; ++s) {
+    for (int s = 0; s < p.depth; ++s) {
       if (packed) mbar_init(&sh.landed[s], 1);
       mbar_init(&sh.full[s], kScaleWarps * 32 + !packed + !held);
       mbar_init(&sh.ready[s], 1);
@@ -216,17 +234,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t stage0 = smem_u32(smem);
-  const int rank = blockIdx.x % p.splits, block = blockIdx.x / p.splits;
+  const int rank = blockIdx.x % p.splits;
   const int K = p.m.K, chunks = (K + kChunk - 1) / kChunk;
-  // Sums [M][128]: over the stages, once those have been read; kDown, which adds to them: behind, and behind them its slots.
-  // What the cluster's other blocks send: behind, or, where two blocks an SM need the room, over the stages too, once all of
-  // the cluster's blocks have read theirs.  A linear's tokens last.
-  float* const sums = reinterpret_cast<float*>(kMode == kDown ? smem + kDepth * p.stage : smem);
-  float* const behind = reinterpret_cast<float*>(smem + kDepth * p.stage) + (kMode == kDown ? p.M * kRows : 0);
+  // Sums [M][128]: over the stages, once those have been read; where there are more runs, behind them.  Then slots, and what the
+  // cluster's other blocks send (or over the stages too, where two blocks an SM need the room, once all of the cluster's blocks
+  // have read theirs).  A linear's tokens last.
+  const bool many = kMode == kDown || in_turn;
+  float* const sums = reinterpret_cast<float*>(many ? smem + p.depth * p.stage : smem);
+  float* const behind = reinterpret_cast<float*>(smem + p.depth * p.stage) + (many ? p.M * kRows : 0);
   FewSlot* const table = reinterpret_cast<FewSlot*>(behind);
-  float* const received = p.late ? reinterpret_cast<float*>(smem) + (kMode == kDown ? 0 : p.M * kRows)
-                                 : behind + (kMode == kDown ? p.slots * 4 : 0);
-  const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
+  float* const received = p.late ? reinterpret_cast<float*>(smem) + (many ? 0 : p.M * kRows) : behind + p.slots * 4;
 
   // What the plan says.  The plan is older than the kernel before this one, which waited for it before it let this one
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
@@ -235,39 +252,58 @@ __global__ void __launch_bounds__(kThreads, 2)
   if constexpr (kMode == kUp) {
     grid_wait();
     grid_release();
-    const int active = few_active(p.plan);
-    one = few_slot(p.plan, p.choices, blockIdx.y);
-    if (static_cast<int>(blockIdx.y) >= active) return;  // with its whole cluster
+    slots = few_active(p.plan);
+    if (!in_turn) {
+      one = few_slot(p.plan, p.choices, blockIdx.y);
+      if (static_cast<int>(blockIdx.y) >= slots) return;  // with its whole cluster
+    } else if (static_cast<int>(blockIdx.x) >= slots * p.tiles) {
+      return;
+    }
   } else if constexpr (kMode == kDown) {
     slots = few_active(p.plan);
   }
   const AbortFlag ab{&sh.abort};
-  const auto slot_at = [&](int i) { return kMode == kDown ? table[i] : one; };
 
-  // The block's chunks: t0 .. t1 of all matrices', one behind the other; in runs of one matrix.
-  const uint32_t all = slots * chunks;
-  const int t0 = static_cast<int>(all * rank / p.splits), t1 = static_cast<int>(all * (rank + 1) / p.splits);
-  const int slot0 = slots == 1 ? 0 : t0 / chunks, c0 = t0 - slot0 * chunks;
-  const auto run_of = [&](int c, int t) { return min(chunks - c, t1 - t); };  // chunks of the run that begins with chunk c
-  // The block's first row in a matrix (kUp: of each half), and its last valid row.
+  // The runs.  t0 .. t1: the block's chunks of all matrices' one behind the other; in turn: runs.
+  const uint32_t all = (kMode == kDown ? slots : 1) * chunks;
+  const int t0 = in_turn ? blockIdx.x : static_cast<int>(all * rank / p.splits);
+  const int t1 = in_turn ? slots * p.tiles : static_cast<int>(all * (rank + 1) / p.splits);
+  const auto run_at = [&](int t, bool from_plan) {
+    Run r;
+    if (in_turn) {
+      r.at = t / p.tiles, r.block = t - r.at * p.tiles, r.c = 0, r.n = chunks;
+    } else {
+      r.at = kMode == kDown && slots > 1 ? t / chunks : 0;
+      r.block = blockIdx.x / p.splits, r.c = t - r.at * chunks, r.n = min(chunks - r.c, t1 - t);
+    }
+    r.slot = !many ? one : from_plan ? few_slot(p.plan, p.choices, r.at) : table[r.at];
+    return r;
+  };
+  const auto after = [&](int t, const Run& r) { return t + (in_turn ? static_cast<int>(gridDim.x) : r.n); };
+  // A block's first row in a matrix (kUp: of each half), and its last valid row.
   const int tile = kMode == kUp ? kRows / 2 : kRows;
-  const int64_t row0 = static_cast<int64_t>(block) * tile;
-  const int last = static_cast<int>(min((kMode == kUp ? p.m.rows / 2 : p.m.rows) - row0, static_cast<int64_t>(tile))) - 1;
+  const int64_t half = kMode == kUp ? p.m.rows / 2 : 0;  // from a row of gate to its row of up
+  const auto row_of = [&](const Run& r) { return static_cast<int64_t>(r.block) * tile; };
+  const auto last_of = [&](const Run& r) {
+    return static_cast<int>(min((kMode == kUp ? half : p.m.rows) - row_of(r), static_cast<int64_t>(tile))) - 1;
+  };
   const uint32_t tokens_at = kCodes, scales_at = kCodes + p.tokens, packed_at = scales_at + kScales;
   // Rows of the tokens of a slot: kDown has those of its columns, the others every token's for every expert.
   const auto rows_of = [&](const FewSlot& s) { return (kMode == kDown ? s.n : p.M) * kParts; };
-
-  const uint32_t held_codes = stage0 + kDepth * p.stage + p.held_at, held_scales = held_codes + p.share * kHeld;
+  const uint32_t held_codes = stage0 + p.depth * p.stage + p.held_at, held_scales = held_codes + p.share * kHeld;
+  const auto come_together = [&]() {
+    __syncthreads();
+    if (p.splits > 1 && !p.late) cluster_arrive();  // the others may write to this block's memory once it runs
+  };
 
   if (warp >= kDrainWarps && warp < kWeights) {
     // ------------------------------------------------------------ scales of the weights
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    come_together();
+    if (held) grid_wait();
     // Of a chunk a thread copies the four bytes of row tid.
     const int tid = threadIdx.x - kDrainWarps * 32;
     const uint32_t scale_pitch = K / 32;
-    const int64_t half = kMode == kUp ? p.m.rows / 2 : 0;  // from a row of gate to its row of up
-    const int64_t scale_row = kMode == kUp ? min(tid & 63, last) + (tid >= 64 ? half : 0) : static_cast<int64_t>(min(tid, last));
+    const bool whole_words = K % kChunk == 0;  // a row's scale bytes are whole words
     const uint32_t scale_to = scales_at + (tid & 31) * 16 + (tid >> 5) * 4;
     // Spreads the packed codes: pieces of 16 bytes, tid % 4 of rows tid / 4 + 32 j, to twice 8 bytes each.
     const uint32_t spread_from = packed_at + tid * 16;
@@ -279,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t* at = reinterpret_cast<const uint32_t*>(p.m.e8 + word);
       uint32_t lo = 0, hi = 0;
       if (word + 8 <= p.m.scale_end) {
-        lo = __ldg(at), hi = __ldg(at + 1);
+        lo = load_after(at), hi = load_after(at + 1);
       } else {  // the array's last bytes, one by one
 #pragma unroll 1
         for (int i = 0; i < 8 && word + i < p.m.scale_end; ++i)
@@ -288,23 +324,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       return make_uint2(lo, hi);
     };
 
-    Ring<kDepth> ring;
-    bool refill = false;
-    int c = c0, slot = slot0;
+    Ring ring(p.depth);
+    bool refill = false, alive = true;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++slot, c = 0) {
-      int64_t scale = (slot_at(slot).expert * p.m.rows + row0 + scale_row) * scale_pitch + c * 4;
-      const int end = t + run_of(c, t);
+    for (int t = t0; t < t1 && alive;) {
+      const Run r = run_at(t, false);
+      t = after(t, r);
+      const int last = last_of(r);
+      const int64_t row = row_of(r) + (kMode == kUp ? min(tid & 63, last) + (tid >= 64 ? half : 0) : min(tid, last));
+      int64_t scale = (r.slot.expert * p.m.rows + row) * scale_pitch + r.c * 4;
       const uint32_t shift = (static_cast<uint32_t>(scale) & 3) * 8;
       uint2 words[2] = {};
       if (!whole_words) {
         words[0] = scale_word(scale);
-        if (t + 1 < end) words[1] = scale_word(scale + 4);
+        if (r.n > 1) words[1] = scale_word(scale + 4);
       }
 #pragma unroll 1
-      for (; t < end; ++t) {
+      for (int i = 0; i < r.n; ++i) {
         if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
-          t = t1;
+          alive = false;
           break;
         }
         const uint32_t stage = stage0 + ring.s * p.stage;
@@ -314,16 +352,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
           uint32_t word;
           if (whole_words) {
-            word = __ldg(reinterpret_cast<const uint32_t*>(p.m.e8 + scale));
+            word = load_after(reinterpret_cast<const uint32_t*>(p.m.e8 + scale));
           } else {
             word = __funnelshift_r(words[0].x, words[0].y, shift);
             words[0] = words[1];
-            if (t + 2 < end) words[1] = scale_word(scale + 8);
+            if (i + 2 < r.n) words[1] = scale_word(scale + 8);
           }
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(word) : "memory");
           if (packed) {
             if (!all_of(mbar_wait(&sh.landed[ring.s], ring.phase, ab, p.status))) {
-              t = t1;
+              alive = false;
               break;
             }
 #pragma unroll
@@ -347,41 +385,44 @@ __global__ void __launch_bounds__(kThreads, 2)
     cp_async_wait_all();
   } else if (warp == kWeights) {
     // ------------------------------------------------------------ weights
-    Ring<kDepth> ring;
-    int t = t0, c = c0, slot = slot0, end = t0, issued = 0;
+    Ring ring(p.depth);
+    int t = t0, issued = 0;
+    Run r{};
     int32_t row = 0;
-    const auto begin_run = [&](const FewSlot& s) {
-      row = static_cast<int32_t>(s.expert * p.m.rows + row0);
-      end = t + run_of(c, t);
+    const auto begin_run = [&](bool from_plan) {
+      r = run_at(t, from_plan);
+      t = after(t, r);
+      row = static_cast<int32_t>(r.slot.expert * p.m.rows + row_of(r));
     };
     const auto load = [&]() {
       const uint32_t stage = stage0 + ring.s * p.stage;
       uint64_t* bar = packed ? &sh.landed[ring.s] : &sh.full[ring.s];
       // Codes that TMA spreads out count as they are in memory.
       mbar_arrive_expect_tx(bar, kRows * kRowBytes);
-      const uint32_t to = packed ? stage + packed_at : stage, half = packed ? kPacked / 2 : kCodes / 2;
-      const int x = c * (packed ? kChunk / 2 : kChunk);
+      const uint32_t to = packed ? stage + packed_at : stage, second = to + (packed ? kPacked / 2 : kCodes / 2);
+      const int x = r.c * (packed ? kChunk / 2 : kChunk);
       tile_load(to, &weights_map, x, row, bar);
-      if (kMode == kUp) tile_load(to + half, &weights_map, x, row + static_cast<int32_t>(p.m.rows / 2), bar);
+      if (kMode == kUp) tile_load(second, &weights_map, x, row + static_cast<int32_t>(half), bar);
       ring.next();
-      ++t, ++c, ++issued;
+      ++r.c, --r.n, ++issued;
     };
     // The first chunks before the others of the block have come together.
-    if (lane == 0 && t0 < t1) {
-      begin_run(kMode == kDown ? few_slot(p.plan, p.choices, slot) : one);
-      while (t < end && issued < kDepth) load();
+    if (lane == 0 && t < t1) {
+      if (held) {
+        grid_wait();
+        fence_proxy_async_global();
+      }
+      begin_run(true);
+      while (r.n > 0 && issued < p.depth) load();
     }
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    __syncwarp();
+    come_together();
     if (lane == 0) {
       bool alive = true;
 #pragma unroll 1
-      while (t < t1) {
-        if (t == end) {
-          c = 0;
-          begin_run(slot_at(++slot));
-        }
-        if (issued >= kDepth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+      while (r.n > 0 || t < t1) {
+        if (r.n == 0) begin_run(false);
+        if (issued >= p.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
           alive = false;
           break;
         }
@@ -392,23 +433,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == kTokens) {
     // ------------------------------------------------------------ tokens
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    come_together();
     if (lane == 0 && !held) {
       if (kMode != kUp) grid_wait();
       fence_proxy_async_global();  // the kernel before wrote what the bulk copies read
-      Ring<kDepth> ring;
+      Ring ring(p.depth);
       bool alive = true;
-      int c = c0, slot = slot0, issued = 0;
+      int issued = 0;
 #pragma unroll 1
-      for (int t = t0; t < t1 && alive; ++slot, c = 0) {
-        const FewSlot s = slot_at(slot);
-        const uint32_t record = static_cast<uint32_t>(few_record(rows_of(s)));
-        const uint8_t* from = p.t + (kMode == kDown ? few_act_at(slot, s.start, chunks) : 0) + static_cast<int64_t>(c) * record;
-        const int end = t + run_of(c, t);
+      for (int t = t0; t < t1 && alive;) {
+        const Run r = run_at(t, false);
+        t = after(t, r);
+        const uint32_t record = static_cast<uint32_t>(few_record(rows_of(r.slot)));
+        const uint8_t* from =
+            p.t + (kMode == kDown ? few_act_at(r.at, r.slot.start, chunks) : 0) + static_cast<int64_t>(r.c) * record;
 #pragma unroll 1
-        for (; t < end; ++t, ++issued) {
-          if (issued >= kDepth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+        for (int i = 0; i < r.n; ++i, ++issued) {
+          if (issued >= p.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
             alive = false;
             break;
           }
@@ -423,34 +464,40 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == kScaler) {
     // ------------------------------------------------------------ scales
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    come_together();
     // cp.async wrote what the tensor core reads: the fence between the two, and the copies, stay off the thread that issues
     // the products (together 250 to 800 cycles a chunk).
-    named_sync<(kDrainWarps + 2) * 32>();
+    named_sync<1, (kDrainWarps + 2) * 32>();
     tc_fence_after();
-    const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (kMode == kDown ? 2 : 1) * p.columns;
+    const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (many ? 2 : 1) * p.columns;
     const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at);
     const uint64_t sb0 = sdesc_plain_128b_rows(held ? held_scales : stage0 + tokens_at);
     const bool elected = elect_one();
-    Ring<kDepth> ring;
-    if (held && !all_of(mbar_wait(&sh.tokens, 0, ab, p.status))) sh.abort = 1;
+    Ring ring(p.depth);
+    bool alive = !held || all_of(mbar_wait(&sh.tokens, 0, ab, p.status));
 #pragma unroll 1
-    for (int t = t0, c = c0, slot = slot0; t < t1; ++t) {
-      if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) break;
-      fence_proxy_async_smem();
-      tc_fence_after();
-      const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
-      const uint64_t sb = held ? sb0 + (t - t0) * (kScales >> 4) : sb0 + stage + rows_of(slot_at(slot)) * (128 >> 4);
-      if (elected) {
-        // The columns were last read by products that were complete before the stage was filled again.
-        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
-        tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, sb);
-        mma_commit(&sh.ready[ring.s]);
+    for (int t = t0; t < t1 && alive;) {
+      const Run r = run_at(t, false);
+      t = after(t, r);
+      const uint64_t token_scales = sb0 + (held ? 0 : rows_of(r.slot) * (128 >> 4));
+#pragma unroll 1
+      for (int i = 0; i < r.n; ++i) {
+        if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) {
+          alive = false;
+          break;
+        }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+        if (elected) {
+          // The columns were last read by products that were complete before the stage was filled again.
+          tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
+          tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, token_scales + (held ? static_cast<uint64_t>(i * (kScales >> 4)) : stage));
+          mma_commit(&sh.ready[ring.s]);
+        }
+        __syncwarp();
+        ring.next();
       }
-      __syncwarp();
-      ring.next();
-      if (++c == chunks) c = 0, ++slot;
     }
     if (elected) {  // nothing may be under way when tensor memory is given back
       mma_commit(&sh.drain[0]);
@@ -460,31 +507,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    come_together();
     tmem_alloc(&sh.tmem, p.tmem);
     tmem_relinquish();
     tc_fence_before();
-    named_sync<(kDrainWarps + 2) * 32>();
+    named_sync<1, (kDrainWarps + 2) * 32>();
     tc_fence_after();
     // All lanes walk through the loop, so that what the products take stays in uniform registers; one issues them.
-    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + (kMode == kDown ? 2 : 1) * p.columns;
+    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + (many ? 2 : 1) * p.columns;
     const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(held ? held_codes : stage0 + tokens_at);
     const bool elected = elect_one();
     bool alive = true;
-    Ring<kDepth> ring;
-    int c = c0, slot = slot0, sum = 0;
+    Ring ring(p.depth);
+    int sum = 0;
 #pragma unroll 1
-    for (int t = t0; t < t1 && alive; ++slot, c = 0, ++sum) {
-      const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0);
-      if (kMode == kDown && sum >= 2 && !all_of(mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status))) break;
-      const uint32_t N = (__shfl_sync(kAll, rows_of(slot_at(slot)), 0) + 15) & ~15;
+    for (int t = t0; t < t1 && alive; ++sum) {
+      const Run r = run_at(t, false);
+      t = after(t, r);
+      const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0);
+      if (many && sum >= 2 && !all_of(mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status))) break;
+      const uint32_t N = (__shfl_sync(kAll, rows_of(r.slot), 0) + 15) & ~15;
       const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
-      const int end = t + run_of(c, t);
-      int left = K / 32 - c * 4;  // blocks of 32
-      uint32_t more = 0;          // whether there is something in the accumulator
+      int left = K / 32 - r.c * 4;  // blocks of 32
+      uint32_t more = 0;            // whether there is something in the accumulator
 #pragma unroll 1
-      for (; t < end; ++t, left -= 4) {
+      for (int i = 0; i < r.n; ++i, left -= 4) {
         if (!all_of(mbar_wait(&sh.ready[ring.s], ring.phase, ab, p.status))) {
           alive = false;
           break;
@@ -492,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
         const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
-        const uint64_t a = a0 + stage, b = b0 + (held ? static_cast<uint64_t>((t - t0) * (kHeld >> 4)) : stage);
+        const uint64_t a = a0 + stage, b = b0 + (held ? static_cast<uint64_t>(i * (kHeld >> 4)) : stage);
         if (elected) {
           mma_mx_e4m3(acc, a, b, kind, sfa, sfb, more);
           if (left > 1) mma_mx_e4m3_k<true>(acc, a + 2, b + 2, kind | idesc_mx_e4m3(0, 0, 1, 1), sfa, sfb);
@@ -515,14 +562,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ sums
-    if constexpr (kMode == kDown) {
+    if (many)
       for (int i = threadIdx.x; i < slots; i += kDrainWarps * 32) table[i] = few_slot(p.plan, p.choices, i);
+    if (kMode == kDown)
       for (int i = threadIdx.x; i < p.M * kRows; i += kDrainWarps * 32) sums[i] = 0.f;
-    }
-    __syncthreads();
-    if (p.splits > 1 && !p.late) cluster_arrive();
+    come_together();
     if (held) {
       // One or two tokens: the block's share of them stays in shared memory, in tiles of 16 rows.
+      grid_wait();
       const int pieces = (min(t1 * kChunk, K) - t0 * kChunk) / 8, work = pieces * p.M;  // of 8 values
 #pragma unroll 1
       for (int i0 = warp * 32; i0 < work; i0 += kDrainWarps * 32) {
@@ -531,26 +578,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint8_t* codes = smem + (held_codes - stage0) + (k >> 7) * kHeld;
         uint8_t* scales = smem + (held_scales - stage0) + (k >> 7) * kScales;
         few::split8(
-            __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * K + t0 * kChunk + k)),
+            load_after(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(token) * K + t0 * kChunk + k)),
             [&](int part) { return codes + (r + part) * 128 + (((b >> 4) ^ (r + part)) << 4) + (b & 15); },
             [&](int part) { return scales + (r + part) * 16 + (b >> 5); });
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.tokens);
     }
-    named_sync<(kDrainWarps + 2) * 32>();
+    named_sync<1, (kDrainWarps + 2) * 32>();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int row = threadIdx.x;  // warps 0-3
     const float* weights = kMode == kDown ? few_weights(p.plan) : nullptr;
-    int c = c0, slot = slot0, sum = 0;
+    int sum = 0;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++slot, c = 0, ++sum) {
-      const FewSlot s = slot_at(slot);
-      t += run_of(c, t);
+    for (int t = t0; t < t1; ++sum) {
+      const Run r = run_at(t, false);
+      t = after(t, r);
+      const FewSlot& s = r.slot;
       if (!all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (kMode == kDown ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
+      const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
       uint32_t mask = s.mask;
       if constexpr (kMode == kDown) {
 #pragma unroll 1
@@ -565,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             float f = 0.f;
 #pragma unroll
             for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[(i * kParts + q) / 16][(i * kParts + q) % 16]);
-            sums[(__ffs(mask) - 1) * kRows + row] += f * __ldcg(weights + s.start + n0 + i);
+            sums[(__ffs(mask) - 1) * kRows + row] +=
+                f * __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + n0 + i)));
             mask &= mask - 1;
           }
         }
@@ -573,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // The tokens of the mask, four at a time (past the last one that one again).
 #pragma unroll 1
         for (int n0 = 0; n0 < s.n; n0 += 4) {
-          uint32_t v[4][kParts];
+          uint32_t v[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             tmem_ld_32x32b_x2(acc + (__ffs(mask) - 1) * kParts, v[i]);
@@ -588,8 +637,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sum_empty[sum & 1]);
+      if (in_turn) {
+        named_sync<2, kDrainWarps * 32>();
+        for (int i = warp; i < s.n * 2; i += kDrainWarps)
+          activate(p, r, i >> 1, i & 1, sums[(i >> 1) * kRows + (i & 1) * 32 + lane],
+                   sums[(i >> 1) * kRows + 64 + (i & 1) * 32 + lane]);
+        named_sync<2, kDrainWarps * 32>();
+      }
     }
-    if (kMode != kDown && t0 == t1)  // no share of a short contraction
+    if (!many && t0 == t1)  // no share of a short contraction
       for (int i = 0; i < one.n; ++i) sums[i * kRows + row] = 0.f;
   }
   tc_fence_before();
@@ -598,16 +654,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     tmem_dealloc(sh.tmem, p.tmem);
   }
+  if (in_turn) return;
 
   // The sums of the cluster's blocks.  Block r of them brings home items r, r + splits, ...: for each the others send theirs,
   // item i of block q to received[i / splits * splits + q].  An item: 32 rows of a token (kUp: of gate and of up).
-  constexpr int kItemRows = kMode == kUp ? 64 : 32, kItems = kRows / kItemRows;  // of a token
+  constexpr int kHalves = kMode == kUp ? 2 : 1, kItems = kRows / 32 / kHalves;  // of an item, of a token
   const int items = (kMode == kUp ? one.n : p.M) * kItems;
   const auto value_of = [&](int item, int h) {  // row `lane` of its half h
-    const int token = item / kItems, i = item % kItems;
-    return sums[token * kRows + i * 32 + h * 64 + lane];
+    return sums[item / kItems * kRows + item % kItems * 32 + h * 64 + lane];
   };
-  constexpr int kHalves = kItemRows / 32;
   if (p.splits > 1) {
     if (p.late) cluster_arrive();
     cluster_wait();
@@ -621,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_arrive();
     cluster_wait();
   }
+  Run r{one, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) / p.splits, 0, 0};
   for (int item = rank + warp * p.splits; item < items; item += (kIssuer + 1) * p.splits) {
     float v[kHalves];
 #pragma unroll
@@ -630,15 +686,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int q = 0; q < p.splits; ++q)
           v[h] += q == rank ? value_of(item, h) : received[((item / p.splits * p.splits + q) * kHalves + h) * 32 + lane];
     }
-    const int token = item / kItems, i = item % kItems;
+    const int token = item / kItems, row = item % kItems * 32 + lane;
     if constexpr (kMode == kUp) {
-      const int64_t f = row0 + i * 32;
-      if (f >= p.m.rows / 2) continue;
-      few::split1(v[0] / (1.f + expf(-v[0])) * v[1],
-                  p.act + few_act_at(blockIdx.y, one.start, few_chunks(p.m.rows / 2)), one.n, f + lane, token);
+      activate(p, r, token, item % kItems, v[0], v[1]);
     } else {
-      const int row = i * 32 + lane;
-      if (row <= last) p.y[token * p.m.rows + row0 + row] = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
+      if (row <= last_of(r)) p.y[token * p.m.rows + row_of(r) + row] = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f) & 0xFFFFu);
     }
   }
 }
@@ -647,18 +699,49 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Shared memory of a block beside its fixed part, alone on an SM and as one of two: an SM has 228 KB, of which each block takes
 // 1 KB more than it asks for.
-constexpr uint32_t kMostSmem = 226 * 1024, kHalfSmem = 112 * 1024;
+constexpr uint32_t kMostSmem = 226 * 1024, kHalfSmem = 111 * 1024;
+static_assert(sizeof(Shared) <= 1024, "of the kilobyte that this leaves");
 
-// Blocks of a cluster for `tiles` row tiles over `chunks` chunks of contraction, with room for `slots` blocks at a time: the
-// fewest rounds of blocks, each of which costs about as much as six chunks besides its own.
-int splits_of(int64_t tiles, int64_t chunks, int64_t slots) {
-  int best = 1;
+// Blocks of clusters of `size` that run at once, two to an SM or alone: shared memory decides.  Clusters stay within a part of
+// the chip, whose SMs do not always come out even: of 304 places, 296 in clusters of four and 288 of eight; of 152, 144 and 120.
+// The query goes by a kernel without tensor memory; of one that takes some it counts a block an SM, where two do run.
+int places(int size, bool alone) {
+  const int smem = static_cast<int>(alone ? kMostSmem : kHalfSmem);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostSmem)) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, few_tokens_kernel, &cfg) == cudaSuccess && clusters > 0)
+    return clusters * size;
+  (void)cudaGetLastError();
+  return size;
+}
+
+// Blocks of a cluster, a power of two up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in
+// chunks' time (0.2 us): those of a block, half as long again where it brings its tokens into parts itself, for each round of
+// blocks; the cluster's start and exchange, 2.0, 2.6 and 4.0 us for 2, 4 and 8; and the sums that change hands.  On both sides
+// of the choice (us, clusters of 1, 2, 4, 8; a linear of 8192 x 5120 or a layer's decode step): linear, one token, 4 bits 10.5,
+// 10.5, 9.6, 14.6; 32 tokens 13.5, 12.5, 13.4, 21.3; down of two experts 4096 -> 5120 in a layer of 41.4, 35.2, 32.1, 35.5;
+// up of four experts 2048 -> 1024 in 20.1, 21.7, 22.1, 27.2.
+int splits_of(int64_t tiles, int64_t chunks, int tokens, bool held, const int (&room)[4]) {
+  int best = 0;
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= 8 && s <= (chunks + 1) / 2; ++s) {
-    const int64_t cost = (tiles * s + slots - 1) / slots * ((chunks + s - 1) / s + 6);
-    if (cost < least) best = s, least = cost;
+  const int64_t exchange[4] = {0, 80, 104, 160};
+  for (int i = 0; i < 4 && (1 << i) <= chunks; ++i) {
+    const int64_t s = 1 << i, rounds = (tiles * s + room[i] - 1) / room[i];
+    const int64_t cost = rounds * ((chunks + s - 1) / s) * (held ? 12 : 8) + exchange[i] + (i > 0 ? tokens * s : 0);
+    if (cost < least) best = i, least = cost;
   }
-  return best;
+  return 1 << best;
 }
 
 // The weights as TMA reads them, boxes of `box` rows by a chunk: e4m3 codes as bytes; e2m1 codes spread out, or, where rows are
@@ -679,9 +762,9 @@ bool weights_map(CUtensorMap* map, const Matrix& m, int64_t rows, int bits, bool
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Mode kMode, int kBits, int kDepth>
+template <Mode kMode, int kBits>
 cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3 grid, cudaStream_t st) {
-  auto* kernel = few_kernel<kMode, kBits, kDepth>;
+  auto* kernel = few_kernel<kMode, kBits>;
   static thread_local bool allowed[64] = {};  // by device
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -697,15 +780,16 @@ cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attrs;
-  if (p.x == nullptr) {  // there is a kernel before that lets this one start
-    attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  // The kernel starts under the one before and waits for it itself.
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   if (p.splits > 1) {
-    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attrs[cfg.numAttrs].val.clusterDim.x = p.splits;
-    attrs[cfg.numAttrs].val.clusterDim.y = 1;
-    attrs[cfg.numAttrs++].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = p.splits;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   return cudaLaunchKernelEx(&cfg, kernel, map, p);
 }
@@ -716,39 +800,61 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   const int parts = kMode == kDown ? kActParts : kTokenParts;
   const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t tiles = (rows + tile - 1) / tile;
-  p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
-  const uint32_t columns = (kMode == kDown ? 2 : 1) * p.columns + kMostDepth * 8;
-  p.tmem = 32;
-  while (p.tmem < columns) p.tmem *= 2;
   const int chunks = (p.m.K + kChunk - 1) / kChunk;
+  // Enough runs for every block to have some: whole ones in turn, which leaves the stages no gaps.
+  const bool in_turn = kMode == kUp && tiles * copies >= 3 * num_sms;
+  const bool many = kMode == kDown || in_turn;
+  p.tiles = in_turn ? static_cast<int>(tiles) : 0;
+  p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
   p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
   p.tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales;
   p.stage = (kCodes + p.tokens + kScales + (p.packed ? kPacked : 0) + 1023) / 1024 * 1024;
   // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
   const uint32_t received = (p.M * kRows + 7 * 64) * 4;
   p.late = p.M > 16;
-  p.slots = matrices;
-  const uint32_t behind = (p.late ? 0 : received) +
-                          (kMode == kDown ? p.M * kRows * 4 + matrices * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
-  const auto splits = [&](int per_sm) {
-    return splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, num_sms * per_sm);
+  p.slots = many ? (kMode == kDown ? matrices : copies) : 0;
+  const uint32_t behind = (p.late || in_turn ? 0 : received) +
+                          (many ? p.M * kRows * 4 + p.slots * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
+  // Two blocks an SM, of four stages or three (a block before the next product's, or before the next call's, then has the
+  // other's time to start); alone, with more stages, where three are too many for that.
+  const auto smem = [&](int depth) {
+    return 1024 + depth * p.stage + (p.x != nullptr ? p.held_at + p.share * (kHeld + kScales) : behind);
   };
-  if (p.x != nullptr) {
-    const int least = (chunks + kMostHeld - 1) / kMostHeld;
-    p.splits = splits(2) > least ? splits(2) : least;
-    p.share = (chunks + p.splits - 1) / p.splits;
-    p.held_at = (behind + 1023) / 1024 * 1024;
+  const auto pick_depth = [&] {
+    p.depth = smem(4) <= kHalfSmem ? 4 : 3;
+    if (smem(3) > kHalfSmem)
+      while (p.depth < kMostDepth && smem(p.depth + 1) <= kMostSmem) ++p.depth;
+  };
+  if (p.x != nullptr) p.held_at = (behind + 1023) / 1024 * 1024;
+  pick_depth();  // held tokens take no more than kMostHeld chunks of it, which leaves room for two blocks
+  const bool alone = smem(p.depth) > kHalfSmem;
+  if (in_turn) {
+    p.splits = 1;
+  } else {
+    static thread_local int room[64][2][4] = {};  // by device
+    int dev = 0, here[2][4] = {};
+    if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+    int(*const mine)[4] = dev < 64 ? room[dev] : here;
+    if (mine[alone][0] == 0) {
+      for (int i = 3; i >= 0; --i) mine[alone][i] = places(1 << i, alone);
+    }
+    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr, mine[alone]);
   }
-  const uint32_t held = p.held_at + p.share * (kHeld + kScales);
-  const auto smem = [&](int depth) { return 1024 + depth * p.stage + (p.x != nullptr ? held : behind); };
-  // Two blocks an SM, with three stages where four are too many for that.
-  const int depth = smem(4) > kHalfSmem && smem(3) <= kHalfSmem ? 3 : 4;
-  if (p.x == nullptr) p.splits = splits(smem(depth) <= kHalfSmem ? 2 : 1);
-  if (smem(depth) > kMostSmem) return cudaErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
+  if (p.x != nullptr) {
+    while (p.splits * kMostHeld < chunks) p.splits *= 2;
+    p.share = (chunks + p.splits - 1) / p.splits;
+    pick_depth();
+  }
+  if (smem(p.depth) > kMostSmem) return cudaErrorInvalidConfiguration;
+  const uint32_t columns = (many ? 2 : 1) * p.columns + p.depth * 8;
+  p.tmem = 32;
+  while (p.tmem < columns) p.tmem *= 2;
+  const int64_t blocks = num_sms * (smem(p.depth) <= kHalfSmem ? 2 : 1);
+  const dim3 grid = in_turn ? dim3(static_cast<unsigned>(blocks))
+                            : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
   CUtensorMap map{};
   if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, static_cast<uint32_t>(tile))) return cudaErrorInvalidValue;
-  return depth == 3 ? launch<kMode, kBits, 3>(map, p, smem(3), grid, st) : launch<kMode, kBits, 4>(map, p, smem(4), grid, st);
+  return launch<kMode, kBits>(map, p, smem(p.depth), grid, st);
 }
 
 template <Mode kMode>
@@ -779,8 +885,16 @@ cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
     uint8_t* tokens = static_cast<uint8_t*>(a.workspace);
     p.t = tokens;
     const dim3 grid(static_cast<unsigned>((a.K / 8 + 255) / 256), static_cast<unsigned>(a.M));
-    few_tokens_kernel<<<grid, 256, 0, st>>>(a.x, a.K, tokens);
-    if (const cudaError_t e = cudaGetLastError()) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, few_tokens_kernel, a.x, a.K, tokens)) return e;
   }
   return launch_product<kLinear>(p, a.bits, 1, 1, 1, a.num_sms, st);
 }

@@ -40,11 +40,30 @@ __device__ __forceinline__ float* few_weights(const FewPlan* p) {
 __device__ __forceinline__ FewSlot* few_slots(const FewPlan* p, int choices) {
   return reinterpret_cast<FewSlot*>(reinterpret_cast<uint8_t*>(few_weights(p)) + few_weights_bytes(choices));
 }
-// Read past the first-level cache: the plan may be written by a kernel this one overlaps with the end of.
-__device__ __forceinline__ int few_active(const FewPlan* p) { return __ldcg(&p->active); }
+// Loads that stay behind a wait for the kernel before: the compiler moves none of these, as it may plain loads of what it
+// takes for constant.
+__device__ __forceinline__ uint32_t load_after(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load_after(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_after(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int few_active(const FewPlan* p) {
+  return static_cast<int>(load_after(reinterpret_cast<const uint32_t*>(&p->active)));
+}
 __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i) {
-  const int4 v = __ldcg(reinterpret_cast<const int4*>(few_slots(p, choices) + i));
-  return FewSlot{v.x, v.y, static_cast<uint32_t>(v.z), v.w};
+  const uint4 v = load_after(reinterpret_cast<const uint4*>(few_slots(p, choices) + i));
+  return FewSlot{static_cast<int>(v.x), static_cast<int>(v.y), v.z, static_cast<int>(v.w)};
 }
 
 // Values as the products read them (few_tokens.cuh): a record for every chunk of 128 of the contraction, of `rows` rows of

@@ -89,7 +89,7 @@ struct Choice {
   int expert;
   float score, sum;
 };
-__device__ Choice choose_row(float* s, uint32_t* key, const float* __restrict__ bias, const RouteShape& p) {
+__device__ Choice choose_row(float* s, uint32_t* key, const float* bias, const RouteShape& p) {
   const int lane = threadIdx.x & 31, E = p.E;
   float top = -INFINITY;
   for (int e = lane; e < E; e += 32) top = fmaxf(top, s[e]);
@@ -111,7 +111,7 @@ __device__ Choice choose_row(float* s, uint32_t* key, const float* __restrict__ 
     for (int e = lane; e < E; e += 32) s[e] = sigmoid_of(s[e]);
   }
   for (int e = lane, i = 0; e < E; e += 32, ++i) {
-    const float b = bias != nullptr ? bias[e] : 0.f;
+    const float b = bias != nullptr ? __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(bias + e))) : 0.f;
     key[e] = ((masked >> i) & 1) || b == -INFINITY ? 0u : ordered(s[e] + b);
   }
   __syncwarp();
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
   const Layout at = layout_of(M, E, k, p.slices);
   asm volatile("griddepcontrol.launch_dependents;");  // they wait for this kernel's end before they read the plan
   cluster_arrive();  // blocks may write to each other's memory once they run
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // 1. Logits.
   uint32_t* const received = reinterpret_cast<uint32_t*>(smem + at.received);
@@ -191,11 +192,13 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
       float4 r[4];
       uint2 x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = __ldg(reinterpret_cast<const float4*>(p.router + static_cast<int64_t>(min(e0 + i, E - 1)) * p.C + c));
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = load_after(reinterpret_cast<const uint4*>(p.router + static_cast<int64_t>(min(e0 + i, E - 1)) * p.C + c));
+        r[i] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (t0 + j < M) x[j] = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t0 + j) * p.C + c));
+        if (t0 + j < M) x[j] = load_after(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t0 + j) * p.C + c));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (t0 + j >= M) break;
@@ -243,7 +246,15 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
       s[e] = sum;
     }
     const Choice c = choose_row(s, reinterpret_cast<uint32_t*>(smem + at.keys) + warp * padded(E), p.bias, p.how);
-    if (lane < k) {
+    if (M == 1) {  // the choices are the slots
+      const uint32_t some = __ballot_sync(kAll, c.expert >= 0);
+      const int at = __popc(some & ((1u << lane) - 1));
+      if (c.expert >= 0) {
+        few_slots(p.plan, k)[at] = FewSlot{c.expert, at, 1, 1};
+        few_weights(p.plan)[at] = (p.how.renorm ? c.score / (c.sum + 1e-20f) : c.score) * p.how.scale;
+      }
+      if (lane == 0) p.plan->active = __popc(some);
+    } else if (lane < k) {
       const float w = (p.how.renorm ? c.score / (c.sum + 1e-20f) : c.score) * p.how.scale;
       const int entry = (rank + warp * kBlocks) * k + lane;
       store_remote(smem_u32(experts + entry), 0, static_cast<uint32_t>(c.expert));
@@ -259,11 +270,12 @@ __global__ void __launch_bounds__(kThreads) few_route_kernel(const __grid_consta
       for (int i0 = (warp - kMostRows) * 32; i0 < pieces; i0 += (kWarps - kMostRows) * 32) {
         const int i = i0 + lane < pieces ? i0 + lane : i0 + lane % 4;  // past the end the same four again
         few::split8(
-            __ldg(row + i), [&](int part) { return few::code_at(p.held, M * kTokenParts, i * 8, t * kTokenParts + part); },
+            load_after(row + i), [&](int part) { return few::code_at(p.held, M * kTokenParts, i * 8, t * kTokenParts + part); },
             [&](int part) { return few::scale_at(p.held, M * kTokenParts, i * 8, t * kTokenParts + part); });
       }
     }
   }
+  if (M == 1) return;
   __syncwarp();
   cluster_arrive();
   if (rank != 0) return;
@@ -333,18 +345,20 @@ cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, uint8_t* tokens
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed[dev] = true;
   }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kBlocks;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attrs[2]{};
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = kBlocks;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it waits itself
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kBlocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, few_route_kernel, p);
 }
 
