@@ -66,17 +66,29 @@ struct Matrix {
   int K;
 };
 
+// Stages: weight codes, tokens, their scales, packed codes.
+struct Stages {
+  int depth;        // how many
+  uint32_t tokens;  // bytes of tokens
+  uint32_t bytes;
+};
+__host__ __device__ inline Stages stages_of(int depth, uint32_t ring, uint32_t tokens, bool packed) {
+  const uint32_t bytes = (kCodes + tokens + kScales + (packed ? kPacked : 0) + 1023) / 1024 * 1024;
+  const int room = static_cast<int>(ring / bytes);
+  return Stages{room < depth ? room : depth, tokens, bytes};
+}
+
 struct Product {
   Matrix m;
-  int M, splits, depth;  // depth: stages
+  int M, splits;
   int tiles;            // kUp, in turn: tiles of an expert; else 0
   bool late;            // the cluster's sums meet in the stages
   int slots;            // kDown: room for as many
   bool packed;          // 4-bit weights land as they are in memory, for whole chunks of 128 only TMA can spread them
   int columns;          // of an accumulator: token rows, a multiple of 16
-  uint32_t tokens;      // bytes of tokens in a stage
+  Stages stages;        // kDown: of slots of M tokens; there are more where the plan's are smaller
+  uint32_t ring;        // bytes of all stages
   uint32_t tmem;        // columns of tensor memory
-  uint32_t stage;       // bytes
   int share;            // kLinear, one or two tokens: most chunks of a block,
   uint32_t held_at;     // and where they are, behind the stages
   const uint16_t* x;    // kLinear, one or two tokens: bf16 [M, K]
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const bool packed = kBits == 4 && p.packed, held = kMode == kLinear && p.x != nullptr, in_turn = kMode == kUp && p.tiles > 0;
   if (warp == kWeights && lane == 0) {
     tma_prefetch_desc(&weights_map);
-    for (int s = 0; s < p.depth; ++s) {
+    for (int s = 0; s < kMostDepth; ++s) {
       if (packed) mbar_init(&sh.landed[s], 1);
       mbar_init(&sh.full[s], kScaleWarps * 32 + !packed + !held);
       mbar_init(&sh.ready[s], 1);
@@ -240,19 +252,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   // cluster's other blocks send (or over the stages too, where two blocks an SM need the room, once all of the cluster's blocks
   // have read theirs).  A linear's tokens last.
   const bool many = kMode == kDown || in_turn;
-  float* const sums = reinterpret_cast<float*>(many ? smem + p.depth * p.stage : smem);
-  float* const behind = reinterpret_cast<float*>(smem + p.depth * p.stage) + (many ? p.M * kRows : 0);
+  float* const sums = reinterpret_cast<float*>(many ? smem + p.ring : smem);
+  float* const behind = reinterpret_cast<float*>(smem + p.ring) + (many ? p.M * kRows : 0);
   FewSlot* const table = reinterpret_cast<FewSlot*>(behind);
   float* const received = p.late ? reinterpret_cast<float*>(smem) + (many ? 0 : p.M * kRows) : behind + p.slots * 4;
 
   // What the plan says.  The plan is older than the kernel before this one, which waited for it before it let this one
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
   int slots = 1;
+  Stages stages = p.stages;
   FewSlot one{0, 0, 0xffffffffu >> (32 - p.M), p.M};
   if constexpr (kMode == kUp) {
     grid_wait();
     grid_release();
-    slots = few_active(p.plan);
+    slots = few_header(p.plan).active;
     if (!in_turn) {
       one = few_slot(p.plan, p.choices, blockIdx.y);
       if (static_cast<int>(blockIdx.y) >= slots) return;  // with its whole cluster
@@ -260,7 +273,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       return;
     }
   } else if constexpr (kMode == kDown) {
-    slots = few_active(p.plan);
+    // Stages have room for the tokens that slots have, not for all of the batch's: 32 tokens of 8 experts, two each, take 4 or 5
+    // stages of the room of 3.
+    const FewPlan plan = few_header(p.plan);
+    slots = plan.active;
+    stages = stages_of(kMostDepth, p.ring, (plan.most * kParts + 15) / 16 * 16 * 128 + kScales, packed);
   }
   const AbortFlag ab{&sh.abort};
 
@@ -287,10 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const auto last_of = [&](const Run& r) {
     return static_cast<int>(min((kMode == kUp ? half : p.m.rows) - row_of(r), static_cast<int64_t>(tile))) - 1;
   };
-  const uint32_t tokens_at = kCodes, scales_at = kCodes + p.tokens, packed_at = scales_at + kScales;
+  const uint32_t tokens_at = kCodes, scales_at = kCodes + stages.tokens, packed_at = scales_at + kScales;
   // Rows of the tokens of a slot: kDown has those of its columns, the others every token's for every expert.
   const auto rows_of = [&](const FewSlot& s) { return (kMode == kDown ? s.n : p.M) * kParts; };
-  const uint32_t held_codes = stage0 + p.depth * p.stage + p.held_at, held_scales = held_codes + p.share * kHeld;
+  const uint32_t held_codes = stage0 + p.ring + p.held_at, held_scales = held_codes + p.share * kHeld;
   const auto come_together = [&]() {
     __syncthreads();
     if (p.splits > 1 && !p.late) cluster_arrive();  // the others may write to this block's memory once it runs
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return make_uint2(lo, hi);
     };
 
-    Ring ring(p.depth);
+    Ring ring(stages.depth);
     bool refill = false, alive = true;
 #pragma unroll 1
     for (int t = t0; t < t1 && alive;) {
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           alive = false;
           break;
         }
-        const uint32_t stage = stage0 + ring.s * p.stage;
+        const uint32_t stage = stage0 + ring.s * stages.bytes;
         if (whole_words && !packed) {
           cp_async<4>(stage + scale_to, p.m.e8 + scale);
           cp_async_arrive(&sh.full[ring.s]);
@@ -385,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     cp_async_wait_all();
   } else if (warp == kWeights) {
     // ------------------------------------------------------------ weights
-    Ring ring(p.depth);
+    Ring ring(stages.depth);
     int t = t0, issued = 0;
     Run r{};
     int32_t row = 0;
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       row = static_cast<int32_t>(r.slot.expert * p.m.rows + row_of(r));
     };
     const auto load = [&]() {
-      const uint32_t stage = stage0 + ring.s * p.stage;
+      const uint32_t stage = stage0 + ring.s * stages.bytes;
       uint64_t* bar = packed ? &sh.landed[ring.s] : &sh.full[ring.s];
       // Codes that TMA spreads out count as they are in memory.
       mbar_arrive_expect_tx(bar, kRows * kRowBytes);
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_proxy_async_global();
       }
       begin_run(true);
-      while (r.n > 0 && issued < p.depth) load();
+      while (r.n > 0 && issued < stages.depth) load();
     }
     __syncwarp();
     come_together();
@@ -422,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
       while (r.n > 0 || t < t1) {
         if (r.n == 0) begin_run(false);
-        if (issued >= p.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+        if (issued >= stages.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
           alive = false;
           break;
         }
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0 && !held) {
       if (kMode != kUp) grid_wait();
       fence_proxy_async_global();  // the kernel before wrote what the bulk copies read
-      Ring ring(p.depth);
+      Ring ring(stages.depth);
       bool alive = true;
       int issued = 0;
 #pragma unroll 1
@@ -449,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             p.t + (kMode == kDown ? few_act_at(r.at, r.slot.start, chunks) : 0) + static_cast<int64_t>(r.c) * record;
 #pragma unroll 1
         for (int i = 0; i < r.n; ++i, ++issued) {
-          if (issued >= p.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+          if (issued >= stages.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
             alive = false;
             break;
           }
           mbar_arrive_expect_tx(&sh.full[ring.s], record);
-          bulk_load(stage0 + ring.s * p.stage + tokens_at, from, record, &sh.full[ring.s]);
+          bulk_load(stage0 + ring.s * stages.bytes + tokens_at, from, record, &sh.full[ring.s]);
           from += record;
           ring.next();
         }
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at);
     const uint64_t sb0 = sdesc_plain_128b_rows(held ? held_scales : stage0 + tokens_at);
     const bool elected = elect_one();
-    Ring ring(p.depth);
+    Ring ring(stages.depth);
     bool alive = !held || all_of(mbar_wait(&sh.tokens, 0, ab, p.status));
 #pragma unroll 1
     for (int t = t0; t < t1 && alive;) {
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+        const uint64_t stage = static_cast<uint64_t>(ring.s * (stages.bytes >> 4));
         if (elected) {
           // The columns were last read by products that were complete before the stage was filled again.
           tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
@@ -518,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(held ? held_codes : stage0 + tokens_at);
     const bool elected = elect_one();
     bool alive = true;
-    Ring ring(p.depth);
+    Ring ring(stages.depth);
     int sum = 0;
 #pragma unroll 1
     for (int t = t0; t < t1 && alive; ++sum) {
@@ -537,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         tc_fence_after();
-        const uint64_t stage = static_cast<uint64_t>(ring.s * (p.stage >> 4));
+        const uint64_t stage = static_cast<uint64_t>(ring.s * (stages.bytes >> 4));
         const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
         const uint64_t a = a0 + stage, b = b0 + (held ? static_cast<uint64_t>(i * (kHeld >> 4)) : stage);
         if (elected) {
@@ -596,6 +613,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Run r = run_at(t, false);
       t = after(t, r);
       const FewSlot& s = r.slot;
+      // Lane i has the weight of column i.
+      const float weight =
+          kMode == kDown && lane < s.n ? __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + lane))) : 0.f;
       if (!all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
@@ -613,8 +633,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float f = 0.f;
 #pragma unroll
             for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[(i * kParts + q) / 16][(i * kParts + q) % 16]);
-            sums[(__ffs(mask) - 1) * kRows + row] +=
-                f * __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + n0 + i)));
+            sums[(__ffs(mask) - 1) * kRows + row] += f * __shfl_sync(kAll, weight, n0 + i);
             mask &= mask - 1;
           }
         }
@@ -807,8 +826,7 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   p.tiles = in_turn ? static_cast<int>(tiles) : 0;
   p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
   p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
-  p.tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales;
-  p.stage = (kCodes + p.tokens + kScales + (p.packed ? kPacked : 0) + 1023) / 1024 * 1024;
+  const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales, stage = stages_of(0, 0, tokens, p.packed).bytes;
   // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
   const uint32_t received = (p.M * kRows + 7 * 64) * 4;
   p.late = p.M > 16;
@@ -816,18 +834,21 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   const uint32_t behind = (p.late || in_turn ? 0 : received) +
                           (many ? p.M * kRows * 4 + p.slots * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
   // Two blocks an SM, of four stages or three (a block before the next product's, or before the next call's, then has the
-  // other's time to start); alone, with more stages, where three are too many for that.
-  const auto smem = [&](int depth) {
-    return 1024 + depth * p.stage + (p.x != nullptr ? p.held_at + p.share * (kHeld + kScales) : behind);
+  // other's time to start); alone, with more stages, where three are too many for that.  kDown takes what it may of that and
+  // divides it by the plan.
+  int depth = 2;
+  const auto smem = [&](int n) {
+    return 1024 + n * stage + (p.x != nullptr ? p.held_at + p.share * (kHeld + kScales) : behind);
   };
   const auto pick_depth = [&] {
-    p.depth = smem(4) <= kHalfSmem ? 4 : 3;
+    if (kMode == kDown) return;
+    depth = smem(4) <= kHalfSmem ? 4 : 3;
     if (smem(3) > kHalfSmem)
-      while (p.depth < kMostDepth && smem(p.depth + 1) <= kMostSmem) ++p.depth;
+      while (depth < kMostDepth && smem(depth + 1) <= kMostSmem) ++depth;
   };
   if (p.x != nullptr) p.held_at = (behind + 1023) / 1024 * 1024;
   pick_depth();  // held tokens take no more than kMostHeld chunks of it, which leaves room for two blocks
-  const bool alone = smem(p.depth) > kHalfSmem;
+  const bool alone = smem(depth) > kHalfSmem;
   if (in_turn) {
     p.splits = 1;
   } else {
@@ -845,16 +866,19 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
     p.share = (chunks + p.splits - 1) / p.splits;
     pick_depth();
   }
-  if (smem(p.depth) > kMostSmem) return cudaErrorInvalidConfiguration;
-  const uint32_t columns = (many ? 2 : 1) * p.columns + p.depth * 8;
+  p.ring = kMode == kDown ? (kHalfSmem - (smem(depth) - depth * stage)) / 1024 * 1024 : depth * stage;
+  p.stages = Stages{depth, tokens, stage};
+  const uint32_t bytes = smem(depth) - depth * stage + p.ring;
+  if (bytes > (kMode == kDown ? kHalfSmem : kMostSmem) || p.ring < depth * stage) return cudaErrorInvalidConfiguration;
+  const uint32_t columns = (many ? 2 : 1) * p.columns + (kMode == kDown ? kMostDepth : depth) * 8;
   p.tmem = 32;
   while (p.tmem < columns) p.tmem *= 2;
-  const int64_t blocks = num_sms * (smem(p.depth) <= kHalfSmem ? 2 : 1);
+  const int64_t blocks = num_sms * (bytes <= kHalfSmem ? 2 : 1);
   const dim3 grid = in_turn ? dim3(static_cast<unsigned>(blocks))
                             : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
   CUtensorMap map{};
   if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, static_cast<uint32_t>(tile))) return cudaErrorInvalidValue;
-  return launch<kMode, kBits>(map, p, smem(p.depth), grid, st);
+  return launch<kMode, kBits>(map, p, bytes, grid, st);
 }
 
 template <Mode kMode>

@@ -26,6 +26,7 @@ constexpr int kFewTokens = 32;
 // slots.
 struct alignas(16) FewPlan {
   int active;  // slots
+  int most;    // tokens of a slot, at most
 };
 
 __host__ __device__ inline int64_t few_weights_bytes(int64_t choices) { return (choices * 4 + 15) / 16 * 16; }
@@ -58,8 +59,9 @@ __device__ __forceinline__ uint4 load_after(const uint4* p) {
   return v;
 }
 
-__device__ __forceinline__ int few_active(const FewPlan* p) {
-  return static_cast<int>(load_after(reinterpret_cast<const uint32_t*>(&p->active)));
+__device__ __forceinline__ FewPlan few_header(const FewPlan* p) {
+  const uint2 v = load_after(reinterpret_cast<const uint2*>(p));
+  return FewPlan{static_cast<int>(v.x), static_cast<int>(v.y)};
 }
 __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i) {
   const uint4 v = load_after(reinterpret_cast<const uint4*>(few_slots(p, choices) + i));

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kPer == 32 ? 1 : 2) few_route_kernel
           few_slots(p.plan, k)[place] = FewSlot{c.expert, place, 1, 1};
           few_weights(p.plan)[place] = w;
         }
-        if (lane == 0) p.plan->active = __popc(some);
+        if (lane == 0) p.plan->active = __popc(some), p.plan->most = 1;
       } else if (lane < k) {
         store_remote(smem_u32(experts + t * k + lane), 0, static_cast<uint32_t>(c.expert));
         if (c.expert >= 0) {
@@ -320,12 +320,13 @@ __global__ void __launch_bounds__(kThreads, kPer == 32 ? 1 : 2) few_route_kernel
   int* const starts = reinterpret_cast<int*>(smem + at.starts);
   if (warp == 0) {
     FewSlot* slots = few_slots(p.plan, M * k);
-    int before = 0;  // slots in the upper half word, choices in the lower
+    int before = 0, most = 0;  // before: slots in the upper half word, choices in the lower
 #pragma unroll 1
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       const uint32_t mask = e < E ? masks[e] : 0;
       const int mine = mask != 0 ? (1 << 16) | __popc(mask) : 0;
+      most = max(most, __popc(mask));
       int up = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -339,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, kPer == 32 ? 1 : 2) few_route_kernel
       }
       before += __shfl_sync(kAll, up, 31);
     }
-    if (lane == 0) p.plan->active = before >> 16;
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) p.plan->active = before >> 16, p.plan->most = most;
   }
   __syncthreads();
   float* const out = few_weights(p.plan);
