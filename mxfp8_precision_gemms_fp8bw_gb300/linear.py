@@ -182,21 +182,33 @@ class Mx4Weights:
     e8: torch.Tensor               # E8M0 [G*N, K/32], blocks of 32 along K
 
 
+def _on(stream):
+    """What a call on ``stream`` allocates belongs to that stream, so that its memory is not handed out again too early."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 def mx4_quantize(w: torch.Tensor, mode: int = B.MX_RCEIL, stream=None) -> Mx4Weights:
-    """MXFP4 codes of bf16 w [N, K] or [G, N, K], blocks of 32 along K."""
+    """MXFP4 codes of bf16 w [N, K] or [G, N, K], blocks of 32 along K.  With a
+    ``stream``, here and below, as under ``torch.cuda.stream(stream)``."""
+    if stream is not None:
+        with _on(stream):
+            return mx4_quantize(w, mode)
     *lead, K = w.shape
     q = torch.empty((*lead, K // 2), dtype=torch.uint8, device=w.device)
     e8 = torch.empty((math.prod(lead), K // 32), dtype=torch.uint8, device=w.device)
-    FB.mxfp4_quant_1x32_row(w, q, e8, mode, stream)
+    FB.mxfp4_quant_1x32_row(w, q, e8, mode)
     return Mx4Weights(q, e8)
 
 
 def mx4_widen(w: Mx4Weights, stream=None) -> MxExpertWeights:
     """The same weights as rowwise MXFP8 codes, exactly: for the products of a
     prompt (``mx_moe_forward``, ``MxMoEFFN``).  The scales are shared."""
+    if stream is not None:
+        with _on(stream):
+            return mx4_widen(w)
     *lead, half = w.q.shape
     q = torch.empty((*lead, 2 * half), dtype=torch.uint8, device=w.q.device)
-    FB.mxfp4_to_mxfp8(w.q, q, stream)
+    FB.mxfp4_to_mxfp8(w.q, q)
     return MxExpertWeights(q, w.e8, None, None)
 
 
@@ -216,6 +228,9 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     [N, K] in MX codes, 4 bits (``mx4_quantize``) or 8 (the rowwise codes of
     ``mx_quantize_experts``).  x is not rounded to MXFP8, and sums are fp32: a
     product for decoding, bound by the bytes of W.  It has no gradient."""
+    if stream is not None:
+        with _on(stream):
+            return mx_linear_few(x, w)
     _refuse_grad("mx_linear_few", x)
     q, e8, bits = _held(w)
     if q.dim() == 3 and q.shape[0] == 1:
@@ -225,7 +240,7 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     if M > 0:
         n = _few_workspace(M, K)
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-        FB.mx_few_linear(x, q, e8, bits, y, workspace, stream)
+        FB.mx_few_linear(x, q, e8, bits, y, workspace)
     return y
 
 

@@ -83,6 +83,37 @@ def test_against_64_bits(M, E, k, C, F, bits):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M,E,k,C,F", [(16, 32, 4, 128, 1056), (32, 32, 4, 96, 1056), (27, 48, 2, 160, 704), (17, 16, 4, 384, 2048)])
+def test_more_tiles_than_blocks(M, E, k, C, F, bits):
+    """Enough experts and rows for blocks to take one tile after the other."""
+    c = Case(M, E, k, C, F, bits)
+    c.check(c.run())
+
+
+def test_as_many_choices_as_there_may_be():
+    c = Case(32, 1024, 32, 32, 32, 4, score="sigmoid")
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("M", [1, 3, 9, 32])
+def test_choice_by_the_router_s_last_bit(M):
+    """Experts whose logits differ by one unit in the last place of fp32: tokens with one element other than zero."""
+    E, C, F = 40, 96, 32
+    c = Case(M, E, 1, C, F, 4)
+    rng = np.random.default_rng(M)
+    router = np.ones((E, C), np.float32)
+    best = rng.integers(0, E, C)
+    router[best, np.arange(C)] = 1 + np.float32(2.0 ** -23)
+    x = np.zeros((M, C), np.float32)
+    at = rng.integers(0, C, M)
+    x[np.arange(M), at] = 1.0
+    c.x, c.router = x, router
+    c.tx, c.trouter = torch.from_numpy(x).bfloat16().cuda(), torch.from_numpy(router).cuda()
+    assert (c.want()[2][:, 0] == best[at]).all()
+    c.check(c.run(renormalize=True))
+
+
 @pytest.mark.parametrize("M", range(1, 33))
 def test_every_token_count(M):
     c = Case(M, 6, 2, 96, 128, 4 if M % 2 else 8)
@@ -166,6 +197,37 @@ def test_calls_repeat_bit_for_bit_on_two_streams_at_once(M):
                 got.append(c.run())
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("Ms", [(1, 1, 1), (5, 1, 32), (32, 17, 2)])
+def test_one_behind_the_other(Ms):
+    """Layers and linears that read what the call before wrote, none waited for, as a decoder's step runs them."""
+    c = [Case(M, 16, 4, 256, F, bits) for M, F, bits in zip((4, 4, 4), (160, 512, 1056), (4, 8, 4))]
+    x0 = Case(32, 16, 4, 256, 32, 4).tx
+    proj = L.mx4_quantize((torch.randn(256, 256, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) * 0.06).bfloat16())
+
+    def walk(wait):
+        x, out = x0.clone(), []
+        for step in range(12):
+            M, case = Ms[step % len(Ms)], c[step % 3]
+            h = L.mx_linear_few(x[:M], proj)
+            wait()
+            y = case.run(h)
+            wait()
+            z = case.run(y)  # right behind, with a workspace that may be the same memory
+            wait()
+            x[:M].copy_(z / z.float().norm(dim=1, keepdim=True).clamp_min(1e-3) * 16)
+            wait()
+            out += [h.clone(), y.clone(), z.clone()]
+            wait()
+        return out
+
+    want = walk(torch.cuda.synchronize)
+    assert all(bool(torch.isfinite(w).all()) for w in want) and bool(want[-1].any())
+    for _ in range(5):
+        got = walk(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
 
 
 def test_tokens_one_at_a_time():

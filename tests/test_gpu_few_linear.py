@@ -180,6 +180,85 @@ def test_captured_and_replayed_with_new_tokens():
         check(y, x, w)
 
 
+def test_on_a_stream_of_its_own():
+    """The result and the workspace are the stream's: what the current stream allocates meanwhile is other memory."""
+    cases = [inputs(M, 3000, 4096, 4) for M in (1, 9, 32)]
+    want = [L.mx_linear_few(x, w) for x, w in cases]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, 0):
+        for (x, w), expected in zip(cases, want):
+            got, junk = [], []
+            for _ in range(20):
+                got.append(L.mx_linear_few(x, w, stream=stream))
+                junk.append(torch.full((1 << 16,), 7.0, device="cuda"))
+                junk = junk[-2:]
+            torch.cuda.synchronize()
+            assert all(torch.equal(g, expected) for g in got)
+    w = torch.randn(96, 160, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    q = L.mx4_quantize(w, stream=side)
+    wide = L.mx4_widen(q, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(q.q, L.mx4_quantize(w).q) and torch.equal(wide.q_row, L.mx4_widen(q).q_row)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 140, 256), (4, 300, 1024), (32, 70, 640)])
+def test_codes_at_every_16th_byte(M, N, K):
+    """Rows of whole chunks whose codes start 16 bytes past what TMA spreads out."""
+    x, w = inputs(M, N, K, 4)
+    room = torch.empty(w.q.numel() + 64, dtype=torch.uint8, device="cuda")
+    want = L.mx_linear_few(x, w)
+    for at in (0, 16, 32, 48):
+        q = room[at:at + w.q.numel()].view(w.q.shape)
+        q.copy_(w.q)
+        got = L.mx_linear_few(x, L.Mx4Weights(q, w.e8))
+        check(got, x, w)
+        assert torch.equal(got, want)
+    with pytest.raises(B.Fp8bwError):
+        L.mx_linear_few(x, L.Mx4Weights(room[8:8 + w.q.numel()].view(w.q.shape), w.e8))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 500, 12320), (2, 200, 16352), (2, 130, 4064), (1, 129, 32)])
+def test_one_or_two_tokens_of_odd_rows(M, N, K):
+    x, w = inputs(M, N, K, 4)
+    check(L.mx_linear_few(x, w), x, w)
+
+
+@pytest.mark.parametrize("Ms", [(1, 1, 1, 1), (2, 3, 2, 9), (32, 32, 1, 32), (17, 1, 5, 2)])
+def test_one_behind_the_other(Ms):
+    """Each call reads what the one before wrote, and weights and tokens are written over right after a call: a kernel starts
+    under the one before, and none may read or write too early."""
+    rng = np.random.default_rng(3)
+    weights = [[held(torch.from_numpy((0.05 * rng.standard_normal((512, 512))).astype(np.float32)).bfloat16().cuda(), bits)
+                for bits in (4, 8)] for _ in range(2)]
+    x0 = torch.from_numpy(rng.standard_normal((32, 512)).astype(np.float32)).bfloat16().cuda()
+
+    def walk(wait):
+        x, out = x0.clone(), []
+        w = [L.Mx4Weights(weights[0][0].q.clone(), weights[0][0].e8.clone()), weights[0][1]]
+        for step in range(12):
+            M = Ms[step % len(Ms)]
+            y = L.mx_linear_few(x[:M], w[step % 2])
+            wait()
+            x[:M].copy_(y)
+            wait()
+            w[0].q.copy_(weights[(step + 1) % 2][0].q), w[0].e8.copy_(weights[(step + 1) % 2][0].e8)
+            wait()
+            if step % 3 == 2:  # codes written by a kernel right before they are read
+                w[0] = L.mx4_quantize((x[:, :, None].expand(32, 512, 16).permute(0, 2, 1).reshape(512, 512) * 0.05).contiguous())
+                wait()
+            out.append(y.clone())
+            wait()
+        return out
+
+    want = walk(torch.cuda.synchronize)
+    for _ in range(5):
+        got = walk(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_refusals_on_the_device():
     x, w = inputs(4, 50, 96, 4)
     for bad, error in ((x.t().contiguous().t(), ValueError), (x.float(), TypeError), (x[:, :64], ValueError),
