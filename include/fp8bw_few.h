@@ -42,9 +42,9 @@ int mxfp4_quant_1x32_row(const fp8bw_bf16* w, int64_t R, int64_t C, uint8_t* q, 
  *   q4 : e2m1 [R, C/2]    q8 : e4m3 [R, C]      C a positive multiple of 32. */
 int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q8, void* stream);
 
-/* Bytes of workspace mx_few_linear needs: 0 for one or two tokens that are not
- * very long, and for invalid dims.  Host-only. */
-size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K);
+/* Bytes of workspace mx_few_linear needs: 0 for one or two tokens and a matrix
+ * that is not large, and for invalid dims.  Host-only. */
+size_t mx_few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* y = x W^T.
  *   x : bf16 [M, K]    w : codes of W[N, K]    e8 : E8M0 [N][K/32]    y : bf16 [M, N]

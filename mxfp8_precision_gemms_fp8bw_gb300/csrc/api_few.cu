@@ -53,8 +53,8 @@ FP8BW_API int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q
   return launched(launch_mxfp4_to_mxfp8(q4, R * C, q8, d->num_sms, as_stream(stream)), name);
 }
 
-FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t K) {
-  return linear_dims_ok(M, 1, K) ? few_linear_workspace_bytes(M, K) : 0;
+FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return linear_dims_ok(M, N, K) ? few_linear_workspace_bytes(M, N, K) : 0;
 }
 
 FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
@@ -68,7 +68,7 @@ FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t
                 name, (long long)M, (long long)N, (long long)K);
   if (!all_aligned({x, w, e8, y, workspace})) return fail(FP8BW_ERR_ALIGN, "%s: pointers must be 16-byte aligned", name);
   if (!bits_ok(bits)) return fail(FP8BW_ERR_ARG, "%s: bits %d is neither 4 nor 8", name, bits);
-  const size_t need = few_linear_workspace_bytes(M, K);
+  const size_t need = few_linear_workspace_bytes(M, N, K);
   if (need > 0 && !workspace)
     return fail(FP8BW_ERR_NULL, "%s: these dims need a workspace of %zu bytes", name, need);
   if (workspace_bytes < need)

@@ -102,12 +102,8 @@ struct Product {
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrives on `bar` once the thread's copies so far have landed.
@@ -118,9 +114,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Whether a wait came to its end for all lanes: they go on, or unwind, together.
 __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 
-// A chunk of tokens that stay in shared memory, and the most of them: with four stages as much as two blocks an SM have.
+// A chunk of tokens that stay in shared memory, and the most of them: beside three stages of packed codes as much as two blocks
+// an SM have room for.
 constexpr uint32_t kHeld = 16 * 128;
-constexpr int kMostHeld = 16;
+constexpr int kMostHeld = 12;
 constexpr int kMostDepth = 8;
 struct Shared {
   // Of a stage: packed codes have landed, all of it has, its scales are in tensor memory, it has been read.
@@ -364,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const uint32_t stage = stage0 + ring.s * stages.bytes;
         if (whole_words && !packed) {
-          cp_async<4>(stage + scale_to, p.m.e8 + scale);
+          cp_async4(stage + scale_to, p.m.e8 + scale);
           cp_async_arrive(&sh.full[ring.s]);
         } else {
           uint32_t word;
@@ -746,18 +743,19 @@ int places(int size, bool alone) {
 }
 
 // Blocks of a cluster, a power of two up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in
-// chunks' time (0.2 us): those of a block, half as long again where it brings its tokens into parts itself, for each round of
-// blocks; the cluster's start and exchange, 2.0, 2.6 and 4.0 us for 2, 4 and 8; and the sums that change hands.  On both sides
+// chunks' time (0.2 us): those of a block, half as long again where it brings its tokens into parts itself or spreads packed
+// codes, for each round of blocks; the cluster's start and exchange, 2.0, 2.6 and 4.0 us for 2, 4 and 8; and the sums that change hands.  On both sides
 // of the choice (us, clusters of 1, 2, 4, 8; a linear of 8192 x 5120 or a layer's decode step): linear, one token, 4 bits 10.5,
 // 10.5, 9.6, 14.6; 32 tokens 13.5, 12.5, 13.4, 21.3; down of two experts 4096 -> 5120 in a layer of 41.4, 35.2, 32.1, 35.5;
-// up of four experts 2048 -> 1024 in 20.1, 21.7, 22.1, 27.2.
-int splits_of(int64_t tiles, int64_t chunks, int tokens, bool held, const int (&room)[4]) {
+// up of four experts 2048 -> 1024 in 20.1, 21.7, 22.1, 27.2;
+// packed, three tokens of 2048 x 2080 10.5 alone, 7.5 in fours.
+int splits_of(int64_t tiles, int64_t chunks, int tokens, bool slow, const int (&room)[4]) {
   int best = 0;
   int64_t least = INT64_MAX;
   const int64_t exchange[4] = {0, 80, 104, 160};
   for (int i = 0; i < 4 && (1 << i) <= chunks; ++i) {
     const int64_t s = 1 << i, rounds = (tiles * s + room[i] - 1) / room[i];
-    const int64_t cost = rounds * ((chunks + s - 1) / s) * (held ? 12 : 8) + exchange[i] + (i > 0 ? tokens * s : 0);
+    const int64_t cost = rounds * ((chunks + s - 1) / s) * (slow ? 12 : 8) + exchange[i] + (i > 0 ? tokens * s : 0);
     if (cost < least) best = i, least = cost;
   }
   return 1 << best;
@@ -859,7 +857,7 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
     if (mine[alone][0] == 0) {
       for (int i = 3; i >= 0; --i) mine[alone][i] = places(1 << i, alone);
     }
-    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr, mine[alone]);
+    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr || p.packed, mine[alone]);
   }
   if (p.x != nullptr) {
     while (p.splits * kMostHeld < chunks) p.splits *= 2;
@@ -892,11 +890,17 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 
 }  // namespace
 
-// One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages:
-// 9.6 us for one of 8192 x 5120 in 4 bits, 13.8 with the kernel in front.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
-static bool held_tokens(int64_t M, int64_t K) { return M <= 2 && K <= 8 * kMostHeld * kChunk; }
+// One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages and
+// no block follows another, with the tokens once more: 9.6 us for one token of 8192 x 5120 in 4 bits, 13.8 with the kernel in
+// front; but 44 us for 65536 x 4096, 32 with it.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
+static bool held_tokens(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kPlaces = 288;  // two blocks an SM in clusters of eight
+  int64_t splits = 1;
+  while (splits * kMostHeld * kChunk < K) splits *= 2;
+  return M <= 2 && splits <= 8 && (N + kRows - 1) / kRows * splits <= kPlaces;
+}
 
-size_t few_linear_workspace_bytes(int64_t M, int64_t K) { return held_tokens(M, K) ? 0 : few_tokens_bytes(M, K); }
+size_t few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return held_tokens(M, N, K) ? 0 : few_tokens_bytes(M, K); }
 
 cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   Product p{};
@@ -904,7 +908,7 @@ cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   p.M = static_cast<int>(a.M);
   p.y = a.y;
   p.status = a.status;
-  if (held_tokens(a.M, a.K)) {
+  if (held_tokens(a.M, a.N, a.K)) {
     p.x = a.x;
   } else {
     uint8_t* tokens = static_cast<uint8_t*>(a.workspace);

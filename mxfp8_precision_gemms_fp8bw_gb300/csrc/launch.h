@@ -194,7 +194,7 @@ struct FewLinearArgs {
   int* status;
   int num_sms;
 };
-size_t few_linear_workspace_bytes(int64_t M, int64_t K);
+size_t few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st);
 
 struct FewMoeArgs {

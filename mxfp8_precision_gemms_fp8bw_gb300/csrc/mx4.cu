@@ -1,7 +1,7 @@
 // MXFP4 weights: bf16 to e2m1 codes with E8M0 scales, and those codes widened
 // to e4m3.
+#include "common.cuh"
 #include "launch.h"
-#include "mx_weight.cuh"
 
 namespace fp8bw {
 namespace {

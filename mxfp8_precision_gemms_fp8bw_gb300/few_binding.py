@@ -17,7 +17,7 @@ FEW_TOKENS = 32
 _SIGNATURES = {
     "mxfp4_quant_1x32_row": [_P, _I64, _I64, _P, _P, _INT, _P],
     "mxfp4_to_mxfp8": [_P, _I64, _I64, _P, _P],
-    "mx_few_linear_workspace_bytes": [_I64, _I64],
+    "mx_few_linear_workspace_bytes": [_I64, _I64, _I64],
     "mx_few_linear": [_P, _P, _P, _INT, _I64, _I64, _I64, _P, _P, _SIZE, _P],
     "mx_few_moe_workspace_bytes": [_I64, _I64, _I64, _I64, _I64],
     "mx_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C, _P,
@@ -53,8 +53,8 @@ def mxfp4_to_mxfp8(q4, q8, stream=None) -> None:
                                   _stream(stream, q4)))
 
 
-def mx_few_linear_workspace_bytes(M: int, K: int) -> int:
-    return int(lib().mx_few_linear_workspace_bytes(M, K))
+def mx_few_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().mx_few_linear_workspace_bytes(M, N, K))
 
 
 def mx_few_linear(x, w, e8, bits, y, workspace=None, stream=None) -> None:

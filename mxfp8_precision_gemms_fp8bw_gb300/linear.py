@@ -238,7 +238,7 @@ def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None)
     M, K = x.shape
     y = torch.empty((M, q.shape[0]), dtype=torch.bfloat16, device=x.device)
     if M > 0:
-        n = _few_workspace(M, K)
+        n = _few_workspace(M, q.shape[0], K)
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
         FB.mx_few_linear(x, q, e8, bits, y, workspace)
     return y

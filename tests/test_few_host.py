@@ -58,14 +58,16 @@ def test_widen_refusals(lib, code, kw):
 ])
 def test_linear_refusals(lib, code, kw):
     M, N, K = 32, 65, 2048
-    ok = [P, 2 * P, 30 * P, 4, M, N, K, 40 * P, 50 * P, lib.mx_few_linear_workspace_bytes(M, K), None]
+    ok = [P, 2 * P, 30 * P, 4, M, N, K, 40 * P, 50 * P, lib.mx_few_linear_workspace_bytes(M, N, K), None]
     assert lib.mx_few_linear(*[kw.get(f"a{i}", v) for i, v in enumerate(ok)]) == getattr(B, "ERR_" + code)
 
 
 def test_linear_workspace(lib):
     size = lib.mx_few_linear_workspace_bytes
-    assert size(2, 5120) == 0 and size(32, 5120) >= 32 * 5120 * 2 and size(1, 1 << 20) >= 2 << 20
-    assert size(0, 5120) == size(33, 5120) == size(32, 5100) == size(32, (1 << 22) + 32) == 0
+    assert size(2, 640, 5120) == 0 and size(32, 640, 5120) >= 32 * 5120 * 2 and size(1, 640, 1 << 20) >= 2 << 20
+    assert size(1, 1 << 20, 5120) >= 2 * 5120
+    assert size(0, 640, 5120) == size(33, 640, 5120) == size(32, 640, 5100) == size(32, 640, (1 << 22) + 32) == 0
+    assert size(32, 0, 5120) == size(32, 1 << 31, 5120) == 0
 
 
 def test_layer_workspace(lib):

@@ -158,7 +158,7 @@ def test_calls_repeat_bit_for_bit_on_two_streams_at_once(M, N, K, bits):
 def test_nothing_is_written_behind_the_result(M, N, K):
     x, w = inputs(M, N, K, 4)
     buf = torch.full((M * N + 512,), 3.0, dtype=torch.bfloat16, device="cuda")
-    n = FB.mx_few_linear_workspace_bytes(M, K)
+    n = FB.mx_few_linear_workspace_bytes(M, N, K)
     for fill in (0x00, 0xFF):  # whatever was in the workspace before
         ws = torch.full((n + 256,), fill, dtype=torch.uint8, device="cuda")
         FB.mx_few_linear(x, w.q, w.e8, 4, buf[:M * N].view(M, N), ws[:n] if n else None)
