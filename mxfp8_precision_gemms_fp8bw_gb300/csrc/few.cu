@@ -742,23 +742,26 @@ int places(int size, bool alone) {
   return size;
 }
 
-// Blocks of a cluster, a power of two up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in
-// chunks' time (0.2 us): those of a block, half as long again where it brings its tokens into parts itself or spreads packed
-// codes, for each round of blocks; the cluster's start and exchange, 2.0, 2.6 and 4.0 us for 2, 4 and 8; and the sums that change hands.  On both sides
-// of the choice (us, clusters of 1, 2, 4, 8; a linear of 8192 x 5120 or a layer's decode step): linear, one token, 4 bits 10.5,
-// 10.5, 9.6, 14.6; 32 tokens 13.5, 12.5, 13.4, 21.3; down of two experts 4096 -> 5120 in a layer of 41.4, 35.2, 32.1, 35.5;
-// up of four experts 2048 -> 1024 in 20.1, 21.7, 22.1, 27.2;
-// packed, three tokens of 2048 x 2080 10.5 alone, 7.5 in fours.
-int splits_of(int64_t tiles, int64_t chunks, int tokens, bool slow, const int (&room)[4]) {
-  int best = 0;
+// Blocks of a cluster, up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in eighths of a chunk's
+// time (0.2 us): the chunks of a block, half as long again where it brings its tokens into parts itself or spreads packed codes,
+// for each round of blocks; the cluster's start and exchange, 2.0 us for two blocks to 4.0 for eight; and the sums that change
+// hands.  On both sides of the choice (us, by blocks of a cluster; a linear of 8192 x 5120 or a layer's decode step):
+//   linear, one token, 4 bits          1: 10.5   2: 10.5   4: 9.6 *  8: 14.6 (more blocks than places)
+//   linear, 32 tokens, 4 bits          1: 13.5   2: 12.5 * 3: 14.6   4: 13.4   8: 21.3
+//   linear, 5 tokens, 6001 x 7136      2: 17.0   4: 15.4   5: 14.4 * 6: 19.8
+//   linear, 3 tokens, 2048 x 2080      1: 10.5   4: 7.5 *
+//   up of four experts 2048 -> 1024    1: 17.4 * 2: 18.5
+//   down of 8 experts 4096 -> 5120     4: 99.6   5: 97.9   6: 97.1 * 8: 109
+int splits_of(int64_t tiles, int64_t chunks, int tokens, bool slow, const int (&room)[8]) {
+  int best = 1;
   int64_t least = INT64_MAX;
-  const int64_t exchange[4] = {0, 80, 104, 160};
-  for (int i = 0; i < 4 && (1 << i) <= chunks; ++i) {
-    const int64_t s = 1 << i, rounds = (tiles * s + room[i] - 1) / room[i];
-    const int64_t cost = rounds * ((chunks + s - 1) / s) * (slow ? 12 : 8) + exchange[i] + (i > 0 ? tokens * s : 0);
-    if (cost < least) best = i, least = cost;
+  const int64_t exchange[8] = {0, 80, 110, 104, 118, 132, 146, 160};
+  for (int s = 1; s <= 8 && s <= chunks; ++s) {
+    const int64_t rounds = (tiles * s + room[s - 1] - 1) / room[s - 1];
+    const int64_t cost = rounds * ((chunks + s - 1) / s) * (slow ? 12 : 8) + exchange[s - 1] + (s > 1 ? tokens * s : 0);
+    if (cost < least) best = s, least = cost;
   }
-  return 1 << best;
+  return best;
 }
 
 // The weights as TMA reads them, boxes of `box` rows by a chunk: e4m3 codes as bytes; e2m1 codes spread out, or, where rows are
@@ -850,17 +853,17 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   if (in_turn) {
     p.splits = 1;
   } else {
-    static thread_local int room[64][2][4] = {};  // by device
-    int dev = 0, here[2][4] = {};
+    static thread_local int room[64][2][8] = {};  // by device
+    int dev = 0, here[2][8] = {};
     if (const cudaError_t e = cudaGetDevice(&dev)) return e;
-    int(*const mine)[4] = dev < 64 ? room[dev] : here;
+    int(*const mine)[8] = dev < 64 ? room[dev] : here;
     if (mine[alone][0] == 0) {
-      for (int i = 3; i >= 0; --i) mine[alone][i] = places(1 << i, alone);
+      for (int i = 7; i >= 0; --i) mine[alone][i] = places(i + 1, alone);
     }
     p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr || p.packed, mine[alone]);
   }
   if (p.x != nullptr) {
-    while (p.splits * kMostHeld < chunks) p.splits *= 2;
+    while (p.splits * kMostHeld < chunks) ++p.splits;  // at most eight, as held_tokens has it
     p.share = (chunks + p.splits - 1) / p.splits;
     pick_depth();
   }
@@ -895,8 +898,7 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 // front; but 44 us for 65536 x 4096, 32 with it.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
 static bool held_tokens(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kPlaces = 288;  // two blocks an SM in clusters of eight
-  int64_t splits = 1;
-  while (splits * kMostHeld * kChunk < K) splits *= 2;
+  const int64_t splits = (K + kMostHeld * kChunk - 1) / (kMostHeld * kChunk);
   return M <= 2 && splits <= 8 && (N + kRows - 1) / kRows * splits <= kPlaces;
 }
 

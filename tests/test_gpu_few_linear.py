@@ -219,9 +219,12 @@ def test_codes_at_every_16th_byte(M, N, K):
         L.mx_linear_few(x, L.Mx4Weights(room[8:8 + w.q.numel()].view(w.q.shape), w.e8))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 500, 12320), (2, 200, 16352), (2, 130, 4064), (1, 129, 32)])
-def test_one_or_two_tokens_of_odd_rows(M, N, K):
-    x, w = inputs(M, N, K, 4)
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M,N,K", [(1, 500, 12320), (2, 200, 16352), (2, 130, 4064), (1, 129, 32), (1, 4608, 12288), (2, 4500, 12256),
+                                   (2, 4609, 12288), (1, 640, 7680), (2, 1000, 10752), (1, 36865, 128), (1, 36864, 1536)])
+def test_one_or_two_tokens(M, N, K, bits):
+    """Around the lengths and heights up to which the product brings the tokens into parts itself."""
+    x, w = inputs(M, N, K, bits)
     check(L.mx_linear_few(x, w), x, w)
 
 
