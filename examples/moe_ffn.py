@@ -3,7 +3,7 @@
     python examples/moe_ffn.py [--steps 30]
 
 Every step goes through routing, dispatch, the grouped products, the gated activation with its 8-bit checkpoint, combine,
-and all of their gradients; the last part is the same layer as a decoder calls it, a token at a time.
+and all of their gradients; the last part is the same layer as a decoder calls it, a token at a time and in one call for a few.
 """
 import argparse
 import os
@@ -37,8 +37,10 @@ def main(steps: int = 30, tokens: int = 1000, dim: int = 256, hidden: int = 512,
         codes = layer.weight_codes(colwise=False)  # the weights stay as they are from here on
         together = layer(x[:4], codes)
         alone = torch.cat([layer(x[i:i + 1], codes) for i in range(4)])
+        few = layer.decode(x[:4], layer.weight_codes(bits=4))  # for up to 32 tokens, weights in 4 bits
     B.fp8bw_sync_status()
     print("tokens one at a time equal the batch:", bool(torch.equal(together, alone)))
+    print(f"with weights in 4 bits {float((few - together).float().norm() / together.float().norm()):.3f} of the result away")
     return [float(v) for v in losses], together, alone
 
 

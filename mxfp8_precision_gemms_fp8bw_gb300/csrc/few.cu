@@ -8,7 +8,22 @@
 // operand; the tokens are the narrow one (N), in e4m3 as well, as the sum of
 // two or three parts (few_tokens.cuh) that are columns of their own.  (A
 // version that turned weights into f16 for mma.sync took 55 instructions for
-// 32 weights of 32 rows, 2 to 4 times the time that memory allows.)
+// 32 weights of 32 rows: 33 us for 32 tokens of 8192 x 5120 in 4 bits, 12.6
+// here.)
+//
+// Measured, one call behind the other, of weights larger than the cache where
+// they are: up of 8 experts 5120 -> 4096, 8 bits, 32 tokens 59 us (5.9 TB/s),
+// their down product 38 us (4.6 TB/s).  A linear of 8192 x 16384 for 4 tokens
+// 28 us in 8 bits (4.9 TB/s), 20 in 4 (3.5 TB/s); of 8192 x 5120 14 and 10; of
+// 2048 x 2048, one token, 5.5.  What bounds them:
+//   8 bits, many tiles   memory: 87 % of the copy bandwidth while it streams
+//   4 bits               the rate of TMA, which reads 64 bytes to a row: it takes
+//                        about as long for a row as with 128.  With no products,
+//                        no scales and the weights in the cache the 20 us of
+//                        8192 x 16384 are still 18; asking for chunks ahead of
+//                        the stages, into the cache, takes 0 to 15 % longer.
+//   short products       a start of about 2 us, the pipeline's first chunk,
+//                        and, of a cluster, 2 to 4 us for blocks to meet and sum
 #include <cuda.h>
 
 #include "few.h"
