@@ -437,10 +437,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     // The first chunks before the others of the block have come together.
     if (lane == 0 && t < t1) {
-      if (held) {
-        grid_wait();
-        fence_proxy_async_global();
-      }
+      if (held) grid_wait();
+      fence_proxy_async_global();  // codes that a kernel wrote may be read at once
       begin_run(true);
       while (r.n > 0 && issued < stages.depth) load();
     }

@@ -1,4 +1,9 @@
 """The mixture-of-experts layer for a few tokens, against the formulas in 64 bits (oracle.few has its error bound)."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -263,6 +268,52 @@ def test_captured_in_two_graphs_and_replayed_with_new_tokens():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_threads_with_streams_of_their_own():
+    cases = [Case(M, 16, 4, 256, 160, bits) for M, bits in ((1, 4), (9, 8), (32, 4), (2, 8))]
+    proj = [L.mx4_quantize((torch.randn(300, 256, device="cuda") * 0.06).bfloat16()) for _ in cases]
+    want = [(c.run(), L.mx_linear_few(c.tx, w)) for c, w in zip(cases, proj)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                got = (cases[i].run(), L.mx_linear_few(cases[i].tx, proj[i]))
+            torch.cuda.current_stream().synchronize()
+        if not all(torch.equal(g, w) for g, w in zip(got, want[i])):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    [t.start() for t in threads], [t.join() for t in threads]
+    assert wrong == []
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from mxfp8_precision_gemms_fp8bw_gb300 import linear as L, moe
+g = torch.Generator("cuda").manual_seed(2)
+new = lambda *s: (torch.randn(s, device="cuda", generator=g) * 0.1).bfloat16()
+x, r, w = new(5, 256), new(8, 256).float(), [new(8, 256, 256), new(8, 256, 128), new(300, 256)]
+w13, w2, w1 = map(L.mx4_quantize, w)  # the library's first call is eager; the products' first ones are captured
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def step():
+    return moe.ffn_few(x, r, w13, w2, 2), L.mx_linear_few(x, w1), L.mx_linear_few(x[:1], w1)
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step())), "captured and eager differ"
+"""
+
+
+def test_first_call_under_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_rows_behind_the_result_and_the_workspace_stay():
