@@ -15,7 +15,7 @@
 // they are: up of 8 experts 5120 -> 4096, 8 bits, 32 tokens 59 us (5.9 TB/s),
 // their down product 38 us (4.6 TB/s).  A linear of 8192 x 16384 for 4 tokens
 // 28 us in 8 bits (4.9 TB/s), 20 in 4 (3.5 TB/s); of 8192 x 5120 14 and 10; of
-// 2048 x 2048, one token, 5.5.  What bounds them:
+// 2048 x 2048, one token, 4.8.  What bounds them:
 //   8 bits, many tiles   memory: 87 % of the copy bandwidth while it streams
 //   4 bits               the rate of TMA, which reads 64 bytes to a row: it takes
 //                        about as long for a row as with 128.  With no products,
@@ -412,6 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     cp_async_wait_all();
+    // The next call's first kernel may start: it waits for the end of this one before it reads or writes anything.  One token of
+    // 8192 x 5120 9.6 -> 9.1 us; a linear behind a kernel of its own for the tokens gains nothing, 32 tokens 12.5 -> 13.3.
+    if (kMode == kDown || held) grid_release();
   } else if (warp == kWeights) {
     // ------------------------------------------------------------ weights
     Ring ring(stages.depth);
@@ -907,7 +910,7 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 }  // namespace
 
 // One or two tokens are brought into parts by the product itself, as long as a block's share of them fits beside the stages and
-// no block follows another, with the tokens once more: 9.6 us for one token of 8192 x 5120 in 4 bits, 13.8 with the kernel in
+// no block follows another, with the tokens once more: 9.1 us for one token of 8192 x 5120 in 4 bits, 13.8 with the kernel in
 // front; but 44 us for 65536 x 4096, 32 with it.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
 static bool held_tokens(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kPlaces = 288;  // two blocks an SM in clusters of eight
