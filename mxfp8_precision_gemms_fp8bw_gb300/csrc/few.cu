@@ -133,7 +133,7 @@ __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 // an SM have room for.
 constexpr uint32_t kHeld = 16 * 128;
 constexpr int kMostHeld = 12;
-constexpr int kMostDepth = 8;
+constexpr int kMostDepth = 5;  // of 19 KB, as small as they are, in kHalfSmem
 struct Shared {
   // Of a stage: packed codes have landed, all of it has, its scales are in tensor memory, it has been read.
   uint64_t landed[kMostDepth], full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
@@ -729,16 +729,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ---------------------------------------------------------------- launches
 
-// Shared memory of a block beside its fixed part, alone on an SM and as one of two: an SM has 228 KB, of which each block takes
-// 1 KB more than it asks for.
-constexpr uint32_t kMostSmem = 226 * 1024, kHalfSmem = 111 * 1024;
+// Shared memory of a block beside its fixed part, as one of two on an SM, which has 228 KB; each block takes 1 KB more than it
+// asks for.
+constexpr uint32_t kHalfSmem = 111 * 1024;
 static_assert(sizeof(Shared) <= 1024, "of the kilobyte that this leaves");
 
-// Blocks of clusters of `size` that run at once, two to an SM or alone: shared memory decides.  Clusters stay within a part of
-// the chip, whose SMs do not always come out even: of 304 places, 296 in clusters of four and 288 of eight; of 152, 144 and 120.
-// The query goes by a kernel without tensor memory; of one that takes some it counts a block an SM, where two do run.
-int places(int size, bool alone) {
-  const int smem = static_cast<int>(alone ? kMostSmem : kHalfSmem);
+// Blocks of clusters of `size` that run at once, two to an SM: shared memory decides.  Clusters stay within a part of the chip,
+// whose SMs do not always come out even: of 304 places, 296 in clusters of four, 276 of six and 288 of eight.  The query goes by a
+// kernel without tensor memory; of one that takes some it counts a block an SM, where two do run.
+int places(int size) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = size;
@@ -747,11 +746,11 @@ int places(int size, bool alone) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(size);
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kHalfSmem;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int clusters = 0;
-  if (cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostSmem)) == cudaSuccess &&
+  if (cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kHalfSmem)) == cudaSuccess &&
       cudaOccupancyMaxActiveClusters(&clusters, few_tokens_kernel, &cfg) == cudaSuccess && clusters > 0)
     return clusters * size;
   (void)cudaGetLastError();
@@ -805,7 +804,7 @@ cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
   if (dev >= 64 || !allowed[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostSmem));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kHalfSmem));
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed[dev] = true;
   }
@@ -837,65 +836,54 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t tiles = (rows + tile - 1) / tile;
   const int chunks = (p.m.K + kChunk - 1) / kChunk;
-  // Enough runs for every block to have some: whole ones in turn, which leaves the stages no gaps.
-  const bool in_turn = kMode == kUp && tiles * copies >= 3 * num_sms;
-  const bool many = kMode == kDown || in_turn;
-  p.tiles = in_turn ? static_cast<int>(tiles) : 0;
   p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
   p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
   const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales, stage = stages_of(0, 0, tokens, p.packed).bytes;
+  // Enough runs for every block to have some: whole ones in turn, which leaves the stages no gaps (17 tokens over 64 experts 46.8
+  // us, otherwise 50.5), where their sums leave room for two blocks of three stages an SM.
+  const uint32_t sums = p.M * kRows * 4, slot = sizeof(FewSlot);
+  const bool in_turn = kMode == kUp && tiles * copies >= 3 * num_sms && 1024 + 3 * stage + sums + copies * slot <= kHalfSmem;
+  const bool many = kMode == kDown || in_turn;
+  p.tiles = in_turn ? static_cast<int>(tiles) : 0;
   // Room to receive: whole rounds of items, a round a share of every block, which is under 7 items more than there are.
   const uint32_t received = (p.M * kRows + 7 * 64) * 4;
   p.late = p.M > 16;
   p.slots = many ? (kMode == kDown ? matrices : copies) : 0;
   const uint32_t behind = (p.late || in_turn ? 0 : received) +
-                          (many ? p.M * kRows * 4 + p.slots * static_cast<uint32_t>(sizeof(FewSlot)) : 0);
-  // Two blocks an SM, of four stages or three (a block before the next product's, or before the next call's, then has the
-  // other's time to start); alone, with more stages, where three are too many for that.  kDown takes what it may of that and
-  // divides it by the plan.
-  int depth = 2;
-  const auto smem = [&](int n) {
-    return 1024 + n * stage + (p.x != nullptr ? p.held_at + p.share * (kHeld + kScales) : behind);
-  };
-  const auto pick_depth = [&] {
-    if (kMode == kDown) return;
-    depth = smem(4) <= kHalfSmem ? 4 : 3;
-    if (smem(3) > kHalfSmem)
-      while (depth < kMostDepth && smem(depth + 1) <= kMostSmem) ++depth;
-  };
-  if (p.x != nullptr) p.held_at = (behind + 1023) / 1024 * 1024;
-  pick_depth();  // held tokens take no more than kMostHeld chunks of it, which leaves room for two blocks
-  const bool alone = smem(depth) > kHalfSmem;
+                          (many ? sums + p.slots * slot : 0);
   if (in_turn) {
     p.splits = 1;
   } else {
-    static thread_local int room[64][2][8] = {};  // by device
-    int dev = 0, here[2][8] = {};
+    static thread_local int room[64][8] = {};  // by device
+    int dev = 0, here[8] = {};
     if (const cudaError_t e = cudaGetDevice(&dev)) return e;
-    int(*const mine)[8] = dev < 64 ? room[dev] : here;
-    if (mine[alone][0] == 0) {
-      for (int i = 7; i >= 0; --i) mine[alone][i] = places(i + 1, alone);
-    }
-    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr || p.packed, mine[alone]);
+    int(&mine)[8] = dev < 64 ? room[dev] : here;
+    if (mine[0] == 0)
+      for (int i = 7; i >= 0; --i) mine[i] = places(i + 1);
+    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr || p.packed, mine);
   }
+  uint32_t beside = 1024 + behind;
   if (p.x != nullptr) {
     while (p.splits * kMostHeld < chunks) ++p.splits;  // at most eight, as held_tokens has it
     p.share = (chunks + p.splits - 1) / p.splits;
-    pick_depth();
+    p.held_at = (behind + 1023) / 1024 * 1024;
+    beside = 1024 + p.held_at + p.share * (kHeld + kScales);
   }
-  p.ring = kMode == kDown ? (kHalfSmem - (smem(depth) - depth * stage)) / 1024 * 1024 : depth * stage;
+  // Two blocks an SM, of four stages or three (a block before the next product's, or before the next call's, then has the
+  // other's time to start: alone, with eight stages, a token of 8192 x 5120 took 13.9 us, so 9.6).  kDown takes what there is and
+  // divides it by the plan.
+  const int depth = kMode == kDown ? 2 : beside + 4 * stage <= kHalfSmem ? 4 : 3;
+  p.ring = kMode == kDown ? (kHalfSmem - beside) / 1024 * 1024 : depth * stage;
   p.stages = Stages{depth, tokens, stage};
-  const uint32_t bytes = smem(depth) - depth * stage + p.ring;
-  if (bytes > (kMode == kDown ? kHalfSmem : kMostSmem) || p.ring < depth * stage) return cudaErrorInvalidConfiguration;
+  if (beside + p.ring > kHalfSmem || p.ring < depth * stage) return cudaErrorInvalidConfiguration;
   const uint32_t columns = (many ? 2 : 1) * p.columns + (kMode == kDown ? kMostDepth : depth) * 8;
   p.tmem = 32;
   while (p.tmem < columns) p.tmem *= 2;
-  const int64_t blocks = num_sms * (bytes <= kHalfSmem ? 2 : 1);
-  const dim3 grid = in_turn ? dim3(static_cast<unsigned>(blocks))
+  const dim3 grid = in_turn ? dim3(static_cast<unsigned>(2 * num_sms))
                             : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
   CUtensorMap map{};
   if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, static_cast<uint32_t>(tile))) return cudaErrorInvalidValue;
-  return launch<kMode, kBits>(map, p, bytes, grid, st);
+  return launch<kMode, kBits>(map, p, beside + p.ring, grid, st);
 }
 
 template <Mode kMode>
