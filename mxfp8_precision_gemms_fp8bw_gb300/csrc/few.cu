@@ -152,6 +152,17 @@ __device__ __forceinline__ void named_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kBarrier), "n"(kCount) : "memory");
 }
 
+// The same, with a word on whether all may go on.
+template <int kBarrier, int kCount>
+__device__ __forceinline__ bool named_all(bool ok) {
+  uint32_t all;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(all)
+               : "r"(static_cast<uint32_t>(ok)), "n"(kBarrier), "n"(kCount)
+               : "memory");
+  return all != 0;
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
@@ -629,7 +640,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Lane i has the weight of column i.
       const float weight =
           kMode == kDown && lane < s.n ? __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + lane))) : 0.f;
-      if (!all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status))) break;
+      bool landed = all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status));
+      // Together: the sums of the run before have been read, and a warp that gave up would leave the others at a barrier.
+      if (in_turn) landed = named_all<2, kDrainWarps * 32>(landed);
+      if (!landed) break;
       tc_fence_after();
       const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
       uint32_t mask = s.mask;
@@ -674,7 +688,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = warp; i < s.n * 2; i += kDrainWarps)
           activate(p, r, i >> 1, i & 1, sums[(i >> 1) * kRows + (i & 1) * 32 + lane],
                    sums[(i >> 1) * kRows + 64 + (i & 1) * 32 + lane]);
-        named_sync<2, kDrainWarps * 32>();
       }
     }
     if (!many && t0 == t1)  // no share of a short contraction
