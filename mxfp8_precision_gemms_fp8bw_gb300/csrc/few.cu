@@ -882,10 +882,12 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
     p.held_at = (behind + 1023) / 1024 * 1024;
     beside = 1024 + p.held_at + p.share * (kHeld + kScales);
   }
-  // Two blocks an SM, of four stages or three (a block before the next product's, or before the next call's, then has the
-  // other's time to start: alone, with eight stages, a token of 8192 x 5120 took 13.9 us, so 9.6).  kDown takes what there is and
-  // divides it by the plan.
-  const int depth = kMode == kDown ? 2 : beside + 4 * stage <= kHalfSmem ? 4 : 3;
+  // Two blocks an SM, of five stages to three (a block before the next product's, or before the next call's, then has the
+  // other's time to start: alone, with eight stages, a token of 8192 x 5120 took 13.9 us, so 9.6).  Five, where there is room,
+  // took 28.7 us for a layer's step of one token and 30.9 for a linear of 65536 x 4096, four 29.4 and 31.9.  kDown takes what
+  // there is and divides it by the plan.
+  const auto fits = [&](int n) { return beside + n * stage <= kHalfSmem; };
+  const int depth = kMode == kDown ? 2 : fits(5) ? 5 : fits(4) ? 4 : 3;
   p.ring = kMode == kDown ? (kHalfSmem - beside) / 1024 * 1024 : depth * stage;
   p.stages = Stages{depth, tokens, stage};
   if (beside + p.ring > kHalfSmem || p.ring < depth * stage) return cudaErrorInvalidConfiguration;
