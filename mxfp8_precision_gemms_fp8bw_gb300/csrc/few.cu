@@ -14,17 +14,23 @@
 // Measured, one call behind the other, of weights larger than the cache where
 // they are: up of 8 experts 5120 -> 4096, 8 bits, 32 tokens 59 us (5.9 TB/s),
 // their down product 38 us (4.6 TB/s).  A linear of 8192 x 16384 for 4 tokens
-// 28 us in 8 bits (4.9 TB/s), 20 in 4 (3.5 TB/s); of 8192 x 5120 14 and 10; of
+// 28 us in 8 bits (4.9 TB/s), 20 in 4 (3.5 TB/s); of 8192 x 5120 13 and 9; of
 // 2048 x 2048, one token, 4.8.  What bounds them:
-//   8 bits, many tiles   memory: 87 % of the copy bandwidth while it streams
-//   4 bits               the rate of TMA, which reads 64 bytes to a row: it takes
-//                        about as long for a row as with 128.  With no products,
-//                        no scales and the weights in the cache the 20 us of
-//                        8192 x 16384 are still 18; asking for chunks ahead of
-//                        the stages, into the cache, takes 0 to 15 % longer.
-//   short products       a start of about 2 us, the pipeline's first chunk,
-//                        and, of a cluster, 2 to 4 us for blocks to meet and sum
+//   8 bits          memory: longer rows come at 6.6 TB/s, 0.97 of the copy
+//                   bandwidth
+//   4 bits          the way of a chunk: longer rows come at 4.8 TB/s.  No part of
+//                   it alone holds them there: of the 20 us of 8192 x 16384, 19
+//                   remain without products, 19 without scales, 18 without both
+//                   and 18 with the weights in the cache; half of the rows by
+//                   cp.async in place of TMA, a fifth stage, or chunks asked for
+//                   ahead into the cache change 2 % or cost some
+//   short products  a start of about 4 us with the pipeline's first chunks, and,
+//                   of a cluster, 1 to 2 us for blocks to meet and sum (3 for
+//                   more than 16 tokens)
 #include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
 
 #include "few.h"
 #include "few_tokens.cuh"
@@ -770,23 +776,34 @@ int places(int size) {
   return size;
 }
 
-// Blocks of a cluster, up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in eighths of a chunk's
-// time (0.2 us): the chunks of a block, half as long again where it brings its tokens into parts itself or spreads packed codes,
-// for each round of blocks; the cluster's start and exchange, 2.0 us for two blocks to 4.0 for eight; and the sums that change
-// hands.  On both sides of the choice (us, by blocks of a cluster; a linear of 8192 x 5120 or a layer's decode step):
-//   linear, one token, 4 bits          1: 10.5   2: 10.5   4: 9.6 *  8: 14.6 (more blocks than places)
-//   linear, 32 tokens, 4 bits          1: 13.5   2: 12.5 * 3: 14.6   4: 13.4   8: 21.3
-//   linear, 5 tokens, 6001 x 7136      2: 17.0   4: 15.4   5: 14.4 * 6: 19.8
-//   linear, 3 tokens, 2048 x 2080      1: 10.5   4: 7.5 *
-//   up of four experts 2048 -> 1024    1: 17.4 * 2: 18.5
-//   down of 8 experts 4096 -> 5120     4: 99.6   5: 97.9   6: 97.1 * 8: 109
-int splits_of(int64_t tiles, int64_t chunks, int tokens, bool slow, const int (&room)[8]) {
+// Blocks of a cluster, up to eight, for `tiles` row tiles over `chunks` chunks of contraction.  The cost in chunks' time of a
+// block (0.185 us):
+//   a block's own chunks, for each round of blocks, 1.3 times as long where it brings its tokens into parts itself or where rows
+//   are not whole chunks; or what memory takes for all blocks' chunks, 118 (4 bits) or 60 (8) in that time for 128 blocks, 124 or
+//   69 for 256; whichever is more, and some of the other;
+//   the cluster's meeting and exchange (three blocks do not divide the parts of the chip), more for more than 16 tokens, whose
+//   sums meet where the stages were, once all blocks have read theirs;
+//   and blocks that share SMs.
+// The numbers are fitted to 64 linears (1 to 32 tokens, 2048 x 2048 to 8192 x 16384) and six products of layers, each with every
+// size of cluster: the choice takes 0.6 % longer than the best on average, 17 % at most.  By blocks of a cluster, us:
+//   linear, 4 bits,  4 tokens, 2048 x 2048     1: 6.7    2: 6.8    4: 5.9 *  8: 7.5
+//                              8192 x 5120     1: 11.2   2: 9.1 *  4: 10.2   8: 15.5 (more blocks than places)
+//                              8192 x 16384    1: 31.7   2: 21.5   4: 20.1 * 8: 25.4
+//                              1024 x 8192     1: 15.5   2: 11.4   4: 8.6    8: 7.5 *
+//                   32 tokens, 4096 x 4096     1: 12.7   2: 11.8   4: 9.9 *  8: 12.7
+//   up of two experts 5120 -> 4096, 4 bits     1: 27.6 * 2: 28.7   4: 33.3 (the whole layer)
+//   down of 8 experts 4096 -> 5120, 8 bits     4: 99.5   5: 97.0   6: 95.6 * 8: 106.6
+int splits_of(int64_t tiles, int64_t chunks, int bits, int tokens, bool slow, int num_sms, const int (&room)[8]) {
+  const double exchange[8] = {0., 5.4, 11.8, 6.2, 6.9, 7.8, 9.3, 9.5};
+  const double rates[2] = {bits == 4 ? 118. : 60., bits == 4 ? 124. : 69.};  // with 128 blocks, with 256
   int best = 1;
-  int64_t least = INT64_MAX;
-  const int64_t exchange[8] = {0, 80, 110, 104, 118, 132, 146, 160};
+  double least = INFINITY;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
-    const int64_t rounds = (tiles * s + room[s - 1] - 1) / room[s - 1];
-    const int64_t cost = rounds * ((chunks + s - 1) / s) * (slow ? 12 : 8) + exchange[s - 1] + (s > 1 ? tokens * s : 0);
+    const double blocks = static_cast<double>(tiles) * s, rounds = std::ceil(blocks / room[s - 1]);
+    const double own = rounds * static_cast<double>((chunks + s - 1) / s) * (slow ? 1.3 : 1.);
+    const double all = static_cast<double>(tiles) * chunks / (rates[0] + (rates[1] - rates[0]) * (std::min(blocks, 256.) - 128.) / 128.);
+    const double cost = std::max(own, all) + 0.15 * std::min(own, all) + exchange[s - 1] + (s > 1 && tokens > 16 ? 7.3 : 0.) +
+                        (blocks > num_sms ? 7.2 : 0.);
     if (cost < least) best = s, least = cost;
   }
   return best;
@@ -873,7 +890,8 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
     int(&mine)[8] = dev < 64 ? room[dev] : here;
     if (mine[0] == 0)
       for (int i = 7; i >= 0; --i) mine[i] = places(i + 1);
-    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, p.M, p.x != nullptr || p.packed, mine);
+    p.splits = splits_of(tiles * copies, static_cast<int64_t>(chunks) * matrices, kBits, p.M, p.x != nullptr || p.m.K % kChunk != 0,
+                         num_sms, mine);
   }
   uint32_t beside = 1024 + behind;
   if (p.x != nullptr) {
