@@ -61,10 +61,10 @@ size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C
 /* A mixture-of-experts layer of gated feed-forward experts on M tokens:
  *   logits = x router^T (fp32);  experts e_j, weights w_j: fp8bw_moe_route's of them
  *   [gate; up] = W13[e_j] x;  a_j = gate * sigmoid(gate) * up;  y = sum_j w_j W2[e_j] a_j
- * A choice without an expert adds nothing.  h = [gate; up] stays fp32; the
- * activation is held between the two products with 12 significant bits (2^-25
- * of the largest of its block of 32 where that is more); one that leaves fp32
- * gives NaN.
+ * A choice without an expert adds nothing.  h = [gate; up] stays fp32, and so
+ * does the activation between the two products, down to 2^-12 of the largest
+ * of its block of 32 (below that it is off by at most 2^-36 of that largest);
+ * one that leaves fp32 gives NaN.
  *   x   : bf16 [M, C]           router : fp32 [E, C]      bias : fp32 [E] or NULL
  *   w13 : codes of [E, 2F, C]   e13    : E8M0 [E][2F][C/32]
  *   w2  : codes of [E, C, F]    e2     : E8M0 [E][C][F/32]     y : bf16 [M, C]

@@ -47,7 +47,7 @@ using few::kAll;
 //   kLinear  one run of the one matrix                    y
 //   kUp      64 rows of gate and the 64 of up that go with them, of an active
 //            expert: one run, or, where there are many, whole ones of tiles
-//            and experts in turn                          the activation, in three parts
+//            and experts in turn                          the activation, in five parts
 //   kDown    128 rows of all active experts, one run behind the other; the sum
 //            over each is drained from tensor memory, weighted and added to its
 //            tokens in shared memory                      y
@@ -99,6 +99,11 @@ __host__ __device__ inline Stages stages_of(int depth, uint32_t ring, uint32_t t
   return Stages{room < depth ? room : depth, tokens, bytes};
 }
 
+// Columns of tensor memory for a stage's scales: 4 for the weights', and 4 or 8 for up to 128 or 256 token rows.
+__host__ __device__ constexpr int scale_columns_of(int rows) { return rows > 128 ? 16 : 8; }
+// Columns of tensor memory behind the accumulators: the stages' scales, and no fewer than a load may read past an accumulator.
+__host__ __device__ inline int tmem_scales(int of_stage, int depth) { return of_stage * depth > 16 ? of_stage * depth : 16; }
+
 struct Product {
   Matrix m;
   int M, splits;
@@ -106,7 +111,7 @@ struct Product {
   bool late;            // the cluster's sums meet in the stages
   int slots;            // kDown: room for as many
   bool packed;          // 4-bit weights land as they are in memory, for whole chunks of 128 only TMA can spread them
-  int columns;          // of an accumulator: token rows, a multiple of 16
+  int columns;          // of an accumulator: token rows, a multiple of 16; kDown: by the plan
   Stages stages;        // kDown: of slots of M tokens; there are more where the plan's are smaller
   uint32_t ring;        // bytes of all stages
   uint32_t tmem;        // columns of tensor memory
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
   int slots = 1;
   Stages stages = p.stages;
+  int columns = p.columns, scale_columns = scale_columns_of(1), accs = many ? 2 : 1;  // of an accumulator, of a stage's scales; accumulators
   FewSlot one{0, 0, 0xffffffffu >> (32 - p.M), p.M};
   if constexpr (kMode == kUp) {
     grid_wait();
@@ -306,7 +312,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     // stages of the room of 3.
     const FewPlan plan = few_header(p.plan);
     slots = plan.active;
-    stages = stages_of(kMostDepth, p.ring, (plan.most * kParts + 15) / 16 * 16 * 128 + kScales, packed);
+    columns = (plan.most * kParts + 15) / 16 * 16;
+    scale_columns = scale_columns_of(columns);
+    stages = stages_of(kMostDepth, p.ring, columns * 128 + static_cast<uint32_t>(few_scale_bytes(columns)), packed);
+    // Two accumulators, so that one is drained while the next run's products go to the other, where half of tensor memory, a
+    // block's share, has room for them: up to 19 to 22 tokens of an expert.
+    accs = 2 * columns + tmem_scales(scale_columns, stages.depth) <= static_cast<int>(p.tmem) ? 2 : 1;
   }
   const AbortFlag ab{&sh.abort};
 
@@ -516,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the products (together 250 to 800 cycles a chunk).
     named_sync<1, (kDrainWarps + 2) * 32>();
     tc_fence_after();
-    const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + (many ? 2 : 1) * p.columns;
+    const uint32_t sf0 = __shfl_sync(kAll, sh.tmem, 0) + accs * columns;
     const uint64_t sa0 = sdesc_plain_128b_rows(stage0 + scales_at);
     const uint64_t sb0 = sdesc_plain_128b_rows(held ? held_scales : stage0 + tokens_at);
     const bool elected = elect_one();
@@ -527,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Run r = run_at(t, false);
       t = after(t, r);
       const uint64_t token_scales = sb0 + (held ? 0 : rows_of(r.slot) * (128 >> 4));
+      const bool two_blocks = rows_of(r.slot) > 128;
 #pragma unroll 1
       for (int i = 0; i < r.n; ++i) {
         if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) {
@@ -538,8 +550,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint64_t stage = static_cast<uint64_t>(ring.s * (stages.bytes >> 4));
         if (elected) {
           // The columns were last read by products that were complete before the stage was filled again.
-          tmem_cp_32x128b_warpx4(sf0 + ring.s * 8, sa0 + stage);
-          tmem_cp_32x128b_warpx4(sf0 + ring.s * 8 + 4, token_scales + (held ? static_cast<uint64_t>(i * (kScales >> 4)) : stage));
+          const uint32_t sf = sf0 + ring.s * scale_columns;
+          const uint64_t sb = token_scales + (held ? static_cast<uint64_t>(i * (kScales >> 4)) : stage);
+          tmem_cp_32x128b_warpx4(sf, sa0 + stage);
+          tmem_cp_32x128b_warpx4(sf + 4, sb);
+          if (kMode == kDown && two_blocks) tmem_cp_32x128b_warpx4(sf + 8, sb + (512 >> 4));
           mma_commit(&sh.ready[ring.s]);
         }
         __syncwarp();
@@ -561,18 +576,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     named_sync<1, (kDrainWarps + 2) * 32>();
     tc_fence_after();
     // All lanes walk through the loop, so that what the products take stays in uniform registers; one issues them.
-    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + (many ? 2 : 1) * p.columns;
+    const uint32_t tmem = __shfl_sync(kAll, sh.tmem, 0), sf0 = tmem + accs * columns;
     const uint64_t a0 = sdesc_kmajor_sw128(stage0), b0 = sdesc_kmajor_sw128(held ? held_codes : stage0 + tokens_at);
     const bool elected = elect_one();
     bool alive = true;
     Ring ring(stages.depth);
-    int sum = 0;
+    Ring sum(accs);
+    bool again = false;  // whether the accumulator has been used before
 #pragma unroll 1
-    for (int t = t0; t < t1 && alive; ++sum) {
+    for (int t = t0; t < t1 && alive;) {
       const Run r = run_at(t, false);
       t = after(t, r);
-      const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0);
-      if (many && sum >= 2 && !all_of(mbar_wait(&sh.sum_empty[sum & 1], (sum / 2 - 1) & 1, ab, p.status))) break;
+      const uint32_t acc = tmem + sum.s * columns;
+      if (many && again && !all_of(mbar_wait(&sh.sum_empty[sum.s], sum.phase ^ 1, ab, p.status))) break;
       const uint32_t N = (__shfl_sync(kAll, rows_of(r.slot), 0) + 15) & ~15;
       const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
       int left = K / 32 - r.c * 4;  // blocks of 32
@@ -585,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tc_fence_after();
         const uint64_t stage = static_cast<uint64_t>(ring.s * (stages.bytes >> 4));
-        const uint32_t sfa = sf0 + ring.s * 8, sfb = sfa + 4;
+        const uint32_t sfa = sf0 + ring.s * scale_columns, sfb = sfa + 4;
         const uint64_t a = a0 + stage, b = b0 + (held ? static_cast<uint64_t>(i * (kHeld >> 4)) : stage);
         if (elected) {
           mma_mx_e4m3(acc, a, b, kind, sfa, sfb, more);
@@ -598,8 +614,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         more = 1;
         ring.next();
       }
-      if (elected) mma_commit(&sh.sum_full[sum & 1]);
+      if (elected) mma_commit(&sh.sum_full[sum.s]);
       __syncwarp();
+      sum.next();
+      again |= sum.s == 0;
     }
     if (elected) {
       mma_commit(&sh.drain[1]);
@@ -637,35 +655,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tmem = sh.tmem;
     const int row = threadIdx.x;  // warps 0-3
     const float* weights = kMode == kDown ? few_weights(p.plan) : nullptr;
-    int sum = 0;
+    Ring sum(accs);
 #pragma unroll 1
-    for (int t = t0; t < t1; ++sum) {
+    for (int t = t0; t < t1; sum.next()) {
       const Run r = run_at(t, false);
       t = after(t, r);
       const FewSlot& s = r.slot;
       // Lane i has the weight of column i.
       const float weight =
           kMode == kDown && lane < s.n ? __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + lane))) : 0.f;
-      bool landed = all_of(mbar_wait(&sh.sum_full[sum & 1], (sum / 2) & 1, ab, p.status));
+      bool landed = all_of(mbar_wait(&sh.sum_full[sum.s], sum.phase, ab, p.status));
       // Together: the sums of the run before have been read, and a warp that gave up would leave the others at a barrier.
       if (in_turn) landed = named_all<2, kDrainWarps * 32>(landed);
       if (!landed) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (many ? (sum & 1) * p.columns : 0) + (static_cast<uint32_t>(warp * 32) << 16);
+      const uint32_t acc = tmem + sum.s * columns + (static_cast<uint32_t>(warp * 32) << 16);
       uint32_t mask = s.mask;
       if constexpr (kMode == kDown) {
 #pragma unroll 1
-        for (int n0 = 0; n0 < s.n; n0 += 16) {  // 16 columns' parts at a time
-          uint32_t v[kParts][16];
-#pragma unroll
-          for (int q = 0; q < kParts; ++q) tmem_ld_32x32b_x16(acc + (n0 * kParts + q * 16), v[q]);
+        for (int n0 = 0; n0 < s.n; n0 += 6) {  // twice three tokens' parts at a time, and a column that is not read
+          uint32_t v[2][16];
+          static_assert(3 * kActParts <= 16, "of a load");
+          tmem_ld_32x32b_x16(acc + n0 * kParts, v[0]);
+          if (n0 + 3 < s.n) tmem_ld_32x32b_x16(acc + (n0 + 3) * kParts, v[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 6; ++i) {
             if (n0 + i >= s.n) break;
             float f = 0.f;
 #pragma unroll
-            for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[(i * kParts + q) / 16][(i * kParts + q) % 16]);
+            for (int q = kParts - 1; q >= 0; --q) f += __uint_as_float(v[i / 3][i % 3 * kParts + q]);
             sums[(__ffs(mask) - 1) * kRows + row] += f * __shfl_sync(kAll, weight, n0 + i);
             mask &= mask - 1;
           }
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.sum_empty[sum & 1]);
+      if (lane == 0) mbar_arrive(&sh.sum_empty[sum.s]);
       if (in_turn) {
         named_sync<2, kDrainWarps * 32>();
         for (int i = warp; i < s.n * 2; i += kDrainWarps)
@@ -866,9 +885,9 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t tiles = (rows + tile - 1) / tile;
   const int chunks = (p.m.K + kChunk - 1) / kChunk;
-  p.columns = kMode == kDown ? (p.M + 15) / 16 * 16 * parts : (p.M * parts + 15) / 16 * 16;
+  p.columns = (p.M * parts + 15) / 16 * 16;
   p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
-  const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + kScales, stage = stages_of(0, 0, tokens, p.packed).bytes;
+  const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + static_cast<uint32_t>(few_scale_bytes(p.columns)), stage = stages_of(0, 0, tokens, p.packed).bytes;
   // Enough runs for every block to have some: whole ones in turn, which leaves the stages no gaps (17 tokens over 64 experts 46.8
   // us, otherwise 50.5), where their sums leave room for two blocks of three stages an SM.
   const uint32_t sums = p.M * kRows * 4, slot = sizeof(FewSlot);
@@ -905,13 +924,16 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
   // took 28.7 us for a layer's step of one token and 30.9 for a linear of 65536 x 4096, four 29.4 and 31.9.  kDown takes what
   // there is and divides it by the plan.
   const auto fits = [&](int n) { return beside + n * stage <= kHalfSmem; };
-  const int depth = kMode == kDown ? 2 : fits(5) ? 5 : fits(4) ? 4 : 3;
+  const int depth = kMode == kDown ? 1 : fits(5) ? 5 : fits(4) ? 4 : 3;
   p.ring = kMode == kDown ? (kHalfSmem - beside) / 1024 * 1024 : depth * stage;
   p.stages = Stages{depth, tokens, stage};
   if (beside + p.ring > kHalfSmem || p.ring < depth * stage) return cudaErrorInvalidConfiguration;
-  const uint32_t columns = (many ? 2 : 1) * p.columns + (kMode == kDown ? kMostDepth : depth) * 8;
+  // At most half of tensor memory, which two blocks an SM share: a block that had to wait for another's, which may wait for
+  // this one's kernel to end, would wait for ever.
+  const int columns = kMode == kDown ? 2 * p.columns + tmem_scales(scale_columns_of(p.columns), kMostDepth)
+                                     : (many ? 2 : 1) * p.columns + tmem_scales(scale_columns_of(1), depth);
   p.tmem = 32;
-  while (p.tmem < columns) p.tmem *= 2;
+  while (p.tmem < columns && p.tmem < 256) p.tmem *= 2;
   const dim3 grid = in_turn ? dim3(static_cast<unsigned>(2 * num_sms))
                             : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
   CUtensorMap map{};

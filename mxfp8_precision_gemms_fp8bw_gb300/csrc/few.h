@@ -69,17 +69,18 @@ __device__ __forceinline__ FewSlot few_slot(const FewPlan* p, int choices, int i
 }
 
 // Values as the products read them (few_tokens.cuh): a record for every chunk of 128 of the contraction, of `rows` rows of
-// e4m3 codes, 128 bytes each and already in the order of 128-byte swizzling, and their scales in the layout of tcgen05.cp.  A
-// stage of the products takes a record as it is.
-// Tokens come in two parts, rows 2 t and 2 t + 1 of the batch's records; activations in three, rows 3 i .. of the records of an
+// e4m3 codes, 128 bytes each and already in the order of 128-byte swizzling, and their scales in the layout of tcgen05.cp, 512
+// bytes for 128 rows.  A stage of the products takes a record as it is.
+// Tokens come in two parts, rows 2 t and 2 t + 1 of the batch's records; activations in five, rows 5 i .. of the records of an
 // expert's slot, which has a record for every chunk.
-constexpr int kTokenParts = 2, kActParts = 3;
-__host__ __device__ inline int64_t few_record(int64_t rows) { return rows * 128 + 512; }
+constexpr int kTokenParts = 2, kActParts = 5;
+__host__ __device__ constexpr int64_t few_scale_bytes(int64_t rows) { return (rows + 127) / 128 * 512; }
+__host__ __device__ inline int64_t few_record(int64_t rows) { return rows * 128 + few_scale_bytes(rows); }
 __host__ __device__ inline int64_t few_chunks(int64_t K) { return (K + 127) / 128; }
 inline int64_t few_tokens_bytes(int64_t M, int64_t K) { return few_chunks(K) * few_record(M * kTokenParts); }
 // Where the records of a slot begin that has `start` choices before it.
 __host__ __device__ inline int64_t few_act_at(int64_t slot, int64_t start, int64_t chunks) {
-  return chunks * (start * kActParts * 128 + slot * 512);
+  return chunks * (start * kActParts * 128 + slot * few_scale_bytes(kFewTokens * kActParts));
 }
 inline int64_t few_act_bytes(int64_t choices, int64_t slots, int64_t F) { return few_act_at(slots, choices, few_chunks(F)); }
 

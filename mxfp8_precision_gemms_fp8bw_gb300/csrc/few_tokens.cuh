@@ -11,10 +11,18 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 // A block of 32 values is the sum of parts, each a block of MXFP8 codes under a
 // power of two of its own: the codes of the values, the codes of what those
-// leave, and so on.  e4m3 has 4 significant bits, so two parts hold the 8 bits
-// of bf16 exactly down to 2^-12 of the block's largest value, and to 2^-21 of
-// it below that; three hold 12 bits of fp32.  An infinity becomes a NaN, which
-// e4m3 has.
+// leave, and so on.  e4m3 has 4 significant bits and what rounding to the
+// nearest leaves starts 5 bits further down.  So two parts hold the 8 bits of
+// bf16 exactly down to 2^-12 of the block's largest value, and to 2^-21 of it
+// below that; and five hold the 24 bits of fp32 exactly down to 2^-12 of the
+// block's largest, and to 2^-36 of it below that: what the second product adds
+// up has no fewer bits than the sums of the first.  With codes down to 2^E of
+// a part that are 2^(E-9) apart, the largest of a block in [224, 448] 2^E, E
+// falls by at least 4 from the first part to the second and by 5 from each of
+// the others to the next, so that the fifth's codes are 2^-28 of the first's
+// power of two apart, and a value of 24 bits from 2^-5 of it on, which is at
+// most 2^-12 of the largest, is a multiple of that.  An infinity becomes a NaN,
+// which e4m3 has.
 __device__ __forceinline__ float without_infinity(float v) {
   return fabsf(v) == INFINITY ? __uint_as_float(0x7FFFFFFFu) : v;
 }
@@ -29,7 +37,7 @@ __device__ __forceinline__ uint8_t* code_at(uint8_t* records, int64_t rows, int6
   return records + (k >> 7) * few_record(rows) + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15);
 }
 __device__ __forceinline__ uint8_t* scale_at(uint8_t* records, int64_t rows, int64_t k, int r) {
-  return records + (k >> 7) * few_record(rows) + rows * 128 + (r & 31) * 16 + (r >> 5) * 4 + ((k & 127) >> 5);
+  return records + (k >> 7) * few_record(rows) + rows * 128 + (r >> 7) * 512 + (r & 31) * 16 + (r >> 5 & 3) * 4 + ((k & 127) >> 5);
 }
 
 // Eight values of a block that four neighbouring lanes hold, in kTokenParts parts: codes to code(part), and by the first of

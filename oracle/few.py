@@ -78,7 +78,7 @@ def few_layer(x, router, w13, w2, top_k, bias=None, **how):
     y, bound = np.zeros_like(x), np.zeros_like(x)
     F, C = w2.shape[2], x.shape[1]
     # Sums of n terms in fp32, products exact: at most n roundings of at most 2^-23 of the sum of magnitudes.  Tokens are held to
-    # 2^-21 of a block's largest element, activations, in three parts, to 2^-12 of each or 2^-25 of the block's largest.
+    # 2^-21 of a block's largest element, activations, in five parts, to 2^-36 of it.
     sums = lambda n: n * 2.0 ** -23  # noqa: E731
     for t in range(x.shape[0]):
         dlogit = sums(C) * float((np.abs(x[t]) * np.abs(np.asarray(router, np.float64))).sum(axis=1).max())
@@ -92,8 +92,8 @@ def few_layer(x, router, w13, w2, top_k, bias=None, **how):
                 silu = gate / (1 + np.exp(-gate))
             a = silu * up
             # |silu'| < 1.1; the sigmoid in fp32 is off by a few ulp and |gate| roundings of its argument
-            da = 1.1 * dg * (np.abs(up) + du) + np.abs(silu) * du + np.abs(a) * (2.0 ** -12 + (8 + np.abs(gate)) * 2.0 ** -23)
-            da += 2.0 ** -25 * np.abs(a).max()
+            da = 1.1 * dg * (np.abs(up) + du) + np.abs(silu) * du + np.abs(a) * (8 + np.abs(gate)) * 2.0 ** -23
+            da += 2.0 ** -36 * np.abs(a).max()
             part = w2[e] @ a
             dpart = np.abs(w2[e]) @ da + sums(F * len(experts[t])) * (np.abs(w2[e]) @ np.abs(a))
             y[t] += w * part
