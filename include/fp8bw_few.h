@@ -76,6 +76,20 @@ int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, cons
                int64_t groups, int64_t groups_kept, int64_t group_top, int score, int renorm, float scale, fp8bw_bf16* y,
                void* workspace, size_t workspace_bytes, void* stream);
 
+/* mx_few_linear and mx_few_moe whose kernels wait for no longer than wait_ns at
+ * a time inside a block (0: not at all; 2,000,000,000 as the calls themselves
+ * do).  Where that runs out the kernels give up, their copies land, FP8BW_ERR_TIMEOUT
+ * is recorded in the error word and y means nothing: a test sees what becomes of
+ * a wait that expires, without a fault.  The calls after it are not affected. */
+int fp8bw_selftest_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
+                              int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, uint32_t wait_ns,
+                              void* stream);
+int fp8bw_selftest_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13,
+                           const uint8_t* e13, const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E,
+                           int64_t top_k, int64_t C, int64_t F, int64_t groups, int64_t groups_kept, int64_t group_top,
+                           int score, int renorm, float scale, fp8bw_bf16* y, void* workspace, size_t workspace_bytes,
+                           uint32_t wait_ns, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,6 +9,8 @@ namespace {
 
 constexpr int64_t kMaxWidth = int64_t{1} << 22;  // contraction lengths and rows of an expert
 
+constexpr uint64_t kWaitNs = 2000000000;  // legitimate waits last microseconds
+
 bool bits_ok(int bits) { return bits == 4 || bits == 8; }
 
 bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
@@ -53,13 +55,10 @@ FP8BW_API int mxfp4_to_mxfp8(const uint8_t* q4, int64_t R, int64_t C, uint8_t* q
   return launched(launch_mxfp4_to_mxfp8(q4, R * C, q8, d->num_sms, as_stream(stream)), name);
 }
 
-FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return linear_dims_ok(M, N, K) ? few_linear_workspace_bytes(M, N, K) : 0;
-}
+namespace {
 
-FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
-                            int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream) {
-  const char* name = "mx_few_linear";
+int few_linear(const char* name, const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N, int64_t K,
+               fp8bw_bf16* y, void* workspace, size_t workspace_bytes, uint64_t wait_ns, void* stream) {
   if (!x || !w || !e8 || !y) return fail(FP8BW_ERR_NULL, "%s: x, w, e8 and y must be non-NULL", name);
   if (!linear_dims_ok(M, N, K))
     return fail(FP8BW_ERR_SHAPE,
@@ -79,20 +78,15 @@ FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t
     return fail(FP8BW_ERR_LAYOUT, "%s: y or the workspace overlaps an input or each other", name);
   DeviceState* d;
   if (int rc = current_device(&d)) return rc;
-  return launched(launch_few_linear(FewLinearArgs{x, w, e8, bits, M, N, K, y, workspace, d->error_word, d->num_sms}, as_stream(stream)),
+  return launched(launch_few_linear(FewLinearArgs{x, w, e8, bits, M, N, K, y, workspace, d->error_word, d->num_sms, wait_ns},
+                                    as_stream(stream)),
                   name);
 }
 
-FP8BW_API size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {
-  return layer_dims_ok(M, E, top_k, C, F) ? few_moe_workspace_bytes(M, E, top_k, C, F) : 0;
-}
-
-FP8BW_API int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13,
-                         const uint8_t* e13, const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E,
-                         int64_t top_k, int64_t C, int64_t F, int64_t groups, int64_t groups_kept, int64_t group_top,
-                         int score, int renorm, float scale, fp8bw_bf16* y, void* workspace, size_t workspace_bytes,
-                         void* stream) {
-  const char* name = "mx_few_moe";
+int few_moe(const char* name, const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13, const uint8_t* e13,
+            const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F, int64_t groups,
+            int64_t groups_kept, int64_t group_top, int score, int renorm, float scale, fp8bw_bf16* y, void* workspace,
+            size_t workspace_bytes, uint64_t wait_ns, void* stream) {
   if (!x || !router || !w13 || !e13 || !w2 || !e2 || !y || !workspace)
     return fail(FP8BW_ERR_NULL, "%s: every pointer but bias must be non-NULL", name);
   if (!layer_dims_ok(M, E, top_k, C, F))
@@ -147,5 +141,49 @@ FP8BW_API int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* 
   a.y = y;
   a.workspace = workspace;
   a.num_sms = d->num_sms;
+  a.wait_ns = wait_ns;
   return launched(launch_few_moe(a, as_stream(stream)), name);
+}
+
+}  // namespace
+
+FP8BW_API size_t mx_few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return linear_dims_ok(M, N, K) ? few_linear_workspace_bytes(M, N, K) : 0;
+}
+
+FP8BW_API int mx_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
+                            int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return few_linear("mx_few_linear", x, w, e8, bits, M, N, K, y, workspace, workspace_bytes, kWaitNs, stream);
+}
+
+FP8BW_API size_t mx_few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F) {
+  return layer_dims_ok(M, E, top_k, C, F) ? few_moe_workspace_bytes(M, E, top_k, C, F) : 0;
+}
+
+FP8BW_API int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13,
+                         const uint8_t* e13, const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E,
+                         int64_t top_k, int64_t C, int64_t F, int64_t groups, int64_t groups_kept, int64_t group_top,
+                         int score, int renorm, float scale, fp8bw_bf16* y, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  return few_moe("mx_few_moe", x, router, bias, w13, e13, w2, e2, bits, M, E, top_k, C, F, groups, groups_kept, group_top, score, renorm,
+                 scale, y, workspace, workspace_bytes, kWaitNs, stream);
+}
+
+FP8BW_API int fp8bw_selftest_few_linear(const fp8bw_bf16* x, const uint8_t* w, const uint8_t* e8, int bits, int64_t M, int64_t N,
+                                        int64_t K, fp8bw_bf16* y, void* workspace, size_t workspace_bytes, uint32_t wait_ns,
+                                        void* stream) {
+  const char* name = "fp8bw_selftest_few_linear";
+  if (wait_ns > kWaitNs) return fail(FP8BW_ERR_ARG, "%s: wait_ns=%u is over 2000000000", name, wait_ns);
+  return few_linear(name, x, w, e8, bits, M, N, K, y, workspace, workspace_bytes, wait_ns, stream);
+}
+
+FP8BW_API int fp8bw_selftest_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, const uint8_t* w13,
+                                     const uint8_t* e13, const uint8_t* w2, const uint8_t* e2, int bits, int64_t M, int64_t E,
+                                     int64_t top_k, int64_t C, int64_t F, int64_t groups, int64_t groups_kept, int64_t group_top,
+                                     int score, int renorm, float scale, fp8bw_bf16* y, void* workspace, size_t workspace_bytes,
+                                     uint32_t wait_ns, void* stream) {
+  const char* name = "fp8bw_selftest_few_moe";
+  if (wait_ns > kWaitNs) return fail(FP8BW_ERR_ARG, "%s: wait_ns=%u is over 2000000000", name, wait_ns);
+  return few_moe(name, x, router, bias, w13, e13, w2, e2, bits, M, E, top_k, C, F, groups, groups_kept, group_top, score, renorm, scale,
+                 y, workspace, workspace_bytes, wait_ns, stream);
 }

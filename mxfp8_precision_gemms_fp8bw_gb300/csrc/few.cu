@@ -124,6 +124,7 @@ struct Product {
   uint8_t* act;         // kUp: records of activations
   uint16_t* y;          // bf16 [M, rows]
   int* status;
+  uint64_t wait_ns;  // of a role, at most
 };
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -153,6 +154,7 @@ struct Shared {
   uint64_t drain[2];
   uint32_t tmem;
   int abort;
+  int issued[kScaleWarps + 2];  // where a wait expired: chunks that the warps of scales, weights and tokens have asked for
 };
 
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
@@ -242,13 +244,35 @@ __device__ void activate(const Product& p, const Run& r, int column, int i, floa
               f + (threadIdx.x & 31), column);
 }
 
-// After a wait that expired: the last copies land before the block ends, or never will.
-__device__ void unwind(Ring ring, uint64_t* bars, int issued, int* status) {
-  int none = 0;
-  for (int i = min(issued, ring.depth); i > 0; --i) {
-    if (--ring.s < 0) ring.s = ring.depth - 1, ring.phase ^= 1;
-    mbar_wait(bars + ring.s, ring.phase, AbortFlag{&none}, status, 1000000ull);
+// Waits of the roles: for as long as the call says, 0 not at all (a self-test).
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, AbortFlag ab, const Product& p) {
+  if (mbar_test_wait(bar, parity)) return true;
+  if (p.wait_ns != 0) return mbar_wait(bar, parity, ab, p.status, p.wait_ns);
+  *ab.flag = 1;
+  atomicExch(p.status, kStatusTimeout);
+  return false;
+}
+
+// After a wait of any role has expired, and all roles have come to their ends: copies that are under way land before the block
+// ends, whose shared memory is another's then.  A barrier tells that a stage's copies have landed only once all have arrived at
+// it, so those that had not come so far arrive for the others' last chunks, without copies of their own.  None is more than
+// `depth` chunks ahead of another: it waited for a stage to be read, which takes all.  Bytes of a copy that has been asked for
+// land in microseconds, and the limit is for those that never will.
+__device__ void land_copies(Shared& sh, int warp, int lane, int depth, bool packed, bool held, int* status) {
+  constexpr uint64_t kLimitNs = 10000000;
+  const int me = warp - kDrainWarps;
+  if (me < 0 || me > kScaleWarps + 1 || (me > kScaleWarps && held)) return;
+  int most = 0;
+  for (int i = 0; i < kScaleWarps + 2; ++i)
+    if (!(i == kScaleWarps && packed) && !(i > kScaleWarps && held)) most = max(most, sh.issued[i]);
+  uint64_t* bars = sh.full;
+  if (me == kScaleWarps && packed) {
+    bars = sh.landed, most = sh.issued[me];
+  } else if (me < kScaleWarps || lane == 0) {
+    for (int c = sh.issued[me]; c < most; ++c) mbar_arrive(&bars[c % depth]);
   }
+  int none = 0;
+  for (int c = max(0, most - depth); c < most; ++c) mbar_wait(&bars[c % depth], c / depth & 1, AbortFlag{&none}, status, kLimitNs);
 }
 
 template <Mode kMode, int kBits>
@@ -383,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     Ring ring(stages.depth);
     bool refill = false, alive = true;
+    int issued = 0;
 #pragma unroll 1
     for (int t = t0; t < t1 && alive;) {
       const Run r = run_at(t, false);
@@ -398,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll 1
       for (int i = 0; i < r.n; ++i) {
-        if (refill && !all_of(mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status))) {
+        if (refill && !all_of(wait_for(&sh.empty[ring.s], ring.phase ^ 1, ab, p))) {
           alive = false;
           break;
         }
@@ -417,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + scale_to), "r"(word) : "memory");
           if (packed) {
-            if (!all_of(mbar_wait(&sh.landed[ring.s], ring.phase, ab, p.status))) {
+            if (!all_of(wait_for(&sh.landed[ring.s], ring.phase, ab, p))) {
               alive = false;
               break;
             }
@@ -435,11 +460,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive(&sh.full[ring.s]);
         }
         scale += 4;
+        ++issued;
         ring.next();
         refill |= ring.s == 0;
       }
     }
     cp_async_wait_all();
+    if (lane == 0) sh.issued[warp - kDrainWarps] = issued;
     // The next call's first kernel may start: it waits for the end of this one before it reads or writes anything.  One token of
     // 8192 x 5120 9.6 -> 9.1 us; a linear behind a kernel of its own for the tokens gains nothing, 32 tokens 12.5 -> 13.3.
     if (kMode == kDown || held) grid_release();
@@ -476,17 +503,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     come_together();
     if (lane == 0) {
-      bool alive = true;
 #pragma unroll 1
       while (r.n > 0 || t < t1) {
         if (r.n == 0) begin_run(false);
-        if (issued >= stages.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
-          alive = false;
-          break;
-        }
+        if (issued >= stages.depth && !wait_for(&sh.empty[ring.s], ring.phase ^ 1, ab, p)) break;
         load();
       }
-      if (!alive) unwind(ring, packed ? sh.landed : sh.full, issued, p.status);
+      sh.issued[kScaleWarps] = issued;
     }
     __syncwarp();
   } else if (warp == kTokens) {
@@ -507,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             p.t + (kMode == kDown ? few_act_at(r.at, r.slot.start, chunks) : 0) + static_cast<int64_t>(r.c) * record;
 #pragma unroll 1
         for (int i = 0; i < r.n; ++i, ++issued) {
-          if (issued >= stages.depth && !mbar_wait(&sh.empty[ring.s], ring.phase ^ 1, ab, p.status)) {
+          if (issued >= stages.depth && !wait_for(&sh.empty[ring.s], ring.phase ^ 1, ab, p)) {
             alive = false;
             break;
           }
@@ -517,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ring.next();
         }
       }
-      if (!alive) unwind(ring, sh.full, issued, p.status);
+      sh.issued[kScaleWarps + 1] = issued;
     }
     __syncwarp();
   } else if (warp == kScaler) {
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t sb0 = sdesc_plain_128b_rows(held ? held_scales : stage0 + tokens_at);
     const bool elected = elect_one();
     Ring ring(stages.depth);
-    bool alive = !held || all_of(mbar_wait(&sh.tokens, 0, ab, p.status));
+    bool alive = !held || all_of(wait_for(&sh.tokens, 0, ab, p));
 #pragma unroll 1
     for (int t = t0; t < t1 && alive;) {
       const Run r = run_at(t, false);
@@ -541,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool two_blocks = rows_of(r.slot) > 128;
 #pragma unroll 1
       for (int i = 0; i < r.n; ++i) {
-        if (!all_of(mbar_wait(&sh.full[ring.s], ring.phase, ab, p.status))) {
+        if (!all_of(wait_for(&sh.full[ring.s], ring.phase, ab, p))) {
           alive = false;
           break;
         }
@@ -588,14 +611,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Run r = run_at(t, false);
       t = after(t, r);
       const uint32_t acc = tmem + sum.s * columns;
-      if (many && again && !all_of(mbar_wait(&sh.sum_empty[sum.s], sum.phase ^ 1, ab, p.status))) break;
+      if (many && again && !all_of(wait_for(&sh.sum_empty[sum.s], sum.phase ^ 1, ab, p))) break;
       const uint32_t N = (__shfl_sync(kAll, rows_of(r.slot), 0) + 15) & ~15;
       const uint32_t kind = idesc_mx_e4m3(kRows, N, 0, 0) | (kBits == 4 ? 5u << 7 : 0u);  // A: e2m1
       int left = K / 32 - r.c * 4;  // blocks of 32
       uint32_t more = 0;            // whether there is something in the accumulator
 #pragma unroll 1
       for (int i = 0; i < r.n; ++i, left -= 4) {
-        if (!all_of(mbar_wait(&sh.ready[ring.s], ring.phase, ab, p.status))) {
+        if (!all_of(wait_for(&sh.ready[ring.s], ring.phase, ab, p))) {
           alive = false;
           break;
         }
@@ -664,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Lane i has the weight of column i.
       const float weight =
           kMode == kDown && lane < s.n ? __uint_as_float(load_after(reinterpret_cast<const uint32_t*>(weights + s.start + lane))) : 0.f;
-      bool landed = all_of(mbar_wait(&sh.sum_full[sum.s], sum.phase, ab, p.status));
+      bool landed = all_of(wait_for(&sh.sum_full[sum.s], sum.phase, ab, p));
       // Together: the sums of the run before have been read, and a warp that gave up would leave the others at a barrier.
       if (in_turn) landed = named_all<2, kDrainWarps * 32>(landed);
       if (!landed) break;
@@ -720,6 +743,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
+  if (*ab.flag) {  // raised by a wait, of which there are no more
+    land_copies(sh, warp, lane, stages.depth, packed, held, p.status);
+    __syncthreads();
+  }
   if (warp == kIssuer) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, p.tmem);
@@ -969,6 +996,7 @@ cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   p.M = static_cast<int>(a.M);
   p.y = a.y;
   p.status = a.status;
+  p.wait_ns = a.wait_ns;
   if (held_tokens(a.M, a.N, a.K)) {
     p.x = a.x;
   } else {
@@ -1022,6 +1050,7 @@ cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
   up.choices = static_cast<int>(M * k);
   up.act = s.act;
   up.status = a.route.status;
+  up.wait_ns = a.wait_ns;
   if (const cudaError_t e = launch_product<kUp>(up, a.bits, E, 1, active, a.num_sms, st)) return e;
   Product down{};
   down.m = Matrix{a.w2, a.e2, E * a.C * (a.F / 32), a.C, static_cast<int>(a.F)};
@@ -1031,6 +1060,7 @@ cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
   down.choices = static_cast<int>(M * k);
   down.y = a.y;
   down.status = a.route.status;
+  down.wait_ns = a.wait_ns;
   return launch_product<kDown>(down, a.bits, E, active, 1, a.num_sms, st);
 }
 

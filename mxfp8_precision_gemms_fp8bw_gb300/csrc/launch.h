@@ -193,6 +193,7 @@ struct FewLinearArgs {
   void* workspace;  // few_linear_workspace_bytes
   int* status;
   int num_sms;
+  uint64_t wait_ns;  // of a wait in the kernels, at most
 };
 size_t few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st);
@@ -210,6 +211,7 @@ struct FewMoeArgs {
   uint16_t* y;
   void* workspace;
   int num_sms;
+  uint64_t wait_ns;
 };
 size_t few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F);
 cudaError_t launch_few_moe(const FewMoeArgs& args, cudaStream_t st);

@@ -13,6 +13,7 @@ from . import binding as B
 from .moe_binding import _BF16, _F32, _F32C, _I64, _INT, _P, _SIZE, _U8, SCORE_SOFTMAX, _arg, _stream
 
 FEW_TOKENS = 32
+_U32 = ctypes.c_uint32
 
 _SIGNATURES = {
     "mxfp4_quant_1x32_row": [_P, _I64, _I64, _P, _P, _INT, _P],
@@ -22,6 +23,9 @@ _SIGNATURES = {
     "mx_few_moe_workspace_bytes": [_I64, _I64, _I64, _I64, _I64],
     "mx_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C, _P,
                    _P, _SIZE, _P],
+    "fp8bw_selftest_few_linear": [_P, _P, _P, _INT, _I64, _I64, _I64, _P, _P, _SIZE, _U32, _P],
+    "fp8bw_selftest_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C,
+                               _P, _P, _SIZE, _U32, _P],
 }
 
 _LIB = None
@@ -57,25 +61,42 @@ def mx_few_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib().mx_few_linear_workspace_bytes(M, N, K))
 
 
-def mx_few_linear(x, w, e8, bits, y, workspace=None, stream=None) -> None:
+def _linear_args(x, w, e8, bits, y, workspace):
     M, K = x.shape
     N, n = w.shape[0], 0 if workspace is None else workspace.shape[0]
-    B._check(lib().mx_few_linear(_arg(x, _BF16, "x", M, K), _arg(w, _U8, "w", N, K * bits // 8),
-                                 _arg(e8, _U8, "e8", N, K // 32), bits, M, N, K, _arg(y, _BF16, "y", M, N),
-                                 _arg(workspace, _U8, "workspace", n), n, _stream(stream, x)))
+    return (_arg(x, _BF16, "x", M, K), _arg(w, _U8, "w", N, K * bits // 8), _arg(e8, _U8, "e8", N, K // 32), bits, M, N, K,
+            _arg(y, _BF16, "y", M, N), _arg(workspace, _U8, "workspace", n), n)
+
+
+def mx_few_linear(x, w, e8, bits, y, workspace=None, stream=None) -> None:
+    B._check(lib().mx_few_linear(*_linear_args(x, w, e8, bits, y, workspace), _stream(stream, x)))
+
+
+def fp8bw_selftest_few_linear(x, w, e8, bits, y, workspace=None, wait_ns=0, stream=None) -> None:
+    B._check(lib().fp8bw_selftest_few_linear(*_linear_args(x, w, e8, bits, y, workspace), wait_ns, _stream(stream, x)))
 
 
 def mx_few_moe_workspace_bytes(M: int, E: int, top_k: int, C: int, F: int) -> int:
     return int(lib().mx_few_moe_workspace_bytes(M, E, top_k, C, F))
 
 
-def mx_few_moe(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups=1, groups_kept=1, group_top=1,
-               score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None) -> None:
+def _moe_args(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups, groups_kept, group_top, score, renorm, scale):
     M, C = x.shape
     E, F2 = w13.shape[:2]
     F, n = F2 // 2, workspace.shape[0]
-    B._check(lib().mx_few_moe(_arg(x, _BF16, "x", M, C), _arg(router, _F32, "router", E, C), _arg(bias, _F32, "bias", E),
-                              _arg(w13, _U8, "w13", E, 2 * F, C * bits // 8), _arg(e13, _U8, "e13", E * 2 * F, C // 32),
-                              _arg(w2, _U8, "w2", E, C, F * bits // 8), _arg(e2, _U8, "e2", E * C, F // 32), bits, M, E,
-                              top_k, C, F, groups, groups_kept, group_top, score, int(renorm), scale,
-                              _arg(y, _BF16, "y", M, C), _arg(workspace, _U8, "workspace", n), n, _stream(stream, x)))
+    return (_arg(x, _BF16, "x", M, C), _arg(router, _F32, "router", E, C), _arg(bias, _F32, "bias", E),
+            _arg(w13, _U8, "w13", E, 2 * F, C * bits // 8), _arg(e13, _U8, "e13", E * 2 * F, C // 32),
+            _arg(w2, _U8, "w2", E, C, F * bits // 8), _arg(e2, _U8, "e2", E * C, F // 32), bits, M, E, top_k, C, F, groups,
+            groups_kept, group_top, score, int(renorm), scale, _arg(y, _BF16, "y", M, C), _arg(workspace, _U8, "workspace", n), n)
+
+
+def mx_few_moe(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups=1, groups_kept=1, group_top=1,
+               score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None) -> None:
+    B._check(lib().mx_few_moe(*_moe_args(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups, groups_kept,
+                                         group_top, score, renorm, scale), _stream(stream, x)))
+
+
+def fp8bw_selftest_few_moe(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups=1, groups_kept=1, group_top=1,
+                           score=SCORE_SOFTMAX, renorm=True, scale=1.0, wait_ns=0, stream=None) -> None:
+    B._check(lib().fp8bw_selftest_few_moe(*_moe_args(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups,
+                                                     groups_kept, group_top, score, renorm, scale), wait_ns, _stream(stream, x)))
