@@ -16,7 +16,7 @@
  * below; weights are what their codes stand for, sums run in fp32, and the
  * result is rounded once to bf16.  (The grouped GEMM of fp8bw.h reads tokens
  * that are rounded to MXFP8 once.)  A token with an infinity or a NaN gives
- * NaN.  No result depends on the order in which blocks run.
+ * NaN (of a layer whose bias leaves no expert, zeros as of any token).  No result depends on the order in which blocks run.
  */
 #ifndef FP8BW_FEW_H
 #define FP8BW_FEW_H

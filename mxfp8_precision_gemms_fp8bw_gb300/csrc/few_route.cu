@@ -70,6 +70,14 @@ __device__ __forceinline__ void thirds(float a, float b, uint32_t (&out)[3]) {
   out[2] = pair(a - cut(a), b - cut(b));
 }
 
+// Two bf16 whose infinities have become NaN (times 0, and that on top): a token with one has no logit that means anything, and
+// one of -inf would leave the token without the expert.
+__device__ __forceinline__ uint32_t finite_or_nan(uint32_t v) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(d) : "r"(v), "r"(0u));
+  return d;
+}
+
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -228,13 +236,15 @@ __global__ void __launch_bounds__(kThreads, kPer == 32 ? 1 : 2) few_route_kernel
     for (int c = first + slice * 16 + q * 4; c < last; c += p.slices * 16) {
       // The sum goes over 16 features at a time, in an order that suits the loads: a lane has four next to each other.
       uint4 r[2];
-      uint2 x[4];
+      uint2 x[4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         r[h] = load_shared_after(reinterpret_cast<const uint4*>(p.router + static_cast<int64_t>(min(e0 + g + h * 8, E - 1)) * p.C + c));
 #pragma unroll
       for (int t = 0; t < 4; ++t)  // past the last token that one again
         if (t < tiles) x[t] = load_shared_after(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(min(t * 8 + g, M - 1)) * p.C + c));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) x[t].x = finite_or_nan(x[t].x), x[t].y = finite_or_nan(x[t].y);
       uint32_t part[4][3];  // as the product takes them: rows g, g + 8, features 4 q and the next; the two after those
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
