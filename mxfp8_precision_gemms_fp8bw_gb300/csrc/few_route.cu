@@ -19,7 +19,8 @@ namespace {
 //      the features as well), and sends each logit's share to the block that
 //      makes the token's choice.  The products are the tensor core's: a weight
 //      of the router, fp32, is the sum of three bf16, exactly, a token's value is
-//      one, products of two are exact and sums fp32: 2.2 us for 17 tokens and 64
+//      one, products of two are exact and sums fp32 (16 features by the tensor
+//      core, those then added as ever): 2.2 us for 17 tokens and 64
 //      experts of 2048 features, 1.0 for one token.  Fused multiply-adds took 5.5
 //      (shared memory or the cache, whichever the operands came from, had more to
 //      hand out than this step has time for) and 0.7.
@@ -254,11 +255,16 @@ __global__ void __launch_bounds__(kThreads, kPer == 32 ? 1 : 2) few_route_kernel
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if (t >= tiles) break;
+        // 16 features alone: the tensor core cuts off what is below the last bit of the largest term, which on top of the sum
+        // so far would be of the whole logit.  That one is rounded to the nearest.
+        float f[4] = {};
 #pragma unroll
         for (int i = 2; i >= 0; --i) {
           const uint32_t a[4] = {part[0][i], part[1][i], part[2][i], part[3][i]};
-          mma_bf16(v[t], a, x[t].x, x[t].y);
+          mma_bf16(f, a, x[t].x, x[t].y);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[t][i] += f[i];
       }
     }
     const auto each = [&](auto&& to) {
