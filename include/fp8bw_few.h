@@ -10,13 +10,13 @@
  * first: bit 3 the sign, codes 0 to 7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4
  * and 6.  An E8M0 byte of 255 makes its block NaN.
  *
- * Products here round nothing that matters on the way in: a token is read as
- * the sum of two MXFP8 numbers, which is the bf16 value itself down to 2^-12 of
- * the largest element of its block of 32, and off by at most 2^-21 of that
- * below; weights are what their codes stand for, sums run in fp32, and the
+ * Products read a token as the sum of two MXFP8 numbers: that is the bf16 value
+ * itself down to 2^-12 of the largest element of its block of 32, and off by at
+ * most 2^-21 of that largest below that; weights are what their codes stand for, sums run in fp32, and the
  * result is rounded once to bf16.  (The grouped GEMM of fp8bw.h reads tokens
  * that are rounded to MXFP8 once.)  A token with an infinity or a NaN gives
- * NaN (of a layer whose bias leaves no expert, zeros as of any token).  No result depends on the order in which blocks run.
+ * NaN (of a layer whose bias leaves no expert, zeros as of any token).  No result
+ * depends on the order in which blocks run.
  */
 #ifndef FP8BW_FEW_H
 #define FP8BW_FEW_H

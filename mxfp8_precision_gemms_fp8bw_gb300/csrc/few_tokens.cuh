@@ -23,6 +23,12 @@ constexpr uint32_t kAll = 0xffffffffu;
 // power of two apart, and a value of 24 bits from 2^-5 of it on, which is at
 // most 2^-12 of the largest, is a multiple of that.  An infinity becomes a NaN,
 // which e4m3 has.
+//
+// A third part of the tokens would bring 2^-21 to 2^-26 and take half as many
+// columns again: 32 tokens of 8192 x 5120 in 4 bits 14.1 us where two take 12.7,
+// 8 in 8 bits 14.2 and 13.6, one 9.4 and 9.1.  What two leave counts only where
+// a weight is so small beside the block's largest element that its product is
+// too: the largest's own rounding in an fp32 sum is 2^-24 of its product.
 __device__ __forceinline__ float without_infinity(float v) {
   return fabsf(v) == INFINITY ? __uint_as_float(0x7FFFFFFFu) : v;
 }

@@ -226,8 +226,9 @@ def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
 def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None) -> torch.Tensor:
     """y = x W^T in bf16 for 0 to 32 tokens x (bf16 [M, K]) and one matrix W
     [N, K] in MX codes, 4 bits (``mx4_quantize``) or 8 (the rowwise codes of
-    ``mx_quantize_experts``).  x is not rounded to MXFP8, and sums are fp32: a
-    product for decoding, bound by the bytes of W.  It has no gradient."""
+    ``mx_quantize_experts``).  x is not rounded to MXFP8 but taken as
+    bf16 (elements below 2^-12 of the largest of their block of 32 to 2^-21 of
+    that), and sums are fp32: a product for decoding, bound by the bytes of W.  It has no gradient."""
     if stream is not None:
         with _on(stream):
             return mx_linear_few(x, w)

@@ -203,7 +203,8 @@ def ffn_few(x: torch.Tensor, router: torch.Tensor, w13: L.Mx4Weights | L.MxExper
     and ``route``, the gated experts W13 [E, 2F, C] and W2 [E, C, F] in MX codes,
     both in 4 bits or both in 8, and the weighted sum, bf16 [M, C].
 
-    Nothing is rounded to MXFP8 on the way: tokens stay bf16, h and the
+    Nothing is rounded to MXFP8 on the way: tokens stay bf16 (elements below
+    2^-12 of the largest of their block of 32 to 2^-21 of that), h and the
     activation fp32, sums are fp32 and the result is rounded once.  So it is
     closer to the weights' own product than ``MxMoEFFN.forward``, which holds
     tokens and activations in MXFP8.  C and F are multiples of 32.  It has no
