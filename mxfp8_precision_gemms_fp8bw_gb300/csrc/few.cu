@@ -240,7 +240,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x2(uint32_t taddr, uint32_t (&r)[
 __device__ void activate(const Product& p, const Run& r, int column, int i, float gate, float up) {
   const int64_t F = p.m.rows / 2, f = static_cast<int64_t>(r.block) * (kRows / 2) + i * 32;
   if (f >= F) return;
-  few::split1(gate / (1.f + expf(-gate)) * up, p.act + few_act_at(r.at, r.slot.start, few_chunks(F)), r.slot.n,
+  // gate * sigmoid(gate): far below 0 that is gate * exp(gate), which lasts where 1 + exp(-gate) is over fp32, below -88.7.
+  const bool far = gate < -80.f;
+  const float e = expf(far ? gate : -gate), silu = far ? gate * e : gate / (1.f + e);
+  few::split1(silu * up, p.act + few_act_at(r.at, r.slot.start, few_chunks(F)), r.slot.n,
               f + (threadIdx.x & 31), column);
 }
 
