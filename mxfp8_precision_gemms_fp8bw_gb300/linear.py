@@ -21,6 +21,7 @@ import math
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 from . import few_binding as FB
@@ -218,9 +219,14 @@ def _held(w: Mx4Weights | MxExpertWeights) -> tuple[torch.Tensor, torch.Tensor, 
 
 
 def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
+    """Backward and forward mode: a tensor that requires a gradient, a dual tensor whose tangent would be dropped."""
     for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
+        if t is None:
+            continue
+        if t.requires_grad and torch.is_grad_enabled():
             raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad()")
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{name} has no gradient: its input is a dual tensor of forward-mode differentiation")
 
 
 def mx_linear_few(x: torch.Tensor, w: Mx4Weights | MxExpertWeights, stream=None) -> torch.Tensor:

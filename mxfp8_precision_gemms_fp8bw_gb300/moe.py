@@ -424,7 +424,9 @@ class MxMoEFFN(torch.nn.Module):
 
     def decode(self, x: torch.Tensor, codes: tuple) -> torch.Tensor:
         """The layer for 0 to 32 tokens without gradients, with ``weight_codes()`` of either width: ``ffn_few``.  Tokens
-        and activations are not quantized, so results are not bit for bit ``forward``'s."""
+        and activations are not quantized, so results are not bit for bit ``forward``'s.  An x that requires a gradient is
+        refused while gradients are on; the layer's own parameters are constants here, so that a layer being trained can
+        decode between its steps, and the result has no graph."""
         L._refuse_grad("decode", x)
         for got, w in zip(codes, (self.w13, self.w2)):
             _check_codes(got, w, False)
