@@ -145,7 +145,7 @@ __device__ __forceinline__ bool all_of(bool ok) { return __all_sync(kAll, ok); }
 // an SM have room for.
 constexpr uint32_t kHeld = 16 * 128;
 constexpr int kMostHeld = 12;
-constexpr int kMostDepth = 5;  // of 19 KB, as small as they are, in kHalfSmem
+constexpr int kMostDepth = 5;  // of 17 KB beside tokens that are held, from 19 KB on with tokens of their own, in kHalfSmem
 struct Shared {
   // Of a stage: packed codes have landed, all of it has, its scales are in tensor memory, it has been read.
   uint64_t landed[kMostDepth], full[kMostDepth], ready[kMostDepth], empty[kMostDepth];
@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const AbortFlag ab{&sh.abort};
 
   // The runs.  t0 .. t1: the block's chunks of all matrices' one behind the other; in turn: runs.
+  // (A cluster has no more blocks than a matrix has chunks; of kDown's, which go by the most slots, some may have none.)
   const uint32_t all = (kMode == kDown ? slots : 1) * chunks;
   const int t0 = in_turn ? blockIdx.x : static_cast<int>(all * rank / p.splits);
   const int t1 = in_turn ? slots * p.tiles : static_cast<int>(all * (rank + 1) / p.splits);
@@ -741,8 +742,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                    sums[(i >> 1) * kRows + 64 + (i & 1) * 32 + lane]);
       }
     }
-    if (!many && t0 == t1)  // no share of a short contraction
-      for (int i = 0; i < one.n; ++i) sums[i * kRows + row] = 0.f;
   }
   tc_fence_before();
   __syncthreads();

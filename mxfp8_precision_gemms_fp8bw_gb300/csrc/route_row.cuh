@@ -9,7 +9,7 @@
 #include "route_math.cuh"
 
 namespace fp8bw {
-namespace {  // included by two units
+namespace {  // included by three units
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLowest = -3.4028234663852886e38f;
