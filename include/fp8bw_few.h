@@ -76,6 +76,17 @@ int mx_few_moe(const fp8bw_bf16* x, const float* router, const float* bias, cons
                int64_t groups, int64_t groups_kept, int64_t group_top, int score, int renorm, float scale, fp8bw_bf16* y,
                void* workspace, size_t workspace_bytes, void* stream);
 
+/* How the two calls divide their products on the current device, for tests and
+ * profiles (codes aligned to 32 bytes).  Of a product, six numbers: blocks of a
+ * cluster, which share the contraction; stages of a block's pipeline, at least;
+ * chunks of 128 of the contraction that a block walks through, at most (past its
+ * stages it fills them again); and whether blocks take whole tiles in turn, hold
+ * the tokens themselves, and have warps spread the 4-bit codes (0 or 1).  slices:
+ * warps of a block that share the features of 16 experts in the router's logits. */
+int mx_few_linear_shape(int64_t M, int64_t N, int64_t K, int bits, int32_t* product);
+int mx_few_moe_shape(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F, int bits, int32_t* up, int32_t* down,
+                     int32_t* slices);
+
 /* mx_few_linear and mx_few_moe whose kernels wait for no longer than wait_ns at
  * a time inside a block (0: not at all; 2,000,000,000 as the calls themselves
  * do).  Where that runs out the kernels give up, their copies land, FP8BW_ERR_TIMEOUT

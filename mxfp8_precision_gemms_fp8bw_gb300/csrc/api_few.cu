@@ -13,6 +13,11 @@ constexpr uint64_t kWaitNs = 2000000000;  // legitimate waits last microseconds
 
 bool bits_ok(int bits) { return bits == 4 || bits == 8; }
 
+void put_shape(const FewShape& s, int32_t* out) {
+  const int32_t all[6] = {s.cluster, s.stages, s.chunks, s.in_turn, s.held, s.spread};
+  for (int i = 0; i < 6; ++i) out[i] = all[i];
+}
+
 bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
   return dim_ok(M, 1) && M <= FP8BW_FEW_TOKENS && dim_ok(N, 1) && dim_ok(K, 32) && K <= kMaxWidth;
 }
@@ -186,4 +191,48 @@ FP8BW_API int fp8bw_selftest_few_moe(const fp8bw_bf16* x, const float* router, c
   if (wait_ns > kWaitNs) return fail(FP8BW_ERR_ARG, "%s: wait_ns=%u is over 2000000000", name, wait_ns);
   return few_moe(name, x, router, bias, w13, e13, w2, e2, bits, M, E, top_k, C, F, groups, groups_kept, group_top, score, renorm, scale,
                  y, workspace, workspace_bytes, wait_ns, stream);
+}
+
+FP8BW_API int mx_few_linear_shape(int64_t M, int64_t N, int64_t K, int bits, int32_t* product) {
+  const char* name = "mx_few_linear_shape";
+  if (!product) return fail(FP8BW_ERR_NULL, "%s: product must be non-NULL", name);
+  if (!linear_dims_ok(M, N, K)) return fail(FP8BW_ERR_SHAPE, "%s: dims that mx_few_linear refuses", name);
+  if (!bits_ok(bits)) return fail(FP8BW_ERR_ARG, "%s: bits %d is neither 4 nor 8", name, bits);
+  DeviceState* d;
+  if (int rc = current_device(&d)) return rc;
+  FewLinearArgs a{};
+  a.bits = bits;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.num_sms = d->num_sms;
+  a.x = reinterpret_cast<const uint16_t*>(kMaxWidth);  // some address: nothing is read
+  FewShape shape{};
+  const int rc = launched(launch_few_linear(a, nullptr, &shape), name);
+  put_shape(shape, product);
+  return rc;
+}
+
+FP8BW_API int mx_few_moe_shape(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F, int bits, int32_t* up, int32_t* down,
+                               int32_t* slices) {
+  const char* name = "mx_few_moe_shape";
+  if (!up || !down || !slices) return fail(FP8BW_ERR_NULL, "%s: up, down and slices must be non-NULL", name);
+  if (!layer_dims_ok(M, E, top_k, C, F)) return fail(FP8BW_ERR_SHAPE, "%s: dims that mx_few_moe refuses", name);
+  if (!bits_ok(bits)) return fail(FP8BW_ERR_ARG, "%s: bits %d is neither 4 nor 8", name, bits);
+  DeviceState* d;
+  if (int rc = current_device(&d)) return rc;
+  FewMoeArgs a{};
+  a.bits = bits;
+  a.C = C;
+  a.F = F;
+  a.route.M = M;
+  a.route.E = E;
+  a.route.top_k = top_k;
+  a.num_sms = d->num_sms;
+  FewShape of_up{}, of_down{};
+  const int rc = launched(launch_few_moe(a, nullptr, &of_up, &of_down), name);
+  put_shape(of_up, up);
+  put_shape(of_down, down);
+  *slices = few_route_slices(E, C);
+  return rc;
 }

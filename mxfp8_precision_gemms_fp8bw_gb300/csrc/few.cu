@@ -907,9 +907,10 @@ cudaError_t launch(const CUtensorMap& map, const Product& p, uint32_t smem, dim3
   return cudaLaunchKernelEx(&cfg, kernel, map, p);
 }
 
-// matrices: how many lie behind each other along the contraction (kDown), copies: how many share the grid (kUp).
+// How a product is divided: p's sizes, the grid and the shared memory of a block.  matrices: how many lie behind each other along
+// the contraction (kDown), copies: how many share the grid (kUp).
 template <Mode kMode, int kBits>
-cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st) {
+cudaError_t divide(Product& p, int matrices, int copies, int num_sms, dim3* grid, uint32_t* smem) {
   const int parts = kMode == kDown ? kActParts : kTokenParts;
   const int64_t rows = kMode == kUp ? p.m.rows / 2 : p.m.rows, tile = kMode == kUp ? kRows / 2 : kRows;
   const int64_t tiles = (rows + tile - 1) / tile;
@@ -963,20 +964,43 @@ cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, i
                                      : (many ? 2 : 1) * p.columns + tmem_scales(scale_columns_of(1), depth);
   p.tmem = 32;
   while (p.tmem < columns && p.tmem < 256) p.tmem *= 2;
-  const dim3 grid = in_turn ? dim3(static_cast<unsigned>(2 * num_sms))
-                            : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
-  CUtensorMap map{};
-  if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, static_cast<uint32_t>(tile))) return cudaErrorInvalidValue;
-  return launch<kMode, kBits>(map, p, beside + p.ring, grid, st);
+  *grid = in_turn ? dim3(static_cast<unsigned>(2 * num_sms))
+                  : dim3(static_cast<unsigned>(tiles * p.splits), static_cast<unsigned>(copies));
+  *smem = beside + p.ring;
+  return cudaSuccess;
 }
 
+template <Mode kMode, int kBits>
+cudaError_t launch_sized(Product p, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st) {
+  dim3 grid;
+  uint32_t smem = 0;
+  if (const cudaError_t e = divide<kMode, kBits>(p, matrices, copies, num_sms, &grid, &smem)) return e;
+  CUtensorMap map{};
+  const uint32_t box = kMode == kUp ? kRows / 2 : kRows;
+  if (!weights_map(&map, p.m, experts * p.m.rows, kBits, p.packed, box)) return cudaErrorInvalidValue;
+  return launch<kMode, kBits>(map, p, smem, grid, st);
+}
+
+// Launches a product, or, with a shape to fill, says how it would be divided.
 template <Mode kMode>
-cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st) {
+cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matrices, int copies, int num_sms, cudaStream_t st,
+                           FewShape* shape) {
   // A runtime call binds the device's context to a thread that has made none yet; the driver's encoder does not.
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev)) return e;
-  return bits == 4 ? launch_sized<kMode, 4>(p, experts, matrices, copies, num_sms, st)
-                   : launch_sized<kMode, 8>(p, experts, matrices, copies, num_sms, st);
+  if (shape == nullptr)
+    return bits == 4 ? launch_sized<kMode, 4>(p, experts, matrices, copies, num_sms, st)
+                     : launch_sized<kMode, 8>(p, experts, matrices, copies, num_sms, st);
+  Product q = p;
+  dim3 grid;
+  uint32_t smem = 0;
+  if (const cudaError_t e = bits == 4 ? divide<kMode, 4>(q, matrices, copies, num_sms, &grid, &smem)
+                                      : divide<kMode, 8>(q, matrices, copies, num_sms, &grid, &smem))
+    return e;
+  const int chunks = (q.m.K + kChunk - 1) / kChunk * (kMode == kDown ? matrices : 1);
+  *shape = FewShape{q.splits, stages_of(kMode == kDown ? kMostDepth : q.stages.depth, q.ring, q.stages.tokens, q.packed).depth,
+                    (chunks + q.splits - 1) / q.splits, q.tiles > 0, q.x != nullptr, q.packed};
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -992,7 +1016,7 @@ static bool held_tokens(int64_t M, int64_t N, int64_t K) {
 
 size_t few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return held_tokens(M, N, K) ? 0 : few_tokens_bytes(M, K); }
 
-cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
+cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st, FewShape* shape) {
   Product p{};
   p.m = Matrix{a.w, a.e8, a.N * (a.K / 32), a.N, static_cast<int>(a.K)};
   p.M = static_cast<int>(a.M);
@@ -1001,7 +1025,7 @@ cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
   p.wait_ns = a.wait_ns;
   if (held_tokens(a.M, a.N, a.K)) {
     p.x = a.x;
-  } else {
+  } else if (shape == nullptr) {
     uint8_t* tokens = static_cast<uint8_t*>(a.workspace);
     p.t = tokens;
     const dim3 grid(static_cast<unsigned>((a.K / 8 + 255) / 256), static_cast<unsigned>(a.M));
@@ -1016,7 +1040,7 @@ cudaError_t launch_few_linear(const FewLinearArgs& a, cudaStream_t st) {
     cfg.numAttrs = 1;
     if (const cudaError_t e = cudaLaunchKernelEx(&cfg, few_tokens_kernel, a.x, a.K, tokens)) return e;
   }
-  return launch_product<kLinear>(p, a.bits, 1, 1, 1, a.num_sms, st);
+  return launch_product<kLinear>(p, a.bits, 1, 1, 1, a.num_sms, st, shape);
 }
 
 namespace {
@@ -1039,11 +1063,12 @@ size_t few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, i
   return scratch_of(nullptr, M, E, top_k, C, F).bytes;
 }
 
-cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
+cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st, FewShape* up_shape, FewShape* down_shape) {
   const int64_t E = a.route.E, M = a.route.M, k = a.route.top_k;
   const int active = static_cast<int>(E < M * k ? E : M * k);  // at most
   const MoeScratch s = scratch_of(a.workspace, M, E, k, a.C, a.F);
-  if (const cudaError_t e = launch_few_route(a, s.plan, s.tokens, st)) return e;
+  if (up_shape == nullptr)
+    if (const cudaError_t e = launch_few_route(a, s.plan, s.tokens, st)) return e;
   Product up{};
   up.m = Matrix{a.w13, a.e13, E * 2 * a.F * (a.C / 32), 2 * a.F, static_cast<int>(a.C)};
   up.M = static_cast<int>(M);
@@ -1053,7 +1078,7 @@ cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
   up.act = s.act;
   up.status = a.route.status;
   up.wait_ns = a.wait_ns;
-  if (const cudaError_t e = launch_product<kUp>(up, a.bits, E, 1, active, a.num_sms, st)) return e;
+  if (const cudaError_t e = launch_product<kUp>(up, a.bits, E, 1, active, a.num_sms, st, up_shape)) return e;
   Product down{};
   down.m = Matrix{a.w2, a.e2, E * a.C * (a.F / 32), a.C, static_cast<int>(a.F)};
   down.M = static_cast<int>(M);
@@ -1063,7 +1088,7 @@ cudaError_t launch_few_moe(const FewMoeArgs& a, cudaStream_t st) {
   down.y = a.y;
   down.status = a.route.status;
   down.wait_ns = a.wait_ns;
-  return launch_product<kDown>(down, a.bits, E, active, 1, a.num_sms, st);
+  return launch_product<kDown>(down, a.bits, E, active, 1, a.num_sms, st, down_shape);
 }
 
 }  // namespace fp8bw

@@ -32,6 +32,8 @@ namespace {
 constexpr int kBlocks = 16, kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMostRows = kFewTokens / kBlocks;  // tokens of a block
 
+int share_of(int64_t C) { return static_cast<int>((C + 32 * kBlocks - 1) / (32 * kBlocks) * 32); }
+
 struct RouteFew {
   const uint16_t* x;
   const float* router;
@@ -420,6 +422,11 @@ static cudaError_t launch(const RouteFew& p, int smem, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+int few_route_slices(int64_t E, int64_t C) {
+  const int most = share_of(C) / 16, work = static_cast<int>((E + 15) / 16);
+  return work >= kWarps ? 1 : kWarps / work < most ? kWarps / work : most;
+}
+
 cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, uint8_t* tokens, cudaStream_t st) {
   RouteFew p{};
   p.x = a.x;
@@ -427,10 +434,9 @@ cudaError_t launch_few_route(const FewMoeArgs& a, FewPlan* plan, uint8_t* tokens
   p.bias = a.route.bias;
   p.how = shape_of(a.route);
   p.C = static_cast<int>(a.C);
-  p.share = (p.C + 32 * kBlocks - 1) / (32 * kBlocks) * 32;
+  p.share = share_of(a.C);
   const int M = static_cast<int>(a.route.M), E = p.how.E;
-  const int most = p.share / 16, work = (E + 15) / 16;
-  p.slices = work >= kWarps ? 1 : kWarps / work < most ? kWarps / work : most;
+  p.slices = few_route_slices(E, a.C);
   p.plan = plan;
   p.held = tokens;
   const int smem = layout_of(M, E, p.how.k, p.slices, p.how.groups).total * 4;

@@ -196,7 +196,12 @@ struct FewLinearArgs {
   uint64_t wait_ns;  // of a wait in the kernels, at most
 };
 size_t few_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
-cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st);
+// How a product of a few tokens is divided (fp8bw_few.h).
+struct FewShape {
+  int cluster, stages, chunks, in_turn, held, spread;
+};
+// With a shape to fill nothing is launched, here and below.
+cudaError_t launch_few_linear(const FewLinearArgs& args, cudaStream_t st, FewShape* shape = nullptr);
 
 struct FewMoeArgs {
   const uint16_t* x;
@@ -214,7 +219,8 @@ struct FewMoeArgs {
   uint64_t wait_ns;
 };
 size_t few_moe_workspace_bytes(int64_t M, int64_t E, int64_t top_k, int64_t C, int64_t F);
-cudaError_t launch_few_moe(const FewMoeArgs& args, cudaStream_t st);
+cudaError_t launch_few_moe(const FewMoeArgs& args, cudaStream_t st, FewShape* up = nullptr, FewShape* down = nullptr);
+int few_route_slices(int64_t E, int64_t C);  // warps that share the features of 16 experts
 
 cudaError_t launch_selftest_bounded_wait(uint32_t timeout_us, int* status, cudaStream_t st);
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from typing import NamedTuple
 
 from . import binding as B
 from .moe_binding import _BF16, _F32, _F32C, _I64, _INT, _P, _SIZE, _U8, SCORE_SOFTMAX, _arg, _stream
@@ -23,6 +24,8 @@ _SIGNATURES = {
     "mx_few_moe_workspace_bytes": [_I64, _I64, _I64, _I64, _I64],
     "mx_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C, _P,
                    _P, _SIZE, _P],
+    "mx_few_linear_shape": [_I64, _I64, _I64, _INT, _P],
+    "mx_few_moe_shape": [_I64, _I64, _I64, _I64, _I64, _INT, _P, _P, _P],
     "fp8bw_selftest_few_linear": [_P, _P, _P, _INT, _I64, _I64, _I64, _P, _P, _SIZE, _U32, _P],
     "fp8bw_selftest_few_moe": [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _F32C,
                                _P, _P, _SIZE, _U32, _P],
@@ -100,3 +103,26 @@ def fp8bw_selftest_few_moe(x, router, bias, w13, e13, w2, e2, bits, top_k, y, wo
                            score=SCORE_SOFTMAX, renorm=True, scale=1.0, wait_ns=0, stream=None) -> None:
     B._check(lib().fp8bw_selftest_few_moe(*_moe_args(x, router, bias, w13, e13, w2, e2, bits, top_k, y, workspace, groups,
                                                      groups_kept, group_top, score, renorm, scale), wait_ns, _stream(stream, x)))
+
+
+class ProductShape(NamedTuple):
+    """How a product is divided."""
+    cluster: int
+    stages: int
+    chunks: int
+    in_turn: int
+    held: int
+    spread: int
+
+
+def mx_few_linear_shape(M: int, N: int, K: int, bits: int) -> ProductShape:
+    product = (ctypes.c_int32 * 6)()
+    B._check(lib().mx_few_linear_shape(M, N, K, bits, product))
+    return ProductShape(*product)
+
+
+def mx_few_moe_shape(M: int, E: int, top_k: int, C: int, F: int, bits: int) -> tuple[ProductShape, ProductShape, int]:
+    """Of the two products, and the slices of the logits."""
+    up, down, slices = (ctypes.c_int32 * 6)(), (ctypes.c_int32 * 6)(), (ctypes.c_int32 * 1)()
+    B._check(lib().mx_few_moe_shape(M, E, top_k, C, F, bits, up, down, slices))
+    return ProductShape(*up), ProductShape(*down), slices[0]

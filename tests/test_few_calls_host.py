@@ -1,4 +1,6 @@
 """More host-side checks of the calls for a few tokens (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 from torch.autograd import forward_ad
@@ -77,3 +79,14 @@ def test_decode_takes_a_layer_whose_parameters_require_gradients():
     assert all(p.requires_grad for p in layer.parameters())
     with pytest.raises(ValueError, match="CUDA"):
         layer.decode(torch.zeros(2, 256, dtype=torch.bfloat16), (codes4(4, 1024, 256), codes4(4, 256, 512)))
+
+
+def test_shapes_refuse_what_the_calls_refuse(lib):
+    out = (ctypes.c_int32 * 6)()
+    assert lib.mx_few_linear_shape(33, 64, 2048, 4, out) == B.ERR_SHAPE
+    assert lib.mx_few_linear_shape(1, 64, 2048, 5, out) == B.ERR_ARG
+    assert lib.mx_few_linear_shape(1, 64, 2048, 4, None) == B.ERR_NULL
+    assert lib.mx_few_moe_shape(1, 8, 9, 64, 96, 4, out, out, out) == B.ERR_SHAPE
+    assert lib.mx_few_moe_shape(1, 8, 2, 64, 96, 6, out, out, out) == B.ERR_ARG
+    for i in range(3):
+        assert lib.mx_few_moe_shape(1, 8, 2, 64, 96, 4, *(None if i == j else out for j in range(3))) == B.ERR_NULL
