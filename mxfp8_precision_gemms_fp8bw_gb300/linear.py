@@ -220,12 +220,14 @@ def _held(w: Mx4Weights | MxExpertWeights) -> tuple[torch.Tensor, torch.Tensor, 
 
 def _refuse_grad(name: str, *tensors: torch.Tensor | None) -> None:
     """Backward and forward mode: a tensor that requires a gradient, a dual tensor whose tangent would be dropped."""
+    # outside of a dual level there are none, and unpack_dual takes half a microsecond a tensor
+    forward = getattr(forward_ad, "_current_level", 0) >= 0
     for t in tensors:
         if t is None:
             continue
         if t.requires_grad and torch.is_grad_enabled():
             raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad()")
-        if forward_ad.unpack_dual(t).tangent is not None:
+        if forward and forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{name} has no gradient: its input is a dual tensor of forward-mode differentiation")
 
 
