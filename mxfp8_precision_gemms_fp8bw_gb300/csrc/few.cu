@@ -13,17 +13,20 @@
 //
 // Measured, one call behind the other, of weights larger than the cache where
 // they are: up of 8 experts 5120 -> 4096, 8 bits, 32 tokens 59 us (5.9 TB/s),
-// their down product 38 us (4.6 TB/s).  A linear of 8192 x 16384 for 4 tokens
+// their down product 40 us (4.3 TB/s).  A linear of 8192 x 16384 for 4 tokens
 // 28 us in 8 bits (4.9 TB/s), 20 in 4 (3.5 TB/s); of 8192 x 5120 13 and 9; of
 // 2048 x 2048, one token, 4.8.  What bounds them:
 //   8 bits          memory: longer rows come at 6.6 TB/s, 0.97 of the copy
 //                   bandwidth
-//   4 bits          the way of a chunk: longer rows come at 4.8 TB/s.  No part of
-//                   it alone holds them there: of the 20 us of 8192 x 16384, 19
-//                   remain without products, 19 without scales, 18 without both
-//                   and 18 with the weights in the cache; half of the rows by
-//                   cp.async in place of TMA, a fifth stage, or chunks asked for
-//                   ahead into the cache change 2 % or cost some
+//   4 bits          the way of a chunk, 0.4 us in each of two blocks an SM, as
+//                   long as one of 8 bits takes from the cache: longer rows come
+//                   at 4.8 TB/s.  Of the 20 us of 8192 x 16384, 19 remain without
+//                   products, 19 without scales, 18 without both, 18 with the
+//                   weights in the cache, 19 with codes left packed, and 18 with
+//                   six stages of such codes in place of five.  Not the rows that
+//                   TMA asks for (8 bits in boxes of 64 bytes a row take 3 %
+//                   more), and half of those by cp.async, a fifth stage, or chunks
+//                   asked for ahead into the cache change 2 % or cost some
 //   short products  a start of about 4 us with the pipeline's first chunks, and,
 //                   of a cluster, 1 to 2 us for blocks to meet and sum (3 for
 //                   more than 16 tokens)
@@ -833,14 +836,16 @@ int places(int size) {
 //   sums meet where the stages were, once all blocks have read theirs;
 //   and blocks that share SMs.
 // The numbers are fitted to 64 linears (1 to 32 tokens, 2048 x 2048 to 8192 x 16384) and six products of layers, each with every
-// size of cluster: the choice takes 0.6 % longer than the best on average, 17 % at most.  By blocks of a cluster, us:
+// size of cluster.  Of those same products, none of others, the choice takes 0.6 % longer than the best on average, 17 % at most:
+// that is where one block a tile gives under 128 blocks, to which the rates are only drawn out (8192 x 5120, 8 bits, 32 tokens:
+// 18.2 us with one block a tile, as chosen, 16.7 with two, 16.2 with four).  By blocks of a cluster, us:
 //   linear, 4 bits,  4 tokens, 2048 x 2048     1: 6.7    2: 6.8    4: 5.9 *  8: 7.5
 //                              8192 x 5120     1: 11.2   2: 9.1 *  4: 10.2   8: 15.5 (more blocks than places)
 //                              8192 x 16384    1: 31.7   2: 21.5   4: 20.1 * 8: 25.4
 //                              1024 x 8192     1: 15.5   2: 11.4   4: 8.6    8: 7.5 *
 //                   32 tokens, 4096 x 4096     1: 12.7   2: 11.8   4: 9.9 *  8: 12.7
-//   up of two experts 5120 -> 4096, 4 bits     1: 27.6 * 2: 28.7   4: 33.3 (the whole layer)
-//   down of 8 experts 4096 -> 5120, 8 bits     4: 99.5   5: 97.0   6: 95.6 * 8: 106.6
+//   up of two experts 5120 -> 4096, 4 bits     1: 28.0 * 2: 31.0   4: 35.9 (the whole layer, here and below)
+//   down of 8 experts 4096 -> 5120, 8 bits     4: 103.2  5: 100.4  6: 99.2 * 8: 112.5
 int splits_of(int64_t tiles, int64_t chunks, int bits, int tokens, bool slow, int num_sms, const int (&room)[8]) {
   const double exchange[8] = {0., 5.4, 11.8, 6.2, 6.9, 7.8, 9.3, 9.5};
   const double rates[2] = {bits == 4 ? 118. : 60., bits == 4 ? 124. : 69.};  // with 128 blocks, with 256
@@ -1009,7 +1014,9 @@ cudaError_t launch_product(const Product& p, int bits, int64_t experts, int matr
 // no block follows another, with the tokens once more: 9.1 us for one token of 8192 x 5120 in 4 bits, 13.8 with the kernel in
 // front; but 44 us for 65536 x 4096, 32 with it.  Eight tokens (8 bits) took 16.9 us so, 14.1 with it.
 static bool held_tokens(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t kPlaces = 288;  // two blocks an SM in clusters of eight
+  // Two blocks an SM in clusters of eight on a GB300.  The workspace's size goes by it, which a host without the device may ask
+  // for; on another number of SMs the choice would be as right, and slower or faster.
+  constexpr int64_t kPlaces = 288;
   const int64_t splits = (K + kMostHeld * kChunk - 1) / (kMostHeld * kChunk);
   return M <= 2 && splits <= 8 && (N + kRows - 1) / kRows * splits <= kPlaces;
 }

@@ -19,10 +19,10 @@ constexpr uint32_t kAll = 0xffffffffu;
 // up has no fewer bits than the sums of the first.  With codes down to 2^E of
 // a part that are 2^(E-9) apart, the largest of a block in [224, 448] 2^E, E
 // falls by 4 from the first part to the second and by 5 from each of the
-// others to the next, which keeps what is left under 448 2^E, so that the fifth's codes are 2^-28 of the first's
-// power of two apart, and a value of 24 bits from 2^-5 of it on, which is at
-// most 2^-12 of the largest, is a multiple of that.  An infinity becomes a NaN,
-// which e4m3 has.
+// others to the next, which keeps what is left under 448 2^E, so that the
+// fifth's codes are 2^-28 of the first's power of two apart, and a value of 24
+// bits from 2^-5 of it on, which is at most 2^-12 of the largest, is a multiple
+// of that.  An infinity becomes a NaN, which e4m3 has.
 //
 // A third part of the tokens would bring 2^-21 to 2^-26 and take half as many
 // columns again: 32 tokens of 8192 x 5120 in 4 bits 14.1 us where two take 12.7,
