@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // start, so kDown reads it, and starts on the weights, while that kernel still runs.
   int slots = 1;
   Stages stages = p.stages;
-  int columns = p.columns, scale_columns = scale_columns_of(1), accs = many ? 2 : 1;  // of an accumulator, of a stage's scales; accumulators
+  int columns = p.columns, scale_columns = scale_columns_of(1), accs = many ? 2 : 1;  // accumulators, and columns of one
   FewSlot one{0, 0, 0xffffffffu >> (32 - p.M), p.M};
   if constexpr (kMode == kUp) {
     grid_wait();
@@ -922,7 +922,8 @@ cudaError_t divide(Product& p, int matrices, int copies, int num_sms, dim3* grid
   const int chunks = (p.m.K + kChunk - 1) / kChunk;
   p.columns = (p.M * parts + 15) / 16 * 16;
   p.packed = kBits == 4 && (p.m.K % kChunk != 0 || (reinterpret_cast<uintptr_t>(p.m.w) & 31) != 0);
-  const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + static_cast<uint32_t>(few_scale_bytes(p.columns)), stage = stages_of(0, 0, tokens, p.packed).bytes;
+  const uint32_t tokens = p.x != nullptr ? 0 : p.columns * 128 + static_cast<uint32_t>(few_scale_bytes(p.columns));
+  const uint32_t stage = stages_of(0, 0, tokens, p.packed).bytes;
   // Enough runs for every block to have some: whole ones in turn, which leaves the stages no gaps (17 tokens over 64 experts 46.8
   // us, otherwise 50.5), where their sums leave room for two blocks of three stages an SM.
   const uint32_t sums = p.M * kRows * 4, slot = sizeof(FewSlot);
